@@ -350,8 +350,8 @@ def _scores(x, score):
     p = torch.exp(x - top)
     width = 1 << (x.shape[1] - 1).bit_length()
     t = torch.nn.functional.pad(p, (0, width - x.shape[1]))
-    while t.shape[1] > 1:   # the sum by halving: v[j] + v[j + n/2]
-        t = t[:, : t.shape[1] // 2] + t[:, t.shape[1] // 2:]
+    while t.shape[1] > 1:   # the sum by adjacent pairs
+        t = t[:, 0::2] + t[:, 1::2]
     return torch.where(top == -math.inf, 0.0, p / t)
 
 
