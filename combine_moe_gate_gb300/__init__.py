@@ -8,7 +8,9 @@ is missing, importing the entry points raises.
 Functions keep the C names:
     moe_gate_topk, moe_capacity_locations, moe_capacity_locations_noalloc,
     moe_encode, moe_expert_ffn,
-    moe_decode, moe_decode_bwd, moe_encode_bwd, moe_layer_forward, moe_gate_bwd
+    moe_decode, moe_decode_bwd, moe_encode_bwd, moe_layer_forward, moe_gate_bwd,
+    moe_route_topk, moe_route_bwd,
+    moe_quantize_fp4, moe_dequantize_fp4, moe_product_fp4, moe_expert_ffn_fp4
 plus the size queries and `MoEError`.
 """
 
@@ -23,6 +25,8 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_gate.h")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_CAPACITY, MOE_ERR_TIMEOUT = range(6)
 MOE_F32, MOE_BF16 = 0, 1
 ACT = {"relu": 0, "gelu": 1, "swiglu": 2}
+SCORE = {"softmax": 0, "sigmoid": 1}
+FP4 = {"mx": 0, "nv": 1}
 MOE_FLAG_NORMALIZE_GATES = 1
 MOE_FLAG_ZERO_FILL = 2
 
@@ -76,6 +80,15 @@ def load():
         "moe_quantize_rows_fp8": (I, [P, I64, I64, I, P, P, P, P, P, P]),
         "moe_expert_ffn_fp8_workspace_size": (SZ, [I, I64, I, I]),
         "moe_expert_ffn_fp8": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I64, I, I, P, SZ, P, P, P]),
+        "moe_route_topk": (I, [P, I, P, I64, I, I, I, I, I, I, F, U, P, P, P, P]),
+        "moe_route_bwd": (I, [P, I, P, P, I64, I, I, I, F, U, P, I, P, P]),
+        "moe_fp4_scale_bytes": (SZ, [I, I64, I]),
+        "moe_quantize_fp4": (I, [P, I, I64, I64, I, I, P, P, P, P, P, P, P]),
+        "moe_dequantize_fp4": (I, [P, P, I64, I64, I, I, P, P, P, P, I, P, P]),
+        "moe_product_fp4": (I, [P, P, P, P, P, P, P, P, P, I, I, I64, I, I, P, P, P]),
+        "moe_expert_ffn_fp4_workspace_size": (SZ, [I, I, I, I64, I, I]),
+        "moe_expert_ffn_fp4": (I, [P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, I, I, I, I64, I,
+                                   I, P, SZ, P, P, P]),
         "moe_status_str": (ctypes.c_char_p, [I]),
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_debug_stall_gemms": (I, [I]),
@@ -168,6 +181,14 @@ def _check(code, where):
 
 def _act(act):
     return ACT[act] if isinstance(act, str) else int(act)
+
+
+def _code(table, v, name):
+    if isinstance(v, str):
+        if v not in table:
+            raise ValueError(f"{name}: {v!r}, expected one of {sorted(table)}")
+        return table[v]
+    return int(v)
 
 
 # ------------------------------------------------------------------ sizes
@@ -315,6 +336,138 @@ def moe_expert_ffn_fp8(buf_q, buf_scale, counts, c_dev, w1_q, w1_scale, b1, w2_q
         m, h, _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         _ptr(out, "out", bf, (e, c_max, m)), _ptr(dev_status, "dev_status", I), _stream(stream)),
         "moe_expert_ffn_fp8")
+
+
+# ------------------------------------------------------- routing from logits
+def moe_route_topk(logits, bias, k, idx, gates, dev_status, score="softmax", groups=1,
+                   topk_groups=1, group_top=1, scale=1.0, flags=0, stream=None):
+    """logits [s, e] fp32 or bf16; bias [e] fp32 or None (steers the choice
+    only) -> idx [k, s] int32, gates [k, s] fp32.  score "softmax" or
+    "sigmoid"; the experts of the topk_groups best of `groups` runs compete, a
+    group ranked by the sum of its group_top best; MOE_FLAG_NORMALIZE_GATES
+    divides the gates by their sum, then `scale` multiplies them."""
+    s, e = logits.shape
+    k = int(k)
+    I, F = _i32(), _f32()
+    _check(load().moe_route_topk(
+        _ptr(logits, "logits"), _dt(logits), _ptr(bias, "bias", F, (e,)), s, e, k,
+        _code(SCORE, score, "score"), int(groups), int(topk_groups), int(group_top), float(scale),
+        int(flags), _ptr(idx, "idx", I, (k, s)), _ptr(gates, "gates", F, (k, s)),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_route_topk")
+
+
+def moe_route_bwd(logits, idx, d_gates, d_logits, dev_status, score="softmax", scale=1.0, flags=0,
+                  stream=None):
+    """Gradient of moe_route_topk's gates: d_gates [k, s] fp32 -> d_logits
+    [s, e] (fp32 or bf16); score, scale and flags as given to the forward."""
+    s, e = logits.shape
+    k = idx.shape[0]
+    I, F = _i32(), _f32()
+    _check(load().moe_route_bwd(
+        _ptr(logits, "logits"), _dt(logits), _ptr(idx, "idx", I, (k, s)),
+        _ptr(d_gates, "d_gates", F, (k, s)), s, e, k, _code(SCORE, score, "score"), float(scale),
+        int(flags), _ptr(d_logits, "d_logits", None, (s, e)), _dt(d_logits),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_route_bwd")
+
+
+# ------------------------------------------------- microscaled 4-bit operands
+def moe_fp4_scale_bytes(fmt, rows, cols) -> int:
+    """Bytes of one batch's tiled block scales (0: cols not a multiple of 32)."""
+    return int(load().moe_fp4_scale_bytes(_code(FP4, fmt, "fmt"), int(rows), int(cols)))
+
+
+def _fp4(q, scale, fmt, name, batches, rows, cols):
+    """Addresses of a 4-bit operand's codes and scales."""
+    import torch
+
+    n = moe_fp4_scale_bytes(fmt, rows, cols)
+    return (_ptr(q, name, torch.uint8, (batches, rows, cols // 2)),
+            _ptr(scale, name + "_scale", torch.uint8, (batches, n)))
+
+
+def _batched(t):
+    return tuple(t.shape) if t.dim() == 3 else (1,) + tuple(t.shape)
+
+
+def moe_quantize_fp4(src, fmt, q, scale, dev_status, global_scale=None, counts=None, c_dev=None,
+                     stream=None):
+    """4-bit codes (uint8 [..., cols/2], two a byte) and tiled block scales
+    (uint8 [batches, moe_fp4_scale_bytes]) of src [rows, cols] or [batches,
+    rows, cols] (bf16 or fp32); fmt "mx" or "nv", the latter with a factor per
+    batch (global_scale [batches] fp32, None: 1); with counts / c_dev only the
+    kept rows of each batch."""
+    b, r, c = _batched(src)
+    I = _i32()
+    qp, sp = _fp4(q if src.dim() == 3 else q.unsqueeze(0), scale, fmt, "q", b, r, c)
+    _check(load().moe_quantize_fp4(
+        _ptr(src, "src"), _dt(src), b, r, c, _code(FP4, fmt, "fmt"),
+        _ptr(global_scale, "global_scale", _f32(), (b,)), _ptr(counts, "counts", I, (b,)),
+        _ptr(c_dev, "c_dev", I), qp, sp, _ptr(dev_status, "dev_status", I), _stream(stream)),
+        "moe_quantize_fp4")
+
+
+def moe_dequantize_fp4(q, scale, fmt, dst, dev_status, global_scale=None, counts=None, c_dev=None,
+                       stream=None):
+    """The values of moe_quantize_fp4's codes and scales, into dst [rows, cols]
+    or [batches, rows, cols] (bf16 or fp32)."""
+    b, r, c = _batched(dst)
+    I = _i32()
+    qp, sp = _fp4(q if dst.dim() == 3 else q.unsqueeze(0), scale, fmt, "q", b, r, c)
+    _check(load().moe_dequantize_fp4(
+        qp, sp, b, r, c, _code(FP4, fmt, "fmt"), _ptr(global_scale, "global_scale", _f32(), (b,)),
+        _ptr(counts, "counts", I, (b,)), _ptr(c_dev, "c_dev", I), _ptr(dst, "dst"), _dt(dst),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_dequantize_fp4")
+
+
+def moe_product_fp4(a_q, a_scale, a_global, counts, c_dev, b_q, b_scale, b_global, bias, fmt, out,
+                    dev_status, stream=None):
+    """out[j] = a[j] b[j]^T (+ bias[j]) over the kept rows of every expert:
+    a_q [e, c_max, k/2], b_q [e, n, k/2] with their scales and factors ([e] fp32
+    or None), bias [e, n] bf16 or None, out [e, c_max, n] bf16."""
+    import torch
+
+    e, c_max, n = out.shape
+    k = 2 * a_q.shape[2]
+    I, F, bf = _i32(), _f32(), torch.bfloat16
+    ap, asp = _fp4(a_q, a_scale, fmt, "a_q", e, c_max, k)
+    bp, bsp = _fp4(b_q, b_scale, fmt, "b_q", e, n, k)
+    _check(load().moe_product_fp4(
+        ap, asp, _ptr(a_global, "a_global", F, (e,)), _ptr(counts, "counts", I, (e,)),
+        _ptr(c_dev, "c_dev", I), bp, bsp, _ptr(b_global, "b_global", F, (e,)),
+        _ptr(bias, "bias", bf, (e, n)), _code(FP4, fmt, "fmt"), e, c_max, k, n,
+        _ptr(out, "out", bf), _ptr(dev_status, "dev_status", I), _stream(stream)),
+        "moe_product_fp4")
+
+
+def moe_expert_ffn_fp4_workspace_size(fmt, act, e, c_max, m, h) -> int:
+    return int(load().moe_expert_ffn_fp4_workspace_size(_code(FP4, fmt, "fmt"), _act(act), int(e),
+                                                        int(c_max), int(m), int(h)))
+
+
+def moe_expert_ffn_fp4(buf_q, buf_scale, buf_global, hid_global, counts, c_dev, w1_q, w1_scale,
+                       w1_global, b1, w3_q, w3_scale, w3_global, w2_q, w2_scale, w2_global, b2, fmt,
+                       act, workspace, out, dev_status, stream=None):
+    """The expert FFN on 4-bit operands (moe_quantize_fp4 of the buffer's kept
+    rows and of the weights [e, h, m], [e, h, m], [e, m, h]); factors [e] fp32
+    or None; w3 and its scales only for SwiGLU, which takes no biases."""
+    import torch
+
+    e, c_max, m = out.shape
+    h = w1_q.shape[1]
+    I, F, bf = _i32(), _f32(), torch.bfloat16
+    xp, xsp = _fp4(buf_q, buf_scale, fmt, "buf_q", e, c_max, m)
+    w1p, w1sp = _fp4(w1_q, w1_scale, fmt, "w1_q", e, h, m)
+    w3p, w3sp = _fp4(w3_q, w3_scale, fmt, "w3_q", e, h, m)
+    w2p, w2sp = _fp4(w2_q, w2_scale, fmt, "w2_q", e, m, h)
+    _check(load().moe_expert_ffn_fp4(
+        xp, xsp, _ptr(buf_global, "buf_global", F, (e,)), _ptr(hid_global, "hid_global", F, (e,)),
+        _ptr(counts, "counts", I, (e,)), _ptr(c_dev, "c_dev", I), w1p, w1sp,
+        _ptr(w1_global, "w1_global", F, (e,)), _ptr(b1, "b1", bf, (e, h)), w3p, w3sp,
+        _ptr(w3_global, "w3_global", F, (e,)), w2p, w2sp, _ptr(w2_global, "w2_global", F, (e,)),
+        _ptr(b2, "b2", bf, (e, m)), _code(FP4, fmt, "fmt"), _act(act), e, c_max, m, h,
+        _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _ptr(out, "out", bf), _ptr(dev_status, "dev_status", I), _stream(stream)),
+        "moe_expert_ffn_fp4")
 
 
 def moe_expert_ffn_bwd(buf, hid, counts, c_dev, w1, b1, w3, w2, act, d_out, workspace, d_buf,

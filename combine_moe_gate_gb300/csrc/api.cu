@@ -2,6 +2,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "fp4.cuh"
 
 namespace moe {
 
@@ -62,6 +63,35 @@ moe_status ffn_tc_fp8_launch(const void *buf_q, const float *buf_scale, const in
                              const void *b2, moe_act act, int e, int64_t c_max, int m, int h,
                              void *hid, void *hid_q, float *hid_scale, void *out, int32_t *st,
                              cudaStream_t stream);
+moe_status route_topk_launch(const void *logits, moe_dtype ldt, const float *bias, int64_t s, int e,
+                             int k, moe_score score, int groups, int topk_groups, int group_top,
+                             float scale, unsigned flags, int32_t *idx, float *gates, int32_t *st,
+                             cudaStream_t stream);
+moe_status route_bwd_launch(const void *logits, moe_dtype ldt, const int32_t *idx,
+                            const float *d_gates, int64_t s, int e, int k, moe_score score,
+                            float scale, unsigned flags, void *d_logits, moe_dtype ddt, int32_t *st,
+                            cudaStream_t stream);
+moe_status quantize_fp4_launch(const void *src, moe_dtype sdt, int64_t batches, int64_t rpb, int cols,
+                               moe_fp4 fmt, const float *global, const int32_t *counts,
+                               const int32_t *c_dev, void *q, void *scale, int32_t *st,
+                               cudaStream_t stream);
+moe_status dequantize_fp4_launch(const void *q, const void *scale, int64_t batches, int64_t rpb,
+                                 int cols, moe_fp4 fmt, const float *global, const int32_t *counts,
+                                 const int32_t *c_dev, void *dst, moe_dtype ddt, int32_t *st,
+                                 cudaStream_t stream);
+moe_status product_fp4_launch(const void *a_q, const void *a_scale, const float *a_global,
+                              const int32_t *counts, const int32_t *c_dev, const void *b_q,
+                              const void *b_scale, const float *b_global, const void *bias,
+                              moe_fp4 fmt, int e, int64_t c_max, int k, int n, void *out,
+                              int32_t *st, cudaStream_t stream);
+moe_status ffn_fp4_launch(const void *buf_q, const void *buf_scale, const float *buf_global,
+                          const float *hid_global, const int32_t *counts, const int32_t *c_dev,
+                          const void *w1_q, const void *w1_scale, const float *w1_global,
+                          const void *b1, const void *w3_q, const void *w3_scale,
+                          const float *w3_global, const void *w2_q, const void *w2_scale,
+                          const float *w2_global, const void *b2, moe_fp4 fmt, moe_act act, int e,
+                          int64_t c_max, int m, int h, void *hid_q, void *hid_scale, void *out,
+                          int32_t *st, cudaStream_t stream);
 moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *counts,
                              const int32_t *c_dev, const void *w1, const void *b1, const void *w3,
                              const void *w2, moe_act act, int e, int64_t c_max, int m, int h,
@@ -520,6 +550,139 @@ moe_status moe_expert_ffn_fp8(const void *buf_q, const float *buf_scale, const i
     return ffn_tc_fp8_launch(buf_q, buf_scale, counts, c_dev, w1_q, w1_scale, b1, w2_q, w2_scale, b2,
                              act, e, c_max, m, h, hid, hid_q, hid_scale, out, dev_status,
                              as_stream(stream));
+}
+
+moe_status moe_route_topk(const void *logits, moe_dtype ldt, const float *bias, int64_t s, int e,
+                          int k, moe_score score, int groups, int topk_groups, int group_top,
+                          float scale, unsigned flags, int32_t *idx, float *gates,
+                          int32_t *dev_status, void *stream) {
+    if (!routing_shape_ok(s, e, k) || !valid_dt(ldt) || !ok16(logits) || !opt16(bias) ||
+        (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) || groups < 1 || groups > e ||
+        e % groups || topk_groups < 1 || topk_groups > groups ||
+        (int64_t)topk_groups * (e / groups) < k || (group_top != 1 && group_top != 2) ||
+        scale != scale || !ok4(idx) || !ok4(gates) || !ok4(dev_status) ||
+        (flags & ~MOE_FLAG_NORMALIZE_GATES))
+        return MOE_ERR_INVALID_ARG;
+    if (groups > 32) return MOE_ERR_UNSUPPORTED;
+    return route_topk_launch(logits, ldt, bias, s, e, k, score, groups, topk_groups, group_top, scale,
+                             flags, idx, gates, dev_status, as_stream(stream));
+}
+
+moe_status moe_route_bwd(const void *logits, moe_dtype ldt, const int32_t *idx,
+                         const float *d_gates, int64_t s, int e, int k, moe_score score,
+                         float scale, unsigned flags, void *d_logits, moe_dtype ddt,
+                         int32_t *dev_status, void *stream) {
+    if (!routing_shape_ok(s, e, k) || !valid_dt(ldt) || !valid_dt(ddt) || !ok16(logits) ||
+        (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) || scale != scale || !ok4(idx) ||
+        !ok4(d_gates) || !ok16(d_logits) || !ok4(dev_status) || (flags & ~MOE_FLAG_NORMALIZE_GATES))
+        return MOE_ERR_INVALID_ARG;
+    return route_bwd_launch(logits, ldt, idx, d_gates, s, e, k, score, scale, flags, d_logits, ddt,
+                            dev_status, as_stream(stream));
+}
+
+static bool fp4_ok(moe_fp4 fmt, int64_t rows, int cols) {
+    return (fmt == MOE_FP4_MX || fmt == MOE_FP4_NV) && rows >= 1 && rows <= 0x7fffffff && cols >= 32 &&
+           cols % 32 == 0;
+}
+
+size_t moe_fp4_scale_bytes(moe_fp4 fmt, int64_t rows, int cols) {
+    return fp4_ok(fmt, rows, cols) ? (size_t)fp4_scale_bytes(fp4_blk(fmt), rows, cols) : 0;
+}
+
+// What both directions of the conversion check alike.
+static bool fp4_rows_ok(const void *wide, moe_dtype dt, int64_t batches, int64_t rows, int cols,
+                        moe_fp4 fmt, const float *global, const int32_t *counts,
+                        const int32_t *c_dev, const void *q, const void *scale, const int32_t *st) {
+    return fp4_ok(fmt, rows, cols) && batches >= 1 && batches <= 0x7fffffff && valid_dt(dt) &&
+           batches * rows <= ((int64_t)1 << 40) && ok16(wide) && ok16(q) && ok16(scale) && ok4(st) &&
+           (global == nullptr || (fmt == MOE_FP4_NV && ok4(global))) &&
+           (counts == nullptr) == (c_dev == nullptr) && (!counts || (ok4(counts) && ok4(c_dev)));
+}
+
+moe_status moe_quantize_fp4(const void *src, moe_dtype sdt, int64_t batches,
+                            int64_t rows_per_batch, int cols, moe_fp4 fmt,
+                            const float *global_scale, const int32_t *counts,
+                            const int32_t *c_dev, void *q, void *scale, int32_t *dev_status,
+                            void *stream) {
+    if (!fp4_rows_ok(src, sdt, batches, rows_per_batch, cols, fmt, global_scale, counts, c_dev, q, scale,
+                     dev_status))
+        return MOE_ERR_INVALID_ARG;
+    return quantize_fp4_launch(src, sdt, batches, rows_per_batch, cols, fmt, global_scale, counts, c_dev,
+                               q, scale, dev_status, as_stream(stream));
+}
+
+moe_status moe_dequantize_fp4(const void *q, const void *scale, int64_t batches,
+                              int64_t rows_per_batch, int cols, moe_fp4 fmt,
+                              const float *global_scale, const int32_t *counts,
+                              const int32_t *c_dev, void *dst, moe_dtype ddt, int32_t *dev_status,
+                              void *stream) {
+    if (!fp4_rows_ok(dst, ddt, batches, rows_per_batch, cols, fmt, global_scale, counts, c_dev, q, scale,
+                     dev_status))
+        return MOE_ERR_INVALID_ARG;
+    return dequantize_fp4_launch(q, scale, batches, rows_per_batch, cols, fmt, global_scale, counts,
+                                 c_dev, dst, ddt, dev_status, as_stream(stream));
+}
+
+// Rows and columns within the 32-bit coordinates of the operands' tensor maps.
+static bool fp4_range_ok(int e, int64_t c_max, int64_t k, int64_t n) {
+    return (int64_t)e * c_max < ((int64_t)1 << 31) && (int64_t)e * n < ((int64_t)1 << 31) &&
+           (int64_t)e * k < ((int64_t)1 << 31);
+}
+
+static bool fp4_factor_ok(moe_fp4 fmt, const float *g) {
+    return g == nullptr || (fmt == MOE_FP4_NV && ok4(g));
+}
+
+moe_status moe_product_fp4(const void *a_q, const void *a_scale, const float *a_global,
+                           const int32_t *counts, const int32_t *c_dev, const void *b_q,
+                           const void *b_scale, const float *b_global, const void *bias,
+                           moe_fp4 fmt, int e, int64_t c_max, int k, int n, void *out,
+                           int32_t *dev_status, void *stream) {
+    if (!fp4_ok(fmt, c_max, k) || e < 1 || e > kMaxE || n < 8 || n % 8 || !ok16(a_q) ||
+        !ok16(a_scale) || !fp4_factor_ok(fmt, a_global) || !ok4(counts) || !ok4(c_dev) || !ok16(b_q) ||
+        !ok16(b_scale) || !fp4_factor_ok(fmt, b_global) || !opt16(bias) || !ok16(out) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (!fp4_range_ok(e, c_max, k, n)) return MOE_ERR_UNSUPPORTED;
+    return product_fp4_launch(a_q, a_scale, a_global, counts, c_dev, b_q, b_scale, b_global, bias, fmt, e,
+                              c_max, k, n, out, dev_status, as_stream(stream));
+}
+
+size_t moe_expert_ffn_fp4_workspace_size(moe_fp4 fmt, moe_act act, int e, int64_t c_max, int m,
+                                         int h) {
+    if (!fp4_ok(fmt, c_max, m) || !fp4_ok(fmt, c_max, h) || e < 1 || e > kMaxE ||
+        (act != MOE_ACT_RELU && act != MOE_ACT_GELU && act != MOE_ACT_SWIGLU))
+        return 0;
+    return up256((size_t)e * c_max * (h / 2)) + up256((size_t)e * moe_fp4_scale_bytes(fmt, c_max, h));
+}
+
+moe_status moe_expert_ffn_fp4(const void *buf_q, const void *buf_scale, const float *buf_global,
+                              const float *hid_global, const int32_t *counts,
+                              const int32_t *c_dev, const void *w1_q, const void *w1_scale,
+                              const float *w1_global, const void *b1, const void *w3_q,
+                              const void *w3_scale, const float *w3_global, const void *w2_q,
+                              const void *w2_scale, const float *w2_global, const void *b2,
+                              moe_fp4 fmt, moe_act act, int e, int64_t c_max, int m, int h,
+                              void *workspace, size_t workspace_bytes, void *out,
+                              int32_t *dev_status, void *stream) {
+    const size_t need = moe_expert_ffn_fp4_workspace_size(fmt, act, e, c_max, m, h);
+    if (need == 0 || !ok16(buf_q) || !ok16(buf_scale) || !fp4_factor_ok(fmt, buf_global) ||
+        !fp4_factor_ok(fmt, hid_global) || !ok4(counts) || !ok4(c_dev) || !ok16(w1_q) ||
+        !ok16(w1_scale) || !fp4_factor_ok(fmt, w1_global) || !opt16(b1) || !ok16(w2_q) ||
+        !ok16(w2_scale) || !fp4_factor_ok(fmt, w2_global) || !opt16(b2) || !ok16(workspace) ||
+        workspace_bytes < need || !ok16(out) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (act == MOE_ACT_SWIGLU) {
+        if (!ok16(w3_q) || !ok16(w3_scale) || !fp4_factor_ok(fmt, w3_global) || b1 || b2)
+            return MOE_ERR_INVALID_ARG;
+    } else if (w3_q || w3_scale || w3_global) {
+        return MOE_ERR_INVALID_ARG;
+    }
+    if (!fp4_range_ok(e, c_max, m, h) || !fp4_range_ok(e, c_max, h, m)) return MOE_ERR_UNSUPPORTED;
+    char *w = (char *)workspace;
+    return ffn_fp4_launch(buf_q, buf_scale, buf_global, hid_global, counts, c_dev, w1_q, w1_scale,
+                          w1_global, b1, w3_q, w3_scale, w3_global, w2_q, w2_scale, w2_global, b2, fmt,
+                          act, e, c_max, m, h, w, w + up256((size_t)e * c_max * (h / 2)), out,
+                          dev_status, as_stream(stream));
 }
 
 moe_status moe_probe_fp32_fma(int packed, int blocks, int iters, float *out, void *stream) {

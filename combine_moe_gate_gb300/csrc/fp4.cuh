@@ -1,0 +1,99 @@
+// Microscaled 4-bit blocks: the arithmetic and the storage order that the
+// quantiser, the products' epilogues and the expander share.
+//
+// A block of B values (MX: 32, NV: 16) is stored as e2m1 codes and one scale
+// byte; value = code * scale.  The order of the scale bytes (tiles of 128 rows
+// x 4 blocks, 512 bytes) is the one tcgen05.cp .32x128b reads: 32 rows of 16
+// bytes, row r of the tile at 16-byte row r % 32, 4-byte column r / 32.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+template <int FMT> struct Fp4;
+template <> struct Fp4<MOE_FP4_MX> {
+    static constexpr int BLK = 32;
+    static constexpr uint32_t NAN_SCALE = 0xFFu;
+};
+template <> struct Fp4<MOE_FP4_NV> {
+    static constexpr int BLK = 16;
+    static constexpr uint32_t NAN_SCALE = 0x7Fu;
+};
+
+__host__ __device__ inline int fp4_blk(moe_fp4 fmt) { return fmt == MOE_FP4_MX ? 32 : 16; }
+// 512-byte scale tiles along one row of `cols` values, and bytes per batch.
+__host__ __device__ inline int64_t fp4_scale_tiles(int blk, int cols) { return (cols / blk + 3) / 4; }
+__host__ __device__ inline int64_t fp4_scale_bytes(int blk, int64_t rows, int cols) {
+    return (rows + 127) / 128 * fp4_scale_tiles(blk, cols) * 512;
+}
+// Byte of (row, block) within a batch's scales (ntiles = fp4_scale_tiles()).
+__device__ __forceinline__ int64_t fp4_scale_at(int64_t row, int b, int64_t ntiles) {
+    return ((row >> 7) * ntiles + (b >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (b & 3);
+}
+
+// Nearest e4m3 code of v >= 0 (ties to even, at most 448).
+__device__ __forceinline__ uint32_t e4m3_of(float v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+    return r & 0xFFu;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+    const uint32_t ex = (code >> 3) & 15u, man = code & 7u;
+    if ((code & 0x7Fu) == 0x7Fu) return NAN;
+    const float v = ex ? __uint_as_float(((ex + 120u) << 23) | (man << 20)) : (float)man * 0x1p-9f;
+    return code & 0x80u ? -v : v;
+}
+// 2^(code - 127); code 0 is the subnormal 2^-127.
+__device__ __forceinline__ float e8m0_value(uint32_t code) {
+    return code == 0xFFu ? NAN : __uint_as_float(code ? code << 23 : 1u << 22);
+}
+
+// Scale byte of a block with largest magnitude amax, and what its values are
+// multiplied by (1 / scale; 0 where the scale is 0).  g6 = 6 g (NV).
+template <int FMT>
+__device__ __forceinline__ uint32_t fp4_scale(float amax, float g, float g6, float &inv) {
+    if (!(amax < INFINITY)) {   // an infinity (a NaN comes in as one)
+        inv = 0.0f;
+        return Fp4<FMT>::NAN_SCALE;
+    }
+    if (FMT == MOE_FP4_MX) {
+        const int ex = (int)(__float_as_uint(amax) >> 23);   // biased exponent
+        const int sc = amax == 0.0f ? 127 : max(ex - 2, 0);
+        inv = __uint_as_float((uint32_t)(254 - sc) << 23);
+        return (uint32_t)sc;
+    }
+    const uint32_t s8 = e4m3_of(__fdiv_rn(amax, g6));
+    const float s = __fmul_rn(e4m3_value(s8), g);
+    inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    return s8;
+}
+
+// Eight codes, value i in bits 4i .. 4i + 3 (nearest-even, saturating).
+__device__ __forceinline__ uint32_t e2m1x8(const float *v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// max |v| where a NaN counts as an infinity.
+__device__ __forceinline__ float amax_nan(float m, float v) {
+    return v != v ? INFINITY : fmaxf(m, fabsf(v));
+}
+
+// The value of an e2m1 code: magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 as (1 + m/2)
+// 2^(e-1), or m/2 at e = 0.
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+    const uint32_t ex = (c >> 1) & 3u, man = c & 1u;
+    const float v = ex ? __uint_as_float(((ex + 126u) << 23) | (man << 22)) : 0.5f * (float)man;
+    return c & 8u ? -v : v;
+}
+
+}  // namespace moe

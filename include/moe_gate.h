@@ -68,6 +68,14 @@ typedef enum {
     MOE_ACT_SWIGLU = 2  /* y = (silu(x W1^T) * (x W3^T)) W2^T, no biases */
 } moe_act;
 
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* Microscaled 4-bit formats: e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6, signed). */
+typedef enum {
+    MOE_FP4_MX = 0,  /* blocks of 32 along the row, one e8m0 (power of two) scale each */
+    MOE_FP4_NV = 1   /* blocks of 16, one e4m3 scale each, one fp32 factor per batch */
+} moe_fp4;
+
 #define MOE_FLAG_NORMALIZE_GATES 1u /* divide the k selected gates by their sum */
 #define MOE_FLAG_ZERO_FILL 2u       /* zero the unoccupied rows 0..c-1 of each expert */
 
@@ -369,6 +377,145 @@ moe_status moe_expert_ffn_fp8(const void *buf_q, const float *buf_scale, const i
                               const int32_t *c_dev, const void *w1_q, const float *w1_scale,
                               const void *b1, const void *w2_q, const float *w2_scale,
                               const void *b2, moe_act act, int e, int64_t c_max, int m, int h,
+                              void *workspace, size_t workspace_bytes, void *out,
+                              int32_t *dev_status, void *stream);
+
+/*
+ * Routing from router logits, for gates that moe_gate_topk does not form:
+ * sigmoid scores, a balance bias, group-limited selection, scaled gates.
+ * Per token, with l its e logits:
+ *   score_j = 1 / (1 + exp(-l_j))                       (MOE_SCORE_SIGMOID)
+ *           = exp(l_j - max l) / sum_i exp(l_i - max l)  (MOE_SCORE_SOFTMAX),
+ *     the sum taken by adjacent pairs (v[2j] + v[2j+1], level by level) over e
+ *     padded with zeros to a power of two, divisions rounded correctly;
+ *   choice_j = score_j + bias_j (bias NULL: score_j);
+ *   the experts are cut into `groups` equal runs of consecutive experts; a
+ *     group's value is the sum of its group_top (1 or 2) best choices, and the
+ *     topk_groups groups of the largest value (ties to the lower index) stay;
+ *   idx[r, t]: the r-th expert of the groups that stay by (choice descending,
+ *     index ascending);
+ *   gates[r, t] = score[idx[r, t]], with MOE_FLAG_NORMALIZE_GATES divided by
+ *     the sum of the k of them in route order, then times `scale`.
+ * The bias steers the choice and is not part of the gates, so that a balance
+ * update of it changes which experts run and not what they weigh.
+ * A logit of -inf masks its expert: score 0, chosen only where fewer than k
+ * others stay, after them, with gate 0; it does not count in its group's value
+ * (a group with none left ranks last).  A row of -inf alone gets the gates 0.
+ * A NaN choice ranks like a masked expert; a NaN score passes into its gate
+ * (softmax: a NaN or +inf logit makes every score of the row NaN).
+ * logits [s, e] in `ldt` (no alignment beyond the element's: e may be odd);
+ * bias [e] fp32 or NULL; idx [k, s] int32 and gates [k, s] fp32 are written.
+ * e <= 1024; e a multiple of groups, groups <= 32, 1 <= topk_groups <= groups,
+ * k <= topk_groups * (e / groups).
+ */
+moe_status moe_route_topk(const void *logits, moe_dtype ldt, const float *bias, int64_t s, int e,
+                          int k, moe_score score, int groups, int topk_groups, int group_top,
+                          float scale, unsigned flags, int32_t *idx, float *gates,
+                          int32_t *dev_status, void *stream);
+
+/*
+ * Gradient of moe_route_topk's gates with respect to the logits, the selection
+ * taken as constant (the bias has no gradient).  With g the selected scores,
+ * G = g / sum g, A = sum_r d_gates[r] G[r]:
+ *   softmax, normalised: scale G (d_gates - A) at the selection, else 0;
+ *   softmax, raw:  scale p_j (d_gates_j [selected] - sum_r d_gates[r] p_idx[r]);
+ *   sigmoid, normalised: scale G (d_gates - A) (1 - g) at the selection, else 0;
+ *   sigmoid, raw:  scale d_gates g (1 - g) at the selection, else 0.
+ * Rows without a live expert get 0.  logits [s, e] in `ldt` as given to the
+ * forward; idx, d_gates [k, s]; d_logits [s, e] in `ddt`, every element
+ * written, sums in fp32, one rounding.  An idx outside [0, e) stores
+ * MOE_ERR_INVALID_ARG in dev_status.
+ */
+moe_status moe_route_bwd(const void *logits, moe_dtype ldt, const int32_t *idx,
+                         const float *d_gates, int64_t s, int e, int k, moe_score score,
+                         float scale, unsigned flags, void *d_logits, moe_dtype ddt,
+                         int32_t *dev_status, void *stream);
+
+/*
+ * Microscaled 4-bit operands.  A row of `cols` values (a multiple of 32) is cut
+ * into blocks of B = 32 (MOE_FP4_MX) or 16 (MOE_FP4_NV); value = code * scale:
+ *   MX: scale = 2^(floor(log2 amax) - 2), at least 2^-127, stored as e8m0
+ *       (exponent + 127); 1 for a block of zeros;
+ *   NV: scale = s8 * g with g the batch's factor (`global_scale`, NULL: 1) and
+ *       s8 = e4m3(min(amax / (6 g), 448)), nearest-even; where s8 is 0 the
+ *       codes are 0;
+ *   code = e2m1(x * (1 / scale)), nearest-even, saturating at +-6, 1 / scale
+ *       rounded to fp32 (exact for MX).
+ * A block that holds an infinity or a NaN gets the NaN scale (0xFF / 0x7F).
+ * Codes: two a byte, the even column in the low half; [batches, rows, cols/2].
+ * Scales: tiles of 128 rows x 4 blocks, 512 bytes each: row r, block b of a
+ * tile at (r % 32) * 16 + (r / 32) * 4 + b; a batch's tiles ordered by row
+ * tile, then by block tile; moe_fp4_scale_bytes() bytes per batch.  The bytes
+ * of blocks past the row's last must hold a number (the library writes 0);
+ * those of rows past the last are ignored.
+ */
+size_t moe_fp4_scale_bytes(moe_fp4 fmt, int64_t rows, int cols);
+
+/*
+ * src [batches, rows_per_batch, cols] in `sdt` -> q [batches, rows_per_batch,
+ * cols/2], scale [batches, moe_fp4_scale_bytes()].  global_scale [batches]
+ * fp32 > 0, NV only.  With counts [batches] and c_dev (both or neither) only
+ * the rows r < min(counts[b], *c_dev, rows_per_batch) of batch b are written.
+ * The codes and scales match an exact-arithmetic reference bit for bit.
+ */
+moe_status moe_quantize_fp4(const void *src, moe_dtype sdt, int64_t batches,
+                            int64_t rows_per_batch, int cols, moe_fp4 fmt,
+                            const float *global_scale, const int32_t *counts,
+                            const int32_t *c_dev, void *q, void *scale, int32_t *dev_status,
+                            void *stream);
+
+/*
+ * The values that 4-bit rows stand for: dst [batches, rows_per_batch, cols] in
+ * `ddt` = code * scale (NV: s8 * g rounded to fp32 first), one rounding.  Rows
+ * past the kept ones (counts, c_dev as above) are not written.
+ */
+moe_status moe_dequantize_fp4(const void *q, const void *scale, int64_t batches,
+                              int64_t rows_per_batch, int cols, moe_fp4 fmt,
+                              const float *global_scale, const int32_t *counts,
+                              const int32_t *c_dev, void *dst, moe_dtype ddt, int32_t *dev_status,
+                              void *stream);
+
+/*
+ * Grouped product of 4-bit operands: for the kept rows i < min(counts[j],
+ * *c_dev, c_max) of every expert j
+ *   out[j,i,:] = bf16(a_global[j] b_global[j] sum_k a[j,i,k] b[j,:,k] + bias[j])
+ * with exact products and fp32 accumulation (tcgen05 block-scaled MMA).
+ * a_q [e, c_max, k/2] with a_scale; b_q [e, n, k/2] with b_scale; a_global,
+ * b_global [e] fp32 (NV; NULL: 1; must be NULL for MX); bias [e, n] bf16 or
+ * NULL; out [e, c_max, n] bf16, other rows not written.  e = 1 is a plain
+ * dense product.  k a multiple of 32, n a multiple of 8.
+ */
+moe_status moe_product_fp4(const void *a_q, const void *a_scale, const float *a_global,
+                           const int32_t *counts, const int32_t *c_dev, const void *b_q,
+                           const void *b_scale, const float *b_global, const void *bias,
+                           moe_fp4 fmt, int e, int64_t c_max, int k, int n, void *out,
+                           int32_t *dev_status, void *stream);
+
+/* Bytes of device workspace moe_expert_ffn_fp4 needs (0: bad shape). */
+size_t moe_expert_ffn_fp4_workspace_size(moe_fp4 fmt, moe_act act, int e, int64_t c_max, int m,
+                                         int h);
+
+/*
+ * The expert FFN on 4-bit operands.  For the kept rows of every expert:
+ *   hid = act(s (x . w1^T) + b1), or silu(s x . w1^T) * (s x . w3^T) (SwiGLU,
+ *         no biases), in fp32 and quantised from there, block by block, as
+ *         moe_quantize_fp4 does with the factor hid_global[j];
+ *   out = bf16(s (hid . w2^T) + b2),
+ * s the operands' factors.  buf_q, buf_scale, buf_global: moe_quantize_fp4 of
+ * the buffer's kept rows; w1, w3 [e, h, m/2], w2 [e, m, h/2] with their scales
+ * and factors ([e] fp32, NV only; NULL: 1).  hid_global [e]: a fixed
+ * (calibrated) factor, because a block's scale has to be known before the
+ * row's other blocks are.  m, h multiples of 32.  b1 [e, h], b2 [e, m] bf16 or
+ * NULL.  Workspace: the hidden's codes [e, c_max, h/2], then, from the next
+ * 256-byte boundary, its scales; a caller may read them after the call.
+ */
+moe_status moe_expert_ffn_fp4(const void *buf_q, const void *buf_scale, const float *buf_global,
+                              const float *hid_global, const int32_t *counts,
+                              const int32_t *c_dev, const void *w1_q, const void *w1_scale,
+                              const float *w1_global, const void *b1, const void *w3_q,
+                              const void *w3_scale, const float *w3_global, const void *w2_q,
+                              const void *w2_scale, const float *w2_global, const void *b2,
+                              moe_fp4 fmt, moe_act act, int e, int64_t c_max, int m, int h,
                               void *workspace, size_t workspace_bytes, void *out,
                               int32_t *dev_status, void *stream);
 
