@@ -1,0 +1,575 @@
+// Grouped products of microscaled 4-bit operands on the tensor cores, and the
+// expert FFN made of them.  Included by ffn_tc.cu, whose barrier, copy, TMEM
+// and store helpers it shares.
+//
+//   out[j] = g_a[j] g_b[j] (A[j] B[j]^T) + bias[j]            (bf16), or
+//   hid[j] = quantise(act(...))   (e2m1 codes and block scales, for fc2)
+//
+// over the first min(counts[j], c) rows of every expert j.  The block scales
+// enter the tensor core with the operands (kind::mxf4 with one e8m0 byte per
+// 32 values, kind::mxf4nvf4 with one e4m3 byte per 16), so the accumulator is
+// the sum of the values the codes stand for, in fp32.
+//
+// One persistent kernel on CTA pairs, 256 x 256 tiles (M = 256 over the pair),
+// the roles of tc_group_gemm: four producer warps, one MMA issuer, eight
+// epilogue warps.  A stage is 256 values of K: 128-byte swizzled rows of 128 A
+// and 128 B rows per CTA, and the 512-byte scale tiles of those A rows and of
+// all 256 B rows (each CTA's half of the product needs every column's scale).
+// tcgen05.cp copies a stage's scale tiles into TMEM (two sets of columns, used
+// in turn) ahead of its four K = 64 MMAs.
+//
+// TMEM: two 256-column accumulators do not fit beside the scales, so they
+// overlap in 128 columns: [0, 256) and [128, 384).  The epilogue first loads
+// the overlapping half of a tile into registers and then lets the next tile's
+// MMAs begin, so all but those loads runs under the next main loop.
+#pragma once
+
+#include "fp4.cuh"
+
+namespace moe {
+namespace {
+
+enum Fp4Epi { FP4_BIAS = 0, FP4_RELU = 1, FP4_GELU = 2, FP4_SWIGLU = 3 };
+
+constexpr int F4_BK = 256;                     // values of K per stage (128 bytes a row)
+constexpr int F4_BOX_BYTES = 64 * 128;         // one operand copy: 64 rows
+constexpr int F4_OP_BYTES = 2 * F4_BOX_BYTES;  // one operand per CTA and stage
+constexpr int F4_STAGES = 5;
+constexpr uint32_t F4_SF_COL = 384;            // first TMEM column of the scales
+constexpr uint32_t F4_ACC_STEP = 128;          // first column of the odd tiles' accumulator
+
+template <int FMT>
+struct F4Tiling {
+    static constexpr int KT = F4_BK / (4 * Fp4<FMT>::BLK);   // scale tiles along a stage's K
+    static constexpr int SF_BYTES = KT * 512;                // of 128 rows
+    static constexpr int STAGE_BYTES = 2 * F4_OP_BYTES + 3 * SF_BYTES;
+    static constexpr uint32_t SF_COLS = 12 * KT;             // TMEM columns of a stage's scales
+    static_assert(F4_SF_COL + 2 * SF_COLS <= TMEM_COLS, "TMEM");
+};
+
+template <int FMT>
+constexpr size_t f4_smem_bytes() {
+    return 1024 + (size_t)F4_STAGES * F4Tiling<FMT>::STAGE_BYTES + (size_t)EPI_WARPS * STG_WARP_BYTES +
+           sizeof(Ctl<F4_STAGES>);
+}
+
+struct F4Args {
+    const int32_t *counts;
+    const int32_t *c_dev;
+    int32_t *status;
+    const float *a_global;      // [e] or nullptr: 1
+    const float *b_global;
+    const float *b3_global;     // SwiGLU
+    const __nv_bfloat16 *bias;  // [e, n_out] or nullptr
+    __nv_bfloat16 *out;         // FP4_BIAS: [e, c_max, n_out]
+    uint8_t *out_q;             // else: codes [e, c_max, n_out / 2],
+    uint8_t *out_scale;         // scale tiles, and
+    const float *out_global;    // factors [e] or nullptr
+    int64_t c_max;
+    int e;
+    int K;
+    int n_out;
+    int32_t stall;
+};
+
+// Instruction descriptor of the block-scaled 4-bit kinds: A and B e2m1 (1 at
+// bits 7 and 10), both K-major, N >> 3 at bit 17, scale type at bit 23 (1:
+// e8m0), M >> 7 at bit 27; which two of a column's four scale bytes a K = 64
+// step uses (0 or 2; four of them: 0) at bits 4 (B) and 29 (A).
+template <int FMT>
+__device__ __forceinline__ uint32_t f4_idesc(uint32_t sf_id) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (FMT == MOE_FP4_MX ? 1u << 23 : 0u) |
+           ((uint32_t)((2 * UM) >> 7) << 27) | (sf_id << 4) | (sf_id << 29);
+}
+
+template <int FMT>
+__device__ __forceinline__ void umma_pair_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if (FMT == MOE_FP4_MX)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// One 512-byte scale tile from each CTA's shared memory into four columns of
+// its own TMEM, the 32 lanes repeated in all four lane quarters.
+__device__ __forceinline__ void cp_scales_pair(uint32_t tmem, uint32_t saddr) {
+    // no swizzle: 8-row groups of 16-byte rows, 128 bytes apart
+    const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                                 uint32_t bar_cluster) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(su32(dst)),
+        "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+        : "memory");
+}
+
+// One lane's 64 hidden values (columns gcol .. of its row) to codes and block
+// scales.  Called in halves of 32 columns: `word` collects the scale bytes.
+template <int FMT>
+__device__ __forceinline__ void f4_quantise32(float (&v)[32], float g, float g6, bool live, uint32_t (&codes)[4],
+                                              uint32_t &word, int half) {
+    constexpr int BLK = Fp4<FMT>::BLK;
+#pragma unroll
+    for (int b = 0; b < 32 / BLK; b++) {
+        float amax = 0.0f, inv;
+#pragma unroll
+        for (int i = 0; i < BLK; i++) amax = amax_nan(amax, v[b * BLK + i]);
+        const uint32_t sc = fp4_scale<FMT>(amax, g, g6, inv);
+        if (live) word |= sc << (8 * (half * (32 / BLK) + b));
+#pragma unroll
+        for (int i = 0; i < BLK; i++) v[b * BLK + i] *= inv;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) codes[i] = e2m1x8(v + 8 * i);
+}
+
+template <int FMT, int EPI>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmB3, const __grid_constant__ CUtensorMap tmSA,
+               const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmSB3,
+               const __grid_constant__ CUtensorMap tmO, const F4Args args) {
+    using TL = F4Tiling<FMT>;
+    constexpr bool SWIGLU = EPI == FP4_SWIGLU;
+    constexpr int NOUT_TILE = SWIGLU ? BN / 2 : BN;
+    constexpr int BLK = Fp4<FMT>::BLK, KT = TL::KT, STAGES = F4_STAGES;
+    __shared__ int32_t s_bad;
+    __shared__ int32_t kept_rows[MAX_E];
+    __shared__ __align__(16) float epi_bias[EPI_WARPS][128];
+    pdl_enter();
+    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
+    __syncthreads();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sA = smem, *sB = smem + STAGES * F4_OP_BYTES, *sSF = sB + STAGES * F4_OP_BYTES;
+    uint8_t *stg_all = smem + STAGES * TL::STAGE_BYTES;
+    Ctl<STAGES> *ctl = (Ctl<STAGES> *)(stg_all + EPI_WARPS * STG_WARP_BYTES);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = args.e;
+    const uint32_t prank = cluster_rank();
+    const int tile0 = (int)(blockIdx.x / 2), tile_step = (int)(gridDim.x / 2);
+    const int ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
+    const int nk = (args.K + F4_BK - 1) / F4_BK;
+
+    if (warp == 0) {
+        const int c_eff = (int)min((int64_t)*args.c_dev, args.c_max);
+        int run = 0;
+        for (int base = 0; base < e; base += 32) {
+            const int j = base + lane;
+            const int rows = j < e ? max(0, min(args.counts[j], c_eff)) : 0;
+            if (j < e) kept_rows[j] = rows;
+            const int mine = ((rows + 2 * UM - 1) / (2 * UM)) * ntn;
+            int v = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (j < e) ctl->tile_start[j] = run + v - mine;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) {
+            ctl->tile_start[e] = run;
+            ctl->total_tiles = run;
+            ctl->abort = 0;
+            for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 4); mbar_init(&ctl->empty[s], 1); }
+            mbar_init(&ctl->tfull[0], 1);
+            mbar_init(&ctl->tempty[0], 2 * EPI_WARPS);
+            mbar_init(&ctl->drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         su32(&ctl->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    int total = ctl->total_tiles;
+    {
+        int bad0, bad1;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad0) : "r"(map_to_rank(su32(&s_bad), 0)));
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad1) : "r"(map_to_rank(su32(&s_bad), 1)));
+        if (bad0 | bad1) total = 0;   // the same decision in both CTAs
+    }
+    int32_t *abort_flag = &ctl->abort;
+
+    if (warp == 0 || warp >= PROD_WARP0) {
+        // Producers 0 and 2: the two row halves of this CTA's A rows; 1 and 3:
+        // those of its B rows (SwiGLU: the first CTA's are W1's, the second's
+        // W3's).  0 also brings the A scales, 1 and 3 the scales of the first
+        // and second 128 columns of the tile.
+        const int prod = warp == 0 ? 0 : warp - PROD_WARP0 + 1;
+        const bool is_a = (prod & 1) == 0;
+        const int hh = prod >> 1;
+        const uint32_t bytes = F4_BOX_BYTES + (prod == 2 ? 0 : TL::SF_BYTES);
+        const CUtensorMap *op = is_a ? &tmA : SWIGLU && prank ? &tmB3 : &tmB;
+        const CUtensorMap *sf = is_a ? &tmSA : SWIGLU && hh ? &tmSB3 : &tmSB;
+        const int a_tiles = (int)((args.c_max + 127) / 128), b_tiles = (args.n_out + 127) / 128;
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        for (int t = tile0; t < total && !args.stall; t += tile_step) {
+            const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
+            int row, sf_row;
+            if (is_a) {
+                row = (int)(T.j * args.c_max + (int64_t)T.mt * 2 * UM) + (int)prank * UM + hh * 64;
+                sf_row = T.j * a_tiles + T.mt * 2 + (int)prank;
+            } else {
+                row = T.j * args.n_out + T.nt * NOUT_TILE + (SWIGLU ? 0 : (int)prank * UM) + hh * 64;
+                sf_row = T.j * b_tiles + (SWIGLU ? T.nt : T.nt * 2 + hh);
+            }
+            uint8_t *dst = (is_a ? sA : sB) + hh * F4_BOX_BYTES;
+            uint8_t *sf_dst = sSF + (is_a ? 0 : (1 + hh) * TL::SF_BYTES);
+            for (int kb = 0; kb < nk; kb++) {
+                int ok = 1;
+                if (lane == 0) {
+                    ok = mbar_wait<true>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status);
+                    if (ok) {
+                        const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), 0);
+                        if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * bytes);
+                        tma_load_2d_pair(dst + stage * F4_OP_BYTES, op, kb * (F4_BK / 2), row, fb);
+                        if (prod != 2)
+                            tma_load_3d_pair(sf_dst + stage * 3 * TL::SF_BYTES, sf, 0, kb * KT, sf_row, fb);
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) goto producer_done;
+                issued++;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+    producer_done:
+        // bounded wait for this thread's copies in flight (the second CTA's are
+        // covered by the MMAs that consume them, or by the delay after an abort)
+        if (lane == 0 && prank == 0) {
+            for (int i = max(0, issued - STAGES); i < issued; i++) {
+                unsigned long long t0 = gtimer();
+                while (!mbar_try<true>(&ctl->full[i % STAGES], (uint32_t)((i / STAGES) & 1)) &&
+                       gtimer() - t0 < WAIT_NS) {
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        if (prank == 0) {
+            int stage = 0;
+            uint32_t phase = 0, sf_set = 0;
+            int done = 0;   // tiles begun by this pair
+            for (int t = tile0; t < total; t += tile_step, done++) {
+                // the previous tile's epilogue has the columns that this tile shares with it
+                if (done && !mbar_wait<true>(&ctl->tempty[0], (uint32_t)((done - 1) & 1), abort_flag, args.status))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(done & 1) * F4_ACC_STEP;
+                bool ok = true;
+                for (int kb = 0; kb < nk; kb++) {
+                    if (!mbar_wait<true>(&ctl->full[stage], phase, abort_flag, args.status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a0 = su32(sA + stage * F4_OP_BYTES), b0 = su32(sB + stage * F4_OP_BYTES);
+                    const uint32_t s0 = su32(sSF + stage * 3 * TL::SF_BYTES);
+                    const uint32_t sfa = tmem + F4_SF_COL + sf_set * TL::SF_COLS, sfb = sfa + 4 * KT;
+                    const int steps = min(F4_BK / 64, (args.K - kb * F4_BK + 63) / 64);
+#pragma unroll
+                    for (int i = 0; i < KT; i++) {
+                        cp_scales_pair(sfa + 4 * i, s0 + i * 512);
+                        cp_scales_pair(sfb + 8 * i, s0 + TL::SF_BYTES + i * 512);
+                        cp_scales_pair(sfb + 8 * i + 4, s0 + 2 * TL::SF_BYTES + i * 512);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < F4_BK / 64; kk++) {
+                        if (kk < steps) {
+                            const int i = FMT == MOE_FP4_MX ? kk / 2 : kk;   // its scale tile
+                            umma_pair_f4<FMT>(d, sdesc<128>(a0 + kk * 32), sdesc<128>(b0 + kk * 32),
+                                              f4_idesc<FMT>(FMT == MOE_FP4_MX ? (kk & 1) * 2 : 0), sfa + 4 * i,
+                                              sfb + 8 * i, (kb | kk) != 0);
+                        }
+                    }
+                    umma_commit_pair(&ctl->empty[stage], 3);
+                    sf_set ^= 1u;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit_pair(&ctl->tfull[0], 3);
+            }
+            umma_commit_pair(&ctl->drain, 3);
+        }
+        unsigned long long t0 = gtimer();
+        while (!mbar_try<true>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
+        }
+    } else if (warp >= 2 && warp < PROD_WARP0) {
+        // Epilogue: warp (sub, half) has rows sub * 32 .. of this CTA and, of the
+        // two 128-column halves, columns half * 64 .. + 63 each.
+        const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
+        uint8_t *stg = stg_all + ew * STG_WARP_BYTES;
+        float *bsl = epi_bias[ew];
+        int done = 0;
+        for (int t = tile0; t < total; t += tile_step, done++) {
+            const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
+            const int row = T.mt * 2 * UM + (int)prank * UM + sub * 32 + lane;
+            const bool valid = row < T.rows, all_kept = row - lane + 31 < T.rows;
+            const int64_t grow = (int64_t)T.j * args.c_max + row;
+            const float ga = args.a_global ? args.a_global[T.j] : 1.0f;
+            const float s1 = ga * (args.b_global ? args.b_global[T.j] : 1.0f);
+            const float s3 = SWIGLU ? ga * (args.b3_global ? args.b3_global[T.j] : 1.0f) : 0.0f;
+            const float og = EPI != FP4_BIAS && args.out_global ? args.out_global[T.j] : 1.0f;
+            const float og6 = __fmul_rn(og, 6.0f);
+            const int64_t ont = fp4_scale_tiles(BLK, args.n_out);   // scale tiles of an output row
+            if (!SWIGLU) {
+                // this warp's bias: columns half * 64 .. of both halves, 64 each
+                const int c = (lane >> 4) * 128 + half * 64 + (lane & 15) * 4;
+                const int g = T.nt * NOUT_TILE + c;
+                float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (args.bias && g < args.n_out) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(args.bias + (int64_t)T.j * args.n_out + g);
+                    b = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+                }
+                reinterpret_cast<float4 *>(bsl)[lane] = b;
+                __syncwarp();
+            }
+            if (!mbar_wait<true>(&ctl->tfull[0], (uint32_t)(done & 1), abort_flag, args.status)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(done & 1) * F4_ACC_STEP + half * 64;
+            const int shared0 = done & 1 ? 0 : 128;   // the half that the next tile overwrites
+            uint32_t r[2][32];
+            tmem_ld32(tb + shared0, r[0]);
+            tmem_ld32(tb + shared0 + 32, r[1]);
+            tmem_wait_ld(r[0]);
+            tmem_tie(r[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
+            if (SWIGLU) {
+                const int gcol = T.nt * NOUT_TILE + half * 64;
+                uint32_t word = 0;
+#pragma unroll
+                for (int h2 = 0; h2 < 2; h2++) {
+                    uint32_t o[32];
+                    tmem_ld32(tb + (128 - shared0) + 32 * h2, o);
+                    tmem_wait_ld(o);
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const float x = __uint_as_float(r[h2][i]), y = __uint_as_float(o[i]);
+                        const float a = (shared0 ? y : x) * s1, b = (shared0 ? x : y) * s3;
+                        v[i] = silu(a) * b;
+                    }
+                    uint32_t codes[4];
+                    const bool live = gcol + 32 * h2 < args.n_out;
+                    f4_quantise32<FMT>(v, og, og6, live, codes, word, h2);
+                    if (valid && live) {
+                        V16 w;
+                        w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
+                        st_v16(args.out_q + (grow * args.n_out + gcol + 32 * h2) / 2, w);
+                    }
+                }
+                if (valid && gcol < ont * 4 * BLK) {
+                    uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
+                                 fp4_scale_at(row, gcol / BLK, ont);
+                    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t *>(p) = word;
+                    else *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
+                }
+            } else {
+#pragma unroll 1
+                for (int part = 0; part < 2; part++) {
+                    const int lcol = part == 0 ? shared0 : 128 - shared0;   // this half's first column
+                    const int gcol = T.nt * NOUT_TILE + lcol + half * 64;
+                    if (part) {
+                        tmem_ld32(tb + lcol, r[0]);
+                        tmem_ld32(tb + lcol + 32, r[1]);
+                        tmem_wait_ld(r[0]);
+                        tmem_tie(r[1]);
+                    }
+                    uint32_t word = 0;
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; h2++) {
+                        const float2 *bp = reinterpret_cast<const float2 *>(bsl + (lcol ? 64 : 0) + 32 * h2);
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h2][2 * i]), __uint_as_float(r[h2][2 * i + 1])),
+                                                  make_float2(s1, s1), bp[i]);
+                            if (EPI == FP4_GELU) a = gelu_erf2(a);
+                            if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                            v[2 * i] = a.x;
+                            v[2 * i + 1] = a.y;
+                        }
+                        if (EPI == FP4_BIAS) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; i++) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                            epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow - lane, gcol + 32 * h2, args.n_out,
+                                        args.out + grow * args.n_out);
+                        } else {
+                            uint32_t codes[4];
+                            const bool live = gcol + 32 * h2 < args.n_out;
+                            f4_quantise32<FMT>(v, og, og6, live, codes, word, h2);
+                            if (valid && live) {
+                                V16 w;
+                                w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
+                                st_v16(args.out_q + (grow * args.n_out + gcol + 32 * h2) / 2, w);
+                            }
+                        }
+                    }
+                    if (EPI != FP4_BIAS && valid && gcol < ont * 4 * BLK) {
+                        uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
+                                     fp4_scale_at(row, gcol / BLK, ont);
+                        if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t *>(p) = word;
+                        else *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
+                    }
+                }
+                __syncwarp();   // the bias slice is rewritten for the next tile
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    if (*(volatile int32_t *)abort_flag) {   // copies may still be landing: they take microseconds
+        unsigned long long t0 = gtimer();
+        while (gtimer() - t0 < 1000000ull) {
+        }
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// Scale tiles of `batches` x `row_tiles` rows of `ntiles`: boxes of kt tiles.
+bool make_map_scales(CUtensorMap *map, const void *base, int64_t row_tiles, int64_t ntiles, int kt) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)ntiles, (cuuint64_t)row_tiles};
+    cuuint64_t strides[2] = {512, (cuuint64_t)ntiles * 512};
+    cuuint32_t box[3] = {128, (cuuint32_t)kt, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct F4Operand {
+    const void *q, *scale;
+    const float *global;
+};
+
+template <int FMT, int EPI>
+moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b3, const F4Args &args_in,
+                      cudaStream_t stream) {
+    F4Args args = args_in;
+    args.a_global = a.global;
+    args.b_global = b.global;
+    args.b3_global = b3.global;
+    args.stall = take_gemm_stall() ? 1 : 0;
+    const int64_t e = args.e;
+    const int64_t nt = fp4_scale_tiles(Fp4<FMT>::BLK, args.K);
+    const int64_t a_tiles = (args.c_max + 127) / 128, b_tiles = (args.n_out + 127) / 128;
+    constexpr int KT = F4Tiling<FMT>::KT;
+    CUtensorMap mA, mB, mB3, mSA, mSB, mSB3, mO;
+    if (!make_map_u8(&mA, a.q, (uint64_t)(e * args.c_max), (uint64_t)args.K / 2, 64) ||
+        !make_map_u8(&mB, b.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
+        !make_map_u8(&mB3, b3.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
+        !make_map_scales(&mSA, a.scale, e * a_tiles, nt, KT) ||
+        !make_map_scales(&mSB, b.scale, e * b_tiles, nt, KT) ||
+        !make_map_scales(&mSB3, b3.scale, e * b_tiles, nt, KT) ||
+        !make_map(&mO, EPI == FP4_BIAS ? (const void *)args.out : a.q, EPI == FP4_BIAS ? (uint64_t)(e * args.c_max) : 32,
+                  EPI == FP4_BIAS ? (uint64_t)args.n_out : 32, 32, 32))
+        return MOE_ERR_CUDA;
+    auto kern = fp4_group_gemm<FMT, EPI>;
+    constexpr size_t SMEM = f4_smem_bytes<FMT>();
+    static int units[64] = {0};   // resident clusters per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    int nunits = dev >= 0 && dev < 64 ? units[dev] : 0;
+    if (!nunits) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        nunits = max_clusters(kern, SMEM, 2);
+        if (dev >= 0 && dev < 64) units[dev] = nunits;
+    }
+    constexpr int NOUT_TILE = EPI == FP4_SWIGLU ? BN / 2 : BN;
+    const int64_t upper = e * ((args.c_max + 2 * UM - 1) / (2 * UM)) * ((args.n_out + NOUT_TILE - 1) / NOUT_TILE);
+    const int64_t grid = upper < nunits ? upper : nunits;
+    return launch_cluster_pdl(kern, dim3((unsigned)(2 * grid)), dim3(NUM_THREADS), SMEM, 2, stream, mA, mB, mB3, mSA,
+                              mSB, mSB3, mO, args);
+}
+
+template <int FMT>
+moe_status fp4_fc(int epi, const F4Operand &a, const F4Operand &b, const F4Operand &b3, const F4Args &args,
+                  cudaStream_t stream) {
+    switch (epi) {
+        case FP4_BIAS: return launch_fp4<FMT, FP4_BIAS>(a, b, b3, args, stream);
+        case FP4_RELU: return launch_fp4<FMT, FP4_RELU>(a, b, b3, args, stream);
+        case FP4_GELU: return launch_fp4<FMT, FP4_GELU>(a, b, b3, args, stream);
+        default: return launch_fp4<FMT, FP4_SWIGLU>(a, b, b3, args, stream);
+    }
+}
+
+moe_status fp4_fc(moe_fp4 fmt, int epi, const F4Operand &a, const F4Operand &b, const F4Operand &b3,
+                  const F4Args &args, cudaStream_t stream) {
+    return fmt == MOE_FP4_MX ? fp4_fc<MOE_FP4_MX>(epi, a, b, b3, args, stream)
+                             : fp4_fc<MOE_FP4_NV>(epi, a, b, b3, args, stream);
+}
+
+}  // namespace
+
+moe_status product_fp4_launch(const void *a_q, const void *a_scale, const float *a_global,
+                              const int32_t *counts, const int32_t *c_dev, const void *b_q,
+                              const void *b_scale, const float *b_global, const void *bias,
+                              moe_fp4 fmt, int e, int64_t c_max, int k, int n, void *out,
+                              int32_t *st, cudaStream_t stream) {
+    F4Args g{};
+    g.counts = counts; g.c_dev = c_dev; g.status = st;
+    g.bias = (const __nv_bfloat16 *)bias;
+    g.out = (__nv_bfloat16 *)out;
+    g.c_max = c_max; g.e = e; g.K = k; g.n_out = n;
+    const F4Operand b{b_q, b_scale, b_global};
+    return fp4_fc(fmt, FP4_BIAS, F4Operand{a_q, a_scale, a_global}, b, b, g, stream);
+}
+
+moe_status ffn_fp4_launch(const void *buf_q, const void *buf_scale, const float *buf_global,
+                          const float *hid_global, const int32_t *counts, const int32_t *c_dev,
+                          const void *w1_q, const void *w1_scale, const float *w1_global,
+                          const void *b1, const void *w3_q, const void *w3_scale,
+                          const float *w3_global, const void *w2_q, const void *w2_scale,
+                          const float *w2_global, const void *b2, moe_fp4 fmt, moe_act act, int e,
+                          int64_t c_max, int m, int h, void *hid_q, void *hid_scale, void *out,
+                          int32_t *st, cudaStream_t stream) {
+    const F4Operand w1{w1_q, w1_scale, w1_global};
+    const F4Operand w3 = act == MOE_ACT_SWIGLU ? F4Operand{w3_q, w3_scale, w3_global} : w1;
+    F4Args g{};
+    g.counts = counts; g.c_dev = c_dev; g.status = st;
+    g.bias = (const __nv_bfloat16 *)b1;
+    g.out_q = (uint8_t *)hid_q;
+    g.out_scale = (uint8_t *)hid_scale;
+    g.out_global = hid_global;
+    g.c_max = c_max; g.e = e; g.K = m; g.n_out = h;
+    const int epi = act == MOE_ACT_SWIGLU ? FP4_SWIGLU : act == MOE_ACT_GELU ? FP4_GELU : FP4_RELU;
+    moe_status r = fp4_fc(fmt, epi, F4Operand{buf_q, buf_scale, buf_global}, w1, w3, g, stream);
+    if (r != MOE_OK) return r;
+    return product_fp4_launch(hid_q, hid_scale, hid_global, counts, c_dev, w2_q, w2_scale, w2_global, b2, fmt, e,
+                              c_max, h, m, out, st, stream);
+}
+
+}  // namespace moe

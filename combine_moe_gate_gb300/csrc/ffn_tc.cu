@@ -1750,3 +1750,6 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
 }
 
 }  // namespace moe
+
+// The products of microscaled 4-bit operands (they share the helpers above).
+#include "ffn_fp4.cuh"
