@@ -60,7 +60,7 @@ quantize_fp4_kernel(const T *__restrict__ src, int64_t batches, int64_t rpb, int
 #pragma unroll
             for (int i = 0; i < 16; i++) amax = amax_nan(amax, f[i]);
         }
-        if (TPB == 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        if (TPB == 2) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         const float g = FMT == MOE_FP4_NV && global && live ? global[b] : 1.0f;
         float inv;
         uint32_t sc = fp4_scale<FMT>(amax, g, __fmul_rn(g, 6.0f), inv);

@@ -53,7 +53,7 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
 // multiplied by (1 / scale; 0 where the scale is 0).  g6 = 6 g (NV).
 template <int FMT>
 __device__ __forceinline__ uint32_t fp4_scale(float amax, float g, float g6, float &inv) {
-    if (!(amax < INFINITY)) {   // an infinity (a NaN comes in as one)
+    if (!(amax < INFINITY)) {   // an infinity or a NaN
         inv = 0.0f;
         return Fp4<FMT>::NAN_SCALE;
     }
@@ -83,9 +83,11 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *v) {
     return r;
 }
 
-// max |v| where a NaN counts as an infinity.
+// max(m, |v|); a NaN stays one.
 __device__ __forceinline__ float amax_nan(float m, float v) {
-    return v != v ? INFINITY : fmaxf(m, fabsf(v));
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
 }
 
 // The value of an e2m1 code: magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 as (1 + m/2)

@@ -18,7 +18,6 @@ namespace moe {
 namespace {
 
 constexpr int RT_WARPS = 8;
-constexpr int MAX_GROUPS = 32;
 
 template <typename T> __device__ __forceinline__ float ld_logit(const T *p);
 template <> __device__ __forceinline__ float ld_logit<float>(const float *p) { return __ldg(p); }
