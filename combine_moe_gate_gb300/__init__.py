@@ -18,6 +18,8 @@ import ctypes
 import os
 import re
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe_gate.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_gate.h")
@@ -126,18 +128,19 @@ def moe_debug_stall_gemms(n):
 def _ptr(t, name="tensor", dtype=None, shape=None):
     """Device address of a contiguous CUDA tensor; checks the dtype and shape
     when given (a mismatch here would let a kernel read or write out of
-    bounds).  None passes through as NULL."""
+    bounds).  None passes through as NULL.  A call of one small kernel spends
+    most of its time here, so the checks are plain comparisons."""
     if t is None:
         return None
-    if shape is not None and tuple(t.shape) != tuple(int(d) for d in shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and (type(dtype) is not tuple or t.dtype not in dtype):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     if not _on_device(t):
         raise ValueError(f"{name}: must be a CUDA tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _on_device(t) -> bool:
@@ -145,33 +148,26 @@ def _on_device(t) -> bool:
 
 
 def _i32():
-    import torch
-
     return torch.int32
 
 
 def _f32():
-    import torch
-
     return torch.float32
 
 
 def _dt(t):
-    import torch
-
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return MOE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return MOE_F32
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
 def _stream(stream):
-    import torch
-
+    """The stream's handle; None: torch's current stream of the current device."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(code, where):
@@ -306,8 +302,6 @@ def moe_quantize_rows_fp8(src, q, scale, dev_status, counts=None, c_dev=None, st
     """e4m3 codes (uint8, src's shape) and per-row fp32 scales of a bf16 tensor
     [rows, cols] or [batches, rows, cols]; with counts / c_dev only the kept
     rows of each batch."""
-    import torch
-
     shape = tuple(src.shape) if src.dim() == 3 else (1,) + tuple(src.shape)
     b, r, c = shape
     I = _i32()
@@ -322,8 +316,6 @@ def moe_quantize_rows_fp8(src, q, scale, dev_status, counts=None, c_dev=None, st
 
 def moe_expert_ffn_fp8(buf_q, buf_scale, counts, c_dev, w1_q, w1_scale, b1, w2_q, w2_scale, b2,
                        act, workspace, out, dev_status, stream=None):
-    import torch
-
     e, c_max, m = buf_q.shape
     h = w1_q.shape[1]
     I, F, U8, bf = _i32(), _f32(), torch.uint8, torch.bfloat16
@@ -377,12 +369,10 @@ def moe_fp4_scale_bytes(fmt, rows, cols) -> int:
 
 
 def _fp4(q, scale, fmt, name, batches, rows, cols):
-    """Addresses of a 4-bit operand's codes and scales."""
-    import torch
-
-    n = moe_fp4_scale_bytes(fmt, rows, cols)
+    """Addresses of a 4-bit operand's codes and scales (fmt: the format's code)."""
+    n = -(-rows // 128) * -(-cols // (128 if fmt == 0 else 64)) * 512   # moe_fp4_scale_bytes
     return (_ptr(q, name, torch.uint8, (batches, rows, cols // 2)),
-            _ptr(scale, name + "_scale", torch.uint8, (batches, n)))
+            _ptr(scale, name[:-1] + "scale", torch.uint8, (batches, n)))
 
 
 def _batched(t):
@@ -397,10 +387,10 @@ def moe_quantize_fp4(src, fmt, q, scale, dev_status, global_scale=None, counts=N
     batch (global_scale [batches] fp32, None: 1); with counts / c_dev only the
     kept rows of each batch."""
     b, r, c = _batched(src)
-    I = _i32()
+    I, fmt = _i32(), _code(FP4, fmt, "fmt")
     qp, sp = _fp4(q if src.dim() == 3 else q.unsqueeze(0), scale, fmt, "q", b, r, c)
     _check(load().moe_quantize_fp4(
-        _ptr(src, "src"), _dt(src), b, r, c, _code(FP4, fmt, "fmt"),
+        _ptr(src, "src"), _dt(src), b, r, c, fmt,
         _ptr(global_scale, "global_scale", _f32(), (b,)), _ptr(counts, "counts", I, (b,)),
         _ptr(c_dev, "c_dev", I), qp, sp, _ptr(dev_status, "dev_status", I), _stream(stream)),
         "moe_quantize_fp4")
@@ -411,10 +401,10 @@ def moe_dequantize_fp4(q, scale, fmt, dst, dev_status, global_scale=None, counts
     """The values of moe_quantize_fp4's codes and scales, into dst [rows, cols]
     or [batches, rows, cols] (bf16 or fp32)."""
     b, r, c = _batched(dst)
-    I = _i32()
+    I, fmt = _i32(), _code(FP4, fmt, "fmt")
     qp, sp = _fp4(q if dst.dim() == 3 else q.unsqueeze(0), scale, fmt, "q", b, r, c)
     _check(load().moe_dequantize_fp4(
-        qp, sp, b, r, c, _code(FP4, fmt, "fmt"), _ptr(global_scale, "global_scale", _f32(), (b,)),
+        qp, sp, b, r, c, fmt, _ptr(global_scale, "global_scale", _f32(), (b,)),
         _ptr(counts, "counts", I, (b,)), _ptr(c_dev, "c_dev", I), _ptr(dst, "dst"), _dt(dst),
         _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_dequantize_fp4")
 
@@ -424,17 +414,15 @@ def moe_product_fp4(a_q, a_scale, a_global, counts, c_dev, b_q, b_scale, b_globa
     """out[j] = a[j] b[j]^T (+ bias[j]) over the kept rows of every expert:
     a_q [e, c_max, k/2], b_q [e, n, k/2] with their scales and factors ([e] fp32
     or None), bias [e, n] bf16 or None, out [e, c_max, n] bf16."""
-    import torch
-
     e, c_max, n = out.shape
     k = 2 * a_q.shape[2]
-    I, F, bf = _i32(), _f32(), torch.bfloat16
+    I, F, bf, fmt = _i32(), _f32(), torch.bfloat16, _code(FP4, fmt, "fmt")
     ap, asp = _fp4(a_q, a_scale, fmt, "a_q", e, c_max, k)
     bp, bsp = _fp4(b_q, b_scale, fmt, "b_q", e, n, k)
     _check(load().moe_product_fp4(
         ap, asp, _ptr(a_global, "a_global", F, (e,)), _ptr(counts, "counts", I, (e,)),
         _ptr(c_dev, "c_dev", I), bp, bsp, _ptr(b_global, "b_global", F, (e,)),
-        _ptr(bias, "bias", bf, (e, n)), _code(FP4, fmt, "fmt"), e, c_max, k, n,
+        _ptr(bias, "bias", bf, (e, n)), fmt, e, c_max, k, n,
         _ptr(out, "out", bf), _ptr(dev_status, "dev_status", I), _stream(stream)),
         "moe_product_fp4")
 
@@ -450,11 +438,9 @@ def moe_expert_ffn_fp4(buf_q, buf_scale, buf_global, hid_global, counts, c_dev, 
     """The expert FFN on 4-bit operands (moe_quantize_fp4 of the buffer's kept
     rows and of the weights [e, h, m], [e, h, m], [e, m, h]); factors [e] fp32
     or None; w3 and its scales only for SwiGLU, which takes no biases."""
-    import torch
-
     e, c_max, m = out.shape
     h = w1_q.shape[1]
-    I, F, bf = _i32(), _f32(), torch.bfloat16
+    I, F, bf, fmt = _i32(), _f32(), torch.bfloat16, _code(FP4, fmt, "fmt")
     xp, xsp = _fp4(buf_q, buf_scale, fmt, "buf_q", e, c_max, m)
     w1p, w1sp = _fp4(w1_q, w1_scale, fmt, "w1_q", e, h, m)
     w3p, w3sp = _fp4(w3_q, w3_scale, fmt, "w3_q", e, h, m)
@@ -464,7 +450,7 @@ def moe_expert_ffn_fp4(buf_q, buf_scale, buf_global, hid_global, counts, c_dev, 
         _ptr(counts, "counts", I, (e,)), _ptr(c_dev, "c_dev", I), w1p, w1sp,
         _ptr(w1_global, "w1_global", F, (e,)), _ptr(b1, "b1", bf, (e, h)), w3p, w3sp,
         _ptr(w3_global, "w3_global", F, (e,)), w2p, w2sp, _ptr(w2_global, "w2_global", F, (e,)),
-        _ptr(b2, "b2", bf, (e, m)), _code(FP4, fmt, "fmt"), _act(act), e, c_max, m, h,
+        _ptr(b2, "b2", bf, (e, m)), fmt, _act(act), e, c_max, m, h,
         _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         _ptr(out, "out", bf), _ptr(dev_status, "dev_status", I), _stream(stream)),
         "moe_expert_ffn_fp4")
@@ -494,8 +480,6 @@ def moe_expert_ffn_bwd_saved(buf, hid, pre, counts, c_dev, w1, w3, w2, act, d_ou
     """moe_expert_ffn_bwd with what moe_expert_ffn_train kept: nothing is
     recomputed.  The weight and bias gradients are all bf16 or all fp32
     (kept in fp32); w3 / d_w3 for SwiGLU only."""
-    import torch
-
     e, c_max, m = buf.shape
     h = w1.shape[1]
     I, dt = _i32(), buf.dtype
@@ -645,8 +629,6 @@ def moe_layer_forward_pipelined(x, wg, gate_bias, w1, b1, w3, w2, b2, act, k, ca
 
 
 def torch_current_stream():
-    import torch
-
     return torch.cuda.current_stream()
 
 

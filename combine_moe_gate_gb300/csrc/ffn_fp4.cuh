@@ -498,15 +498,16 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
     const int64_t nt = fp4_scale_tiles(Fp4<FMT>::BLK, args.K);
     const int64_t a_tiles = (args.c_max + 127) / 128, b_tiles = (args.n_out + 127) / 128;
     constexpr int KT = F4Tiling<FMT>::KT;
-    CUtensorMap mA, mB, mB3, mSA, mSB, mSB3, mO;
+    CUtensorMap mA, mB, mSA, mSB;
     if (!make_map_u8(&mA, a.q, (uint64_t)(e * args.c_max), (uint64_t)args.K / 2, 64) ||
         !make_map_u8(&mB, b.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
-        !make_map_u8(&mB3, b3.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
-        !make_map_scales(&mSA, a.scale, e * a_tiles, nt, KT) ||
-        !make_map_scales(&mSB, b.scale, e * b_tiles, nt, KT) ||
-        !make_map_scales(&mSB3, b3.scale, e * b_tiles, nt, KT) ||
-        !make_map(&mO, EPI == FP4_BIAS ? (const void *)args.out : a.q, EPI == FP4_BIAS ? (uint64_t)(e * args.c_max) : 32,
-                  EPI == FP4_BIAS ? (uint64_t)args.n_out : 32, 32, 32))
+        !make_map_scales(&mSA, a.scale, e * a_tiles, nt, KT) || !make_map_scales(&mSB, b.scale, e * b_tiles, nt, KT))
+        return MOE_ERR_CUDA;
+    CUtensorMap mB3 = mB, mSB3 = mSB, mO = mB;   // where the kernel uses one, its own
+    if (EPI == FP4_SWIGLU && (!make_map_u8(&mB3, b3.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
+                              !make_map_scales(&mSB3, b3.scale, e * b_tiles, nt, KT)))
+        return MOE_ERR_CUDA;
+    if (EPI == FP4_BIAS && !make_map(&mO, args.out, (uint64_t)(e * args.c_max), (uint64_t)args.n_out, 32, 32))
         return MOE_ERR_CUDA;
     auto kern = fp4_group_gemm<FMT, EPI>;
     constexpr size_t SMEM = f4_smem_bytes<FMT>();

@@ -218,9 +218,12 @@ route_bwd_kernel(const T *__restrict__ logits, const int32_t *__restrict__ idx,
 }
 
 int grid_for(int64_t s) {
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    static int cached[64] = {0};
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
+        if (!cached[dev]) cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev);
+        if (cached[dev] > 0) sms = cached[dev];
+    }
     const int64_t want = (s + RT_WARPS - 1) / RT_WARPS, cap = (int64_t)sms * 8;
     return (int)(want < cap ? want : cap);
 }
