@@ -5,24 +5,56 @@
 //   score_j  = 1 / (1 + exp(-l_j))                      (sigmoid), or
 //              exp(l_j - max l) / sum_i exp(l_i - max l) (softmax);
 //   choice_j = score_j + bias_j; -inf for a masked expert (l_j = -inf) or NaN;
-//   group value = sum of the group's best group_top live choices (-inf: none);
+//   group value = sum of the group's best group_top (1|2) live choices (-inf: none);
 //   idx = the k best experts of the topk_groups best groups by (choice
 //   descending, index ascending); gates = score[idx] (/ their sum) * scale.
 // The bias steers the choice only, so it has no gradient and the gates stay
 // the scores' own.  Scores use the correctly rounded division and one fixed
 // summation order (adjacent pairs over the width padded to a power of two),
 // so idx is reproducible bit for bit.
+//
+// Forward and backward read or write each logit once; at the sizes of a layer
+// the forward is bound by its instructions (a sigmoid's exp and division are
+// about 20 per expert), so its layout is chosen to spend few of them: L lanes
+// share a token and hold V = width / L consecutive experts each, with V = 8
+// where the width allows, so that 32 / L tokens run in one warp.
 #include "common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int RT_WARPS = 8;
+constexpr int RT_THREADS = 256;
+constexpr int RT_WARPS = RT_THREADS / 32;
 
 template <typename T> __device__ __forceinline__ float ld_logit(const T *p);
 template <> __device__ __forceinline__ float ld_logit<float>(const float *p) { return __ldg(p); }
 template <> __device__ __forceinline__ float ld_logit<__nv_bfloat16>(const __nv_bfloat16 *p) {
     return __bfloat162float(*p);
+}
+
+// V logits of a token from expert j0 on; -inf past the last expert.  vec: rows
+// are whole 16-byte chunks (e * sizeof(T) % 16 == 0), so a chunk is either
+// inside a row or past it.
+template <typename T, int V>
+__device__ __forceinline__ void ld_logits(const T *row, int j0, int e, bool vec, float (&l)[V]) {
+    constexpr int N = Elt<T>::VEC;
+    if (V % N == 0 && vec) {
+#pragma unroll
+        for (int c = 0; c < V / N; c++) {
+            if (j0 + c * N < e) {
+                float f[N];
+                Elt<T>::unpack(ld_stream(row + j0 + c * N), f);
+#pragma unroll
+                for (int i = 0; i < N; i++) l[c * N + i] = f[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; i++) l[c * N + i] = -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) l[i] = j0 + i < e ? ld_logit(row + j0 + i) : -INFINITY;
+    }
 }
 
 // Order-preserving map of a float to an unsigned key (-0 as +0); never 0.
@@ -34,33 +66,29 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // The sigmoid; the additions and the division are single IEEE operations.
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
-// Scores of one token over a warp: lane holds experts lane * V .. + V - 1.
-// Padding enters as exp = 0.
-template <int V, bool SOFTMAX>
-__device__ __forceinline__ void scores(const float (&l)[V], int e, int lane, float (&sc)[V]) {
+// Scores of a token over its L lanes (sub: this lane's place among them), V
+// consecutive experts a lane.  Padding enters as exp = 0.
+template <int V, int L, bool SOFTMAX>
+__device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, float (&sc)[V]) {
     if (!SOFTMAX) {
 #pragma unroll
         for (int i = 0; i < V; i++) sc[i] = sigmoid_rn(l[i]);
         return;
     }
     float top = -INFINITY;
+    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < V; i++) top = fmaxf(top, l[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top == -INFINITY) {   // nothing left (scores 0), or nothing but NaN and -inf
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < V; i++) nan |= l[i] != l[i];
-        const float v = __any_sync(0xffffffffu, nan) ? NAN : 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; i++) sc[i] = v;
-        return;
+    for (int i = 0; i < V; i++) {
+        top = fmaxf(top, l[i]);
+        nan |= l[i] != l[i];
     }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool none = top == -INFINITY;   // nothing left (scores 0), unless a NaN is there
     float t[V];
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        sc[i] = lane * V + i < e ? expf(__fsub_rn(l[i], top)) : 0.0f;
+        sc[i] = sub * V + i < e && !(none && !nan) ? expf(__fsub_rn(l[i], top)) : 0.0f;
         t[i] = sc[i];
     }
 #pragma unroll
@@ -69,193 +97,394 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int lane, flo
         for (int i = 0; i < n / 2; i++) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
     float sum = t[0];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+    for (int o = 1; o < L; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
 #pragma unroll
-    for (int i = 0; i < V; i++) sc[i] = __fdiv_rn(sc[i], sum);
+    for (int i = 0; i < V; i++) sc[i] = sum == 0.0f ? 0.0f : __fdiv_rn(sc[i], sum);
 }
 
-// One warp per token, V = 2^p / 32 experts per lane in index order.
-template <typename T, int V, bool SOFTMAX>
-__global__ void __launch_bounds__(RT_WARPS * 32)
+// Largest of u over a token's L lanes.
+template <int L>
+__device__ __forceinline__ uint32_t max_over(uint32_t u) {
+    if (L == 32) return __reduce_max_sync(0xffffffffu, u);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
+    return u;
+}
+
+// The lowest of a token's lanes where p holds (0 if nowhere), as its place.
+template <int L>
+__device__ __forceinline__ int first_lane(bool p, int lane) {
+    uint32_t b = __ballot_sync(0xffffffffu, p);
+    if (L < 32) b = (b >> (lane & ~(L - 1))) & ((1u << L) - 1);
+    return max(__ffs(b) - 1, 0);
+}
+
+// Merge the two best (a >= b) of another lane into this lane's.
+__device__ __forceinline__ void merge_top2(float &a, float &b, float oa, float ob) {
+    b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+    a = fmaxf(a, oa);
+}
+
+// Which groups of a token stay, as a bit mask.  A group's two best choices come
+// by shuffles where its lanes are a power of two, else from the choices in
+// shared memory; the groups' keys then meet in `keys` (32 per token).
+template <int V, int L>
+__device__ __forceinline__ uint32_t kept_groups(const float (&ch)[V], float *choices, uint32_t *keys, int sub,
+                                                int groups, int gs, int topk_groups, int group_top) {
+    const int gl = gs / V;   // lanes per group
+    __syncwarp();
+    if (gs % V == 0 && (gl & (gl - 1)) == 0) {
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            b = fmaxf(b, fminf(a, ch[i]));
+            a = fmaxf(a, ch[i]);
+        }
+        for (int o = 1; o < gl; o <<= 1)
+            merge_top2(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
+        if ((sub & (gl - 1)) == 0 && sub / gl < groups)
+            keys[sub / gl] = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) choices[sub * V + i] = ch[i];
+        __syncwarp();
+        for (int g = sub; g < groups; g += L) {
+            float a = -INFINITY, b = -INFINITY;
+            for (int i = 0; i < gs; i++) {
+                const float v = choices[g * gs + i];
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+            }
+            keys[g] = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
+        }
+    }
+    __syncwarp();
+    uint32_t kept = 0;
+    for (int g = sub; g < groups; g += L) {
+        const uint32_t mine = keys[g];
+        int ahead = 0;
+        for (int o = 0; o < groups; o++) {
+            const uint32_t other = keys[o];
+            ahead += other > mine || (other == mine && o < g);
+        }
+        if (ahead < topk_groups) kept |= 1u << g;
+    }
+    if (L == 32) return __reduce_or_sync(0xffffffffu, kept);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, o);
+    return kept;
+}
+
+// L lanes per token.  k <= 32 routes: lane (place) r of a token finishes the
+// routes r, r + L, ...
+template <typename T, int V, int L, bool SOFTMAX>
+__global__ void __launch_bounds__(RT_THREADS)
 route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, int64_t s, int e,
-                  int k, int groups, int topk_groups, int group_top, float scale, int normalize,
+                  int k, int groups, int topk_groups, int group_top, float scale, int normalize, int vec,
                   int32_t *__restrict__ idx, float *__restrict__ gates, int32_t *status) {
-    __shared__ float s_choice[RT_WARPS][V * 32];
+    constexpr int TPW = 32 / L;   // tokens per warp
+    __shared__ float s_val[RT_WARPS][V * 32];    // choices, then scores
+    __shared__ uint2 s_cand[RT_WARPS][32];       // candidates (L = 32)
+    __shared__ int32_t s_sel[RT_WARPS][TPW * 32];   // the selection, by route
     pdl_enter();
     if (status_bad(status)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1), tw = lane / L;
     const int gs = e / groups;
-    for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < s; t += (int64_t)gridDim.x * RT_WARPS) {
-        float l[V], sc[V];
+    float *val = s_val[warp] + tw * (V * L);
+    int32_t *sel = s_sel[warp] + tw * 32;
+    float bs[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) bs[i] = bias && sub * V + i < e ? bias[sub * V + i] : 0.0f;
+    const int64_t step = (int64_t)gridDim.x * RT_WARPS * TPW;
+    for (int64_t t0 = ((int64_t)blockIdx.x * RT_WARPS + warp) * TPW; t0 < s; t0 += step) {
+        const int64_t t = min(t0 + tw, s - 1);   // lanes past the end repeat the last token
+        float l[V], sc[V], ch[V];
+        ld_logits<T, V>(logits + t * e, sub * V, e, vec, l);
+        scores<V, L, SOFTMAX>(l, e, sub, sc);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            const int j = lane * V + i;
-            l[i] = j < e ? ld_logit(logits + t * e + j) : -INFINITY;
-        }
-        scores<V, SOFTMAX>(l, e, lane, sc);
-        float ch[V];
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int j = lane * V + i;
-            ch[i] = bias && j < e ? __fadd_rn(sc[i], bias[j]) : sc[i];
+            ch[i] = bias ? __fadd_rn(sc[i], bs[i]) : sc[i];
             if (l[i] == -INFINITY || ch[i] != ch[i]) ch[i] = -INFINITY;
         }
-        uint32_t kept = 0xffffffffu;
-        if (groups > 1) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < V; i++) s_choice[warp][lane * V + i] = ch[i];
-            __syncwarp();
-            uint32_t gk = 0;   // no group on this lane: below every group
-            if (lane < groups) {
-                float a = -INFINITY, b = -INFINITY;   // the two best of this lane's group
-                for (int i = 0; i < gs; i++) {
-                    const float v = s_choice[warp][lane * gs + i];
-                    b = fmaxf(b, fminf(a, v));
-                    a = fmaxf(a, v);
-                }
-                gk = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
-            }
-            int ahead = 0;
-            for (int g = 0; g < groups; g++) {
-                const uint32_t o = __shfl_sync(0xffffffffu, gk, g);
-                ahead += o > gk || (o == gk && g < lane);
-            }
-            kept = __ballot_sync(0xffffffffu, lane < groups && ahead < topk_groups);
-        }
         uint32_t key[V];
+        uint32_t kept = 0xffffffffu;   // bit g: group g of this token stays
+        if (groups > 1)
+            kept = kept_groups<V, L>(ch, val, reinterpret_cast<uint32_t *>(sel), sub, groups, gs, topk_groups,
+                                     group_top);
+        const int g0 = groups > 1 ? sub * V / gs : 0;
+        const bool one_group = groups > 1 && gs % V == 0;   // this lane's experts share a group
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            const int j = lane * V + i;
-            key[i] = j < e && (groups == 1 || (kept >> (j / gs) & 1)) ? order_key(ch[i]) : 0u;
+            const int j = sub * V + i;
+            const bool in = groups == 1 || (kept >> (one_group ? g0 : min(j / gs, 31)) & 1);
+            key[i] = j < e && in ? order_key(ch[i]) : 0u;
         }
-        float g_mine = 0.0f, sum = 0.0f;
-        int j_mine = 0;
-        for (int r = 0; r < k; r++) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < V; i++) val[sub * V + i] = sc[i];   // scores by expert
+        bool done = false;
+        if (L == 32) {
+            // A token's k best are no less than the k-th largest of its lanes'
+            // maxima; the few that are not go to a list, and their places in it
+            // are counted.  More than 32 of them (equal choices): below.
             uint32_t best = 0;
 #pragma unroll
             for (int i = 0; i < V; i++) best = max(best, key[i]);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-            const int src = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-            int j = 0;
-            float g = 0.0f;
-            bool taken = false;
+            uint32_t m = best, low = 0;
+            for (int r = 0; r < k; r++) {
+                low = __reduce_max_sync(0xffffffffu, m);
+                if (lane == __ffs(__ballot_sync(0xffffffffu, m == low)) - 1) m = 0u;
+            }
+            low = max(low, 1u);
+            int n = 0;
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                if (lane == src && !taken && key[i] == top) {
-                    taken = true;
-                    key[i] = 0u;
-                    j = lane * V + i;
-                    g = sc[i];
+            for (int i = 0; i < V; i++) {
+                const uint32_t b = __ballot_sync(0xffffffffu, key[i] >= low);
+                const int at = n + __popc(b & ((1u << lane) - 1));
+                if (key[i] >= low && at < 32) s_cand[warp][at] = make_uint2(key[i], sub * V + i);
+                n += __popc(b);
+            }
+            __syncwarp();
+            if (n <= 32) {
+                const uint2 c = s_cand[warp][lane];
+                int rank = 0;
+                for (int q = 0; q < n; q++) {
+                    const uint2 o = s_cand[warp][q];
+                    rank += o.x > c.x || (o.x == c.x && o.y < c.y);
                 }
-            j = __shfl_sync(0xffffffffu, j, src);
-            g = __shfl_sync(0xffffffffu, g, src);
-            sum = __fadd_rn(sum, g);
-            if (lane == r) { j_mine = j; g_mine = g; }
+                if (lane < n && rank < k) sel[rank] = (int32_t)c.y;
+                done = true;
+            }
         }
-        if (lane < k) {
-            if (normalize) g_mine = sum == 0.0f ? 0.0f : __fdiv_rn(g_mine, sum);
-            idx[(int64_t)lane * s + t] = j_mine;
-            gates[(int64_t)lane * s + t] = g_mine * scale;
+        if (!done) {
+            for (int r = 0; r < k; r++) {
+                uint32_t best = 0;
+#pragma unroll
+                for (int i = 0; i < V; i++) best = max(best, key[i]);
+                const uint32_t top = max_over<L>(best);
+                const bool mine = first_lane<L>(best == top, lane) == sub;
+                int pos = 0;
+#pragma unroll
+                for (int i = V - 1; i >= 0; i--) pos = key[i] == top ? i : pos;
+#pragma unroll
+                for (int i = 0; i < V; i++) key[i] = mine && i == pos ? 0u : key[i];
+                if (mine) sel[r] = sub * V + pos;
+            }
         }
+        __syncwarp();
+        float sum = 0.0f;
+        if (normalize)
+            for (int r = 0; r < k; r++) sum = __fadd_rn(sum, val[sel[r]]);
+        if (t0 + tw < s)
+            for (int r = sub; r < k; r += L) {
+                const int j = sel[r];
+                float g = val[j];
+                if (normalize) g = sum == 0.0f ? 0.0f : __fdiv_rn(g, sum);
+                idx[(int64_t)r * s + t] = j;
+                gates[(int64_t)r * s + t] = g * scale;
+            }
+        __syncwarp();
     }
 }
 
-// d_logits of one token per warp.  With g the selected scores, G = g / sum g
-// (normalised) and A = sum_r dg_r G_r:
-//   softmax, normalised: scale G (dg - A) at the selection, 0 elsewhere;
-//   softmax, raw:        scale (p dg [selected] - p sum_r dg_r p_r) everywhere;
-//   sigmoid, normalised: scale G (dg - A)(1 - g) at the selection;
-//   sigmoid, raw:        scale dg g (1 - g) at the selection.
-template <typename T, typename D, int V, bool SOFTMAX>
-__global__ void __launch_bounds__(RT_WARPS * 32)
-route_bwd_kernel(const T *__restrict__ logits, const int32_t *__restrict__ idx,
-                 const float *__restrict__ d_gates, int64_t s, int e, int k, float scale,
-                 int normalize, D *__restrict__ d_logits, int32_t *status) {
-    __shared__ float s_d[RT_WARPS][V * 32];
+// ---------------------------------------------------------------- backward
+// A CTA takes `tb` consecutive tokens (a multiple of 8): their rows of
+// d_logits are formed in shared memory and leave as one contiguous run of
+// 16-byte stores, whatever e is.
+constexpr int BWD_FLOATS = 8192;   // 32 tokens of 256 experts, 8 of 1024
+constexpr int BWD_LANES = 8;       // lanes per token for its routes
+
+__host__ __device__ inline int bwd_tokens(int e) { return e <= 256 ? 32 : e <= 512 ? 16 : 8; }
+
+template <typename D>
+__device__ __forceinline__ void store_rows(const float *rows, int64_t n, D *out) {
+    constexpr int N = Elt<D>::VEC;
+    for (int64_t i = threadIdx.x; i < n / N; i += RT_THREADS) st_v16(out + i * N, Elt<D>::pack(rows + i * N));
+    for (int64_t i = n / N * N + threadIdx.x; i < n; i += RT_THREADS) out[i] = (D)rows[i];
+}
+
+// Gradients that live on the selection: with g the selected scores, G = g / sum
+// g and A = sum_r dg_r G_r,
+//   softmax, normalised: scale G (dg - A)         (G needs the selected logits only);
+//   sigmoid, normalised: scale G (dg - A) (1 - g);
+//   sigmoid, raw:        scale dg g (1 - g).
+// Reads k logits a token; bound by the e values written.
+template <typename T, typename D, bool SOFTMAX>
+__global__ void __launch_bounds__(RT_THREADS)
+route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ idx,
+                     const float *__restrict__ d_gates, int64_t s, int e, int k, float scale,
+                     int normalize, D *__restrict__ d_logits, int32_t *status) {
+    __shared__ __align__(16) float rows[BWD_FLOATS];
     pdl_enter();
     if (status_bad(status)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < s; t += (int64_t)gridDim.x * RT_WARPS) {
-        float l[V], sc[V];
+    const int tb = bwd_tokens(e), sub = threadIdx.x % BWD_LANES, tok = threadIdx.x / BWD_LANES;
+    for (int64_t t0 = (int64_t)blockIdx.x * tb; t0 < s; t0 += (int64_t)gridDim.x * tb) {
+        const int nt = (int)min((int64_t)tb, s - t0);
+        const int64_t t = t0 + tok;
+        const bool on = tok < nt;
+        float4 *z = reinterpret_cast<float4 *>(rows);
+        for (int i = threadIdx.x; i < (nt * e + 3) / 4; i += RT_THREADS) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // this lane's routes sub, sub + 8, ... of its token
+        int j[4];
+        float x[4], dg[4], g[4];
+        bool bad = false;
+        float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int j = lane * V + i;
-            l[i] = j < e ? ld_logit(logits + t * e + j) : -INFINITY;
+        for (int q = 0; q < 4; q++) {
+            const int r = sub + q * BWD_LANES;
+            const bool have = on && r < k;
+            j[q] = have ? idx[(int64_t)r * s + t] : -1;
+            dg[q] = have ? d_gates[(int64_t)r * s + t] : 0.0f;
+            if (have && (j[q] < 0 || j[q] >= e)) { bad = true; j[q] = -1; }
+            x[q] = j[q] >= 0 ? ld_logit(logits + t * e + j[q]) : -INFINITY;
+            top = fmaxf(top, x[q]);
         }
-        scores<V, SOFTMAX>(l, e, lane, sc);
-        int j = lane < k ? idx[(int64_t)lane * s + t] : 0;
-        if (__any_sync(0xffffffffu, j < 0 || j >= e)) {
-            if (lane == 0) set_status(status, MOE_ERR_INVALID_ARG);
-            return;
+        if (bad) set_status(status, MOE_ERR_INVALID_ARG);
+        float total = 0.0f, dot = 0.0f;
+        if (SOFTMAX) {
+#pragma unroll
+            for (int o = BWD_LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
-        const float dg = lane < k ? d_gates[(int64_t)lane * s + t] : 0.0f;
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < V; i++) s_d[warp][lane * V + i] = sc[i];
-        __syncwarp();
-        const float g = lane < k ? s_d[warp][j] : 0.0f;
-        float total = g, dot = dg * g;
+        for (int q = 0; q < 4; q++) {
+            if (j[q] < 0 || (SOFTMAX && top == -INFINITY)) g[q] = 0.0f;
+            else g[q] = SOFTMAX ? expf(x[q] - top) : sigmoid_rn(x[q]);
+            total += g[q];
+            dot += dg[q] * g[q];
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+        for (int o = BWD_LANES / 2; o > 0; o >>= 1) {
             total += __shfl_xor_sync(0xffffffffu, total, o);
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        float d;
-        if (normalize) d = total == 0.0f ? 0.0f : scale * (g / total) * (dg - dot / total);
-        else d = scale * dg * g;
-        if (!SOFTMAX) d *= 1.0f - g;
-        const float back = SOFTMAX && !normalize ? scale * dot : 0.0f;
-        __syncwarp();
+        __syncthreads();   // the rows are zero
 #pragma unroll
-        for (int i = 0; i < V; i++) s_d[warp][lane * V + i] = -sc[i] * back;
-        __syncwarp();
-        if (lane < k) s_d[warp][j] += d;
-        __syncwarp();
-        for (int i = lane; i < e; i += 32) d_logits[t * e + i] = (D)s_d[warp][i];
-        __syncwarp();
+        for (int q = 0; q < 4; q++) {
+            if (j[q] < 0) continue;
+            float d;
+            if (normalize) d = total == 0.0f ? 0.0f : scale * (g[q] / total) * (dg[q] - dot / total);
+            else d = scale * dg[q] * g[q];
+            if (!SOFTMAX) d *= 1.0f - g[q];
+            rows[tok * e + j[q]] = d;
+        }
+        __syncthreads();
+        store_rows(rows, (int64_t)nt * e, d_logits + t0 * e);
+        __syncthreads();   // rows is rewritten
     }
 }
 
-int grid_for(int64_t s) {
+// Raw softmax gates: d_j = scale p_j (dg_j [selected] - sum_r dg_r p_r) for every
+// expert.  L lanes a token as in the forward.
+template <typename T, typename D, int V, int L>
+__global__ void __launch_bounds__(RT_THREADS)
+route_bwd_all_kernel(const T *__restrict__ logits, const int32_t *__restrict__ idx,
+                     const float *__restrict__ d_gates, int64_t s, int e, int k, float scale, int vec,
+                     D *__restrict__ d_logits, int32_t *status) {
+    constexpr int TPC = RT_THREADS / L;   // tokens per CTA and pass
+    constexpr int ROUTES = 32 / L;        // routes per lane, at most
+    __shared__ __align__(16) float rows[TPC * V * L];
+    pdl_enter();
+    if (status_bad(status)) return;
+    const int sub = threadIdx.x & (L - 1), tok = threadIdx.x / L;
+    for (int64_t t0 = (int64_t)blockIdx.x * TPC; t0 < s; t0 += (int64_t)gridDim.x * TPC) {
+        const int nt = (int)min((int64_t)TPC, s - t0);
+        const int64_t t = t0 + min(tok, nt - 1);
+        float l[V], p[V];
+        ld_logits<T, V>(logits + t * e, sub * V, e, vec, l);
+        scores<V, L, true>(l, e, sub, p);
+        float *row = rows + tok * e;
+        const bool on = tok < nt;   // lanes past the end repeat the last token's scores, and write nothing
+        if (on)
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (sub * V + i < e) row[sub * V + i] = p[i];
+        __syncwarp();
+        float dot = 0.0f, pj[ROUTES], dg[ROUTES];
+        int j[ROUTES];
+#pragma unroll
+        for (int q = 0; q < ROUTES; q++) {
+            const int r = sub + q * L;
+            j[q] = on && r < k ? idx[(int64_t)r * s + t] : -1;
+            if (on && r < k && (j[q] < 0 || j[q] >= e)) {
+                set_status(status, MOE_ERR_INVALID_ARG);
+                j[q] = -1;
+            }
+            dg[q] = j[q] >= 0 ? d_gates[(int64_t)r * s + t] : 0.0f;
+            pj[q] = j[q] >= 0 ? row[j[q]] : 0.0f;
+            dot += dg[q] * pj[q];
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        __syncwarp();
+        if (on)
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (sub * V + i < e) row[sub * V + i] = -scale * p[i] * dot;
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < ROUTES; q++)
+            if (j[q] >= 0) row[j[q]] = scale * pj[q] * (dg[q] - dot);
+        __syncthreads();
+        store_rows(rows, (int64_t)nt * e, d_logits + t0 * e);
+        __syncthreads();
+    }
+}
+
+// CTAs for `units` CTA-sized pieces of work: at most eight a multiprocessor
+// (the kernels stride).
+int grid_for(int64_t units) {
     static int cached[64] = {0};
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
         if (!cached[dev]) cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev);
         if (cached[dev] > 0) sms = cached[dev];
     }
-    const int64_t want = (s + RT_WARPS - 1) / RT_WARPS, cap = (int64_t)sms * 8;
-    return (int)(want < cap ? want : cap);
+    const int64_t cap = (int64_t)sms * 8;
+    return (int)(units < cap ? units : cap);
 }
 
-template <typename T, int V>
+template <typename T, int V, int L>
 moe_status topk_v(const void *logits, const float *bias, int64_t s, int e, int k, bool softmax,
                   int groups, int topk_groups, int group_top, float scale, int normalize,
                   int32_t *idx, float *gates, int32_t *st, cudaStream_t stream) {
-    auto kern = softmax ? route_topk_kernel<T, V, true> : route_topk_kernel<T, V, false>;
-    return launch_pdl(kern, dim3(grid_for(s)), dim3(RT_WARPS * 32), 0, stream, (const T *)logits,
-                      bias, s, e, k, groups, topk_groups, group_top, scale, normalize, idx, gates, st);
+    auto kern = softmax ? route_topk_kernel<T, V, L, true> : route_topk_kernel<T, V, L, false>;
+    constexpr int TPC = RT_THREADS / L;
+    return launch_pdl(kern, dim3(grid_for((s + TPC - 1) / TPC)), dim3(RT_THREADS), 0, stream, (const T *)logits,
+                      bias, s, e, k, groups, topk_groups, group_top, scale, normalize,
+                      e % Elt<T>::VEC == 0 ? 1 : 0, idx, gates, st);
 }
 
-template <typename T, typename D, int V>
-moe_status bwd_v(const void *logits, const int32_t *idx, const float *d_gates, int64_t s, int e,
-                 int k, bool softmax, float scale, int normalize, void *d_logits, int32_t *st,
-                 cudaStream_t stream) {
-    auto kern = softmax ? route_bwd_kernel<T, D, V, true> : route_bwd_kernel<T, D, V, false>;
-    return launch_pdl(kern, dim3(grid_for(s)), dim3(RT_WARPS * 32), 0, stream, (const T *)logits,
-                      idx, d_gates, s, e, k, scale, normalize, (D *)d_logits, st);
+template <typename T, typename D, int V, int L>
+moe_status bwd_all_v(const void *logits, const int32_t *idx, const float *d_gates, int64_t s, int e, int k,
+                     float scale, void *d_logits, int32_t *st, cudaStream_t stream) {
+    constexpr int TPC = RT_THREADS / L;
+    return launch_pdl(route_bwd_all_kernel<T, D, V, L>, dim3(grid_for((s + TPC - 1) / TPC)), dim3(RT_THREADS), 0,
+                      stream, (const T *)logits, idx, d_gates, s, e, k, scale, e % Elt<T>::VEC == 0 ? 1 : 0,
+                      (D *)d_logits, st);
+}
+
+template <typename T, typename D>
+moe_status bwd_sel(const void *logits, const int32_t *idx, const float *d_gates, int64_t s, int e, int k,
+                   bool softmax, float scale, int normalize, void *d_logits, int32_t *st, cudaStream_t stream) {
+    auto kern = softmax ? route_bwd_sel_kernel<T, D, true> : route_bwd_sel_kernel<T, D, false>;
+    const int tb = bwd_tokens(e);
+    return launch_pdl(kern, dim3(grid_for((s + tb - 1) / tb)), dim3(RT_THREADS), 0, stream, (const T *)logits, idx,
+                      d_gates, s, e, k, scale, normalize, (D *)d_logits, st);
 }
 
 }  // namespace
 
-// Experts per lane: e padded to a power of two of at least 32.
-#define MOE_BY_V(CALL)                 \
-    if (e <= 32) return CALL(1);       \
-    if (e <= 64) return CALL(2);       \
-    if (e <= 128) return CALL(4);      \
-    if (e <= 256) return CALL(8);      \
-    if (e <= 512) return CALL(16);     \
-    return CALL(32)
+// Experts and lanes per token: e padded to a power of two, eight experts a
+// lane between 32 and 256.
+#define MOE_BY_E(CALL)                 \
+    if (e <= 8) return CALL(2, 4);     \
+    if (e <= 16) return CALL(4, 4);    \
+    if (e <= 32) return CALL(8, 4);    \
+    if (e <= 64) return CALL(8, 8);    \
+    if (e <= 128) return CALL(8, 16);  \
+    if (e <= 256) return CALL(8, 32);  \
+    if (e <= 512) return CALL(16, 32); \
+    return CALL(32, 32)
 
 moe_status route_topk_launch(const void *logits, moe_dtype ldt, const float *bias, int64_t s, int e,
                              int k, moe_score score, int groups, int topk_groups, int group_top,
@@ -263,10 +492,11 @@ moe_status route_topk_launch(const void *logits, moe_dtype ldt, const float *bia
                              cudaStream_t stream) {
     const bool sm = score == MOE_SCORE_SOFTMAX;
     const int nrm = (flags & MOE_FLAG_NORMALIZE_GATES) != 0;
-#define MOE_F(V) topk_v<float, V>(logits, bias, s, e, k, sm, groups, topk_groups, group_top, scale, nrm, idx, gates, st, stream)
-#define MOE_B(V) topk_v<__nv_bfloat16, V>(logits, bias, s, e, k, sm, groups, topk_groups, group_top, scale, nrm, idx, gates, st, stream)
-    if (ldt == MOE_F32) { MOE_BY_V(MOE_F); }
-    MOE_BY_V(MOE_B);
+    using bf = __nv_bfloat16;
+#define MOE_F(V, L) topk_v<float, V, L>(logits, bias, s, e, k, sm, groups, topk_groups, group_top, scale, nrm, idx, gates, st, stream)
+#define MOE_B(V, L) topk_v<bf, V, L>(logits, bias, s, e, k, sm, groups, topk_groups, group_top, scale, nrm, idx, gates, st, stream)
+    if (ldt == MOE_F32) { MOE_BY_E(MOE_F); }
+    MOE_BY_E(MOE_B);
 #undef MOE_F
 #undef MOE_B
 }
@@ -278,19 +508,24 @@ moe_status route_bwd_launch(const void *logits, moe_dtype ldt, const int32_t *id
     const bool sm = score == MOE_SCORE_SOFTMAX;
     const int nrm = (flags & MOE_FLAG_NORMALIZE_GATES) != 0;
     using bf = __nv_bfloat16;
-#define MOE_FF(V) bwd_v<float, float, V>(logits, idx, d_gates, s, e, k, sm, scale, nrm, d_logits, st, stream)
-#define MOE_FB(V) bwd_v<float, bf, V>(logits, idx, d_gates, s, e, k, sm, scale, nrm, d_logits, st, stream)
-#define MOE_BF(V) bwd_v<bf, float, V>(logits, idx, d_gates, s, e, k, sm, scale, nrm, d_logits, st, stream)
-#define MOE_BB(V) bwd_v<bf, bf, V>(logits, idx, d_gates, s, e, k, sm, scale, nrm, d_logits, st, stream)
-    if (ldt == MOE_F32 && ddt == MOE_F32) { MOE_BY_V(MOE_FF); }
-    if (ldt == MOE_F32) { MOE_BY_V(MOE_FB); }
-    if (ddt == MOE_F32) { MOE_BY_V(MOE_BF); }
-    MOE_BY_V(MOE_BB);
+    if (!sm || nrm) {
+        auto f = ldt == MOE_F32 ? (ddt == MOE_F32 ? bwd_sel<float, float> : bwd_sel<float, bf>)
+                                : (ddt == MOE_F32 ? bwd_sel<bf, float> : bwd_sel<bf, bf>);
+        return f(logits, idx, d_gates, s, e, k, sm, scale, nrm, d_logits, st, stream);
+    }
+#define MOE_FF(V, L) bwd_all_v<float, float, V, L>(logits, idx, d_gates, s, e, k, scale, d_logits, st, stream)
+#define MOE_FB(V, L) bwd_all_v<float, bf, V, L>(logits, idx, d_gates, s, e, k, scale, d_logits, st, stream)
+#define MOE_BF(V, L) bwd_all_v<bf, float, V, L>(logits, idx, d_gates, s, e, k, scale, d_logits, st, stream)
+#define MOE_BB(V, L) bwd_all_v<bf, bf, V, L>(logits, idx, d_gates, s, e, k, scale, d_logits, st, stream)
+    if (ldt == MOE_F32 && ddt == MOE_F32) { MOE_BY_E(MOE_FF); }
+    if (ldt == MOE_F32) { MOE_BY_E(MOE_FB); }
+    if (ddt == MOE_F32) { MOE_BY_E(MOE_BF); }
+    MOE_BY_E(MOE_BB);
 #undef MOE_FF
 #undef MOE_FB
 #undef MOE_BF
 #undef MOE_BB
 }
-#undef MOE_BY_V
+#undef MOE_BY_E
 
 }  // namespace moe
