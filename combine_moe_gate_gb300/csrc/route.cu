@@ -32,7 +32,7 @@ template <> __device__ __forceinline__ float ld_logit<__nv_bfloat16>(const __nv_
     return __bfloat162float(*p);
 }
 
-// V logits of a token from expert j0 on; -inf past the last expert.  vec: rows
+// V logits of a token from expert j0 on; 0 past the last expert.  vec: rows
 // are whole 16-byte chunks (e * sizeof(T) % 16 == 0), so a chunk is either
 // inside a row or past it.
 template <typename T, int V>
@@ -48,22 +48,40 @@ __device__ __forceinline__ void ld_logits(const T *row, int j0, int e, bool vec,
                 for (int i = 0; i < N; i++) l[c * N + i] = f[i];
             } else {
 #pragma unroll
-                for (int i = 0; i < N; i++) l[c * N + i] = -INFINITY;
+                for (int i = 0; i < N; i++) l[c * N + i] = 0.0f;
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; i++) l[i] = j0 + i < e ? ld_logit(row + j0 + i) : -INFINITY;
+        for (int i = 0; i < V; i++) l[i] = j0 + i < e ? ld_logit(row + j0 + i) : 0.0f;
     }
 }
 
 // Order-preserving map of a float to an unsigned key (-0 as +0); never 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
     const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-// The sigmoid; the additions and the division are single IEEE operations.
+// Correctly rounded reciprocal and quotient by fused corrections of an
+// approximation (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990: with r = fma(-b, y, 1) exact, fma(r, y, y)
+// rounds 1/b correctly; likewise a quotient).  They leave out the range checks
+// of the general operations: rcp_1 is for 1 <= x <= 2^126 (compared with
+// __frcp_rn for every mantissa), div_by for a = 0 or 2^-100 <= a <= 1 and 1 <= b
+// <= 1024, y its reciprocal.
+__device__ __forceinline__ float rcp_1(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return __fmaf_rn(__fmaf_rn(-x, y, 1.0f), y, y);
+}
+__device__ __forceinline__ float div_by(float a, float b, float y) {
+    float q = __fmul_rn(a, y);
+    q = __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+    return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+}
+
+// The sigmoid; the addition and the division are single IEEE operations.
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
 // Scores of a token over its L lanes (sub: this lane's place among them), V
@@ -71,24 +89,36 @@ __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_r
 template <int V, int L, bool SOFTMAX>
 __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, float (&sc)[V]) {
     if (!SOFTMAX) {
+        float x[V];
+        bool general = false;   // logits below -87: a subnormal score, or 0
 #pragma unroll
-        for (int i = 0; i < V; i++) sc[i] = sigmoid_rn(l[i]);
+        for (int i = 0; i < V; i++) {
+            x[i] = __fadd_rn(1.0f, expf(-l[i]));
+            general |= x[i] > 0x1p126f;
+            sc[i] = rcp_1(x[i]);
+        }
+        if (general)
+#pragma unroll
+            for (int i = 0; i < V; i++) sc[i] = __frcp_rn(x[i]);
         return;
     }
+    const int mine = min(max(e - sub * V, 0), V);   // experts on this lane
     float top = -INFINITY;
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        top = fmaxf(top, l[i]);
+        top = i < mine ? fmaxf(top, l[i]) : top;
         nan |= l[i] != l[i];
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool none = top == -INFINITY;   // nothing left (scores 0), unless a NaN is there
+    const bool none = top == -INFINITY && !nan;   // nothing left on this token (or only a NaN elsewhere): scores 0
     float t[V];
+    bool general = false;
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        sc[i] = sub * V + i < e && !(none && !nan) ? expf(__fsub_rn(l[i], top)) : 0.0f;
+        sc[i] = i < mine && !none ? expf(__fsub_rn(l[i], top)) : 0.0f;
+        general |= __float_as_uint(sc[i]) - 1u < __float_as_uint(0x1p-100f) - 1u;
         t[i] = sc[i];
     }
 #pragma unroll
@@ -98,8 +128,15 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, floa
     float sum = t[0];
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+    if (sum == 0.0f) return;   // every score is 0 already
+    const float y = rcp_1(sum);
+    if (general) {
 #pragma unroll
-    for (int i = 0; i < V; i++) sc[i] = sum == 0.0f ? 0.0f : __fdiv_rn(sc[i], sum);
+        for (int i = 0; i < V; i++) sc[i] = __fdiv_rn(sc[i], sum);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) sc[i] = div_by(sc[i], sum, y);
+    }
 }
 
 // Largest of u over a token's L lanes.
@@ -125,38 +162,46 @@ __device__ __forceinline__ void merge_top2(float &a, float &b, float oa, float o
     a = fmaxf(a, oa);
 }
 
-// Which groups of a token stay, as a bit mask.  A group's two best choices come
-// by shuffles where its lanes are a power of two, else from the choices in
-// shared memory; the groups' keys then meet in `keys` (32 per token).
+// Groups whose lanes are a power of two: whether this lane's group stays.  Its
+// two best choices come by shuffles, then every lane meets the other groups' keys.
+template <int V, int L>
+__device__ __forceinline__ bool my_group_stays(const float (&ch)[V], int sub, int groups, int gl, int topk_groups,
+                                               int group_top) {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        b = fmaxf(b, fminf(a, ch[i]));
+        a = fmaxf(a, ch[i]);
+    }
+    for (int o = 1; o < gl; o <<= 1)
+        merge_top2(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
+    const uint32_t gk = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
+    int ahead = 0;
+#pragma unroll 4
+    for (int l = 0; l < groups * gl; l += gl) {
+        const uint32_t o = __shfl_sync(0xffffffffu, gk, l, L);
+        ahead += o > gk || (o == gk && l + gl <= sub);
+    }
+    return ahead < topk_groups;
+}
+
+// Other groups: which of a token's stay, as a bit mask, from its choices in
+// shared memory; the groups' keys meet in `keys` (32 per token).
 template <int V, int L>
 __device__ __forceinline__ uint32_t kept_groups(const float (&ch)[V], float *choices, uint32_t *keys, int sub,
                                                 int groups, int gs, int topk_groups, int group_top) {
-    const int gl = gs / V;   // lanes per group
     __syncwarp();
-    if (gs % V == 0 && (gl & (gl - 1)) == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i++) choices[sub * V + i] = ch[i];
+    __syncwarp();
+    for (int g = sub; g < groups; g += L) {
         float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            b = fmaxf(b, fminf(a, ch[i]));
-            a = fmaxf(a, ch[i]);
+        for (int i = 0; i < gs; i++) {
+            const float v = choices[g * gs + i];
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
         }
-        for (int o = 1; o < gl; o <<= 1)
-            merge_top2(a, b, __shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
-        if ((sub & (gl - 1)) == 0 && sub / gl < groups)
-            keys[sub / gl] = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; i++) choices[sub * V + i] = ch[i];
-        __syncwarp();
-        for (int g = sub; g < groups; g += L) {
-            float a = -INFINITY, b = -INFINITY;
-            for (int i = 0; i < gs; i++) {
-                const float v = choices[g * gs + i];
-                b = fmaxf(b, fminf(a, v));
-                a = fmaxf(a, v);
-            }
-            keys[g] = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
-        }
+        keys[g] = order_key(group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a);
     }
     __syncwarp();
     uint32_t kept = 0;
@@ -175,21 +220,26 @@ __device__ __forceinline__ uint32_t kept_groups(const float (&ch)[V], float *cho
     return kept;
 }
 
-// L lanes per token.  k <= 32 routes: lane (place) r of a token finishes the
-// routes r, r + L, ...
+template <int N> struct alignas(4 * N) Vec { float f[N]; };
+
+// L lanes per token.
 template <typename T, int V, int L, bool SOFTMAX>
 __global__ void __launch_bounds__(RT_THREADS)
 route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, int64_t s, int e,
                   int k, int groups, int topk_groups, int group_top, float scale, int normalize, int vec,
                   int32_t *__restrict__ idx, float *__restrict__ gates, int32_t *status) {
     constexpr int TPW = 32 / L;   // tokens per warp
-    __shared__ float s_val[RT_WARPS][V * 32];    // choices, then scores
+    __shared__ __align__(16) float s_val[RT_WARPS][V * 32];   // choices, then scores
     __shared__ uint2 s_cand[RT_WARPS][32];       // candidates (L = 32)
     __shared__ int32_t s_sel[RT_WARPS][TPW * 32];   // the selection, by route
     pdl_enter();
     if (status_bad(status)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1), tw = lane / L;
-    const int gs = e / groups;
+    constexpr int VS = V < 4 ? V : 4;
+    const int gs = e / groups, gl = gs / V;   // experts and (where whole) lanes per group
+    const bool by_lane = gs % V == 0 && (gl & (gl - 1)) == 0;
+    const bool whole = e == V * L;                    // every lane holds V experts
+    const int mine = min(max(e - sub * V, 0), V);     // experts on this lane
     float *val = s_val[warp] + tw * (V * L);
     int32_t *sel = s_sel[warp] + tw * 32;
     float bs[V];
@@ -203,25 +253,26 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
         scores<V, L, SOFTMAX>(l, e, sub, sc);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            ch[i] = bias ? __fadd_rn(sc[i], bs[i]) : sc[i];
-            if (l[i] == -INFINITY || ch[i] != ch[i]) ch[i] = -INFINITY;
+            const float c = __fadd_rn(sc[i], bs[i]);   // without a bias: + 0
+            ch[i] = l[i] > -INFINITY && c == c && (whole || i < mine) ? c : -INFINITY;
         }
+        // keys: 0 below everything (not an expert, or of a group that does not stay)
         uint32_t key[V];
-        uint32_t kept = 0xffffffffu;   // bit g: group g of this token stays
-        if (groups > 1)
-            kept = kept_groups<V, L>(ch, val, reinterpret_cast<uint32_t *>(sel), sub, groups, gs, topk_groups,
-                                     group_top);
-        const int g0 = groups > 1 ? sub * V / gs : 0;
-        const bool one_group = groups > 1 && gs % V == 0;   // this lane's experts share a group
+        if (groups == 1 || by_lane) {
+            const bool in = groups == 1 || my_group_stays<V, L>(ch, sub, groups, gl, topk_groups, group_top);
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int j = sub * V + i;
-            const bool in = groups == 1 || (kept >> (one_group ? g0 : min(j / gs, 31)) & 1);
-            key[i] = j < e && in ? order_key(ch[i]) : 0u;
+            for (int i = 0; i < V; i++) key[i] = in && (whole || i < mine) ? order_key(ch[i]) : 0u;
+        } else {
+            const uint32_t kept = kept_groups<V, L>(ch, val, reinterpret_cast<uint32_t *>(sel), sub, groups, gs,
+                                                    topk_groups, group_top);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                key[i] = i < mine && (kept >> ((sub * V + i) / gs) & 1) ? order_key(ch[i]) : 0u;
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < V; i++) val[sub * V + i] = sc[i];   // scores by expert
+        for (int i = 0; i < V; i += VS)   // scores by expert
+            *reinterpret_cast<Vec<VS> *>(val + sub * V + i) = *reinterpret_cast<const Vec<VS> *>(sc + i);
         bool done = false;
         if (L == 32) {
             // A token's k best are no less than the k-th largest of its lanes'
@@ -231,9 +282,10 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
 #pragma unroll
             for (int i = 0; i < V; i++) best = max(best, key[i]);
             uint32_t m = best, low = 0;
-            for (int r = 0; r < k; r++) {
+#pragma unroll 4
+            for (int r = 0; r < k; r++) {   // (equal maxima leave together: the bound is lower then, never higher)
                 low = __reduce_max_sync(0xffffffffu, m);
-                if (lane == __ffs(__ballot_sync(0xffffffffu, m == low)) - 1) m = 0u;
+                m = m == low ? 0u : m;
             }
             low = max(low, 1u);
             int n = 0;
@@ -248,6 +300,7 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
             if (n <= 32) {
                 const uint2 c = s_cand[warp][lane];
                 int rank = 0;
+#pragma unroll 4
                 for (int q = 0; q < n; q++) {
                     const uint2 o = s_cand[warp][q];
                     rank += o.x > c.x || (o.x == c.x && o.y < c.y);
@@ -272,13 +325,23 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
             }
         }
         __syncwarp();
-        float sum = 0.0f;
-        if (normalize)
-            for (int r = 0; r < k; r++) sum = __fadd_rn(sum, val[sel[r]]);
+        // lane (place) r: route r, and with fewer lanes than routes r + L, ...
+        int j = sub < k ? sel[sub] : 0;
+        float g = sub < k ? val[j] : 0.0f, sum = 0.0f;
+        if (normalize) {
+            if (k <= L) {
+#pragma unroll 4
+                for (int r = 0; r < k; r++) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, g, r, L));
+            } else {
+                for (int r = 0; r < k; r++) sum = __fadd_rn(sum, val[sel[r]]);
+            }
+        }
         if (t0 + tw < s)
             for (int r = sub; r < k; r += L) {
-                const int j = sel[r];
-                float g = val[j];
+                if (r != sub) {
+                    j = sel[r];
+                    g = val[j];
+                }
                 if (normalize) g = sum == 0.0f ? 0.0f : __fdiv_rn(g, sum);
                 idx[(int64_t)r * s + t] = j;
                 gates[(int64_t)r * s + t] = g * scale;
