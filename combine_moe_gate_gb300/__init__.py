@@ -365,7 +365,10 @@ def moe_route_bwd(logits, idx, d_gates, d_logits, dev_status, score="softmax", s
 # ------------------------------------------------- microscaled 4-bit operands
 def moe_fp4_scale_bytes(fmt, rows, cols) -> int:
     """Bytes of one batch's tiled block scales (0: cols not a multiple of 32)."""
-    return int(load().moe_fp4_scale_bytes(_code(FP4, fmt, "fmt"), int(rows), int(cols)))
+    fmt = _code(FP4, fmt, "fmt")
+    if fmt not in (0, 1) or rows < 1 or rows > 0x7FFFFFFF or cols < 32 or cols % 32:
+        return 0
+    return -(-rows // 128) * -(-cols // (128 if fmt == 0 else 64)) * 512   # moe_fp4_scale_bytes of the C ABI
 
 
 def _fp4(q, scale, fmt, name, batches, rows, cols):

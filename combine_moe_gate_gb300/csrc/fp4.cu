@@ -1,7 +1,5 @@
 // Quantiser and expander of microscaled 4-bit rows (MX: e8m0 scales over 32
 // values; NV: e4m3 scales over 16 with one fp32 factor per batch).
-#include <cuda_fp16.h>
-
 #include "fp4.cuh"
 
 namespace moe {
@@ -21,22 +19,42 @@ __device__ __forceinline__ void st32(void *p, const float (&f)[8]) {
                  : "memory");
 }
 
-// 16 consecutive values (rows start on 64-byte boundaries: cols % 32 == 0).
-__device__ __forceinline__ void ld_values(const float *p, float (&f)[16]) {
-    uint32_t w[8];
+// 16 consecutive values as loaded (rows start on 64-byte boundaries: cols % 32
+// == 0), their largest magnitude (a NaN counts as one above infinity: as bits,
+// magnitudes order like integers) and the values.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    uint32_t w[2][8];
+    __device__ __forceinline__ void load(const float *p) { ld32(p, w[0]); ld32(p + 8, w[1]); }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        ld32(p + 8 * h, w);
-#pragma unroll
-        for (int i = 0; i < 8; i++) f[8 * h + i] = __uint_as_float(w[i]);
+        for (int i = 0; i < 8; i++) w[0][i] = w[1][i] = 0u;
     }
-}
-__device__ __forceinline__ void ld_values(const __nv_bfloat16 *p, float (&f)[16]) {
-    uint32_t w[8];
-    ld32(p, w);
+    __device__ __forceinline__ float amax() const {
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) { f[2 * i] = bf16lo(w[i]); f[2 * i + 1] = bf16hi(w[i]); }
-}
+        for (int i = 0; i < 8; i++) m = max(m, max(w[0][i] & 0x7FFFFFFFu, w[1][i] & 0x7FFFFFFFu));
+        return __uint_as_float(m);
+    }
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(__uint_as_float(w[i / 4][2 * (i % 4)]), __uint_as_float(w[i / 4][2 * (i % 4) + 1]));
+    }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { ld32(p, w); }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = 0u;
+    }
+    __device__ __forceinline__ float amax() const {
+        uint32_t m = 0;   // two at a time, as 16-bit integers
+#pragma unroll
+        for (int i = 0; i < 8; i++) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ float2 pair(int i) const { return make_float2(bf16lo(w[i]), bf16hi(w[i])); }
+};
 
 // Kept rows of batch b.
 __device__ __forceinline__ int64_t live_rows(const int32_t *counts, const int32_t *c_dev, int64_t b, int64_t rpb) {
@@ -44,13 +62,15 @@ __device__ __forceinline__ int64_t live_rows(const int32_t *counts, const int32_
 }
 
 // One lane per 16 values (an MX block is a pair of lanes); T lanes share a row,
-// 32 / T rows a warp.  A row takes a whole number of scale tiles' worth of
-// steps (4 blocks each): the lanes past its last block write the zeros of its
-// last tile.  Four neighbouring lanes gather the bytes that one row has in a
-// tile into one 4-byte store.  Bound by HBM: 2.56 bytes a value.
+// 32 / T rows a warp; a CTA takes its rows' steps of one segment (blockIdx.z).
+// A row takes a whole number of scale tiles' worth of steps (4 blocks each):
+// the lanes past its last block write the zeros of its last tile.  Four
+// neighbouring lanes gather the bytes that one row has in a tile into one
+// 4-byte store.  Bound by HBM (2.56 bytes a value) and, close behind, by
+// instructions: U steps are loaded before the first is used.
 template <typename T_, int FMT, int T>
 __global__ void __launch_bounds__(Q_THREADS)
-quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, int cols, int64_t ntiles,
+quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, int cols, int64_t ntiles, int seg,
                     const float *__restrict__ global, const int32_t *__restrict__ counts,
                     const int32_t *__restrict__ c_dev, uint8_t *__restrict__ q,
                     uint8_t *__restrict__ scale, int32_t *status) {
@@ -58,7 +78,9 @@ quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, in
     if (status_bad(status)) return;
     constexpr int TPB = Fp4<FMT>::BLK / 16;   // lanes per block
     constexpr int RPC = Q_THREADS / T;        // rows per CTA and pass
+    constexpr int U = sizeof(T_) == 2 ? 4 : 2;
     const int steps = (int)ntiles * 4 * TPB, nch = cols / 16;
+    const int first = (int)blockIdx.z * seg, last = min(first + seg, steps);   // seg: a multiple of T
     const int64_t batch_bytes = (rpb + 127) / 128 * ntiles * 512;
     const int lane = threadIdx.x & 31, sub = lane % T;
     for (int64_t b = blockIdx.y; b < batches; b += gridDim.y) {
@@ -69,27 +91,41 @@ quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, in
         // the warp's first row decides how often the warp goes round
         for (int64_t r = (int64_t)blockIdx.x * RPC + row_in; r - lane / T < rows; r += (int64_t)gridDim.x * RPC) {
             const bool live = r < rows;
-            const int64_t at = (b * rpb + r) * cols;
-            uint8_t *srow = scale + b * batch_bytes;
-#pragma unroll 2
-            for (int ch = sub; ch < steps; ch += T) {
-                const bool on = live && ch < nch;
-                float f[16] = {};
-                float amax = 0.0f, inv;
-                if (on) ld_values(src + at + ch * 16, f);
+            const T_ *srow = src + (b * rpb + r) * cols;
+            uint8_t *qrow = q + (b * rpb + r) * cols / 2;
+            uint8_t *scrow = scale + b * batch_bytes + fp4_scale_at(r, 0, ntiles);
+            for (int c0 = first + sub; c0 - sub < last; c0 += U * T) {
+                Raw<T_> v[U];
 #pragma unroll
-                for (int i = 0; i < 16; i++) amax = amax_nan(amax, f[i]);
-                if (TPB == 2) amax = amax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                uint32_t sc = fp4_scale<FMT>(amax, g, g6, inv);
+                for (int u = 0; u < U; u++) {
+                    v[u].zero();
+                    if (live && c0 + u * T < min(last, nch)) v[u].load(srow + (c0 + u * T) * 16);
+                }
 #pragma unroll
-                for (int i = 0; i < 16; i++) f[i] = __fmul_rn(f[i], inv);
-                if (on) *reinterpret_cast<uint2 *>(q + (at + ch * 16) / 2) = make_uint2(e2m1x8(f), e2m1x8(f + 8));
-                else sc = 0;   // past the row's last block
-                uint32_t word = sc;
+                for (int u = 0; u < U; u++) {
+                    const int ch = c0 + u * T;
+                    if (ch - sub >= last) break;   // the same in the lanes of a row's step
+                    float amax = v[u].amax(), inv;
+                    if (TPB == 2)
+                        amax = __uint_as_float(max(__float_as_uint(amax),
+                                                   __shfl_xor_sync(0xffffffffu, __float_as_uint(amax), 1)));
+                    uint32_t sc = fp4_scale<FMT>(amax, g, g6, inv);
+                    float f[16];
 #pragma unroll
-                for (int i = 1; i < 4; i++) word |= __shfl_down_sync(0xffffffffu, sc, i * TPB) << (8 * i);
-                if (live && lane % (4 * TPB) == 0)
-                    *reinterpret_cast<uint32_t *>(srow + fp4_scale_at(r, ch / TPB, ntiles)) = word;
+                    for (int i = 0; i < 8; i++) {
+                        const float2 p = __fmul2_rn(v[u].pair(i), make_float2(inv, inv));
+                        f[2 * i] = p.x;
+                        f[2 * i + 1] = p.y;
+                    }
+                    const bool on = live && ch < nch;
+                    if (on) *reinterpret_cast<uint2 *>(qrow + ch * 8) = make_uint2(e2m1x8(f), e2m1x8(f + 8));
+                    else sc = 0;   // past the row's last block
+                    uint32_t word = sc;
+#pragma unroll
+                    for (int i = 1; i < 4; i++) word |= __shfl_down_sync(0xffffffffu, sc, i * TPB) << (8 * i);
+                    if (live && ch < last && lane % (4 * TPB) == 0)
+                        *reinterpret_cast<uint32_t *>(scrow + (int64_t)(ch / (4 * TPB)) * 512) = word;
+                }
             }
         }
     }
@@ -114,35 +150,49 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, float (&f)[8]) {
     }
 }
 
-// One lane per 8 values, T lanes a row.  Bound by the bytes written.
+// One lane per 16 values, T lanes a row.  Bound by the bytes written.
 template <typename T_, int FMT, int T>
 __global__ void __launch_bounds__(Q_THREADS)
 dequantize_fp4_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t batches,
-                      int64_t rpb, int cols, int64_t ntiles, const float *__restrict__ global,
+                      int64_t rpb, int cols, int64_t ntiles, int seg, const float *__restrict__ global,
                       const int32_t *__restrict__ counts, const int32_t *__restrict__ c_dev,
                       T_ *__restrict__ dst, int32_t *status) {
     pdl_enter();
     if (status_bad(status)) return;
-    constexpr int RPC = Q_THREADS / T;
-    const int nch = cols / 8, sub = (int)threadIdx.x % T;
+    constexpr int RPC = Q_THREADS / T, U = 4;
+    const int first = (int)blockIdx.z * seg, last = min(first + seg, cols / 16), sub = (int)threadIdx.x % T;
     const int64_t batch_bytes = (rpb + 127) / 128 * ntiles * 512;
     for (int64_t b = blockIdx.y; b < batches; b += gridDim.y) {
         const int64_t rows = live_rows(counts, c_dev, b, rpb);
         const float g = FMT == MOE_FP4_NV && global ? global[b] : 1.0f;
         for (int64_t r = (int64_t)blockIdx.x * RPC + threadIdx.x / T; r < rows; r += (int64_t)gridDim.x * RPC) {
-            const int64_t at = (b * rpb + r) * cols;
-            const uint8_t *srow = scale + b * batch_bytes;
-#pragma unroll 4
-            for (int ch = sub; ch < nch; ch += T) {
-                const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(q + at / 2) + ch);
-                const uint32_t code = __ldg(srow + fp4_scale_at(r, ch * 8 / Fp4<FMT>::BLK, ntiles));
-                const float s = FMT == MOE_FP4_MX ? e8m0_value(code) : __fmul_rn(e4m3_value(code), g);
-                float f[8];
-                e2m1_values(w, f);
+            const uint2 *qrow = reinterpret_cast<const uint2 *>(q + (b * rpb + r) * cols / 2);
+            T_ *drow = dst + (b * rpb + r) * cols;
+            const uint8_t *scrow = scale + b * batch_bytes + fp4_scale_at(r, 0, ntiles);
+            for (int c0 = first + sub; c0 < last; c0 += U * T) {
+                uint2 w[U];
+                uint32_t code[U];
 #pragma unroll
-                for (int i = 0; i < 8; i++) f[i] = __fmul_rn(f[i], s);
-                if constexpr (sizeof(T_) == 4) st32(dst + at + ch * 8, f);
-                else st_v16(dst + at + ch * 8, Elt<__nv_bfloat16>::pack(f));
+                for (int u = 0; u < U; u++) {
+                    const int ch = min(c0 + u * T, last - 1), blk = ch * 16 / Fp4<FMT>::BLK;
+                    w[u] = __ldg(qrow + ch);
+                    code[u] = __ldg(scrow + (int64_t)(blk >> 2) * 512 + (blk & 3));
+                }
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int ch = c0 + u * T;
+                    if (ch >= last) break;
+                    const float s = FMT == MOE_FP4_MX ? e8m0_value(code[u]) : __fmul_rn(e4m3_value(code[u]), g);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        float f[8];
+                        e2m1_values(h ? w[u].y : w[u].x, f);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) f[i] = __fmul_rn(f[i], s);
+                        if constexpr (sizeof(T_) == 4) st32(drow + ch * 16 + 8 * h, f);
+                        else st_v16(drow + ch * 16 + 8 * h, Elt<__nv_bfloat16>::pack(f));
+                    }
+                }
             }
         }
     }
@@ -160,30 +210,38 @@ int sms() {
     return cached[dev];
 }
 
-// Batches along y; rows along x, at most about one resident wave of CTAs.
-dim3 grid_for(int64_t batches, int64_t rpb, int rows_per_cta) {
-    const int64_t y = batches < 65535 ? batches : 65535;
-    const int64_t want = (rpb + rows_per_cta - 1) / rows_per_cta;
-    const int64_t cap = ((int64_t)sms() * 8 + y - 1) / y;
-    return dim3((unsigned)(want < cap ? want : cap), (unsigned)y);
+// Rows along x, batches along y, and where those are too few for the device,
+// segments of a row along z: `per` steps of 16 values each, a multiple of T.
+dim3 grid_for(int64_t batches, int64_t rpb, int T, int steps, int &per) {
+    const int64_t y = batches < 65535 ? batches : 65535, want = (int64_t)sms() * 8;
+    const int64_t rows = (rpb * T + Q_THREADS - 1) / Q_THREADS, cap = (want + y - 1) / y;
+    const int64_t x = rows < cap ? rows : cap;
+    const int rounds = (steps + T - 1) / T;   // of a row's lanes
+    const int64_t z = want / (x * y) < rounds ? want / (x * y) : rounds;
+    per = (int)((rounds + (z > 1 ? z : 1) - 1) / (z > 1 ? z : 1)) * T;
+    return dim3((unsigned)x, (unsigned)y, (unsigned)((steps + per - 1) / per));
 }
 
 template <typename T_, int FMT, int T>
 moe_status quantize_t(const void *src, int64_t batches, int64_t rpb, int cols, const float *global,
                       const int32_t *counts, const int32_t *c_dev, void *q, void *scale,
                       int32_t *st, cudaStream_t stream) {
-    return launch_pdl(quantize_fp4_kernel<T_, FMT, T>, grid_for(batches, rpb, Q_THREADS / T), dim3(Q_THREADS), 0,
-                      stream, (const T_ *)src, batches, rpb, cols, fp4_scale_tiles(Fp4<FMT>::BLK, cols), global,
-                      counts, c_dev, (uint8_t *)q, (uint8_t *)scale, st);
+    const int64_t nt = fp4_scale_tiles(Fp4<FMT>::BLK, cols);
+    int per;
+    const dim3 grid = grid_for(batches, rpb, T, (int)nt * (Fp4<FMT>::BLK / 4), per);
+    return launch_pdl(quantize_fp4_kernel<T_, FMT, T>, grid, dim3(Q_THREADS), 0, stream, (const T_ *)src, batches,
+                      rpb, cols, nt, per, global, counts, c_dev, (uint8_t *)q, (uint8_t *)scale, st);
 }
 
 template <typename T_, int FMT, int T>
 moe_status dequantize_t(const void *q, const void *scale, int64_t batches, int64_t rpb, int cols,
                         const float *global, const int32_t *counts, const int32_t *c_dev, void *dst,
                         int32_t *st, cudaStream_t stream) {
-    return launch_pdl(dequantize_fp4_kernel<T_, FMT, T>, grid_for(batches, rpb, Q_THREADS / T), dim3(Q_THREADS), 0,
-                      stream, (const uint8_t *)q, (const uint8_t *)scale, batches, rpb, cols,
-                      fp4_scale_tiles(Fp4<FMT>::BLK, cols), global, counts, c_dev, (T_ *)dst, st);
+    int per;
+    const dim3 grid = grid_for(batches, rpb, T, cols / 16, per);
+    return launch_pdl(dequantize_fp4_kernel<T_, FMT, T>, grid, dim3(Q_THREADS), 0, stream, (const uint8_t *)q,
+                      (const uint8_t *)scale, batches, rpb, cols, fp4_scale_tiles(Fp4<FMT>::BLK, cols), per, global,
+                      counts, c_dev, (T_ *)dst, st);
 }
 
 // Lanes a row: a whole warp from 512 values on, a quarter of one below (rows

@@ -7,6 +7,8 @@
 // bytes, row r of the tile at 16-byte row r % 32, 4-byte column r / 32.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace moe {
@@ -38,11 +40,11 @@ __device__ __forceinline__ uint32_t e4m3_of(float v) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
     return r & 0xFFu;
 }
+// The value of an e4m3 code (exact in fp16).
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
-    const uint32_t ex = (code >> 3) & 15u, man = code & 7u;
-    if ((code & 0x7Fu) == 0x7Fu) return NAN;
-    const float v = ex ? __uint_as_float(((ex + 120u) << 23) | (man << 20)) : (float)man * 0x1p-9f;
-    return code & 0x80u ? -v : v;
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
 }
 // 2^(code - 127); code 0 is the subnormal 2^-127.
 __device__ __forceinline__ float e8m0_value(uint32_t code) {
@@ -88,14 +90,6 @@ __device__ __forceinline__ float amax_nan(float m, float v) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
     return r;
-}
-
-// The value of an e2m1 code: magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 as (1 + m/2)
-// 2^(e-1), or m/2 at e = 0.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t ex = (c >> 1) & 3u, man = c & 1u;
-    const float v = ex ? __uint_as_float(((ex + 126u) << 23) | (man << 22)) : 0.5f * (float)man;
-    return c & 8u ? -v : v;
 }
 
 }  // namespace moe
