@@ -134,6 +134,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, int32_t 
     return __all_sync(0xffffffffu, mbar_wait<true>(b, parity, abort_flag, status));
 }
 
+// silu(a) = a / (1 + e^-a), about 2 units in the last place: e^-a as 2^t with
+// the rounding error of t = -a log2(e) put back, one approximate reciprocal.
+// (The general exp and division spent more than the main loop of a tile with
+// few rows: 16 decoded tokens over 256 experts, 505 us with them.)
+__device__ __forceinline__ float f4_silu(float a) {
+    const float t = a * -1.4426950408889634f;
+    const float r = __fmaf_rn(a, -1.4426950408889634f, -t);
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = e < INFINITY ? __fmaf_rn(e, r * 0.6931471805599453f, e) : e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+    return a * q;
+}
+
+// Accumulators of rows that are not kept may be anything: zeros in their place
+// keep the arithmetic off its slow paths.
+__device__ __forceinline__ void f4_zero_unless(bool valid, uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i++) r[i] = valid ? r[i] : 0u;
+}
+
 // One lane's 64 hidden values (columns gcol .. of its row) to codes and block
 // scales.  Called in halves of 32 columns: `word` collects the scale bytes.
 template <int FMT>
@@ -234,11 +255,12 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // Producers 0 and 2: the two row halves of this CTA's A rows; 1 and 3:
         // those of its B rows (SwiGLU: the first CTA's are W1's, the second's
         // W3's).  0 also brings the A scales, 1 and 3 the scales of the first
-        // and second 128 columns of the tile.
+        // and second 128 columns of the tile.  A rows come in boxes of 32, and
+        // only those that hold kept rows (the others' accumulators are never
+        // stored).
         const int prod = warp == 0 ? 0 : warp - PROD_WARP0 + 1;
         const bool is_a = (prod & 1) == 0;
         const int hh = prod >> 1;
-        const uint32_t bytes = F4_BOX_BYTES + (prod == 2 ? 0 : TL::SF_BYTES);
         const CUtensorMap *op = is_a ? &tmA : SWIGLU && prank ? &tmB3 : &tmB;
         const CUtensorMap *sf = is_a ? &tmSA : SWIGLU && hh ? &tmSB3 : &tmSB;
         const int a_tiles = (int)((args.c_max + 127) / 128), b_tiles = (args.n_out + 127) / 128;
@@ -247,6 +269,14 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         if (elect_one()) {
             for (int t = tile0; t < total && !args.stall; t += tile_step) {
                 const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
+                // this CTA's boxes of A, and the bytes of both CTAs' copies
+                const int left = T.rows - T.mt * 2 * UM - hh * 64;
+                const int n0 = min(max((left + 31) / 32, 0), 2), n1 = min(max((left - UM + 31) / 32, 0), 2);
+                const int boxes = prank ? n1 : n0;
+                const bool sf_here = !is_a || (hh == 0 && boxes > 0);
+                const uint32_t bytes = is_a ? (uint32_t)(n0 + n1) * (F4_BOX_BYTES / 2) +
+                                                  (hh == 0 ? (uint32_t)((n0 > 0) + (n1 > 0)) * TL::SF_BYTES : 0u)
+                                            : 2u * (F4_BOX_BYTES + TL::SF_BYTES);
                 int row, sf_row;
                 if (is_a) {
                     row = (int)(T.j * args.c_max + (int64_t)T.mt * 2 * UM) + (int)prank * UM + hh * 64;
@@ -260,9 +290,11 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 for (int kb = 0; kb < nk; kb++) {
                     if (!mbar_wait<true>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status)) goto producer_done;
                     const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), 0);
-                    if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * bytes);
-                    tma_load_2d_pair(dst + stage * F4_OP_BYTES, op, kb * (F4_BK / 2), row, fb);
-                    if (prod != 2) tma_load_3d_pair(sf_dst + stage * 3 * TL::SF_BYTES, sf, 0, kb * KT, sf_row, fb);
+                    if (prank == 0) mbar_expect_tx(&ctl->full[stage], bytes);
+                    uint8_t *to = dst + stage * F4_OP_BYTES;
+                    if (!is_a || boxes > 0) tma_load_2d_pair(to, op, kb * (F4_BK / 2), row, fb);
+                    if (is_a && boxes > 1) tma_load_2d_pair(to + F4_BOX_BYTES / 2, op, kb * (F4_BK / 2), row + 32, fb);
+                    if (sf_here) tma_load_3d_pair(sf_dst + stage * 3 * TL::SF_BYTES, sf, 0, kb * KT, sf_row, fb);
                     issued++;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -300,18 +332,18 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     const uint32_t sfa = tmem + F4_SF_COL + sf_set * TL::SF_COLS, sfb = sfa + 4 * KT;
                     const int steps = min(F4_BK / 64, (args.K - kb * F4_BK + 63) / 64);
 #pragma unroll
-                    for (int i = 0; i < KT; i++) {
-                        cp_scales_pair(sfa + 4 * i, s0 + i * 512);
-                        cp_scales_pair(sfb + 8 * i, s0 + TL::SF_BYTES + i * 512);
-                        cp_scales_pair(sfb + 8 * i + 4, s0 + 2 * TL::SF_BYTES + i * 512);
+                    for (int x = 0; x < KT; x++) {
+                        cp_scales_pair(sfa + 4 * x, s0 + x * 512);
+                        cp_scales_pair(sfb + 8 * x, s0 + TL::SF_BYTES + x * 512);
+                        cp_scales_pair(sfb + 8 * x + 4, s0 + 2 * TL::SF_BYTES + x * 512);
                     }
 #pragma unroll
                     for (int kk = 0; kk < F4_BK / 64; kk++) {
                         if (kk < steps) {
-                            const int i = FMT == MOE_FP4_MX ? kk / 2 : kk;   // its scale tile
+                            const int x = FMT == MOE_FP4_MX ? kk / 2 : kk;   // its scale tile
                             umma_pair_f4<FMT>(d, sdesc<128>(a0 + kk * 32), sdesc<128>(b0 + kk * 32),
-                                              f4_idesc<FMT>(FMT == MOE_FP4_MX ? (kk & 1) * 2 : 0), sfa + 4 * i,
-                                              sfb + 8 * i, (kb | kk) != 0);
+                                              f4_idesc<FMT>(FMT == MOE_FP4_MX ? (kk & 1) * 2 : 0), sfa + 4 * x,
+                                              sfb + 8 * x, (kb | kk) != 0);
                         }
                     }
                     umma_commit_pair(&ctl->empty[stage], 3);
@@ -336,6 +368,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         for (int t = tile0; t < total; t += tile_step, done++) {
             const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
             const int row = T.mt * 2 * UM + (int)prank * UM + sub * 32 + lane;
+            const bool any = row - lane < T.rows;   // of the warp's rows
             const bool valid = row < T.rows, all_kept = row - lane + 31 < T.rows;
             const int64_t grow = (int64_t)T.j * args.c_max + row;
             const float ga = args.a_global ? args.a_global[T.j] : 1.0f;
@@ -360,6 +393,12 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(done & 1) * F4_ACC_STEP + half * 64;
             const int shared0 = done & 1 ? 0 : 128;   // the half that the next tile overwrites
+            if (!any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
+                continue;
+            }
             uint32_t r[2][32];
             tmem_ld32(tb + shared0, r[0]);
             tmem_ld32(tb + shared0 + 32, r[1]);
@@ -368,6 +407,10 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
+            if (EPI != FP4_BIAS && !all_kept) {
+                f4_zero_unless(valid, r[0]);
+                f4_zero_unless(valid, r[1]);
+            }
             if (SWIGLU) {
                 const int gcol = T.nt * NOUT_TILE + half * 64;
                 uint32_t word = 0;
@@ -376,12 +419,13 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     uint32_t o[32];
                     tmem_ld32(tb + (128 - shared0) + 32 * h2, o);
                     tmem_wait_ld(o);
+                    if (!all_kept) f4_zero_unless(valid, o);
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
                         const float x = __uint_as_float(r[h2][i]), y = __uint_as_float(o[i]);
                         const float a = (shared0 ? y : x) * s1, b = (shared0 ? x : y) * s3;
-                        v[i] = silu(a) * b;
+                        v[i] = f4_silu(a) * b;
                     }
                     uint32_t codes[4];
                     const bool live = gcol + 32 * h2 < args.n_out;
@@ -408,6 +452,10 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         tmem_ld32(tb + lcol + 32, r[1]);
                         tmem_wait_ld(r[0]);
                         tmem_tie(r[1]);
+                        if (EPI != FP4_BIAS && !all_kept) {
+                            f4_zero_unless(valid, r[0]);
+                            f4_zero_unless(valid, r[1]);
+                        }
                     }
                     uint32_t word = 0;
 #pragma unroll
@@ -499,7 +547,7 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
     const int64_t a_tiles = (args.c_max + 127) / 128, b_tiles = (args.n_out + 127) / 128;
     constexpr int KT = F4Tiling<FMT>::KT;
     CUtensorMap mA, mB, mSA, mSB;
-    if (!make_map_u8(&mA, a.q, (uint64_t)(e * args.c_max), (uint64_t)args.K / 2, 64) ||
+    if (!make_map_u8(&mA, a.q, (uint64_t)(e * args.c_max), (uint64_t)args.K / 2, 32) ||
         !make_map_u8(&mB, b.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
         !make_map_scales(&mSA, a.scale, e * a_tiles, nt, KT) || !make_map_scales(&mSB, b.scale, e * b_tiles, nt, KT))
         return MOE_ERR_CUDA;

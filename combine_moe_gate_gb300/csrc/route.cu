@@ -142,7 +142,7 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, floa
 // Largest of u over a token's L lanes.
 template <int L>
 __device__ __forceinline__ uint32_t max_over(uint32_t u) {
-    if (L == 32) return __reduce_max_sync(0xffffffffu, u);
+    if constexpr (L == 32) return __reduce_max_sync(0xffffffffu, u);
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
     return u;
@@ -152,7 +152,7 @@ __device__ __forceinline__ uint32_t max_over(uint32_t u) {
 template <int L>
 __device__ __forceinline__ int first_lane(bool p, int lane) {
     uint32_t b = __ballot_sync(0xffffffffu, p);
-    if (L < 32) b = (b >> (lane & ~(L - 1))) & ((1u << L) - 1);
+    if constexpr (L < 32) b = (b >> (lane & ~(L - 1))) & ((1u << L) - 1);
     return max(__ffs(b) - 1, 0);
 }
 
