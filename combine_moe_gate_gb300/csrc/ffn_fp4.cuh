@@ -49,8 +49,7 @@ struct F4Tiling {
 
 template <int FMT>
 constexpr size_t f4_smem_bytes() {
-    return 1024 + (size_t)F4_STAGES * F4Tiling<FMT>::STAGE_BYTES + (size_t)EPI_WARPS * STG_WARP_BYTES +
-           sizeof(Ctl<F4_STAGES>);
+    return 1024 + (size_t)F4_STAGES * F4Tiling<FMT>::STAGE_BYTES + sizeof(Ctl<F4_STAGES>);
 }
 
 struct F4Args {
@@ -69,6 +68,7 @@ struct F4Args {
     int e;
     int K;
     int n_out;
+    int32_t wide;               // rows of out are whole 32-byte sectors
     int32_t stall;
 };
 
@@ -148,6 +148,28 @@ __device__ __forceinline__ float f4_silu(float a) {
     return a * q;
 }
 
+// GELU, exact erf form, two values at a time: with E(a) = erfc(|a| / sqrt 2),
+// a Phi(a) = max(a, 0) - |a| E(a) / 2 on both sides of zero.  erfc by Abramowitz
+// and Stegun 7.1.28, as in gelu_erf2, its coefficients scaled by 2^(-i/2):
+// |error of GELU| <= 5e-7 at 18 instructions for the pair (23 there).
+__device__ __forceinline__ float2 f4_gelu2(float2 a) {
+    const float2 x = make_float2(fabsf(a.x), fabsf(a.y));
+    float2 p = __ffma2_rn(x, make_float2(5.382975000e-06f, 5.382975000e-06f), make_float2(4.889063564e-05f, 4.889063564e-05f));
+    p = __ffma2_rn(x, p, make_float2(3.800357500e-05f, 3.800357500e-05f));
+    p = __ffma2_rn(x, p, make_float2(3.277626324e-03f, 3.277626324e-03f));
+    p = __ffma2_rn(x, p, make_float2(2.114100615e-02f, 2.114100615e-02f));
+    p = __ffma2_rn(x, p, make_float2(4.986734697e-02f, 4.986734697e-02f));
+    p = __ffma2_rn(x, p, make_float2(1.0f, 1.0f));
+    p = __fmul2_rn(p, p);
+    p = __fmul2_rn(p, p);
+    p = __fmul2_rn(p, p);
+    p = __fmul2_rn(p, p);
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(p.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(p.y));
+    return __ffma2_rn(__fmul2_rn(x, make_float2(-0.5f, -0.5f)), r, make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f)));
+}
+
 // Accumulators of rows that are not kept may be anything: zeros in their place
 // keep the arithmetic off its slow paths.
 __device__ __forceinline__ void f4_zero_unless(bool valid, uint32_t (&r)[32]) {
@@ -155,10 +177,37 @@ __device__ __forceinline__ void f4_zero_unless(bool valid, uint32_t (&r)[32]) {
     for (int i = 0; i < 32; i++) r[i] = valid ? r[i] : 0u;
 }
 
+// One lane's 32 output columns from gcol on, straight to its row: through
+// shared memory and TMA (a box of 32 rows) the copy in and out took as much of
+// shared memory's bandwidth as a fifth of a main loop's MMAs.  `wide`: rows are
+// whole 32-byte sectors.
+__device__ __forceinline__ void f4_store32(__nv_bfloat16 *row, const float (&v)[32], int gcol, int n_out, int wide) {
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+        const int c = gcol + 16 * q;
+        uint32_t p[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) p[i] = pack_bf16(v[16 * q + 2 * i], v[16 * q + 2 * i + 1]);
+        if (wide) {
+            if (c < n_out)
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + c), "r"(p[0]), "r"(p[1]),
+                             "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]), "r"(p[7])
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                V16 w;
+                w.w[0] = p[4 * h]; w.w[1] = p[4 * h + 1]; w.w[2] = p[4 * h + 2]; w.w[3] = p[4 * h + 3];
+                if (c + 8 * h < n_out) st_v16(row + c + 8 * h, w);
+            }
+        }
+    }
+}
+
 // One lane's 64 hidden values (columns gcol .. of its row) to codes and block
 // scales.  Called in halves of 32 columns: `word` collects the scale bytes.
 template <int FMT>
-__device__ __forceinline__ void f4_quantise32(float (&v)[32], float g, float g6, bool live, uint32_t (&codes)[4],
+__device__ __forceinline__ void f4_quantise32(float (&v)[32], const Fp4Factor &g, bool live, uint32_t (&codes)[4],
                                               uint32_t &word, int half) {
     constexpr int BLK = Fp4<FMT>::BLK;
 #pragma unroll
@@ -166,10 +215,14 @@ __device__ __forceinline__ void f4_quantise32(float (&v)[32], float g, float g6,
         float amax = 0.0f, inv;
 #pragma unroll
         for (int i = 0; i < BLK; i++) amax = amax_nan(amax, v[b * BLK + i]);
-        const uint32_t sc = fp4_scale<FMT>(amax, g, g6, inv);
+        const uint32_t sc = fp4_scale<FMT>(fabsf(amax), g, inv);
         if (live) word |= sc << (8 * (half * (32 / BLK) + b));
 #pragma unroll
-        for (int i = 0; i < BLK; i++) v[b * BLK + i] *= inv;
+        for (int i = 0; i < BLK; i += 2) {
+            const float2 p = __fmul2_rn(make_float2(v[b * BLK + i], v[b * BLK + i + 1]), make_float2(inv, inv));
+            v[b * BLK + i] = p.x;
+            v[b * BLK + i + 1] = p.y;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) codes[i] = e2m1x8(v + 8 * i);
@@ -180,22 +233,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmB3, const __grid_constant__ CUtensorMap tmSA,
                const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmSB3,
-               const __grid_constant__ CUtensorMap tmO, const F4Args args) {
+               const F4Args args) {
     using TL = F4Tiling<FMT>;
     constexpr bool SWIGLU = EPI == FP4_SWIGLU;
     constexpr int NOUT_TILE = SWIGLU ? BN / 2 : BN;
     constexpr int BLK = Fp4<FMT>::BLK, KT = TL::KT, STAGES = F4_STAGES;
     __shared__ int32_t s_bad;
     __shared__ int32_t kept_rows[MAX_E];
-    __shared__ __align__(16) float epi_bias[EPI_WARPS][128];
+    __shared__ __align__(16) uint2 epi_bias[EPI_WARPS][32];   // 128 bf16 per epilogue warp
     pdl_enter();
     if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
     __syncthreads();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + STAGES * F4_OP_BYTES, *sSF = sB + STAGES * F4_OP_BYTES;
-    uint8_t *stg_all = smem + STAGES * TL::STAGE_BYTES;
-    Ctl<STAGES> *ctl = (Ctl<STAGES> *)(stg_all + EPI_WARPS * STG_WARP_BYTES);
+    Ctl<STAGES> *ctl = (Ctl<STAGES> *)(smem + STAGES * TL::STAGE_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = args.e;
@@ -362,8 +414,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // Epilogue: warp (sub, half) has rows sub * 32 .. of this CTA and, of the
         // two 128-column halves, columns half * 64 .. + 63 each.
         const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
-        uint8_t *stg = stg_all + ew * STG_WARP_BYTES;
-        float *bsl = epi_bias[ew];
+        uint2 *bsl = epi_bias[ew];
         int done = 0;
         for (int t = tile0; t < total; t += tile_step, done++) {
             const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
@@ -374,19 +425,13 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const float ga = args.a_global ? args.a_global[T.j] : 1.0f;
             const float s1 = ga * (args.b_global ? args.b_global[T.j] : 1.0f);
             const float s3 = SWIGLU ? ga * (args.b3_global ? args.b3_global[T.j] : 1.0f) : 0.0f;
-            const float og = EPI != FP4_BIAS && args.out_global ? args.out_global[T.j] : 1.0f;
-            const float og6 = __fmul_rn(og, 6.0f);
+            const Fp4Factor og = fp4_factor(EPI != FP4_BIAS && args.out_global ? args.out_global[T.j] : 1.0f);
             const int64_t ont = fp4_scale_tiles(BLK, args.n_out);   // scale tiles of an output row
-            if (!SWIGLU) {
+            if (!SWIGLU && args.bias) {
                 // this warp's bias: columns half * 64 .. of both halves, 64 each
-                const int c = (lane >> 4) * 128 + half * 64 + (lane & 15) * 4;
-                const int g = T.nt * NOUT_TILE + c;
-                float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (args.bias && g < args.n_out) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(args.bias + (int64_t)T.j * args.n_out + g);
-                    b = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-                }
-                reinterpret_cast<float4 *>(bsl)[lane] = b;
+                const int g = T.nt * NOUT_TILE + (lane >> 4) * 128 + half * 64 + (lane & 15) * 4;
+                bsl[lane] = g < args.n_out ? *reinterpret_cast<const uint2 *>(args.bias + (int64_t)T.j * args.n_out + g)
+                                           : make_uint2(0u, 0u);
                 __syncwarp();
             }
             if (!warp_wait(&ctl->tfull[0], (uint32_t)(done & 1), abort_flag, args.status)) break;
@@ -429,7 +474,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     uint32_t codes[4];
                     const bool live = gcol + 32 * h2 < args.n_out;
-                    f4_quantise32<FMT>(v, og, og6, live, codes, word, h2);
+                    f4_quantise32<FMT>(v, og, live, codes, word, h2);
                     if (valid && live) {
                         V16 w;
                         w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
@@ -460,27 +505,32 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     uint32_t word = 0;
 #pragma unroll
                     for (int h2 = 0; h2 < 2; h2++) {
-                        const float2 *bp = reinterpret_cast<const float2 *>(bsl + (lcol ? 64 : 0) + 32 * h2);
+                        const uint4 *bp = reinterpret_cast<const uint4 *>(bsl + (lcol ? 16 : 0) + 8 * h2);
                         float v[32];
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h2][2 * i]), __uint_as_float(r[h2][2 * i + 1])),
-                                                  make_float2(s1, s1), bp[i]);
-                            if (EPI == FP4_GELU) a = gelu_erf2(a);
-                            if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
-                            v[2 * i] = a.x;
-                            v[2 * i + 1] = a.y;
+                        for (int q = 0; q < 4; q++) {
+                            uint32_t bw[4] = {0u, 0u, 0u, 0u};   // eight columns' bias
+                            if (args.bias) {
+                                const uint4 u = bp[q];
+                                bw[0] = u.x; bw[1] = u.y; bw[2] = u.z; bw[3] = u.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const int c = 8 * q + 2 * i;
+                                float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h2][c]), __uint_as_float(r[h2][c + 1])),
+                                                      make_float2(s1, s1), make_float2(bf16lo(bw[i]), bf16hi(bw[i])));
+                                if (EPI == FP4_GELU) a = f4_gelu2(a);
+                                if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                                v[c] = a.x;
+                                v[c + 1] = a.y;
+                            }
                         }
                         if (EPI == FP4_BIAS) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int i = 0; i < 16; i++) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                            epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow - lane, gcol + 32 * h2, args.n_out,
-                                        args.out + grow * args.n_out);
+                            if (valid) f4_store32(args.out + grow * args.n_out, v, gcol + 32 * h2, args.n_out, args.wide);
                         } else {
                             uint32_t codes[4];
                             const bool live = gcol + 32 * h2 < args.n_out;
-                            f4_quantise32<FMT>(v, og, og6, live, codes, word, h2);
+                            f4_quantise32<FMT>(v, og, live, codes, word, h2);
                             if (valid && live) {
                                 V16 w;
                                 w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
@@ -498,8 +548,6 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 __syncwarp();   // the bias slice is rewritten for the next tile
             }
         }
-        if (lane == 0) bulk_wait_all();
-        __syncwarp();
     }
 
     tc_fence_before();
@@ -542,6 +590,7 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
     args.b_global = b.global;
     args.b3_global = b3.global;
     args.stall = take_gemm_stall() ? 1 : 0;
+    args.wide = args.n_out % 16 == 0 && ((uintptr_t)args.out & 31) == 0;
     const int64_t e = args.e;
     const int64_t nt = fp4_scale_tiles(Fp4<FMT>::BLK, args.K);
     const int64_t a_tiles = (args.c_max + 127) / 128, b_tiles = (args.n_out + 127) / 128;
@@ -551,11 +600,9 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
         !make_map_u8(&mB, b.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
         !make_map_scales(&mSA, a.scale, e * a_tiles, nt, KT) || !make_map_scales(&mSB, b.scale, e * b_tiles, nt, KT))
         return MOE_ERR_CUDA;
-    CUtensorMap mB3 = mB, mSB3 = mSB, mO = mB;   // where the kernel uses one, its own
+    CUtensorMap mB3 = mB, mSB3 = mSB;   // SwiGLU: its own
     if (EPI == FP4_SWIGLU && (!make_map_u8(&mB3, b3.q, (uint64_t)(e * args.n_out), (uint64_t)args.K / 2, 64) ||
                               !make_map_scales(&mSB3, b3.scale, e * b_tiles, nt, KT)))
-        return MOE_ERR_CUDA;
-    if (EPI == FP4_BIAS && !make_map(&mO, args.out, (uint64_t)(e * args.c_max), (uint64_t)args.n_out, 32, 32))
         return MOE_ERR_CUDA;
     auto kern = fp4_group_gemm<FMT, EPI>;
     constexpr size_t SMEM = f4_smem_bytes<FMT>();
@@ -573,7 +620,7 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
     const int64_t upper = e * ((args.c_max + 2 * UM - 1) / (2 * UM)) * ((args.n_out + NOUT_TILE - 1) / NOUT_TILE);
     const int64_t grid = upper < nunits ? upper : nunits;
     return launch_cluster_pdl(kern, dim3((unsigned)(2 * grid)), dim3(NUM_THREADS), SMEM, 2, stream, mA, mB, mB3, mSA,
-                              mSB, mSB3, mO, args);
+                              mSB, mSB3, args);
 }
 
 template <int FMT>

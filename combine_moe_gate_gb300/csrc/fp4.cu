@@ -8,12 +8,24 @@ namespace {
 constexpr int Q_THREADS = 256;
 
 // 32 bytes at a time (one sector a lane: a warp's access is 1 KB in a row).
-__device__ __forceinline__ void ld32(const void *p, uint32_t (&w)[8]) {
+// `wide`: p lies on a 32-byte boundary (callers' buffers have to on 16 only).
+__device__ __forceinline__ void ld32(const void *p, uint32_t (&w)[8], bool wide) {
+    if (!wide) {
+        const V16 a = ld_stream(p), b = ld_stream(reinterpret_cast<const char *>(p) + 16);
+#pragma unroll
+        for (int i = 0; i < 4; i++) { w[i] = a.w[i]; w[4 + i] = b.w[i]; }
+        return;
+    }
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(p));
 }
-__device__ __forceinline__ void st32(void *p, const float (&f)[8]) {
+__device__ __forceinline__ void st32(void *p, const float (&f)[8], bool wide) {
+    if (!wide) {
+        st_v16(p, Elt<float>::pack(f));
+        st_v16(reinterpret_cast<char *>(p) + 16, Elt<float>::pack(f + 4));
+        return;
+    }
     asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
                  "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
                  : "memory");
@@ -25,7 +37,10 @@ __device__ __forceinline__ void st32(void *p, const float (&f)[8]) {
 template <typename T> struct Raw;
 template <> struct Raw<float> {
     uint32_t w[2][8];
-    __device__ __forceinline__ void load(const float *p) { ld32(p, w[0]); ld32(p + 8, w[1]); }
+    __device__ __forceinline__ void load(const float *p, bool wide) {
+        ld32(p, w[0], wide);
+        ld32(p + 8, w[1], wide);
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < 8; i++) w[0][i] = w[1][i] = 0u;
@@ -42,7 +57,7 @@ template <> struct Raw<float> {
 };
 template <> struct Raw<__nv_bfloat16> {
     uint32_t w[8];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { ld32(p, w); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool wide) { ld32(p, w, wide); }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = 0u;
@@ -71,6 +86,7 @@ __device__ __forceinline__ int64_t live_rows(const int32_t *counts, const int32_
 template <typename T_, int FMT, int T>
 __global__ void __launch_bounds__(Q_THREADS)
 quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, int cols, int64_t ntiles, int seg,
+                    int wide,
                     const float *__restrict__ global, const int32_t *__restrict__ counts,
                     const int32_t *__restrict__ c_dev, uint8_t *__restrict__ q,
                     uint8_t *__restrict__ scale, int32_t *status) {
@@ -85,8 +101,7 @@ quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, in
     const int lane = threadIdx.x & 31, sub = lane % T;
     for (int64_t b = blockIdx.y; b < batches; b += gridDim.y) {
         const int64_t rows = live_rows(counts, c_dev, b, rpb);
-        const float g = FMT == MOE_FP4_NV && global ? global[b] : 1.0f;
-        const float g6 = __fmul_rn(g, 6.0f);
+        const Fp4Factor g = fp4_factor(FMT == MOE_FP4_NV && global ? global[b] : 1.0f);
         const int row_in = (int)threadIdx.x / T;
         // the warp's first row decides how often the warp goes round
         for (int64_t r = (int64_t)blockIdx.x * RPC + row_in; r - lane / T < rows; r += (int64_t)gridDim.x * RPC) {
@@ -99,7 +114,7 @@ quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, in
 #pragma unroll
                 for (int u = 0; u < U; u++) {
                     v[u].zero();
-                    if (live && c0 + u * T < min(last, nch)) v[u].load(srow + (c0 + u * T) * 16);
+                    if (live && c0 + u * T < min(last, nch)) v[u].load(srow + (c0 + u * T) * 16, wide);
                 }
 #pragma unroll
                 for (int u = 0; u < U; u++) {
@@ -109,7 +124,7 @@ quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, in
                     if (TPB == 2)
                         amax = __uint_as_float(max(__float_as_uint(amax),
                                                    __shfl_xor_sync(0xffffffffu, __float_as_uint(amax), 1)));
-                    uint32_t sc = fp4_scale<FMT>(amax, g, g6, inv);
+                    uint32_t sc = fp4_scale<FMT>(amax, g, inv);
                     float f[16];
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
@@ -154,7 +169,8 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, float (&f)[8]) {
 template <typename T_, int FMT, int T>
 __global__ void __launch_bounds__(Q_THREADS)
 dequantize_fp4_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t batches,
-                      int64_t rpb, int cols, int64_t ntiles, int seg, const float *__restrict__ global,
+                      int64_t rpb, int cols, int64_t ntiles, int seg, int wide,
+                      const float *__restrict__ global,
                       const int32_t *__restrict__ counts, const int32_t *__restrict__ c_dev,
                       T_ *__restrict__ dst, int32_t *status) {
     pdl_enter();
@@ -189,7 +205,7 @@ dequantize_fp4_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__
                         e2m1_values(h ? w[u].y : w[u].x, f);
 #pragma unroll
                         for (int i = 0; i < 8; i++) f[i] = __fmul_rn(f[i], s);
-                        if constexpr (sizeof(T_) == 4) st32(drow + ch * 16 + 8 * h, f);
+                        if constexpr (sizeof(T_) == 4) st32(drow + ch * 16 + 8 * h, f, wide);
                         else st_v16(drow + ch * 16 + 8 * h, Elt<__nv_bfloat16>::pack(f));
                     }
                 }
@@ -230,7 +246,7 @@ moe_status quantize_t(const void *src, int64_t batches, int64_t rpb, int cols, c
     int per;
     const dim3 grid = grid_for(batches, rpb, T, (int)nt * (Fp4<FMT>::BLK / 4), per);
     return launch_pdl(quantize_fp4_kernel<T_, FMT, T>, grid, dim3(Q_THREADS), 0, stream, (const T_ *)src, batches,
-                      rpb, cols, nt, per, global, counts, c_dev, (uint8_t *)q, (uint8_t *)scale, st);
+                      rpb, cols, nt, per, ((uintptr_t)src & 31) == 0, global, counts, c_dev, (uint8_t *)q, (uint8_t *)scale, st);
 }
 
 template <typename T_, int FMT, int T>
@@ -240,7 +256,8 @@ moe_status dequantize_t(const void *q, const void *scale, int64_t batches, int64
     int per;
     const dim3 grid = grid_for(batches, rpb, T, cols / 16, per);
     return launch_pdl(dequantize_fp4_kernel<T_, FMT, T>, grid, dim3(Q_THREADS), 0, stream, (const uint8_t *)q,
-                      (const uint8_t *)scale, batches, rpb, cols, fp4_scale_tiles(Fp4<FMT>::BLK, cols), per, global,
+                      (const uint8_t *)scale, batches, rpb, cols, fp4_scale_tiles(Fp4<FMT>::BLK, cols), per,
+                      ((uintptr_t)dst & 31) == 0, global,
                       counts, c_dev, (T_ *)dst, st);
 }
 

@@ -9,7 +9,7 @@
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "exact.cuh"
 
 namespace moe {
 
@@ -51,10 +51,28 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
     return code == 0xFFu ? NAN : __uint_as_float(code ? code << 23 : 1u << 22);
 }
 
+// A batch's factor g (NV) with what its blocks' scales divide by.
+struct Fp4Factor {
+    float g, g6, y6;   // g, 6 g, and 1 / (6 g) rounded (0: not in the middle of the range)
+};
+__device__ __forceinline__ Fp4Factor fp4_factor(float g) {
+    Fp4Factor f;
+    f.g = g;
+    f.g6 = __fmul_rn(g, 6.0f);
+    f.y6 = f.g6 >= 0x1p-40f && f.g6 <= 0x1p40f ? __frcp_rn(f.g6) : 0.0f;
+    return f;
+}
+
 // Scale byte of a block with largest magnitude amax, and what its values are
-// multiplied by (1 / scale; 0 where the scale is 0).  g6 = 6 g (NV).
+// multiplied by (1 / scale; 0 where the scale is 0).
 template <int FMT>
-__device__ __forceinline__ uint32_t fp4_scale(float amax, float g, float g6, float &inv) {
+__device__ __forceinline__ uint32_t fp4_scale(float amax, const Fp4Factor &f, float &inv) {
+    if (FMT == MOE_FP4_NV && f.y6 != 0.0f && amax <= 0x1p60f && (amax >= 0x1p-60f || amax == 0.0f)) {
+        const uint32_t s8 = e4m3_of(div_mid(amax, f.g6, f.y6));
+        const float y = rcp_mid(__fmul_rn(e4m3_value(s8), f.g));
+        inv = s8 ? y : 0.0f;
+        return s8;
+    }
     if (!(amax < INFINITY)) {   // an infinity or a NaN
         inv = 0.0f;
         return Fp4<FMT>::NAN_SCALE;
@@ -65,8 +83,8 @@ __device__ __forceinline__ uint32_t fp4_scale(float amax, float g, float g6, flo
         inv = __uint_as_float((uint32_t)(254 - sc) << 23);
         return (uint32_t)sc;
     }
-    const uint32_t s8 = e4m3_of(__fdiv_rn(amax, g6));
-    const float s = __fmul_rn(e4m3_value(s8), g);
+    const uint32_t s8 = e4m3_of(__fdiv_rn(amax, f.g6));
+    const float s = __fmul_rn(e4m3_value(s8), f.g);
     inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
     return s8;
 }
@@ -85,10 +103,10 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *v) {
     return r;
 }
 
-// max(m, |v|); a NaN stays one.
+// The larger magnitude of the two, with some sign; a NaN stays one.
 __device__ __forceinline__ float amax_nan(float m, float v) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(v));
     return r;
 }
 

@@ -18,7 +18,7 @@
 // about 20 per expert), so its layout is chosen to spend few of them: L lanes
 // share a token and hold V = width / L consecutive experts each, with V = 8
 // where the width allows, so that 32 / L tokens run in one warp.
-#include "common.cuh"
+#include "exact.cuh"
 
 namespace moe {
 namespace {
@@ -63,24 +63,6 @@ __device__ __forceinline__ uint32_t order_key(float f) {
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-// Correctly rounded reciprocal and quotient by fused corrections of an
-// approximation (Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990: with r = fma(-b, y, 1) exact, fma(r, y, y)
-// rounds 1/b correctly; likewise a quotient).  They leave out the range checks
-// of the general operations: rcp_1 is for 1 <= x <= 2^126 (compared with
-// __frcp_rn for every mantissa), div_by for a = 0 or 2^-100 <= a <= 1 and 1 <= b
-// <= 1024, y its reciprocal.
-__device__ __forceinline__ float rcp_1(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return __fmaf_rn(__fmaf_rn(-x, y, 1.0f), y, y);
-}
-__device__ __forceinline__ float div_by(float a, float b, float y) {
-    float q = __fmul_rn(a, y);
-    q = __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
-    return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
-}
-
 // The sigmoid; the addition and the division are single IEEE operations.
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
@@ -95,7 +77,7 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, floa
         for (int i = 0; i < V; i++) {
             x[i] = __fadd_rn(1.0f, expf(-l[i]));
             general |= x[i] > 0x1p126f;
-            sc[i] = rcp_1(x[i]);
+            sc[i] = rcp_mid(x[i]);
         }
         if (general)
 #pragma unroll
@@ -129,13 +111,13 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, floa
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
     if (sum == 0.0f) return;   // every score is 0 already
-    const float y = rcp_1(sum);
+    const float y = rcp_mid(sum);
     if (general) {
 #pragma unroll
         for (int i = 0; i < V; i++) sc[i] = __fdiv_rn(sc[i], sum);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; i++) sc[i] = div_by(sc[i], sum, y);
+        for (int i = 0; i < V; i++) sc[i] = div_mid(sc[i], sum, y);
     }
 }
 
