@@ -241,9 +241,6 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     __shared__ int32_t s_bad;
     __shared__ int32_t kept_rows[MAX_E];
     __shared__ __align__(16) uint2 epi_bias[EPI_WARPS][32];   // 128 bf16 per epilogue warp
-    pdl_enter();
-    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
-    __syncthreads();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + STAGES * F4_OP_BYTES, *sSF = sB + STAGES * F4_OP_BYTES;
@@ -256,26 +253,9 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
     const int nk = (args.K + F4_BK - 1) / F4_BK;
 
+    // what needs no result of the previous kernel: barriers, TMEM, descriptors
     if (warp == 0) {
-        const int c_eff = (int)min((int64_t)*args.c_dev, args.c_max);
-        int run = 0;
-        for (int base = 0; base < e; base += 32) {
-            const int j = base + lane;
-            const int rows = j < e ? max(0, min(args.counts[j], c_eff)) : 0;
-            if (j < e) kept_rows[j] = rows;
-            const int mine = ((rows + 2 * UM - 1) / (2 * UM)) * ntn;
-            int v = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (j < e) ctl->tile_start[j] = run + v - mine;
-            run += __shfl_sync(0xffffffffu, v, 31);
-        }
         if (lane == 0) {
-            ctl->tile_start[e] = run;
-            ctl->total_tiles = run;
             ctl->abort = 0;
             for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 4); mbar_init(&ctl->empty[s], 1); }
             mbar_init(&ctl->tfull[0], 1);
@@ -289,6 +269,36 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                      "r"(TMEM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else if (warp == 2 && lane < 4) {
+        const CUtensorMap *m = lane == 0 ? &tmA : lane == 1 ? &tmB : lane == 2 ? &tmSA : &tmSB;
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory");
+    }
+    pdl_enter();
+    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
+    {
+        const int c_eff = (int)min((int64_t)*args.c_dev, args.c_max);
+        for (int j = threadIdx.x; j < e; j += NUM_THREADS) kept_rows[j] = max(0, min(args.counts[j], c_eff));
+    }
+    __syncthreads();
+    if (warp == 0) {   // first tile of every expert: each lane sums a run of them
+        const int per = (e + 31) / 32, j0 = min(lane * per, e), j1 = min(j0 + per, e);
+        int own = 0;
+        for (int j = j0; j < j1; j++) own += (kept_rows[j] + 2 * UM - 1) / (2 * UM) * ntn;
+        int v = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        int at = v - own;
+        for (int j = j0; j < j1; j++) {
+            ctl->tile_start[j] = at;
+            at += (kept_rows[j] + 2 * UM - 1) / (2 * UM) * ntn;
+        }
+        if (lane == 31) {
+            ctl->tile_start[e] = v;
+            ctl->total_tiles = v;
+        }
     }
     tc_fence_before();
     cluster_sync();
