@@ -641,4 +641,5 @@ def moe_probe_fp32_fma(packed, blocks, iters, out, stream=None):
                                      _ptr(out, "out", _f32()), _stream(stream)), "moe_probe_fp32_fma")
 
 
-from .layer import MoELayerBuffers, alloc_layer, run_layer, run_layer_host  # noqa: E402,F401
+from .layer import (Fp4Operand, MoELayerBuffers, MoELayerFp4Buffers, alloc_layer,  # noqa: E402,F401
+                    alloc_layer_fp4, quantize_weights_fp4, run_layer, run_layer_fp4, run_layer_host)
