@@ -215,7 +215,7 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
     __shared__ uint2 s_cand[RT_WARPS][32];       // candidates (L = 32)
     __shared__ int32_t s_sel[RT_WARPS][TPW * 32];   // the selection, by route
     pdl_enter();
-    if (status_bad(status)) return;
+    const bool stop = status_bad(status);   // asked for now, needed before the first store
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1), tw = lane / L;
     constexpr int VS = V < 4 ? V : 4;
     const int gs = e / groups, gl = gs / V;   // experts and (where whole) lanes per group
@@ -318,6 +318,7 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
                 for (int r = 0; r < k; r++) sum = __fadd_rn(sum, val[sel[r]]);
             }
         }
+        if (__any_sync(0xffffffffu, stop)) return;
         if (t0 + tw < s)
             for (int r = sub; r < k; r += L) {
                 if (r != sub) {
@@ -336,10 +337,11 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
 // A CTA takes `tb` consecutive tokens (a multiple of 8): their rows of
 // d_logits are formed in shared memory and leave as one contiguous run of
 // 16-byte stores, whatever e is.
-constexpr int BWD_FLOATS = 8192;   // 32 tokens of 256 experts, 8 of 1024
+constexpr int BWD_FLOATS = 8192;   // 8 tokens of 1024 experts
 constexpr int BWD_LANES = 8;       // lanes per token for its routes
 
-__host__ __device__ inline int bwd_tokens(int e) { return e <= 256 ? 32 : e <= 512 ? 16 : 8; }
+// Tokens per CTA (16384 x 256: 7.3 us with 16, 8.4 with 32, 9.1 with 8).
+__host__ __device__ inline int bwd_tokens(int e) { return e <= 64 ? 32 : e <= 256 ? 16 : 8; }
 
 template <typename D>
 __device__ __forceinline__ void store_rows(const float *rows, int64_t n, D *out) {
@@ -361,14 +363,12 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
                      int normalize, D *__restrict__ d_logits, int32_t *status) {
     __shared__ __align__(16) float rows[BWD_FLOATS];
     pdl_enter();
-    if (status_bad(status)) return;
+    const bool stop = status_bad(status);
     const int tb = bwd_tokens(e), sub = threadIdx.x % BWD_LANES, tok = threadIdx.x / BWD_LANES;
     for (int64_t t0 = (int64_t)blockIdx.x * tb; t0 < s; t0 += (int64_t)gridDim.x * tb) {
         const int nt = (int)min((int64_t)tb, s - t0);
         const int64_t t = t0 + tok;
         const bool on = tok < nt;
-        float4 *z = reinterpret_cast<float4 *>(rows);
-        for (int i = threadIdx.x; i < (nt * e + 3) / 4; i += RT_THREADS) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         // this lane's routes sub, sub + 8, ... of its token
         int j[4];
         float x[4], dg[4], g[4];
@@ -380,7 +380,12 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
             const bool have = on && r < k;
             j[q] = have ? idx[(int64_t)r * s + t] : -1;
             dg[q] = have ? d_gates[(int64_t)r * s + t] : 0.0f;
-            if (have && (j[q] < 0 || j[q] >= e)) { bad = true; j[q] = -1; }
+        }
+        float4 *z = reinterpret_cast<float4 *>(rows);   // zeros while those loads are on their way
+        for (int i = threadIdx.x; i < (nt * e + 3) / 4; i += RT_THREADS) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            if (on && sub + q * BWD_LANES < k && (j[q] < 0 || j[q] >= e)) { bad = true; j[q] = -1; }
             x[q] = j[q] >= 0 ? ld_logit(logits + t * e + j[q]) : -INFINITY;
             top = fmaxf(top, x[q]);
         }
@@ -402,7 +407,9 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
             total += __shfl_xor_sync(0xffffffffu, total, o);
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
-        __syncthreads();   // the rows are zero
+        // the rows are zero; another CTA's error may have come up meanwhile, so the
+        // threads leave together
+        if (__syncthreads_or(stop)) return;
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             if (j[q] < 0) continue;
@@ -429,7 +436,7 @@ route_bwd_all_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
     constexpr int ROUTES = 32 / L;        // routes per lane, at most
     __shared__ __align__(16) float rows[TPC * V * L];
     pdl_enter();
-    if (status_bad(status)) return;
+    const bool stop = status_bad(status);
     const int sub = threadIdx.x & (L - 1), tok = threadIdx.x / L;
     for (int64_t t0 = (int64_t)blockIdx.x * TPC; t0 < s; t0 += (int64_t)gridDim.x * TPC) {
         const int nt = (int)min((int64_t)TPC, s - t0);
@@ -469,22 +476,22 @@ route_bwd_all_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
 #pragma unroll
         for (int q = 0; q < ROUTES; q++)
             if (j[q] >= 0) row[j[q]] = scale * pj[q] * (dg[q] - dot);
-        __syncthreads();
+        if (__syncthreads_or(stop)) return;
         store_rows(rows, (int64_t)nt * e, d_logits + t0 * e);
         __syncthreads();
     }
 }
 
-// CTAs for `units` CTA-sized pieces of work: at most eight a multiprocessor
+// CTAs for `units` CTA-sized pieces of work: at most `per_sm` a multiprocessor
 // (the kernels stride).
-int grid_for(int64_t units) {
+int grid_for(int64_t units, int per_sm) {
     static int cached[64] = {0};
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
         if (!cached[dev]) cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev);
         if (cached[dev] > 0) sms = cached[dev];
     }
-    const int64_t cap = (int64_t)sms * 8;
+    const int64_t cap = (int64_t)sms * per_sm;
     return (int)(units < cap ? units : cap);
 }
 
@@ -494,8 +501,10 @@ moe_status topk_v(const void *logits, const float *bias, int64_t s, int e, int k
                   int32_t *idx, float *gates, int32_t *st, cudaStream_t stream) {
     auto kern = softmax ? route_topk_kernel<T, V, L, true> : route_topk_kernel<T, V, L, false>;
     constexpr int TPC = RT_THREADS / L;
-    return launch_pdl(kern, dim3(grid_for((s + TPC - 1) / TPC)), dim3(RT_THREADS), 0, stream, (const T *)logits,
-                      bias, s, e, k, groups, topk_groups, group_top, scale, normalize,
+    // about twice what is resident (512 experts: 16.3 us with 4, 20.9 with 8)
+    constexpr int PER_SM = V <= 8 ? 8 : V == 16 ? 4 : 2;
+    return launch_pdl(kern, dim3(grid_for((s + TPC - 1) / TPC, PER_SM)), dim3(RT_THREADS), 0, stream,
+                      (const T *)logits, bias, s, e, k, groups, topk_groups, group_top, scale, normalize,
                       e % Elt<T>::VEC == 0 ? 1 : 0, idx, gates, st);
 }
 
@@ -503,7 +512,7 @@ template <typename T, typename D, int V, int L>
 moe_status bwd_all_v(const void *logits, const int32_t *idx, const float *d_gates, int64_t s, int e, int k,
                      float scale, void *d_logits, int32_t *st, cudaStream_t stream) {
     constexpr int TPC = RT_THREADS / L;
-    return launch_pdl(route_bwd_all_kernel<T, D, V, L>, dim3(grid_for((s + TPC - 1) / TPC)), dim3(RT_THREADS), 0,
+    return launch_pdl(route_bwd_all_kernel<T, D, V, L>, dim3(grid_for((s + TPC - 1) / TPC, 8)), dim3(RT_THREADS), 0,
                       stream, (const T *)logits, idx, d_gates, s, e, k, scale, e % Elt<T>::VEC == 0 ? 1 : 0,
                       (D *)d_logits, st);
 }
@@ -513,7 +522,7 @@ moe_status bwd_sel(const void *logits, const int32_t *idx, const float *d_gates,
                    bool softmax, float scale, int normalize, void *d_logits, int32_t *st, cudaStream_t stream) {
     auto kern = softmax ? route_bwd_sel_kernel<T, D, true> : route_bwd_sel_kernel<T, D, false>;
     const int tb = bwd_tokens(e);
-    return launch_pdl(kern, dim3(grid_for((s + tb - 1) / tb)), dim3(RT_THREADS), 0, stream, (const T *)logits, idx,
+    return launch_pdl(kern, dim3(grid_for((s + tb - 1) / tb, 8)), dim3(RT_THREADS), 0, stream, (const T *)logits, idx,
                       d_gates, s, e, k, scale, normalize, (D *)d_logits, st);
 }
 
