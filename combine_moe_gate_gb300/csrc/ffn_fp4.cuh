@@ -11,7 +11,7 @@
 // the sum of the values the codes stand for, in fp32.
 //
 // One persistent kernel on CTA pairs, 256 x 256 tiles (M = 256 over the pair),
-// the roles of tc_group_gemm: three producer warps, one MMA issuer, twelve
+// the roles of tc_group_gemm: four producer warps, one MMA issuer, eight
 // epilogue warps.  A stage is 256 values of K: 128-byte swizzled rows of 128 A
 // and 128 B rows per CTA, and the 512-byte scale tiles of those A rows and of
 // all 256 B rows (each CTA's half of the product needs every column's scale).
@@ -35,11 +35,6 @@ constexpr int F4_BK = 256;                     // values of K per stage (128 byt
 constexpr int F4_BOX_BYTES = 64 * 128;         // one operand copy: 64 rows
 constexpr int F4_OP_BYTES = 2 * F4_BOX_BYTES;  // one operand per CTA and stage
 constexpr int F4_STAGES = 5;
-// Warps: 0 producer, 1 MMA, 2 .. 13 epilogue, 14 and 15 producers: 16 warps with
-// the 128 registers that the epilogue needs are all of the register file.
-constexpr int F4_EPI = 12;
-constexpr int F4_PROD0 = 2 + F4_EPI;
-constexpr int F4_THREADS = (F4_PROD0 + 2) * 32;
 constexpr uint32_t F4_SF_COL = 384;            // first TMEM column of the scales
 constexpr uint32_t F4_ACC_STEP = 128;          // first column of the odd tiles' accumulator
 
@@ -234,7 +229,7 @@ __device__ __forceinline__ void f4_quantise32(float (&v)[32], const Fp4Factor &g
 }
 
 template <int FMT, int EPI>
-__global__ void __launch_bounds__(F4_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, 1)
 fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmB3, const __grid_constant__ CUtensorMap tmSA,
                const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmSB3,
@@ -245,7 +240,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     constexpr int BLK = Fp4<FMT>::BLK, KT = TL::KT, STAGES = F4_STAGES;
     __shared__ int32_t s_bad;
     __shared__ int32_t kept_rows[MAX_E];
-    __shared__ __align__(16) uint2 epi_bias[F4_EPI][24];   // three chunks of 32 bf16 per epilogue warp
+    __shared__ __align__(16) uint2 epi_bias[EPI_WARPS][32];   // 128 bf16 per epilogue warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem, *sB = smem + STAGES * F4_OP_BYTES, *sSF = sB + STAGES * F4_OP_BYTES;
@@ -262,9 +257,9 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (warp == 0) {
         if (lane == 0) {
             ctl->abort = 0;
-            for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 3); mbar_init(&ctl->empty[s], 1); }
+            for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 4); mbar_init(&ctl->empty[s], 1); }
             mbar_init(&ctl->tfull[0], 1);
-            mbar_init(&ctl->tempty[0], 2 * F4_EPI);
+            mbar_init(&ctl->tempty[0], 2 * EPI_WARPS);
             mbar_init(&ctl->drain, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -282,7 +277,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
     {
         const int c_eff = (int)min((int64_t)*args.c_dev, args.c_max);
-        for (int j = threadIdx.x; j < e; j += F4_THREADS) kept_rows[j] = max(0, min(args.counts[j], c_eff));
+        for (int j = threadIdx.x; j < e; j += NUM_THREADS) kept_rows[j] = max(0, min(args.counts[j], c_eff));
     }
     __syncthreads();
     if (warp == 0) {   // first tile of every expert: each lane sums a run of them
@@ -318,15 +313,16 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     int32_t *abort_flag = &ctl->abort;
 
-    if (warp == 0 || warp >= F4_PROD0) {
-        // Producer 0: this CTA's A rows and their scales; 1 and 2: the two halves
-        // of its B rows (SwiGLU: the first CTA's are W1's, the second's W3's) and
-        // the scales of the tile's first and second 128 columns.  A rows come in
-        // boxes of 32, and only those that hold kept rows (the others'
-        // accumulators are never stored).
-        const int prod = warp == 0 ? 0 : warp - F4_PROD0 + 1;
-        const bool is_a = prod == 0;
-        const int hh = is_a ? 0 : prod - 1;
+    if (warp == 0 || warp >= PROD_WARP0) {
+        // Producers 0 and 2: the two row halves of this CTA's A rows; 1 and 3:
+        // those of its B rows (SwiGLU: the first CTA's are W1's, the second's
+        // W3's).  0 also brings the A scales, 1 and 3 the scales of the first
+        // and second 128 columns of the tile.  A rows come in boxes of 32, and
+        // only those that hold kept rows (the others' accumulators are never
+        // stored).
+        const int prod = warp == 0 ? 0 : warp - PROD_WARP0 + 1;
+        const bool is_a = (prod & 1) == 0;
+        const int hh = prod >> 1;
         const CUtensorMap *op = is_a ? &tmA : SWIGLU && prank ? &tmB3 : &tmB;
         const CUtensorMap *sf = is_a ? &tmSA : SWIGLU && hh ? &tmSB3 : &tmSB;
         const int a_tiles = (int)((args.c_max + 127) / 128), b_tiles = (args.n_out + 127) / 128;
@@ -336,15 +332,16 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             for (int t = tile0; t < total && !args.stall; t += tile_step) {
                 const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
                 // this CTA's boxes of A, and the bytes of both CTAs' copies
-                const int left = T.rows - T.mt * 2 * UM;
-                const int n0 = min((left + 31) / 32, 4), n1 = min(max((left - UM + 31) / 32, 0), 4);
+                const int left = T.rows - T.mt * 2 * UM - hh * 64;
+                const int n0 = min(max((left + 31) / 32, 0), 2), n1 = min(max((left - UM + 31) / 32, 0), 2);
                 const int boxes = prank ? n1 : n0;
+                const bool sf_here = !is_a || (hh == 0 && boxes > 0);
                 const uint32_t bytes = is_a ? (uint32_t)(n0 + n1) * (F4_BOX_BYTES / 2) +
-                                                  (n1 > 0 ? 2u : 1u) * (uint32_t)TL::SF_BYTES
+                                                  (hh == 0 ? (uint32_t)((n0 > 0) + (n1 > 0)) * TL::SF_BYTES : 0u)
                                             : 2u * (F4_BOX_BYTES + TL::SF_BYTES);
                 int row, sf_row;
                 if (is_a) {
-                    row = (int)(T.j * args.c_max + (int64_t)T.mt * 2 * UM) + (int)prank * UM;
+                    row = (int)(T.j * args.c_max + (int64_t)T.mt * 2 * UM) + (int)prank * UM + hh * 64;
                     sf_row = T.j * a_tiles + T.mt * 2 + (int)prank;
                 } else {
                     row = T.j * args.n_out + T.nt * NOUT_TILE + (SWIGLU ? 0 : (int)prank * UM) + hh * 64;
@@ -357,14 +354,9 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), 0);
                     if (prank == 0) mbar_expect_tx(&ctl->full[stage], bytes);
                     uint8_t *to = dst + stage * F4_OP_BYTES;
-                    if (is_a) {
-                        for (int x = 0; x < boxes; x++)
-                            tma_load_2d_pair(to + x * (F4_BOX_BYTES / 2), op, kb * (F4_BK / 2), row + 32 * x, fb);
-                    } else {
-                        tma_load_2d_pair(to, op, kb * (F4_BK / 2), row, fb);
-                    }
-                    if (!is_a || boxes > 0)
-                        tma_load_3d_pair(sf_dst + stage * 3 * TL::SF_BYTES, sf, 0, kb * KT, sf_row, fb);
+                    if (!is_a || boxes > 0) tma_load_2d_pair(to, op, kb * (F4_BK / 2), row, fb);
+                    if (is_a && boxes > 1) tma_load_2d_pair(to + F4_BOX_BYTES / 2, op, kb * (F4_BK / 2), row + 32, fb);
+                    if (sf_here) tma_load_3d_pair(sf_dst + stage * 3 * TL::SF_BYTES, sf, 0, kb * KT, sf_row, fb);
                     issued++;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -428,12 +420,10 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         unsigned long long t0 = gtimer();
         while (!mbar_try<true>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
         }
-    } else if (warp >= 2) {
-        // Epilogue: lane quarter sub has rows sub * 32 .. of this CTA.  Its three
-        // warps share the tile's eight chunks of 32 columns, S0 .. S3 in the half
-        // that the next tile overwrites and O0 .. O3 in the other: S0 S1 O0, S2 O1
-        // O2, and S3 O3.  (SwiGLU: chunk Si with Oi, one holding a, the other b.)
-        const int ew = warp - 2, sub = warp & 3, third = ew >> 2;
+    } else if (warp >= 2 && warp < PROD_WARP0) {
+        // Epilogue: warp (sub, half) has rows sub * 32 .. of this CTA and, of the
+        // two 128-column halves, columns half * 64 .. + 63 each.
+        const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
         uint2 *bsl = epi_bias[ew];
         int done = 0;
         for (int t = tile0; t < total; t += tile_step, done++) {
@@ -446,108 +436,127 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const float s1 = ga * (args.b_global ? args.b_global[T.j] : 1.0f);
             const float s3 = SWIGLU ? ga * (args.b3_global ? args.b3_global[T.j] : 1.0f) : 0.0f;
             const Fp4Factor og = fp4_factor(EPI != FP4_BIAS && args.out_global ? args.out_global[T.j] : 1.0f);
-            const int shared0 = done & 1 ? 0 : 128, other0 = 128 - shared0;
-            // first columns of this warp's chunks within the tile
-            const int c0 = shared0 + 32 * (third ? third + 1 : 0);
-            const int c1 = third == 0 ? shared0 + 32 : other0 + 32 * (third == 1 ? 1 : 3);
-            const int c2 = other0 + 32 * (third == 1 ? 2 : 0);   // not of the last warp
-            if (!SWIGLU && args.bias && lane < 24) {
-                const int g = T.nt * NOUT_TILE + (lane < 8 ? c0 : lane < 16 ? c1 : c2) + (lane & 7) * 4;
+            const int64_t ont = fp4_scale_tiles(BLK, args.n_out);   // scale tiles of an output row
+            if (!SWIGLU && args.bias) {
+                // this warp's bias: columns half * 64 .. of both halves, 64 each
+                const int g = T.nt * NOUT_TILE + (lane >> 4) * 128 + half * 64 + (lane & 15) * 4;
                 bsl[lane] = g < args.n_out ? *reinterpret_cast<const uint2 *>(args.bias + (int64_t)T.j * args.n_out + g)
                                            : make_uint2(0u, 0u);
+                __syncwarp();
             }
-            __syncwarp();
             if (!warp_wait(&ctl->tfull[0], (uint32_t)(done & 1), abort_flag, args.status)) break;
             tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(done & 1) * F4_ACC_STEP;
-            uint32_t r[2][32];
-            if (any) {
-                tmem_ld32(tb + c0, r[0]);
-                if (third == 0) tmem_ld32(tb + c1, r[1]);
-                tmem_wait_ld(r[0]);
-                tmem_tie(r[1]);
+            const uint32_t tb = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(done & 1) * F4_ACC_STEP + half * 64;
+            const int shared0 = done & 1 ? 0 : 128;   // the half that the next tile overwrites
+            if (!any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
+                continue;
             }
+            uint32_t r[2][32];
+            tmem_ld32(tb + shared0, r[0]);
+            tmem_ld32(tb + shared0 + 32, r[1]);
+            tmem_wait_ld(r[0]);
+            tmem_tie(r[1]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
-            if (!any) continue;
-            // 32 hidden values (columns gcol ..) of this lane's row to their place
-            auto put_hidden = [&](float (&v)[32], int gcol) {
-                const int64_t ont = fp4_scale_tiles(BLK, args.n_out);   // scale tiles of a row
-                uint32_t codes[4], word = 0;
-                const bool live = gcol < args.n_out;
-                f4_quantise32<FMT>(v, og, live, codes, word, 0);
-                if (valid && live) {
-                    V16 w;
-                    w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
-                    st_v16(args.out_q + (grow * args.n_out + gcol) / 2, w);
-                }
-                if (valid && gcol < ont * 4 * BLK) {   // the last tile's blocks past the row: zeros
-                    uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
-                                 fp4_scale_at(row, gcol / BLK, ont);
-                    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
-                    else *p = (uint8_t)word;
-                }
-            };
-            if constexpr (SWIGLU) {
-#pragma unroll 1
-                for (int i = 0; i < (third == 0 ? 2 : 1); i++) {
-                    const int c = i == 0 ? c0 : c1;   // in the half loaded first
+            if (EPI != FP4_BIAS && !all_kept) {
+                f4_zero_unless(valid, r[0]);
+                f4_zero_unless(valid, r[1]);
+            }
+            if (SWIGLU) {
+                const int gcol = T.nt * NOUT_TILE + half * 64;
+                uint32_t word = 0;
+#pragma unroll
+                for (int h2 = 0; h2 < 2; h2++) {
                     uint32_t o[32];
-                    tmem_ld32(tb + (c ^ 128), o);
+                    tmem_ld32(tb + (128 - shared0) + 32 * h2, o);
                     tmem_wait_ld(o);
                     if (!all_kept) f4_zero_unless(valid, o);
                     float v[32];
 #pragma unroll
-                    for (int x = 0; x < 32; x++) {
-                        const uint32_t first = i == 0 ? r[0][x] : r[1][x];
-                        const float p = __uint_as_float(all_kept || valid ? first : 0u), q = __uint_as_float(o[x]);
-                        v[x] = f4_silu((shared0 ? q : p) * s1) * ((shared0 ? p : q) * s3);
+                    for (int i = 0; i < 32; i++) {
+                        const float x = __uint_as_float(r[h2][i]), y = __uint_as_float(o[i]);
+                        const float a = (shared0 ? y : x) * s1, b = (shared0 ? x : y) * s3;
+                        v[i] = f4_silu(a) * b;
                     }
-                    put_hidden(v, T.nt * NOUT_TILE + (c & 127));
+                    uint32_t codes[4];
+                    const bool live = gcol + 32 * h2 < args.n_out;
+                    f4_quantise32<FMT>(v, og, live, codes, word, h2);
+                    if (valid && live) {
+                        V16 w;
+                        w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
+                        st_v16(args.out_q + (grow * args.n_out + gcol + 32 * h2) / 2, w);
+                    }
+                }
+                if (valid && gcol < ont * 4 * BLK) {
+                    uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
+                                 fp4_scale_at(row, gcol / BLK, ont);
+                    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t *>(p) = word;
+                    else *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
                 }
             } else {
-                auto finish = [&](uint32_t (&acc)[32], int c, int slot) {
-                    if (EPI != FP4_BIAS && !all_kept) f4_zero_unless(valid, acc);
-                    const int gcol = T.nt * NOUT_TILE + c;
-                    const uint4 *bp = reinterpret_cast<const uint4 *>(bsl + 8 * slot);
-                    float v[32];
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        uint32_t bw[4] = {0u, 0u, 0u, 0u};   // eight columns' bias
-                        if (args.bias) {
-                            const uint4 u = bp[q];
-                            bw[0] = u.x; bw[1] = u.y; bw[2] = u.z; bw[3] = u.w;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int x = 8 * q + 2 * i;
-                            float2 a = __ffma2_rn(make_float2(__uint_as_float(acc[x]), __uint_as_float(acc[x + 1])),
-                                                  make_float2(s1, s1), make_float2(bf16lo(bw[i]), bf16hi(bw[i])));
-                            if (EPI == FP4_GELU) a = f4_gelu2(a);
-                            if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
-                            v[x] = a.x;
-                            v[x + 1] = a.y;
-                        }
-                    }
-                    if (EPI == FP4_BIAS) {
-                        if (valid) f4_store32(args.out + grow * args.n_out, v, gcol, args.n_out, args.wide);
-                    } else {
-                        put_hidden(v, gcol);
-                    }
-                };
-                finish(r[0], c0, 0);
 #pragma unroll 1
-                for (int i = 1; i < (third == 2 ? 2 : 3); i++) {
-                    const int c = i == 1 ? c1 : c2;
-                    if (third || i == 2) {
-                        tmem_ld32(tb + c, r[1]);
-                        tmem_wait_ld(r[1]);
+                for (int part = 0; part < 2; part++) {
+                    const int lcol = part == 0 ? shared0 : 128 - shared0;   // this half's first column
+                    const int gcol = T.nt * NOUT_TILE + lcol + half * 64;
+                    if (part) {
+                        tmem_ld32(tb + lcol, r[0]);
+                        tmem_ld32(tb + lcol + 32, r[1]);
+                        tmem_wait_ld(r[0]);
+                        tmem_tie(r[1]);
+                        if (EPI != FP4_BIAS && !all_kept) {
+                            f4_zero_unless(valid, r[0]);
+                            f4_zero_unless(valid, r[1]);
+                        }
                     }
-                    finish(r[1], c, i);
+                    uint32_t word = 0;
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; h2++) {
+                        const uint4 *bp = reinterpret_cast<const uint4 *>(bsl + (lcol ? 16 : 0) + 8 * h2);
+                        float v[32];
+#pragma unroll
+                        for (int q = 0; q < 4; q++) {
+                            uint32_t bw[4] = {0u, 0u, 0u, 0u};   // eight columns' bias
+                            if (args.bias) {
+                                const uint4 u = bp[q];
+                                bw[0] = u.x; bw[1] = u.y; bw[2] = u.z; bw[3] = u.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const int c = 8 * q + 2 * i;
+                                float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h2][c]), __uint_as_float(r[h2][c + 1])),
+                                                      make_float2(s1, s1), make_float2(bf16lo(bw[i]), bf16hi(bw[i])));
+                                if (EPI == FP4_GELU) a = f4_gelu2(a);
+                                if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                                v[c] = a.x;
+                                v[c + 1] = a.y;
+                            }
+                        }
+                        if (EPI == FP4_BIAS) {
+                            if (valid) f4_store32(args.out + grow * args.n_out, v, gcol + 32 * h2, args.n_out, args.wide);
+                        } else {
+                            uint32_t codes[4];
+                            const bool live = gcol + 32 * h2 < args.n_out;
+                            f4_quantise32<FMT>(v, og, live, codes, word, h2);
+                            if (valid && live) {
+                                V16 w;
+                                w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
+                                st_v16(args.out_q + (grow * args.n_out + gcol + 32 * h2) / 2, w);
+                            }
+                        }
+                    }
+                    if (EPI != FP4_BIAS && valid && gcol < ont * 4 * BLK) {
+                        uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
+                                     fp4_scale_at(row, gcol / BLK, ont);
+                        if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t *>(p) = word;
+                        else *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
+                    }
                 }
+                __syncwarp();   // the bias slice is rewritten for the next tile
             }
-            __syncwarp();   // the bias slice is rewritten for the next tile
         }
     }
 
@@ -614,26 +623,13 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
     if (!nunits) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM) != cudaSuccess)
             return MOE_ERR_CUDA;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(F4_THREADS);
-        cfg.dynamicSmemBytes = SMEM;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&nunits, (const void *)kern, &cfg) != cudaSuccess || nunits < 1) {
-            cudaGetLastError();
-            nunits = sm_count() / 2;
-        }
+        nunits = max_clusters(kern, SMEM, 2);
         if (dev >= 0 && dev < 64) units[dev] = nunits;
     }
     constexpr int NOUT_TILE = EPI == FP4_SWIGLU ? BN / 2 : BN;
     const int64_t upper = e * ((args.c_max + 2 * UM - 1) / (2 * UM)) * ((args.n_out + NOUT_TILE - 1) / NOUT_TILE);
     const int64_t grid = upper < nunits ? upper : nunits;
-    return launch_cluster_pdl(kern, dim3((unsigned)(2 * grid)), dim3(F4_THREADS), SMEM, 2, stream, mA, mB, mB3, mSA,
+    return launch_cluster_pdl(kern, dim3((unsigned)(2 * grid)), dim3(NUM_THREADS), SMEM, 2, stream, mA, mB, mB3, mSA,
                               mSB, mSB3, args);
 }
 
