@@ -560,6 +560,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
     }
 
+    __syncwarp();   // the elected lanes are back
     tc_fence_before();
     if (*(volatile int32_t *)abort_flag) {   // copies may still be landing: they take microseconds
         unsigned long long t0 = gtimer();
