@@ -15,13 +15,23 @@
 // epilogue warps.  A stage is 256 values of K: 128-byte swizzled rows of 128 A
 // and 128 B rows per CTA, and the 512-byte scale tiles of those A rows and of
 // all 256 B rows (each CTA's half of the product needs every column's scale).
-// tcgen05.cp copies a stage's scale tiles into TMEM (two sets of columns, used
-// in turn) ahead of its four K = 64 MMAs.
+// tcgen05.cp copies a stage's scale tiles into TMEM ahead of its four K = 64
+// MMAs; the two run in the order of issue, so a stage's copies wait for the
+// MMAs that still read the columns they overwrite.
 //
 // TMEM: two 256-column accumulators do not fit beside the scales, so they
-// overlap in 128 columns: [0, 256) and [128, 384).  The epilogue first loads
-// the overlapping half of a tile into registers and then lets the next tile's
-// MMAs begin, so all but those loads runs under the next main loop.
+// overlap in 64 columns: [0, 256) and [192, 448).  Each epilogue warp first
+// loads its part of the overlap (one chunk of 32 columns) and then lets the next
+// tile's MMAs begin; the rest of the epilogue runs under that main loop.  (An
+// overlap of 128 columns held twice the registers and spilled: 8 GELU experts
+// of 2048 rows, m 4096, h 8192: 331 us, 306 like this.  Twelve epilogue warps on
+// top of the wide overlap took 318 us, but under a profiler one of its bounded
+// waits ran out now and then; the cause was not found and it is not used.)
+//
+// What bounds it: a stage fills 38 KB of shared memory per SM (NV; MX 35) and
+// its MMAs read 32, against 128 bytes a clock; 8192^3 runs at 7.3 PFLOP/s (MX
+// 7.6), 4096 x 4096 x 8192 (7 tiles a pair) at 5.8 to 6.1.  With few rows an
+// expert it is the weights' bytes: 6.3 TB/s at K = 7168, 5.9 at K = 2048.
 #pragma once
 
 #include "fp4.cuh"
@@ -34,22 +44,24 @@ enum Fp4Epi { FP4_BIAS = 0, FP4_RELU = 1, FP4_GELU = 2, FP4_SWIGLU = 3 };
 constexpr int F4_BK = 256;                     // values of K per stage (128 bytes a row)
 constexpr int F4_BOX_BYTES = 64 * 128;         // one operand copy: 64 rows
 constexpr int F4_OP_BYTES = 2 * F4_BOX_BYTES;  // one operand per CTA and stage
-constexpr int F4_STAGES = 5;
-constexpr uint32_t F4_SF_COL = 384;            // first TMEM column of the scales
-constexpr uint32_t F4_ACC_STEP = 128;          // first column of the odd tiles' accumulator
+constexpr uint32_t F4_SF_COL = 448;            // first TMEM column of the scales
+constexpr uint32_t F4_ACC_STEP = 192;          // first column of the odd tiles' accumulator
 
 template <int FMT>
 struct F4Tiling {
     static constexpr int KT = F4_BK / (4 * Fp4<FMT>::BLK);   // scale tiles along a stage's K
     static constexpr int SF_BYTES = KT * 512;                // of 128 rows
     static constexpr int STAGE_BYTES = 2 * F4_OP_BYTES + 3 * SF_BYTES;
+    static constexpr int STAGES = 215 * 1024 / STAGE_BYTES;  // 5 (NV), 6 (MX)
     static constexpr uint32_t SF_COLS = 12 * KT;             // TMEM columns of a stage's scales
-    static_assert(F4_SF_COL + 2 * SF_COLS <= TMEM_COLS, "TMEM");
+    static constexpr uint32_t SETS = (TMEM_COLS - F4_SF_COL) / SF_COLS;   // stages whose scales TMEM holds
+    static_assert(SETS >= 1, "TMEM");
 };
 
 template <int FMT>
 constexpr size_t f4_smem_bytes() {
-    return 1024 + (size_t)F4_STAGES * F4Tiling<FMT>::STAGE_BYTES + sizeof(Ctl<F4_STAGES>);
+    using TL = F4Tiling<FMT>;
+    return 1024 + (size_t)TL::STAGES * TL::STAGE_BYTES + sizeof(Ctl<TL::STAGES>);
 }
 
 struct F4Args {
@@ -136,8 +148,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, int32_t 
 
 // silu(a) = a / (1 + e^-a), about 2 units in the last place: e^-a as 2^t with
 // the rounding error of t = -a log2(e) put back, one approximate reciprocal.
-// (The general exp and division spent more than the main loop of a tile with
-// few rows: 16 decoded tokens over 256 experts, 505 us with them.)
+// (With the general exp and division the epilogue of a tile with few rows took
+// longer than its main loop: 16 decoded tokens over 256 experts, 505 us; 402.)
 __device__ __forceinline__ float f4_silu(float a) {
     const float t = a * -1.4426950408889634f;
     const float r = __fmaf_rn(a, -1.4426950408889634f, -t);
@@ -204,19 +216,20 @@ __device__ __forceinline__ void f4_store32(__nv_bfloat16 *row, const float (&v)[
     }
 }
 
-// One lane's 64 hidden values (columns gcol .. of its row) to codes and block
-// scales.  Called in halves of 32 columns: `word` collects the scale bytes.
+// One lane's 32 hidden values to codes and the bytes of their block scales (0
+// unless `live`).
 template <int FMT>
 __device__ __forceinline__ void f4_quantise32(float (&v)[32], const Fp4Factor &g, bool live, uint32_t (&codes)[4],
-                                              uint32_t &word, int half) {
+                                              uint32_t &word) {
     constexpr int BLK = Fp4<FMT>::BLK;
 #pragma unroll
     for (int b = 0; b < 32 / BLK; b++) {
-        float amax = 0.0f, inv;
+        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f}, inv;
 #pragma unroll
-        for (int i = 0; i < BLK; i++) amax = amax_nan(amax, v[b * BLK + i]);
+        for (int i = 0; i < BLK; i++) m[i & 3] = amax_nan(m[i & 3], v[b * BLK + i]);
+        const float amax = amax_nan(amax_nan(m[0], m[1]), amax_nan(m[2], m[3]));
         const uint32_t sc = fp4_scale<FMT>(fabsf(amax), g, inv);
-        if (live) word |= sc << (8 * (half * (32 / BLK) + b));
+        if (live) word |= sc << (8 * b);
 #pragma unroll
         for (int i = 0; i < BLK; i += 2) {
             const float2 p = __fmul2_rn(make_float2(v[b * BLK + i], v[b * BLK + i + 1]), make_float2(inv, inv));
@@ -237,7 +250,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     using TL = F4Tiling<FMT>;
     constexpr bool SWIGLU = EPI == FP4_SWIGLU;
     constexpr int NOUT_TILE = SWIGLU ? BN / 2 : BN;
-    constexpr int BLK = Fp4<FMT>::BLK, KT = TL::KT, STAGES = F4_STAGES;
+    constexpr int BLK = Fp4<FMT>::BLK, KT = TL::KT, STAGES = TL::STAGES;
     __shared__ int32_t s_bad;
     __shared__ int32_t kept_rows[MAX_E];
     __shared__ __align__(16) uint2 epi_bias[EPI_WARPS][32];   // 128 bf16 per epilogue warp
@@ -409,7 +422,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         }
                     }
                     umma_commit_pair(&ctl->empty[stage], 3);
-                    sf_set ^= 1u;
+                    if (++sf_set == TL::SETS) sf_set = 0;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
@@ -421,8 +434,10 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         while (!mbar_try<true>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
         }
     } else if (warp >= 2 && warp < PROD_WARP0) {
-        // Epilogue: warp (sub, half) has rows sub * 32 .. of this CTA and, of the
-        // two 128-column halves, columns half * 64 .. + 63 each.
+        // Epilogue: warp (sub, half) has rows sub * 32 .. of this CTA and every other
+        // chunk of 32 columns: half, half + 2, ...  The next tile overwrites the last
+        // two chunks of an even tile and the first two of an odd one: each warp
+        // begins with its own of them and then lets that tile's MMAs go ahead.
         const int ew = warp - 2, sub = warp & 3, half = ew >> 2;
         uint2 *bsl = epi_bias[ew];
         int done = 0;
@@ -436,127 +451,109 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const float s1 = ga * (args.b_global ? args.b_global[T.j] : 1.0f);
             const float s3 = SWIGLU ? ga * (args.b3_global ? args.b3_global[T.j] : 1.0f) : 0.0f;
             const Fp4Factor og = fp4_factor(EPI != FP4_BIAS && args.out_global ? args.out_global[T.j] : 1.0f);
-            const int64_t ont = fp4_scale_tiles(BLK, args.n_out);   // scale tiles of an output row
             if (!SWIGLU && args.bias) {
-                // this warp's bias: columns half * 64 .. of both halves, 64 each
-                const int g = T.nt * NOUT_TILE + (lane >> 4) * 128 + half * 64 + (lane & 15) * 4;
+                // this warp's bias, four chunks of 32: chunk i at bsl + 8 i
+                const int g = T.nt * NOUT_TILE + ((lane >> 3) * 2 + half) * 32 + (lane & 7) * 4;
                 bsl[lane] = g < args.n_out ? *reinterpret_cast<const uint2 *>(args.bias + (int64_t)T.j * args.n_out + g)
                                            : make_uint2(0u, 0u);
-                __syncwarp();
             }
+            __syncwarp();
             if (!warp_wait(&ctl->tfull[0], (uint32_t)(done & 1), abort_flag, args.status)) break;
             tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(done & 1) * F4_ACC_STEP + half * 64;
-            const int shared0 = done & 1 ? 0 : 128;   // the half that the next tile overwrites
-            if (!any) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
-                continue;
+            const uint32_t tb = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(done & 1) * F4_ACC_STEP;
+            const int first = done & 1 ? half : 6 + half;   // the chunk to load first
+            uint32_t r[32];
+            if (any) {
+                tmem_ld32(tb + 32 * first, r);
+                tmem_wait_ld(r);
             }
-            uint32_t r[2][32];
-            tmem_ld32(tb + shared0, r[0]);
-            tmem_ld32(tb + shared0 + 32, r[1]);
-            tmem_wait_ld(r[0]);
-            tmem_tie(r[1]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->tempty[0]), 0));
-            if (EPI != FP4_BIAS && !all_kept) {
-                f4_zero_unless(valid, r[0]);
-                f4_zero_unless(valid, r[1]);
-            }
-            if (SWIGLU) {
-                const int gcol = T.nt * NOUT_TILE + half * 64;
-                uint32_t word = 0;
-#pragma unroll
-                for (int h2 = 0; h2 < 2; h2++) {
-                    uint32_t o[32];
-                    tmem_ld32(tb + (128 - shared0) + 32 * h2, o);
-                    tmem_wait_ld(o);
-                    if (!all_kept) f4_zero_unless(valid, o);
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const float x = __uint_as_float(r[h2][i]), y = __uint_as_float(o[i]);
-                        const float a = (shared0 ? y : x) * s1, b = (shared0 ? x : y) * s3;
-                        v[i] = f4_silu(a) * b;
-                    }
-                    uint32_t codes[4];
-                    const bool live = gcol + 32 * h2 < args.n_out;
-                    f4_quantise32<FMT>(v, og, live, codes, word, h2);
-                    if (valid && live) {
-                        V16 w;
-                        w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
-                        st_v16(args.out_q + (grow * args.n_out + gcol + 32 * h2) / 2, w);
-                    }
+            if (!any) continue;
+            // 32 hidden values (columns gcol ..) of this lane's row to their place
+            auto put_hidden = [&](float (&v)[32], int gcol) {
+                const int64_t ont = fp4_scale_tiles(BLK, args.n_out);   // scale tiles of a row
+                uint32_t codes[4], word = 0;
+                const bool live = gcol < args.n_out;
+                f4_quantise32<FMT>(v, og, live, codes, word);
+                if (valid && live) {
+                    V16 w;
+                    w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
+                    st_v16(args.out_q + (grow * args.n_out + gcol) / 2, w);
                 }
-                if (valid && gcol < ont * 4 * BLK) {
+                if (valid && gcol < ont * 4 * BLK) {   // the last tile's blocks past the row: zeros
                     uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
                                  fp4_scale_at(row, gcol / BLK, ont);
-                    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t *>(p) = word;
-                    else *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
+                    if (FMT == MOE_FP4_NV) *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
+                    else *p = (uint8_t)word;
+                }
+            };
+            if constexpr (SWIGLU) {
+                // output chunk c pairs chunk c (a) with chunk c + 4 (b)
+#pragma unroll 1
+                for (int i = 0; i < 2; i++) {
+                    const int c = (i == 0 ? first : first ^ 2) & 3;
+                    uint32_t o[32];
+                    if (i) {
+                        tmem_ld32(tb + 32 * c, r);
+                        tmem_ld32(tb + 32 * (c + 4), o);
+                    } else {
+                        tmem_ld32(tb + 32 * (first ^ 4), o);
+                    }
+                    tmem_wait_ld(o);
+                    tmem_tie(r);
+                    if (!all_kept) {
+                        f4_zero_unless(valid, o);
+                        f4_zero_unless(valid, r);
+                    }
+                    const bool r_is_b = i == 0 && first >= 4;   // what was loaded first
+                    float v[32];
+#pragma unroll
+                    for (int x = 0; x < 32; x++) {
+                        const float p = __uint_as_float(r[x]), q = __uint_as_float(o[x]);
+                        v[x] = f4_silu((r_is_b ? q : p) * s1) * ((r_is_b ? p : q) * s3);
+                    }
+                    put_hidden(v, T.nt * NOUT_TILE + 32 * c);
                 }
             } else {
 #pragma unroll 1
-                for (int part = 0; part < 2; part++) {
-                    const int lcol = part == 0 ? shared0 : 128 - shared0;   // this half's first column
-                    const int gcol = T.nt * NOUT_TILE + lcol + half * 64;
-                    if (part) {
-                        tmem_ld32(tb + lcol, r[0]);
-                        tmem_ld32(tb + lcol + 32, r[1]);
-                        tmem_wait_ld(r[0]);
-                        tmem_tie(r[1]);
-                        if (EPI != FP4_BIAS && !all_kept) {
-                            f4_zero_unless(valid, r[0]);
-                            f4_zero_unless(valid, r[1]);
+                for (int i = 0; i < 4; i++) {
+                    const int c = (first + 2 * i) & 7;
+                    if (i) {
+                        tmem_ld32(tb + 32 * c, r);
+                        tmem_wait_ld(r);
+                    }
+                    if (EPI != FP4_BIAS && !all_kept) f4_zero_unless(valid, r);
+                    const int gcol = T.nt * NOUT_TILE + 32 * c;
+                    const uint4 *bp = reinterpret_cast<const uint4 *>(bsl + 8 * (c >> 1));
+                    float v[32];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        uint32_t bw[4] = {0u, 0u, 0u, 0u};   // eight columns' bias
+                        if (args.bias) {
+                            const uint4 u = bp[q];
+                            bw[0] = u.x; bw[1] = u.y; bw[2] = u.z; bw[3] = u.w;
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; y++) {
+                            const int x = 8 * q + 2 * y;
+                            float2 a = __ffma2_rn(make_float2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])),
+                                                  make_float2(s1, s1), make_float2(bf16lo(bw[y]), bf16hi(bw[y])));
+                            if (EPI == FP4_GELU) a = f4_gelu2(a);
+                            if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                            v[x] = a.x;
+                            v[x + 1] = a.y;
                         }
                     }
-                    uint32_t word = 0;
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; h2++) {
-                        const uint4 *bp = reinterpret_cast<const uint4 *>(bsl + (lcol ? 16 : 0) + 8 * h2);
-                        float v[32];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            uint32_t bw[4] = {0u, 0u, 0u, 0u};   // eight columns' bias
-                            if (args.bias) {
-                                const uint4 u = bp[q];
-                                bw[0] = u.x; bw[1] = u.y; bw[2] = u.z; bw[3] = u.w;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const int c = 8 * q + 2 * i;
-                                float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h2][c]), __uint_as_float(r[h2][c + 1])),
-                                                      make_float2(s1, s1), make_float2(bf16lo(bw[i]), bf16hi(bw[i])));
-                                if (EPI == FP4_GELU) a = f4_gelu2(a);
-                                if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
-                                v[c] = a.x;
-                                v[c + 1] = a.y;
-                            }
-                        }
-                        if (EPI == FP4_BIAS) {
-                            if (valid) f4_store32(args.out + grow * args.n_out, v, gcol + 32 * h2, args.n_out, args.wide);
-                        } else {
-                            uint32_t codes[4];
-                            const bool live = gcol + 32 * h2 < args.n_out;
-                            f4_quantise32<FMT>(v, og, live, codes, word, h2);
-                            if (valid && live) {
-                                V16 w;
-                                w.w[0] = codes[0]; w.w[1] = codes[1]; w.w[2] = codes[2]; w.w[3] = codes[3];
-                                st_v16(args.out_q + (grow * args.n_out + gcol + 32 * h2) / 2, w);
-                            }
-                        }
-                    }
-                    if (EPI != FP4_BIAS && valid && gcol < ont * 4 * BLK) {
-                        uint8_t *p = args.out_scale + T.j * fp4_scale_bytes(BLK, args.c_max, args.n_out) +
-                                     fp4_scale_at(row, gcol / BLK, ont);
-                        if (FMT == MOE_FP4_NV) *reinterpret_cast<uint32_t *>(p) = word;
-                        else *reinterpret_cast<uint16_t *>(p) = (uint16_t)word;
+                    if (EPI == FP4_BIAS) {
+                        if (valid) f4_store32(args.out + grow * args.n_out, v, gcol, args.n_out, args.wide);
+                    } else {
+                        put_hidden(v, gcol);
                     }
                 }
-                __syncwarp();   // the bias slice is rewritten for the next tile
             }
+            __syncwarp();   // the bias slice is rewritten for the next tile
         }
     }
 
