@@ -57,9 +57,11 @@ __device__ __forceinline__ void ld_logits(const T *row, int j0, int e, bool vec,
     }
 }
 
-// Order-preserving map of a float to an unsigned key (-0 as +0); never 0.
+// Order-preserving map of a float to an unsigned key; never 0.  (A choice is a
+// score, at least +0, or its sum with a bias, and a group's value a sum of
+// choices: none of them is -0.)
 __device__ __forceinline__ uint32_t order_key(float f) {
-    const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
+    const uint32_t b = __float_as_uint(f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
@@ -212,7 +214,8 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
                   int32_t *__restrict__ idx, float *__restrict__ gates, int32_t *status) {
     constexpr int TPW = 32 / L;   // tokens per warp
     __shared__ __align__(16) float s_val[RT_WARPS][V * 32];   // choices, then scores
-    __shared__ uint2 s_cand[RT_WARPS][32];       // candidates (L = 32)
+    constexpr int CAND = V <= 8 ? V * L : 32;    // room for every expert, where it is small
+    __shared__ uint2 s_cand[L == 32 ? RT_WARPS : 1][CAND];   // candidates
     __shared__ int32_t s_sel[RT_WARPS][TPW * 32];   // the selection, by route
     pdl_enter();
     const bool stop = status_bad(status);   // asked for now, needed before the first store
@@ -236,14 +239,22 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const float c = __fadd_rn(sc[i], bs[i]);   // without a bias: + 0
-            ch[i] = l[i] > -INFINITY && c == c && (whole || i < mine) ? c : -INFINITY;
+            ch[i] = l[i] > -INFINITY && c == c ? c : -INFINITY;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < V; i++) ch[i] = i < mine ? ch[i] : -INFINITY;
         }
         // keys: 0 below everything (not an expert, or of a group that does not stay)
         uint32_t key[V];
         if (groups == 1 || by_lane) {
             const bool in = groups == 1 || my_group_stays<V, L>(ch, sub, groups, gl, topk_groups, group_top);
 #pragma unroll
-            for (int i = 0; i < V; i++) key[i] = in && (whole || i < mine) ? order_key(ch[i]) : 0u;
+            for (int i = 0; i < V; i++) key[i] = in ? order_key(ch[i]) : 0u;
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < V; i++) key[i] = i < mine ? key[i] : 0u;
+            }
         } else {
             const uint32_t kept = kept_groups<V, L>(ch, val, reinterpret_cast<uint32_t *>(sel), sub, groups, gs,
                                                     topk_groups, group_top);
@@ -275,7 +286,7 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
             for (int i = 0; i < V; i++) {
                 const uint32_t b = __ballot_sync(0xffffffffu, key[i] >= low);
                 const int at = n + __popc(b & ((1u << lane) - 1));
-                if (key[i] >= low && at < 32) s_cand[warp][at] = make_uint2(key[i], sub * V + i);
+                if (key[i] >= low && (CAND == V * L || at < 32)) s_cand[warp][at] = make_uint2(key[i], sub * V + i);
                 n += __popc(b);
             }
             __syncwarp();
