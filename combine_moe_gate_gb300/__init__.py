@@ -166,7 +166,7 @@ def _dt(t):
 def _stream(stream):
     """The stream's handle; None: torch's current stream of the current device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 

@@ -32,11 +32,11 @@ template <> __device__ __forceinline__ float ld_logit<__nv_bfloat16>(const __nv_
     return __bfloat162float(*p);
 }
 
-// V logits of a token from expert j0 on; 0 past the last expert.  vec: rows
+// V logits of a token from expert j0 on; `pad` past the last expert.  vec: rows
 // are whole 16-byte chunks (e * sizeof(T) % 16 == 0), so a chunk is either
 // inside a row or past it.
 template <typename T, int V>
-__device__ __forceinline__ void ld_logits(const T *row, int j0, int e, bool vec, float (&l)[V]) {
+__device__ __forceinline__ void ld_logits(const T *row, int j0, int e, bool vec, float pad, float (&l)[V]) {
     constexpr int N = Elt<T>::VEC;
     if (V % N == 0 && vec) {
 #pragma unroll
@@ -48,12 +48,12 @@ __device__ __forceinline__ void ld_logits(const T *row, int j0, int e, bool vec,
                 for (int i = 0; i < N; i++) l[c * N + i] = f[i];
             } else {
 #pragma unroll
-                for (int i = 0; i < N; i++) l[c * N + i] = 0.0f;
+                for (int i = 0; i < N; i++) l[c * N + i] = pad;
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; i++) l[i] = j0 + i < e ? ld_logit(row + j0 + i) : 0.0f;
+        for (int i = 0; i < V; i++) l[i] = j0 + i < e ? ld_logit(row + j0 + i) : pad;
     }
 }
 
@@ -68,10 +68,12 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // The sigmoid; the addition and the division are single IEEE operations.
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
 
-// Scores of a token over its L lanes (sub: this lane's place among them), V
-// consecutive experts a lane.  Padding enters as exp = 0.
+// Scores of a token over its L lanes, V consecutive experts a lane.  Padding:
+// logits of 0 (sigmoid; its scores are not looked at) or -inf (softmax; it adds
+// nothing).  Returns whether the choices are numbers where the logits are: not
+// for a softmax with a NaN or +inf in it.
 template <int V, int L, bool SOFTMAX>
-__device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, float (&sc)[V]) {
+__device__ __forceinline__ bool scores(const float (&l)[V], float (&sc)[V]) {
     if (!SOFTMAX) {
         float x[V];
         bool general = false;   // logits below -87: a subnormal score, or 0
@@ -84,25 +86,21 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, floa
         if (general)
 #pragma unroll
             for (int i = 0; i < V; i++) sc[i] = __frcp_rn(x[i]);
-        return;
+        return true;
     }
-    const int mine = min(max(e - sub * V, 0), V);   // experts on this lane
     float top = -INFINITY;
-    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        top = i < mine ? fmaxf(top, l[i]) : top;
-        nan |= l[i] != l[i];
-    }
+    for (int i = 0; i < V; i++) top = fmaxf(top, l[i]);
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool none = top == -INFINITY && !nan;   // nothing left on this token (or only a NaN elsewhere): scores 0
+    // nothing left: exp(-inf - 0) = 0 everywhere (a NaN among the -inf still shows)
+    const float base = top == -INFINITY ? 0.0f : top;
     float t[V];
-    bool general = false;
+    uint32_t least = 0xffffffffu;   // of the exponentials' bits - 1 (0 comes out largest)
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        sc[i] = i < mine && !none ? expf(__fsub_rn(l[i], top)) : 0.0f;
-        general |= __float_as_uint(sc[i]) - 1u < __float_as_uint(0x1p-100f) - 1u;
+        sc[i] = expf(__fsub_rn(l[i], base));
+        least = min(least, __float_as_uint(sc[i]) - 1u);
         t[i] = sc[i];
     }
 #pragma unroll
@@ -112,24 +110,28 @@ __device__ __forceinline__ void scores(const float (&l)[V], int e, int sub, floa
     float sum = t[0];
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-    if (sum == 0.0f) return;   // every score is 0 already
+    if (sum == 0.0f) return true;   // every score is 0 already
     const float y = rcp_mid(sum);
-    if (general) {
+    if (least < __float_as_uint(0x1p-100f) - 1u) {   // tiny exponentials: the general division
 #pragma unroll
         for (int i = 0; i < V; i++) sc[i] = __fdiv_rn(sc[i], sum);
     } else {
 #pragma unroll
         for (int i = 0; i < V; i++) sc[i] = div_mid(sc[i], sum, y);
     }
+    return sum == sum;
 }
 
 // Largest of u over a token's L lanes.
 template <int L>
 __device__ __forceinline__ uint32_t max_over(uint32_t u) {
-    if constexpr (L == 32) return __reduce_max_sync(0xffffffffu, u);
+    if constexpr (L == 32) {
+        return __reduce_max_sync(0xffffffffu, u);
+    } else {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
-    return u;
+        for (int o = L / 2; o > 0; o >>= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, o));
+        return u;
+    }
 }
 
 // The lowest of a token's lanes where p holds (0 if nowhere), as its place.
@@ -198,10 +200,13 @@ __device__ __forceinline__ uint32_t kept_groups(const float (&ch)[V], float *cho
         }
         if (ahead < topk_groups) kept |= 1u << g;
     }
-    if (L == 32) return __reduce_or_sync(0xffffffffu, kept);
+    if constexpr (L == 32) {
+        return __reduce_or_sync(0xffffffffu, kept);
+    } else {
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, o);
-    return kept;
+        for (int o = 1; o < L; o <<= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, o);
+        return kept;
+    }
 }
 
 template <int N> struct alignas(4 * N) Vec { float f[N]; };
@@ -229,17 +234,20 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
     int32_t *sel = s_sel[warp] + tw * 32;
     float bs[V];
 #pragma unroll
-    for (int i = 0; i < V; i++) bs[i] = bias && sub * V + i < e ? bias[sub * V + i] : 0.0f;
+    for (int i = 0; i < V; i++) {
+        bs[i] = bias && sub * V + i < e ? bias[sub * V + i] : 0.0f;
+        if (bs[i] != bs[i]) bs[i] = -INFINITY;   // a NaN choice ranks like a masked expert
+    }
     const int64_t step = (int64_t)gridDim.x * RT_WARPS * TPW;
     for (int64_t t0 = ((int64_t)blockIdx.x * RT_WARPS + warp) * TPW; t0 < s; t0 += step) {
         const int64_t t = min(t0 + tw, s - 1);   // lanes past the end repeat the last token
         float l[V], sc[V], ch[V];
-        ld_logits<T, V>(logits + t * e, sub * V, e, vec, l);
-        scores<V, L, SOFTMAX>(l, e, sub, sc);
+        ld_logits<T, V>(logits + t * e, sub * V, e, vec, SOFTMAX ? -INFINITY : 0.0f, l);
+        const bool numbers = scores<V, L, SOFTMAX>(l, sc);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const float c = __fadd_rn(sc[i], bs[i]);   // without a bias: + 0
-            ch[i] = l[i] > -INFINITY && c == c ? c : -INFINITY;
+            ch[i] = l[i] > -INFINITY && (!SOFTMAX || numbers) ? c : -INFINITY;   // (a NaN is not > -inf)
         }
         if (!whole) {
 #pragma unroll
@@ -312,9 +320,10 @@ route_topk_kernel(const T *__restrict__ logits, const float *__restrict__ bias, 
                 int pos = 0;
 #pragma unroll
                 for (int i = V - 1; i >= 0; i--) pos = key[i] == top ? i : pos;
+                if (mine) sel[r] = sub * V + pos;
+                if (r + 1 == k) break;
 #pragma unroll
                 for (int i = 0; i < V; i++) key[i] = mine && i == pos ? 0u : key[i];
-                if (mine) sel[r] = sub * V + pos;
             }
         }
         __syncwarp();
@@ -380,7 +389,8 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
         const int nt = (int)min((int64_t)tb, s - t0);
         const int64_t t = t0 + tok;
         const bool on = tok < nt;
-        // this lane's routes sub, sub + 8, ... of its token
+        // this lane's routes sub, sub + 8, ... of its token (q * 8 < k is the same
+        // in all threads: up to eight routes skip the other three)
         int j[4];
         float x[4], dg[4], g[4];
         bool bad = false;
@@ -396,36 +406,48 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
         for (int i = threadIdx.x; i < (nt * e + 3) / 4; i += RT_THREADS) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 4; q++) {
+            if (q * BWD_LANES >= k) break;
             if (on && sub + q * BWD_LANES < k && (j[q] < 0 || j[q] >= e)) { bad = true; j[q] = -1; }
             x[q] = j[q] >= 0 ? ld_logit(logits + t * e + j[q]) : -INFINITY;
             top = fmaxf(top, x[q]);
         }
         if (bad) set_status(status, MOE_ERR_INVALID_ARG);
-        float total = 0.0f, dot = 0.0f;
+        float total = 0.0f;
         if (SOFTMAX) {
 #pragma unroll
             for (int o = BWD_LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
 #pragma unroll
         for (int q = 0; q < 4; q++) {
+            if (q * BWD_LANES >= k) break;
             if (j[q] < 0 || (SOFTMAX && top == -INFINITY)) g[q] = 0.0f;
             else g[q] = SOFTMAX ? expf(x[q] - top) : sigmoid_rn(x[q]);
             total += g[q];
-            dot += dg[q] * g[q];
         }
+        // A from the quotients G themselves: of a single route (G = 1) it is dg, and
+        // the gradient 0 without a rounding error
+        float G[4], A = 0.0f;
+        if (normalize) {
 #pragma unroll
-        for (int o = BWD_LANES / 2; o > 0; o >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            for (int o = BWD_LANES / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                if (q * BWD_LANES >= k) break;
+                G[q] = total == 0.0f ? 0.0f : g[q] / total;
+                A += dg[q] * G[q];
+            }
+#pragma unroll
+            for (int o = BWD_LANES / 2; o > 0; o >>= 1) A += __shfl_xor_sync(0xffffffffu, A, o);
         }
         // the rows are zero; another CTA's error may have come up meanwhile, so the
         // threads leave together
         if (__syncthreads_or(stop)) return;
 #pragma unroll
         for (int q = 0; q < 4; q++) {
+            if (q * BWD_LANES >= k) break;
             if (j[q] < 0) continue;
             float d;
-            if (normalize) d = total == 0.0f ? 0.0f : scale * (g[q] / total) * (dg[q] - dot / total);
+            if (normalize) d = scale * G[q] * (dg[q] - A);
             else d = scale * dg[q] * g[q];
             if (!SOFTMAX) d *= 1.0f - g[q];
             rows[tok * e + j[q]] = d;
@@ -453,8 +475,8 @@ route_bwd_all_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
         const int nt = (int)min((int64_t)TPC, s - t0);
         const int64_t t = t0 + min(tok, nt - 1);
         float l[V], p[V];
-        ld_logits<T, V>(logits + t * e, sub * V, e, vec, l);
-        scores<V, L, true>(l, e, sub, p);
+        ld_logits<T, V>(logits + t * e, sub * V, e, vec, -INFINITY, l);
+        scores<V, L, true>(l, p);
         float *row = rows + tok * e;
         const bool on = tok < nt;   // lanes past the end repeat the last token's scores, and write nothing
         if (on)

@@ -601,8 +601,8 @@ uint64_t moe_launch_count(void);
 
 /*
  * Error-path test hook, not for production use.  The next n launches of the
- * tensor-core grouped GEMM in this process (moe_expert_ffn, _fp8, _bwd and the
- * layer calls all use it; fc1 and fc2 are one launch each) issue no operand
+ * tensor-core grouped GEMMs in this process (moe_expert_ffn, _fp8, _fp4, _bwd,
+ * moe_product_fp4 and the layer calls use them; fc1 and fc2 are one launch each) issue no operand
  * copies, so the MMA issuer's bounded wait on its first stage runs out after
  * about one second: the launch sets MOE_ERR_TIMEOUT in the call's status
  * word, drains, releases its tensor memory and returns, and every later

@@ -104,6 +104,12 @@ CASES = [
     (1500, 64, 2, "softmax", False, 1, 1, 1, True, "bf16"),
     (900, 128, 4, "softmax", False, 4, 2, 1, True, "f32"),
     (20, 512, 10, "sigmoid", True, 16, 4, 2, True, "bf16"),
+    # more routes than lanes share a token, and all experts chosen
+    (37, 32, 32, "sigmoid", True, 1, 1, 1, True, "f32"),
+    (41, 16, 10, "softmax", False, 4, 3, 2, False, "bf16"),
+    (29, 64, 32, "softmax", True, 8, 4, 2, True, "bf16"),
+    (19, 128, 32, "sigmoid", False, 16, 5, 1, True, "f32"),
+    (11, 5, 3, "sigmoid", True, 5, 4, 1, True, "f32"),
 ]
 
 
@@ -271,6 +277,16 @@ def test_route_bwd_masked_rows(score, norm):
     assert np.isfinite(got).all() and (got[0] == 0).all() and (got[1, 3:] == 0).all()
     want = grad64(x, idx, dg, score, 1.0, norm)
     assert (np.abs(got - want) <= 1e-5).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_bwd_of_one_renormalised_route_is_zero(score):
+    """The gate is 1 whatever the logit: no rounding error may stand for a gradient."""
+    g = torch.Generator().manual_seed(4)
+    x, dg = torch.randn((300, 24), generator=g).cuda(), torch.randn((1, 300), generator=g).cuda()
+    idx = torch.randint(0, 24, (1, 300), generator=g, dtype=torch.int32).cuda()
+    assert (run_bwd(x, idx, dg, score, 2.5, True) == 0).all()
+    assert (run_bwd(x[:, :1].contiguous(), torch.zeros_like(idx), dg, "softmax", 2.5, False) == 0).all()
 
 
 def test_route_bwd_reports_a_bad_index():
