@@ -138,12 +138,13 @@ def _ptr(t, name="tensor", dtype=None, shape=None):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if not _on_device(t):
+    if not (t.is_cuda or _on_device(t)):
         raise ValueError(f"{name}: must be a CUDA tensor")
     return t.data_ptr()
 
 
 def _on_device(t) -> bool:
+    """What a tensor that is not CUDA's has to pass (a test's stand-in does)."""
     return t.is_cuda
 
 
