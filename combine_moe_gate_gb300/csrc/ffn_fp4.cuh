@@ -160,6 +160,13 @@ __device__ __forceinline__ float f4_silu(float a) {
     return a * q;
 }
 
+// ReLU; a NaN stays one.
+__device__ __forceinline__ float f4_relu(float a) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(0.0f));
+    return r;
+}
+
 // GELU, exact erf form, two values at a time: with E(a) = erfc(|a| / sqrt 2),
 // a Phi(a) = max(a, 0) - |a| E(a) / 2 on both sides of zero.  erfc by Abramowitz
 // and Stegun 7.1.28, as in gelu_erf2, its coefficients scaled by 2^(-i/2):
@@ -541,7 +548,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             float2 a = __ffma2_rn(make_float2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])),
                                                   make_float2(s1, s1), make_float2(bf16lo(bw[y]), bf16hi(bw[y])));
                             if (EPI == FP4_GELU) a = f4_gelu2(a);
-                            if (EPI == FP4_RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                            if (EPI == FP4_RELU) a = make_float2(f4_relu(a.x), f4_relu(a.y));
                             v[x] = a.x;
                             v[x + 1] = a.y;
                         }

@@ -339,8 +339,6 @@ def test_expert_ffn_matches_64_bit(fmt, c):
         s = np.repeat(np.ldexp(1.0, sc - 127) if fmt == "mx" else E4M3[sc] * g, BLK[fmt], 1)
         amax = np.abs(hid).reshape(r, n, -1).max(2)
         t2 = tol.reshape(r, n, -1).max(2)
-        for a, sel in ((np.maximum(amax - t2, 0), sc), (amax + t2, sc)):
-            pass
         if fmt == "mx":
             lo = np.where(amax - t2 > 0, np.maximum(np.frexp(np.maximum(amax - t2, 1e-300))[1] - 3, -127) + 127, 0)
             hi = np.maximum(np.frexp(np.maximum(amax + t2, 1e-300))[1] - 3, -127) + 127
@@ -365,6 +363,35 @@ def test_expert_ffn_matches_64_bit(fmt, c):
         if b2 is not None:
             want = want + b2[j].float().cpu().numpy()
         assert (np.abs(got[j, :r] - want) <= bound(mag, want, h)).all(), j
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("act", ["relu", "gelu", "swiglu"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_token_spoils_its_own_row_only(fmt, act, bad):
+    e, c_max, m, h = 2, 140, 96, 160
+    x = data((e, c_max, m), 51)
+    w = [quant(data((e, h, m), 52), fmt), quant(data((e, h, m), 53), fmt), quant(data((e, m, h), 54), fmt)]
+    if act != "swiglu":
+        w[1] = (None, None)
+    counts = torch.tensor([c_max, 77], dtype=torch.int32, device="cuda")
+    c_dev = torch.tensor([c_max], dtype=torch.int32, device="cuda")
+    outs = []
+    for spoil in (False, True):
+        if spoil:
+            x[1, 70, 5] = bad
+        q, sc = quant(x, fmt)
+        ws = torch.zeros(M.moe_expert_ffn_fp4_workspace_size(fmt, act, e, c_max, m, h), dtype=torch.uint8, device="cuda")
+        out = torch.zeros((e, c_max, m), dtype=torch.bfloat16, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        M.moe_expert_ffn_fp4(q, sc, None, None, counts, c_dev, *w[0], None, None, *w[1], None, *w[2], None, None, fmt,
+                             act, ws, out, st)
+        torch.cuda.synchronize()
+        status_ok(st)
+        outs.append(out)
+    assert torch.isfinite(outs[0].float()).all() and torch.isnan(outs[1][1, 70].float()).all()
+    outs[1][1, 70] = outs[0][1, 70]
+    assert torch.equal(outs[0], outs[1])
 
 
 def test_ffn_skips_after_an_error_and_without_rows():
