@@ -94,6 +94,7 @@ def load():
         "moe_status_str": (ctypes.c_char_p, [I]),
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_debug_stall_gemms": (I, [I]),
+        "moe_debug_lag_gemms": (I, [I]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -123,6 +124,12 @@ def moe_debug_stall_gemms(n):
     operand copies, so each times out after about a second with
     MOE_ERR_TIMEOUT in its status word (n = 0 cancels)."""
     _check(load().moe_debug_stall_gemms(int(n)), "moe_debug_stall_gemms")
+
+
+def moe_debug_lag_gemms(n):
+    """Test hook: in the next n launches of the 4-bit products the copies of the
+    second half of every row tile lag by 20 us a stage (n = 0 cancels)."""
+    _check(load().moe_debug_lag_gemms(int(n)), "moe_debug_lag_gemms")
 
 
 def _ptr(t, name="tensor", dtype=None, shape=None):

@@ -9,13 +9,15 @@ namespace moe {
 static std::atomic<uint64_t> g_launches{0};
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
-static std::atomic<int32_t> g_gemm_stalls{0};
-bool take_gemm_stall() {
-    int32_t n = g_gemm_stalls.load(std::memory_order_relaxed);
-    while (n > 0 && !g_gemm_stalls.compare_exchange_weak(n, n - 1, std::memory_order_relaxed)) {
+static std::atomic<int32_t> g_gemm_stalls{0}, g_gemm_lags{0};
+static bool take_one(std::atomic<int32_t> &pending) {
+    int32_t n = pending.load(std::memory_order_relaxed);
+    while (n > 0 && !pending.compare_exchange_weak(n, n - 1, std::memory_order_relaxed)) {
     }
     return n > 0;
 }
+bool take_gemm_stall() { return take_one(g_gemm_stalls); }
+bool take_gemm_lag() { return take_one(g_gemm_lags); }
 
 // kernels (one translation unit each)
 moe_status gate_topk_launch(const void *x, moe_dtype xdt, const float *wg, const float *bias,
@@ -150,6 +152,12 @@ uint64_t moe_launch_count(void) { return g_launches.load(std::memory_order_relax
 moe_status moe_debug_stall_gemms(int32_t n) {
     if (n < 0) return MOE_ERR_INVALID_ARG;
     g_gemm_stalls.store(n, std::memory_order_relaxed);
+    return MOE_OK;
+}
+
+moe_status moe_debug_lag_gemms(int32_t n) {
+    if (n < 0) return MOE_ERR_INVALID_ARG;
+    g_gemm_lags.store(n, std::memory_order_relaxed);
     return MOE_OK;
 }
 

@@ -17,6 +17,8 @@ void note_launch();
 // True (and one fewer pending) while moe_debug_stall_gemms has stalls pending:
 // the tensor-core GEMM launch being prepared then issues no operand copies.
 bool take_gemm_stall();
+// The same for moe_debug_lag_gemms (4-bit products only).
+bool take_gemm_lag();
 
 inline moe_status launch_status() {
     cudaError_t err = cudaGetLastError();

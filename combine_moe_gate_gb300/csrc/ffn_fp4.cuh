@@ -26,7 +26,8 @@
 // overlap of 128 columns held twice the registers and spilled: 8 GELU experts
 // of 2048 rows, m 4096, h 8192: 331 us, 306 like this.  Twelve epilogue warps on
 // top of the wide overlap took 318 us, but under a profiler one of its bounded
-// waits ran out now and then; the cause was not found and it is not used.)
+// waits ran out now and then: it had the lap that F4_FULL_ARRIVALS closes, which
+// may or may not have been the cause, and it is not used.)
 //
 // What bounds it: a stage fills 38 KB of shared memory per SM (NV; MX 35) and
 // its MMAs read 32, against 128 bytes a clock; 8192^3 runs at 7.3 PFLOP/s (MX
@@ -81,8 +82,29 @@ struct F4Args {
     int K;
     int n_out;
     int32_t wide;               // rows of out are whole 32-byte sectors
-    int32_t stall;
+    int32_t stall;              // tests: the producers issue no copies
+    int32_t lag;                // tests: the second CTA's A producers fall behind
 };
+
+// Arrivals per phase of a stage's full barrier: the four producers of the first
+// CTA (with the bytes of both CTAs) and the two A producers of the second.
+//
+// A wait for a parity is sound while its barrier cannot get two phases ahead of
+// the waiter; the next phase of every barrier needs each of its waiters:
+//   empty (per CTA, a commit of the MMAs): waited for by the CTA's producers, and
+//     the MMAs need the stage's full phase, for which every producer arrives or
+//     brings bytes.  The second CTA's A producers may have nothing to copy, where
+//     a tile's rows all lie in the first CTA: they arrive all the same.  (Without
+//     that the ring could go round twice while one of them looked away, and its
+//     wait ran out.)
+//   full (first CTA): waited for by the MMA issuer, which frees the stage.
+//   tfull (per CTA, a commit): waited for by the epilogue warps; the next tile's
+//     MMAs begin when all 16 of both CTAs have arrived at tempty, each after its
+//     wait.  tempty: waited for by the MMA issuer, which commits the next tfull.
+//   drain: one phase.
+// All roles go through the same tiles: both CTAs form the list from the same
+// counts, and agree on the status word before the first.
+constexpr int F4_FULL_ARRIVALS = 6;
 
 // Instruction descriptor of the block-scaled 4-bit kinds: A and B e2m1 (1 at
 // bits 7 and 10), both K-major, N >> 3 at bit 17, scale type at bit 23 (1:
@@ -277,7 +299,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (warp == 0) {
         if (lane == 0) {
             ctl->abort = 0;
-            for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 4); mbar_init(&ctl->empty[s], 1); }
+            for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], F4_FULL_ARRIVALS); mbar_init(&ctl->empty[s], 1); }
             mbar_init(&ctl->tfull[0], 1);
             mbar_init(&ctl->tempty[0], 2 * EPI_WARPS);
             mbar_init(&ctl->drain, 1);
@@ -370,9 +392,11 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 uint8_t *dst = (is_a ? sA : sB) + hh * F4_BOX_BYTES;
                 uint8_t *sf_dst = sSF + (is_a ? 0 : (1 + hh) * TL::SF_BYTES);
                 for (int kb = 0; kb < nk; kb++) {
+                    if (args.lag && is_a && prank) __nanosleep(20000);
                     if (!mbar_wait<true>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status)) goto producer_done;
                     const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), 0);
                     if (prank == 0) mbar_expect_tx(&ctl->full[stage], bytes);
+                    else if (is_a) mbar_arrive_cluster(fb);
                     uint8_t *to = dst + stage * F4_OP_BYTES;
                     if (!is_a || boxes > 0) tma_load_2d_pair(to, op, kb * (F4_BK / 2), row, fb);
                     if (is_a && boxes > 1) tma_load_2d_pair(to + F4_BOX_BYTES / 2, op, kb * (F4_BK / 2), row + 32, fb);
@@ -605,6 +629,7 @@ moe_status launch_fp4(const F4Operand &a, const F4Operand &b, const F4Operand &b
     args.b_global = b.global;
     args.b3_global = b3.global;
     args.stall = take_gemm_stall() ? 1 : 0;
+    args.lag = take_gemm_lag() ? 1 : 0;
     args.wide = args.n_out % 16 == 0 && ((uintptr_t)args.out & 31) == 0;
     const int64_t e = args.e;
     const int64_t nt = fp4_scale_tiles(Fp4<FMT>::BLK, args.K);

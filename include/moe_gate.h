@@ -613,6 +613,15 @@ uint64_t moe_launch_count(void);
  */
 moe_status moe_debug_stall_gemms(int32_t n);
 
+/*
+ * Test hook, not for production use.  In the next n launches of the 4-bit
+ * grouped products in this process (moe_product_fp4, and two per
+ * moe_expert_ffn_fp4) the copies of the second half of every row tile lag by
+ * 20 us a stage: slower, with the same results.  n = 0 cancels what is pending.
+ * Errors: MOE_ERR_INVALID_ARG for n < 0.
+ */
+moe_status moe_debug_lag_gemms(int32_t n);
+
 #ifdef __cplusplus
 }
 #endif
