@@ -373,18 +373,83 @@ __device__ __forceinline__ void store_rows(const float *rows, int64_t n, D *out)
     for (int64_t i = n / N * N + threadIdx.x; i < n; i += RT_THREADS) out[i] = (D)rows[i];
 }
 
+// A logit's bits as loaded, issued here (a plain load may sink to its use), and
+// its value.
+__device__ __forceinline__ uint32_t ld_early(const float *p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_early(const __nv_bfloat16 *p) {
+    uint16_t r;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    return r;
+}
+template <typename T> __device__ __forceinline__ float of_bits(uint32_t w) {
+    return __uint_as_float(sizeof(T) == 2 ? w << 16 : w);
+}
+
+// The larger of two; a NaN stays one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Of a 16-byte chunk's values.
+template <typename T>
+__device__ __forceinline__ float max_of(const V16 &v) {
+    constexpr int N = Elt<T>::VEC;
+    float f[N];
+    Elt<T>::unpack(v, f);
+#pragma unroll
+    for (int n = N / 2; n > 0; n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; i++) f[i] = max_nan(f[i], f[i + n]);
+    return f[0];
+}
+
+// A row's softmax sum in the forward's order (adjacent pairs over the padded
+// width: a pair is added as soon as its second half is complete), by one thread.
+template <typename T>
+__device__ __noinline__ float softmax_sum(const T *row, int e, float top) {
+    float part[11], v = 0.0f;   // part[n]: the open run of 2^n exponentials
+    for (int i = 0; i < e; i++) {
+        v = expf(__fsub_rn(ld_logit(row + i), top));
+        int n = 0;
+        for (; i >> n & 1; n++) v = __fadd_rn(part[n], v);
+        part[n] = v;
+    }
+    bool any = false;
+    for (int n = 0; n < 11; n++) {
+        if (!(e >> n & 1)) continue;
+        v = any ? __fadd_rn(part[n], v) : part[n];
+        any = true;
+    }
+    return v;
+}
+
 // Gradients that live on the selection: with g the selected scores, G = g / sum
 // g and A = sum_r dg_r G_r,
-//   softmax, normalised: scale G (dg - A)         (G needs the selected logits only);
+//   softmax, normalised: scale G (dg - A);
 //   sigmoid, normalised: scale G (dg - A) (1 - g);
 //   sigmoid, raw:        scale dg g (1 - g).
-// Reads k logits a token; bound by the e values written.
+// A softmax's G is formed from the selected logits alone, exp(l - their largest),
+// which is closer than the quotient of two scores.  What the forward's gates do
+// besides comes from the row's largest logit: they are NaN where that is a NaN or
+// +inf, and the constant 0 where all chosen scores round to 0 (from about 97 below
+// it on; settled by the forward's own operations).
+// Bound by the e values written; sigmoid reads k logits a token, softmax all:
+// 16384 x 256 fp32, k = 8: 6.2 us sigmoid, 7.8 softmax (6.4 if the row is not
+// looked at); 65536 x 64 bf16, k = 2: 11.3 (8.8).  Softmax at four CTAs a
+// multiprocessor, 64 registers (five: the same; three: 8.5 and 12.4).
 template <typename T, typename D, bool SOFTMAX>
-__global__ void __launch_bounds__(RT_THREADS)
+__global__ void __launch_bounds__(RT_THREADS, SOFTMAX ? 4 : 1)
 route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ idx,
                      const float *__restrict__ d_gates, int64_t s, int e, int k, float scale,
                      int normalize, D *__restrict__ d_logits, int32_t *status) {
     __shared__ __align__(16) float rows[BWD_FLOATS];
+    __shared__ float row_top[SOFTMAX ? RT_THREADS / BWD_LANES : 1];   // largest logit by token
     pdl_enter();
     const bool stop = status_bad(status);
     const int tb = bwd_tokens(e), sub = threadIdx.x % BWD_LANES, tok = threadIdx.x / BWD_LANES;
@@ -405,6 +470,28 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
             j[q] = have ? idx[(int64_t)r * s + t] : -1;
             dg[q] = have ? d_gates[(int64_t)r * s + t] : 0.0f;
         }
+        // softmax: RT_THREADS / tb lanes (8, 16 or 32) look for a row's largest logit;
+        // the first loads are on their way together with the selection's
+        constexpr int N = Elt<T>::VEC, AHEAD = 4;
+        const int lg = e <= 64 ? 3 : e <= 256 ? 4 : 5, lanes = 1 << lg;   // bwd_tokens(e) * lanes = RT_THREADS
+        const int rl = threadIdx.x & (lanes - 1), rtok = threadIdx.x >> lg;
+        const T *row = logits + (t0 + min(rtok, nt - 1)) * e;
+        const bool chunks = e % N == 0;
+        V16 ahead[SOFTMAX ? AHEAD : 1];
+        if (SOFTMAX && chunks) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++) {
+                const int c = (rl + i * lanes) * N;
+                if (c < e) ahead[i] = ld_stream(row + c);
+            }
+        } else if (SOFTMAX) {   // single values
+#pragma unroll
+            for (int i = 0; i < 2 * AHEAD; i++) {
+                const int c = rl + i * lanes;
+                ahead[i / 4].w[i % 4] = sizeof(T) == 2 ? 0xFF80u : 0xFF800000u;   // -inf
+                if (c < e) ahead[i / 4].w[i % 4] = ld_early(row + c);
+            }
+        }
         float4 *z = reinterpret_cast<float4 *>(rows);   // zeros while those loads are on their way
         for (int i = threadIdx.x; i < (nt * e + 3) / 4; i += RT_THREADS) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -417,6 +504,21 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
         if (bad) set_status(status, MOE_ERR_INVALID_ARG);
         float total = 0.0f;
         if (SOFTMAX) {
+            float m = -INFINITY;
+            if (chunks) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; i++)
+                    if ((rl + i * lanes) * N < e) m = max_nan(m, max_of<T>(ahead[i]));
+#pragma unroll 1
+                for (int c = (rl + AHEAD * lanes) * N; c < e; c += lanes * N) m = max_nan(m, max_of<T>(ld_stream(row + c)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * AHEAD; i++) m = max_nan(m, of_bits<T>(ahead[i / 4].w[i % 4]));
+#pragma unroll 4
+                for (int c = rl + 2 * AHEAD * lanes; c < e; c += lanes) m = max_nan(m, ld_logit(row + c));
+            }
+            for (int o = lanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (rl == 0) row_top[rtok] = m;
 #pragma unroll
             for (int o = BWD_LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
@@ -445,12 +547,19 @@ route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ i
         // the rows are zero; another CTA's error may have come up meanwhile, so the
         // threads leave together
         if (__syncthreads_or(stop)) return;
+        float f = scale;   // NaN or 0: as the gates are
+        if (SOFTMAX && on) {
+            const float rt = row_top[tok];
+            if (!(rt < INFINITY)) f = NAN;
+            else if (top - rt < -96.0f && __fdiv_rn(expf(__fsub_rn(top, rt)), softmax_sum(logits + t * e, e, rt)) == 0.0f)
+                f = 0.0f;
+        }
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             if (q * BWD_LANES >= k) break;
             if (j[q] < 0) continue;
             float d;
-            if (normalize) d = scale * G[q] * (dg[q] - A);
+            if (normalize) d = f * G[q] * (dg[q] - A);
             else d = scale * dg[q] * g[q];
             if (!SOFTMAX) d *= 1.0f - g[q];
             rows[tok * e + j[q]] = d;

@@ -421,7 +421,12 @@ moe_status moe_route_topk(const void *logits, moe_dtype ldt, const float *bias, 
  *   softmax, raw:  scale p_j (d_gates_j [selected] - sum_r d_gates[r] p_idx[r]);
  *   sigmoid, normalised: scale G (d_gates - A) (1 - g) at the selection, else 0;
  *   sigmoid, raw:  scale d_gates g (1 - g) at the selection, else 0.
- * Rows without a live expert get 0.  logits [s, e] in `ldt` as given to the
+ * The gradient goes with the gates: it is 0 where they are the constant 0 (rows
+ * without a live expert; renormalised gates whose chosen scores all round to 0),
+ * and NaN at the selection where a NaN or +inf in the row makes softmax gates
+ * NaN.  (Elsewhere a renormalised softmax's G is formed from the chosen logits
+ * and their largest, with less rounding than a quotient of scores.)
+ * logits [s, e] in `ldt` as given to the
  * forward; idx, d_gates [k, s]; d_logits [s, e] in `ddt`, every element
  * written, sums in fp32, one rounding.  An idx outside [0, e) stores
  * MOE_ERR_INVALID_ARG in dev_status.
