@@ -64,7 +64,7 @@ __device__ __forceinline__ Fp4Factor fp4_factor(float g) {
 }
 
 // Scale byte of a block with largest magnitude amax, and what its values are
-// multiplied by (1 / scale; 0 where the scale is 0).
+// multiplied by (1 / scale; 0 where that is not finite).
 template <int FMT>
 __device__ __forceinline__ uint32_t fp4_scale(float amax, const Fp4Factor &f, float &inv) {
     if (FMT == MOE_FP4_NV && f.y6 != 0.0f && amax <= 0x1p60f && (amax >= 0x1p-60f || amax == 0.0f)) {
@@ -84,8 +84,8 @@ __device__ __forceinline__ uint32_t fp4_scale(float amax, const Fp4Factor &f, fl
         return (uint32_t)sc;
     }
     const uint32_t s8 = e4m3_of(__fdiv_rn(amax, f.g6));
-    const float s = __fmul_rn(e4m3_value(s8), f.g);
-    inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    const float y = __frcp_rn(__fmul_rn(e4m3_value(s8), f.g));
+    inv = y > 0.0f && y < INFINITY ? y : 0.0f;   // a scale of 0, or below 2^-128: zeros
     return s8;
 }
 

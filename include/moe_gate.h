@@ -442,8 +442,8 @@ moe_status moe_route_bwd(const void *logits, moe_dtype ldt, const int32_t *idx,
  *   MX: scale = 2^(floor(log2 amax) - 2), at least 2^-127, stored as e8m0
  *       (exponent + 127); 1 for a block of zeros;
  *   NV: scale = s8 * g with g the batch's factor (`global_scale`, NULL: 1) and
- *       s8 = e4m3(min(amax / (6 g), 448)), nearest-even; where s8 is 0 the
- *       codes are 0;
+ *       s8 = e4m3(min(amax / (6 g), 448)), nearest-even; where s8 is 0, or s8 * g
+ *       so small that its reciprocal overflows (2^-128), the codes are 0;
  *   code = e2m1(x * (1 / scale)), nearest-even, saturating at +-6, 1 / scale
  *       rounded to fp32 (exact for MX).
  * A block that holds an infinity or a NaN gets the NaN scale (0xFF / 0x7F).

@@ -1,14 +1,66 @@
 """The 4-bit operands at the ends of their ranges."""
 
+import numpy as np
 import pytest
 import torch
 
 import combine_moe_gate_gb300 as M
 
-from test_gpu_fp4 import data, quant
+from test_gpu_fp4 import data, dequant, quant, quantize64, unpack, untile
 from test_gpu_fp4_tiles import check_hidden, ffn, untiled, values
 
 pytestmark = pytest.mark.gpu
+
+
+# Both sides of the ranges in which the quantiser takes the short forms of the
+# division (6 g within 2^-40 .. 2^40, block maxima within 2^-60 .. 2^60).
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lg", [-100, -60, -50, -43, -42, -41, -20, 0, 20, 37, 38, 50, 60, 100])
+def test_factors_over_their_range_are_bit_exact(lg, dt):
+    g = torch.tensor([1.37 * 2.0 ** lg, 2.0 ** lg], dtype=torch.float32, device="cuda")
+    x = data((2, 40, 512), 91 + lg, torch.float32)
+    # rows from far below the smallest scale to beyond the largest
+    x *= torch.exp2(torch.linspace(-14, 12, 40, device="cuda"))[None, :, None] * 2.0 ** min(lg, 100)
+    x = x.clamp(-3e38, 3e38).to(dt)
+    q, sc = quant(x, "nv", g)
+    back = dequant(q, sc, "nv", g=g).cpu().numpy()
+    for j in range(2):
+        qo, so, vo = quantize64(x[j].float().cpu().numpy(), "nv", g[j].item())
+        assert np.array_equal(untile(sc[j].cpu().numpy(), 40, 32), so)
+        assert np.array_equal(unpack(q[j].cpu().numpy()), qo)
+        assert np.array_equal(back[j], vo)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 60, 2.0 ** -60])
+def test_block_maxima_at_the_switch_are_bit_exact(scale):
+    x = data((1, 64, 512), 97, torch.float32)
+    x = x / x.abs().amax(2, keepdim=True) * torch.linspace(0.98, 1.02, 64, device="cuda")[None, :, None] * scale
+    for lg in (20, 30, 39, -25, -39):
+        g = torch.tensor([2.0 ** lg * 1.1], device="cuda")
+        q, sc = quant(x, "nv", g)
+        qo, so, _ = quantize64(x[0].cpu().numpy(), "nv", g[0].item())
+        assert np.array_equal(untile(sc[0].cpu().numpy(), 64, 32), so)
+        assert np.array_equal(unpack(q[0].cpu().numpy()), qo)
+
+
+def test_scales_without_a_reciprocal_give_zeros():
+    """A factor so small that 1 / (s8 g) overflows fp32: the codes are 0, those of
+    zeros too; the first factors whose scales have a reciprocal are exact."""
+    for lg, tiny in ((-124, False), (-126, False), (-132, True), (-140, True), (-149, True)):
+        g = torch.tensor([2.0 ** lg], dtype=torch.float32, device="cuda")
+        x = torch.zeros((1, 3, 64), device="cuda")
+        # blocks with s8 = 1 (the largest is 6 g), and one with zeros between
+        x[0, 0] = 6.0 * 2.0 ** lg * torch.tensor([1.0, -1.0, 0.5, 0.0], dtype=torch.float64).repeat(16).float().cuda()
+        x[0, 1, ::16] = 6.0 * 2.0 ** lg
+        q, sc = quant(x, "nv", g)
+        codes, tiles = unpack(q[0].cpu().numpy()), untile(sc[0].cpu().numpy(), 3, 4)
+        assert (tiles[:2] == 0x38).all() and (tiles[2] == 0).all()
+        if tiny:
+            assert (codes & 7 == 0).all()
+            assert (dequant(q, sc, "nv", g=g) == 0).all()
+        else:
+            qo, _, _ = quantize64(x[0].cpu().numpy(), "nv", g[0].item())
+            assert np.array_equal(codes, qo)
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
