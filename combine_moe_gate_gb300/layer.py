@@ -94,12 +94,13 @@ class Fp4Operand:
 
 def quantize_weights_fp4(w, fmt) -> Fp4Operand:
     """4-bit form of expert weights [e, rows, cols] (bf16 or fp32), made once.
-    "nv": each expert's factor is its largest magnitude / (6 * 448), so that the
-    largest block scale is the largest e4m3 number."""
+    "nv": each expert's factor is its largest finite magnitude / (6 * 448), so
+    that the largest block scale is the largest e4m3 number (an infinity or a NaN
+    makes its own block NaN and has no part in the factor)."""
     e, rows, cols = w.shape
     g = None
     if fmt == "nv":
-        g = w.abs().amax((1, 2)).float() / (6.0 * 448.0)
+        g = w.abs().nan_to_num_(nan=0.0, posinf=0.0).amax((1, 2)).float() / (6.0 * 448.0)
         g = torch.where(g > 0, g, torch.ones_like(g))
     q = torch.empty((e, rows, cols // 2), dtype=torch.uint8, device=w.device)
     scale = torch.empty((e, moe_fp4_scale_bytes(fmt, rows, cols)), dtype=torch.uint8, device=w.device)

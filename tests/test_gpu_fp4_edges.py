@@ -63,6 +63,25 @@ def test_scales_without_a_reciprocal_give_zeros():
             assert np.array_equal(codes, qo)
 
 
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_bad_weight_spoils_its_own_block_only(bad):
+    w = data((3, 40, 128), 95) * 0.02
+    clean = M.quantize_weights_fp4(w, "nv")
+    w[1, 7, 33] = bad
+    op = M.quantize_weights_fp4(w, "nv")
+    torch.cuda.synchronize()
+    # expert 1's factor is still that of its finite values
+    finite = torch.where(torch.isfinite(w), w, torch.zeros_like(w)).float().abs().amax((1, 2)) / (6.0 * 448.0)
+    assert torch.equal(op.global_scale, finite)
+    v, ref = (dequant(o.q, o.scale, "nv", g=o.global_scale) for o in (op, clean))
+    assert bool(torch.isnan(v[1, 7, 32:48]).all())
+    v[1, 7, 32:48] = ref[1, 7, 32:48]
+    assert bool(torch.isfinite(v).all()) and torch.equal(v[0], ref[0]) and torch.equal(v[2], ref[2])
+    w[1, 7, 33] = 0
+    # (block errors: half an e2m1 step of 6 with a scale within 2^-4, and the e4m3 scale's own)
+    assert bool(((v - w.float()).abs() <= 0.2 * w.float().abs().amax((1, 2), keepdim=True)).all())
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_gelu_over_its_range(fmt):
     """Hidden values of prescribed pre-activations, in blocks of like magnitude (a
