@@ -171,11 +171,17 @@ def _dt(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+# The current stream's handle by device index.  Not one of torch's documented
+# calls, so it may be missing; the documented way makes a Stream object first (2.9
+# us against 0.3, of a small call's 7).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     """The stream's handle; None: torch's current stream of the current device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _check(code, where):
