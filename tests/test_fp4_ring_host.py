@@ -1,6 +1,6 @@
-"""The operand ring of the 4-bit products, as a model on the host: the barriers,
-the producers and the MMA issuer of a CTA pair under schedules that hold one of
-them back.  A wait for a phase's parity is only sound while the waiter is at most
+"""The operand ring and the two overlapping accumulators of the 4-bit products, as
+a model on the host: the barriers, the producers, the MMA issuer and the epilogue
+warps of a CTA pair under schedules that hold one of them back.  A wait for a phase's parity is only sound while the waiter is at most
 one phase behind, so every producer has to be needed for every phase, also where
 it has nothing to copy (a row tile that ends in the first CTA)."""
 
@@ -50,6 +50,8 @@ def run_ring(rows, stages, nk, arrivals, first, rng):
     priority (the others at random).  Whether all of them finish, with every
     stage read holding the copies meant for it."""
     full = [Barrier(arrivals) for _ in range(stages)]
+    tfull, tempty = [Barrier(1), Barrier(1)], Barrier(4)   # one epilogue warp per CTA and column half
+    columns = {}     # 32-column chunk of TMEM -> the tile whose sums it holds
     empty = [[Barrier(1) for _ in range(stages)] for _ in range(2)]
     slots = {}       # (stage, cta, producer) -> the use its content belongs to
     copies = []      # in flight
@@ -77,7 +79,10 @@ def run_ring(rows, stages, nk, arrivals, first, rng):
 
     def issuer():
         use = 0
-        for r in rows:
+        for t, r in enumerate(rows):
+            while t and not tempty.passed(t - 1 & 1):
+                yield False
+            columns.update({(t & 1) * 6 + c: t for c in range(8)})
             for _ in range(nk):
                 s, ph = use % stages, use // stages & 1
                 while not full[s].passed(ph):
@@ -90,9 +95,24 @@ def run_ring(rows, stages, nk, arrivals, first, rng):
                     empty[cta][s].arrive()
                 use += 1
                 yield True
+            for cta in (0, 1):
+                tfull[cta].arrive()
+            yield True
+
+    def epilogue(cta, half):
+        for t in range(len(rows)):
+            while not tfull[cta].passed(t & 1):
+                yield False
+            first = half if t & 1 else 6 + half   # in the columns that the next tile shares
+            for i in range(4):
+                assert columns[(t & 1) * 6 + (first + 2 * i & 7)] == t, "an accumulator overwritten before it was read"
+                if i == 0:
+                    tempty.arrive()
+                yield True
 
     actors = {("p", c, i): producer(c, i) for c in (0, 1) for i in range(4)}
     actors["mma"] = issuer()
+    actors.update({("e", c, h): epilogue(c, h) for c in (0, 1) for h in (0, 1)})
     while actors:
         if copies and rng.random() < 0.5:
             s, cta, prod, use, n = copies.pop(rng.randrange(len(copies)))
@@ -114,7 +134,7 @@ def run_ring(rows, stages, nk, arrivals, first, rng):
     return True
 
 
-ALL = [("p", c, i) for c in (0, 1) for i in range(4)] + ["mma"]
+ALL = [("p", c, i) for c in (0, 1) for i in range(4)] + ["mma"] + [("e", c, h) for c in (0, 1) for h in (0, 1)]
 
 
 @pytest.mark.parametrize("stages", [5, 6])
