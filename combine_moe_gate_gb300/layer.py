@@ -159,7 +159,9 @@ def run_layer_fp4(x, logits, bias, w1: Fp4Operand, b1, w3: Optional[Fp4Operand],
     projection of x; moe_route_topk's options) and 4-bit experts (weights from
     quantize_weights_fp4; "nv": buf_global and hid_global [e], the calibrated
     factors of the layer's input and hidden).  Returns bufs.y, with no host
-    synchronisation."""
+    synchronisation.  A route to a masked expert (gate 0) takes a slot like any
+    other: with a capacity_factor other than 0, tokens that have no expert (padding)
+    are better left out of x and logits than masked."""
     B = bufs
     e = logits.shape[1]
     w3 = w3 or Fp4Operand(None, None, None)

@@ -395,7 +395,8 @@ moe_status moe_expert_ffn_fp8(const void *buf_q, const float *buf_scale, const i
  *   idx[r, t]: the r-th expert of the groups that stay by (choice descending,
  *     index ascending);
  *   gates[r, t] = score[idx[r, t]], with MOE_FLAG_NORMALIZE_GATES divided by
- *     the sum of the k of them in route order, then times `scale`.
+ *     the sum of the k of them in route order (0 where that is 0), then times
+ *     `scale`.
  * The bias steers the choice and is not part of the gates, so that a balance
  * update of it changes which experts run and not what they weigh.
  * A logit of -inf masks its expert: score 0, chosen only where fewer than k
@@ -403,7 +404,11 @@ moe_status moe_expert_ffn_fp8(const void *buf_q, const float *buf_scale, const i
  * (a group with none left ranks last).  A row of -inf alone gets the gates 0.
  * A NaN choice ranks like a masked expert; a NaN score passes into its gate
  * (softmax: a NaN or +inf logit makes every score of the row NaN).
- * logits [s, e] in `ldt` (no alignment beyond the element's: e may be odd);
+ * A route to a masked expert is a route like any other: moe_capacity_locations
+ * gives it a slot (a row of -inf alone: of experts 0 .. k-1), so that with a
+ * capacity it can push out a token that weighs something.
+ * logits [s, e] in `ldt` (16-byte aligned as a whole; its rows need not be: e may
+ * be odd);
  * bias [e] fp32 or NULL; idx [k, s] int32 and gates [k, s] fp32 are written.
  * e <= 1024; e a multiple of groups, groups <= 32, 1 <= topk_groups <= groups,
  * k <= topk_groups * (e / groups).
@@ -427,9 +432,10 @@ moe_status moe_route_topk(const void *logits, moe_dtype ldt, const float *bias, 
  * NaN.  (Elsewhere a renormalised softmax's G is formed from the chosen logits
  * and their largest, with less rounding than a quotient of scores.)
  * logits [s, e] in `ldt` as given to the
- * forward; idx, d_gates [k, s]; d_logits [s, e] in `ddt`, every element
- * written, sums in fp32, one rounding.  An idx outside [0, e) stores
- * MOE_ERR_INVALID_ARG in dev_status.
+ * forward; idx, d_gates [k, s], a token's k experts distinct (as the forward
+ * chooses them; of a repeated one some single route's gradient is stored);
+ * d_logits [s, e] in `ddt`, every element written, sums in fp32, one rounding.
+ * An idx outside [0, e) stores MOE_ERR_INVALID_ARG in dev_status.
  */
 moe_status moe_route_bwd(const void *logits, moe_dtype ldt, const int32_t *idx,
                          const float *d_gates, int64_t s, int e, int k, moe_score score,

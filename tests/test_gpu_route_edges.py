@@ -75,3 +75,39 @@ def test_gradient_shows_a_nan_that_the_gates_show(bad, e, k):
     chosen = torch.zeros((s, e), dtype=torch.bool).scatter_(1, idx.t().long().cpu(), True)
     assert torch.equal(torch.isnan(d).cpu(), chosen & rows[:, None])
     assert bool((d.cpu()[~chosen] == 0).all())
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_logits_are_aligned_as_a_whole_only(dt):
+    """Rows of an odd width are no multiple of 16 bytes; the tensor has to start on 16."""
+    s, e, k = 9, 33, 2
+    x = torch.randn((s + 1, e), generator=torch.Generator().manual_seed(1)).to(dt).cuda()
+    dg = torch.ones((k, s), device="cuda")
+    idx, gates, d = forward_then_backward(x[:s], None, k, dg)
+    again = forward_then_backward(x[1:].clone(), None, k, dg)   # the same rows, one later
+    assert torch.equal(idx[:, 1:], again[0][:, :-1]) and torch.equal(gates[:, 1:], again[1][:, :-1])
+    assert torch.equal(d[1:], again[2][:-1])
+    before = M.launch_count()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(M.MoEError):
+        M.moe_route_topk(x[1:], None, k, idx, gates, st)
+    with pytest.raises(M.MoEError):
+        M.moe_route_bwd(x[1:], idx, dg, d, st)
+    assert M.launch_count() == before
+
+
+def test_routes_to_masked_experts_take_slots():
+    s, e, k = 40, 8, 2
+    x = torch.randn((s, e), generator=torch.Generator().manual_seed(2)).cuda()
+    x[5:25] = -float("inf")
+    idx, gates, _ = forward_then_backward(x, None, k, torch.ones((k, s), device="cuda"))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(M.moe_capacity_workspace_size(s, e, k), dtype=torch.uint8, device="cuda")
+    loc, counts = torch.empty_like(idx), torch.empty(e, dtype=torch.int32, device="cuda")
+    c_dev = torch.empty(1, dtype=torch.int32, device="cuda")
+    M.moe_capacity_locations(idx, e, 0.0, s, ws, loc, counts, c_dev, st)
+    torch.cuda.synchronize()
+    status_ok(st)
+    assert bool((gates[:, 5:25] == 0).all())
+    assert torch.equal(counts.long(), idx.long().view(-1).bincount(minlength=e))
+    assert int(counts[0]) >= 20 and int(counts[1]) >= 20
