@@ -441,10 +441,11 @@ __device__ __noinline__ float softmax_sum(const T *row, int e, float top) {
 // it on; settled by the forward's own operations).
 // Bound by the e values written; sigmoid reads k logits a token, softmax all:
 // 16384 x 256 fp32, k = 8: 6.2 us sigmoid, 7.8 softmax (6.4 if the row is not
-// looked at); 65536 x 64 bf16, k = 2: 11.3 (8.8).  Softmax at four CTAs a
-// multiprocessor, 64 registers (five: the same; three: 8.5 and 12.4).
+// looked at); 65536 x 64 bf16, k = 2: 11.3 (8.6 sigmoid).  CTAs a multiprocessor:
+// softmax four, 64 registers (five: 8.0, three: 8.5); sigmoid five, 48 registers
+// (four: 6.6).
 template <typename T, typename D, bool SOFTMAX>
-__global__ void __launch_bounds__(RT_THREADS, SOFTMAX ? 4 : 1)
+__global__ void __launch_bounds__(RT_THREADS, SOFTMAX ? 4 : 5)
 route_bwd_sel_kernel(const T *__restrict__ logits, const int32_t *__restrict__ idx,
                      const float *__restrict__ d_gates, int64_t s, int e, int k, float scale,
                      int normalize, D *__restrict__ d_logits, int32_t *status) {
