@@ -30,8 +30,8 @@
 // may or may not have been the cause, and it is not used.)
 //
 // What bounds it: a stage fills 38 KB of shared memory per SM (NV; MX 35) and
-// its MMAs read 32, against 128 bytes a clock; 8192^3 runs at 7.3 PFLOP/s (MX
-// 7.6), 4096 x 4096 x 8192 (7 tiles a pair) at 5.8 to 6.1.  With few rows an
+// its MMAs read 32, against 128 bytes a clock; 8192^3 runs at 6.5 to 7.3 PFLOP/s
+// (MX 7.1 to 7.6, by the power cap), 4096 x 4096 x 8192 (7 tiles a pair) at 5.8 to 6.1.  With few rows an
 // expert it is the weights' bytes: 6.3 TB/s at K = 7168, 5.9 at K = 2048.
 #pragma once
 

@@ -18,9 +18,9 @@
 // about 20 per expert), so its layout is chosen to spend few of them: L lanes
 // share a token and hold V = width / L consecutive experts each, with V = 8
 // where the width allows, so that 32 / L tokens run in one warp.  Measured: 16384
-// x 256 sigmoid, 8 groups, top 8: 14.6 us (17.9 MB; 73% of the issue slots);
-// 65536 x 64 softmax, top 2: 11.9 us; one token: 2.7 us.  The gradient of 16384
-// x 256: 6.8 us.
+// x 256 sigmoid, 8 groups, top 8: 14.9 us (17.9 MB; 73% of the issue slots);
+// 65536 x 64 softmax, top 2: 12.2 us; one token: 2.9 us.  The gradient of 16384
+// x 256: 6.2 us, renormalised softmax 7.8.
 #include "exact.cuh"
 
 namespace moe {
