@@ -10,7 +10,9 @@ Functions keep the C names:
     moe_encode, moe_expert_ffn,
     moe_decode, moe_decode_bwd, moe_encode_bwd, moe_layer_forward, moe_gate_bwd,
     moe_route_topk, moe_route_bwd,
-    moe_quantize_fp4, moe_dequantize_fp4, moe_product_fp4, moe_expert_ffn_fp4
+    moe_quantize_fp4, moe_dequantize_fp4, moe_product_fp4, moe_expert_ffn_fp4,
+    moe_sort_routes, moe_encode_sorted, moe_encode_sorted_bwd, moe_decode_sorted,
+    moe_decode_sorted_bwd, moe_expert_ffn_sorted, moe_expert_ffn_sorted_bwd
 plus the size queries and `MoEError`.
 """
 
@@ -91,6 +93,16 @@ def load():
         "moe_expert_ffn_fp4_workspace_size": (SZ, [I, I, I, I64, I, I]),
         "moe_expert_ffn_fp4": (I, [P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, I, I, I, I64, I,
                                    I, P, SZ, P, P, P]),
+        "moe_sort_workspace_size": (SZ, [I64, I, I]),
+        "moe_sort_routes": (I, [P, I64, I, I, P, P, P, P, SZ, P, P]),
+        "moe_encode_sorted": (I, [P, I, P, P, I64, I, I, I64, P, P, P]),
+        "moe_encode_sorted_bwd": (I, [P, P, I, P, P, I64, I, I, I64, P, P, P, P]),
+        "moe_decode_sorted": (I, [P, I, P, P, I64, I, I, I64, P, P, P]),
+        "moe_decode_sorted_bwd": (I, [P, P, I, P, P, I64, I, I, I64, P, P, P, P]),
+        "moe_expert_ffn_sorted": (I, [P, I, P, P, P, P, P, P, I, I, I64, I, I, P, P, P, P, P]),
+        "moe_expert_ffn_sorted_bwd_workspace_size": (SZ, [I, I, I64, I, I]),
+        "moe_expert_ffn_sorted_bwd": (I, [P, P, P, I, P, P, P, P, I, I, I64, I, I, P, P, SZ, P, I, P, P, P,
+                                          P, P, P, P]),
         "moe_status_str": (ctypes.c_char_p, [I]),
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_debug_stall_gemms": (I, [I]),
@@ -374,6 +386,104 @@ def moe_route_bwd(logits, idx, d_gates, d_logits, dev_status, score="softmax", s
         _ptr(d_gates, "d_gates", F, (k, s)), s, e, k, _code(SCORE, score, "score"), float(scale),
         int(flags), _ptr(d_logits, "d_logits", None, (s, e)), _dt(d_logits),
         _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_route_bwd")
+
+
+# --------------------------------------------------- rows sorted by expert
+def moe_sort_workspace_size(s, e, k) -> int:
+    return int(load().moe_sort_workspace_size(int(s), int(e), int(k)))
+
+
+def moe_sort_routes(idx, e, rows, offsets, workspace, dev_status, source=None, stream=None):
+    """idx [k, s] int32 (-1: no expert) -> rows [k, s] (each route's row among
+    the rows sorted by expert, -1: none), offsets [e + 1] and, when given,
+    source [k * s] (each row's route r * s + t), all int32."""
+    k, s = idx.shape
+    e, I = int(e), _i32()
+    _check(load().moe_sort_routes(
+        _ptr(idx, "idx", I), s, e, k, _ptr(rows, "rows", I, (k, s)), _ptr(offsets, "offsets", I, (e + 1,)),
+        _ptr(source, "source", I, (k * s,)), _ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status, "dev_status", I), _stream(stream)),
+        "moe_sort_routes")
+
+
+def moe_encode_sorted(x, rows, out, dev_status, gates=None, stream=None):
+    """The tokens x [s, m] into their rows of out [n, m], times gates [k, s] when given."""
+    k, s = rows.shape
+    n, m = out.shape
+    I, dt = _i32(), x.dtype
+    _check(load().moe_encode_sorted(
+        _ptr(x, "x", None, (s, m)), _dt(x), _ptr(rows, "rows", I), _ptr(gates, "gates", _f32(), (k, s)), s, m, k, n,
+        _ptr(out, "out", dt), _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_encode_sorted")
+
+
+def moe_encode_sorted_bwd(d_out, rows, d_x, dev_status, x=None, gates=None, d_gates=None, stream=None):
+    """Gradient of moe_encode_sorted: d_x [s, m] from d_out [n, m] and, with x and
+    gates, d_gates [k, s] fp32 when given."""
+    k, s = rows.shape
+    n, m = d_out.shape
+    I, F, dt = _i32(), _f32(), d_out.dtype
+    _check(load().moe_encode_sorted_bwd(
+        _ptr(d_out, "d_out"), _ptr(x, "x", dt, (s, m)), _dt(d_out), _ptr(rows, "rows", I),
+        _ptr(gates, "gates", F, (k, s)), s, m, k, n, _ptr(d_x, "d_x", dt, (s, m)),
+        _ptr(d_gates, "d_gates", F, (k, s)), _ptr(dev_status, "dev_status", I), _stream(stream)),
+        "moe_encode_sorted_bwd")
+
+
+def moe_decode_sorted(xs, rows, y, dev_status, gates=None, stream=None):
+    """y [s, m]: the sum over each token's rows of xs [n, m], times gates [k, s] when given."""
+    k, s = rows.shape
+    n, m = xs.shape
+    I = _i32()
+    _check(load().moe_decode_sorted(
+        _ptr(xs, "xs"), _dt(xs), _ptr(rows, "rows", I), _ptr(gates, "gates", _f32(), (k, s)), s, m, k, n,
+        _ptr(y, "y", xs.dtype, (s, m)), _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_decode_sorted")
+
+
+def moe_decode_sorted_bwd(dy, xs, rows, gates, d_xs, d_gates, dev_status, stream=None):
+    """Gradient of moe_decode_sorted with gates: d_xs [n, m] and d_gates [k, s] fp32."""
+    k, s = rows.shape
+    n, m = xs.shape
+    I, F, dt = _i32(), _f32(), xs.dtype
+    _check(load().moe_decode_sorted_bwd(
+        _ptr(dy, "dy", dt, (s, m)), _ptr(xs, "xs"), _dt(xs), _ptr(rows, "rows", I), _ptr(gates, "gates", F, (k, s)),
+        s, m, k, n, _ptr(d_xs, "d_xs", dt, (n, m)), _ptr(d_gates, "d_gates", F, (k, s)),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_decode_sorted_bwd")
+
+
+def moe_expert_ffn_sorted(x, offsets, w1, b1, w3, w2, b2, act, hid, out, dev_status, pre=None, stream=None):
+    """The expert FFN on sorted rows x [n, m] (bf16): hid [n, h], out [n, m] and,
+    for training, pre [n, h] (SwiGLU: [n, 2h], a then b)."""
+    n, m = x.shape
+    e, h, _ = w1.shape
+    I, dt, act = _i32(), x.dtype, _act(act)
+    hp = 2 * h if act == ACT["swiglu"] else h
+    _check(load().moe_expert_ffn_sorted(
+        _ptr(x, "x"), _dt(x), _ptr(offsets, "offsets", I, (e + 1,)), _ptr(w1, "w1", dt, (e, h, m)),
+        _ptr(b1, "b1", dt, (e, h)), _ptr(w3, "w3", dt, (e, h, m)), _ptr(w2, "w2", dt, (e, m, h)),
+        _ptr(b2, "b2", dt, (e, m)), act, e, n, m, h, _ptr(hid, "hid", dt, (n, h)), _ptr(pre, "pre", dt, (n, hp)),
+        _ptr(out, "out", dt, (n, m)), _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_expert_ffn_sorted")
+
+
+def moe_expert_ffn_sorted_bwd_workspace_size(act, e, n, m, h) -> int:
+    return int(load().moe_expert_ffn_sorted_bwd_workspace_size(_act(act), int(e), int(n), int(m), int(h)))
+
+
+def moe_expert_ffn_sorted_bwd(x, hid, pre, offsets, w1, w3, w2, act, d_out, workspace, d_x, d_w1, d_w3, d_w2, d_b1,
+                              d_b2, dev_status, stream=None):
+    """Gradient of moe_expert_ffn_sorted from what it kept; the weight and bias
+    gradients all bf16 or all fp32; w3 / d_w3 for SwiGLU only."""
+    n, m = x.shape
+    e, h, _ = w1.shape
+    I, dt, gdt, act = _i32(), x.dtype, d_w1.dtype, _act(act)
+    hp = 2 * h if act == ACT["swiglu"] else h
+    _check(load().moe_expert_ffn_sorted_bwd(
+        _ptr(x, "x"), _ptr(hid, "hid", dt, (n, h)), _ptr(pre, "pre", dt, (n, hp)), _dt(x),
+        _ptr(offsets, "offsets", I, (e + 1,)), _ptr(w1, "w1", dt, (e, h, m)), _ptr(w3, "w3", dt, (e, h, m)),
+        _ptr(w2, "w2", dt, (e, m, h)), act, e, n, m, h, _ptr(d_out, "d_out", dt, (n, m)),
+        _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), _ptr(d_x, "d_x", dt, (n, m)),
+        _dt(d_w1), _ptr(d_w1, "d_w1", gdt, (e, h, m)), _ptr(d_w3, "d_w3", gdt, (e, h, m)),
+        _ptr(d_w2, "d_w2", gdt, (e, m, h)), _ptr(d_b1, "d_b1", gdt, (e, h)), _ptr(d_b2, "d_b2", gdt, (e, m)),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_expert_ffn_sorted_bwd")
 
 
 # ------------------------------------------------- microscaled 4-bit operands

@@ -54,7 +54,7 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
                          const void *w1, const void *b1, const void *w3, const void *w2,
                          const void *b2, moe_act act, int e, int64_t c_max, int m, int h,
                          void *hid, void *out, int32_t *st, cudaStream_t stream, int row_lo,
-                         int row_hi, void *pre = nullptr);
+                         int row_hi, void *pre = nullptr, SortedRows so = {});
 size_t ffn_tc_bwd_workspace_bytes(moe_act act, int e, int64_t c_max, int m, int h);
 moe_status quantize_rows_fp8_launch(const void *src, int64_t batches, int64_t rows_per_batch,
                                     int cols, const int32_t *counts, const int32_t *c_dev,
@@ -99,7 +99,22 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
                              const void *w2, moe_act act, int e, int64_t c_max, int m, int h,
                              const void *d_out, void *ws, void *d_buf, void *d_w1, void *d_w3,
                              void *d_w2, void *d_b1, void *d_b2, int32_t *st, cudaStream_t stream,
-                             const void *pre = nullptr, bool wgrad_f32 = false);
+                             const void *pre = nullptr, bool wgrad_f32 = false,
+                             SortedRows so = {});
+size_t ffn_tc_sorted_bwd_workspace_bytes(moe_act act, int e, int64_t n, int m, int h);
+size_t sort_workspace_bytes(int64_t s, int e, int k);
+moe_status sort_routes_launch(const int32_t *idx, int64_t s, int e, int k, int32_t *rows, int32_t *offsets,
+                              int32_t *source, void *ws, int32_t *st, cudaStream_t stream);
+moe_status encode_sorted_launch(const void *x, moe_dtype dt, const int32_t *rows, const float *gates, int64_t s, int m,
+                                int k, int64_t n, void *out, int32_t *st, cudaStream_t stream);
+moe_status decode_sorted_launch(const void *xs, moe_dtype dt, const int32_t *rows, const float *gates, int64_t s,
+                                int m, int k, int64_t n, void *y, int32_t *st, cudaStream_t stream);
+moe_status decode_sorted_bwd_launch(const void *dy, const void *xs, moe_dtype dt, const int32_t *rows,
+                                    const float *gates, int64_t s, int m, int k, int64_t n, void *d_xs,
+                                    float *d_gates, int32_t *st, cudaStream_t stream);
+moe_status encode_sorted_bwd_launch(const void *d_out, const void *x, moe_dtype dt, const int32_t *rows,
+                                    const float *gates, int64_t s, int m, int k, int64_t n, void *d_x,
+                                    float *d_gates, int32_t *st, cudaStream_t stream);
 moe_status ffn_simt_launch(const void *buf, moe_dtype dt, const int32_t *counts,
                            const int32_t *c_dev, const void *w1, const void *b1, const void *w3,
                            const void *w2, const void *b2, moe_act act, int e, int64_t c_max,
@@ -384,6 +399,113 @@ moe_status moe_expert_ffn_bwd_saved(const void *buf, const void *hid, const void
     return expert_ffn_bwd(buf, hid, pre, dt, counts, c_dev, w1, nullptr, w3, w2, act, e, c_max, m, h,
                           d_out, workspace, workspace_bytes, d_buf, wgrad_dt, d_w1, d_w3, d_w2, d_b1,
                           d_b2, dev_status, stream);
+}
+
+// ------------------------------------------------- rows sorted by expert
+namespace {
+
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1024;
+
+bool sort_shape_ok(int64_t s, int e, int k) {
+    return s >= 1 && e >= 1 && e <= kMaxE && k >= 1 && k <= kMaxK && s <= kMaxRows / k;
+}
+
+bool move_ok(const void *read, const void *written, moe_dtype dt, const int32_t *rows, int64_t s, int m,
+             int k, int64_t n, const int32_t *dev_status) {
+    return s >= 1 && k >= 1 && k <= kMaxK && s <= kMaxRows / k && rows_ok(dt, m) && n >= 1 && n <= kMaxRows &&
+           ok16(read) && ok16(written) && ok4(rows) && ok4(dev_status);
+}
+
+bool act_ok(moe_act act) { return act == MOE_ACT_RELU || act == MOE_ACT_GELU || act == MOE_ACT_SWIGLU; }
+
+bool sorted_ffn_shape_ok(moe_act act, int e, int64_t n, int m, int h) {
+    return act_ok(act) && e >= 1 && e <= kMaxE && n >= 1 && m >= 1 && m % 8 == 0 && h >= 1 && h % 8 == 0;
+}
+
+// within the grouped products' index range
+bool sorted_ffn_supported(moe_act act, int e, int64_t n, int m, int h) {
+    const int64_t lim = (int64_t)1 << 31, h2 = act == MOE_ACT_SWIGLU ? 2 * (int64_t)h : h;
+    return n <= kMaxRows && (int64_t)e * h2 < lim && (int64_t)e * m < lim && h2 < lim;
+}
+
+}  // namespace
+
+size_t moe_sort_workspace_size(int64_t s, int e, int k) {
+    return sort_shape_ok(s, e, k) ? sort_workspace_bytes(s, e, k) : 0;
+}
+
+moe_status moe_sort_routes(const int32_t *idx, int64_t s, int e, int k, int32_t *rows, int32_t *offsets,
+                           int32_t *source, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                           void *stream) {
+    if (!sort_shape_ok(s, e, k) || !ok4(idx) || !ok4(rows) || !ok4(offsets) || (source && !ok4(source)) ||
+        !ok16(workspace) || workspace_bytes < sort_workspace_bytes(s, e, k) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    return sort_routes_launch(idx, s, e, k, rows, offsets, source, workspace, dev_status, as_stream(stream));
+}
+
+moe_status moe_encode_sorted(const void *x, moe_dtype dt, const int32_t *rows, const float *gates, int64_t s, int m,
+                             int k, int64_t n, void *out, int32_t *dev_status, void *stream) {
+    if (!move_ok(x, out, dt, rows, s, m, k, n, dev_status) || (gates && !ok4(gates))) return MOE_ERR_INVALID_ARG;
+    return encode_sorted_launch(x, dt, rows, gates, s, m, k, n, out, dev_status, as_stream(stream));
+}
+
+moe_status moe_encode_sorted_bwd(const void *d_out, const void *x, moe_dtype dt, const int32_t *rows,
+                                 const float *gates, int64_t s, int m, int k, int64_t n, void *d_x, float *d_gates,
+                                 int32_t *dev_status, void *stream) {
+    if (!move_ok(d_out, d_x, dt, rows, s, m, k, n, dev_status) || (gates && !ok4(gates)) || (d_gates && !ok4(d_gates)) ||
+        (d_gates && (!gates || !ok16(x))))
+        return MOE_ERR_INVALID_ARG;
+    return encode_sorted_bwd_launch(d_out, x, dt, rows, gates, s, m, k, n, d_x, d_gates, dev_status,
+                                    as_stream(stream));
+}
+
+moe_status moe_decode_sorted(const void *xs, moe_dtype dt, const int32_t *rows, const float *gates, int64_t s, int m,
+                             int k, int64_t n, void *y, int32_t *dev_status, void *stream) {
+    if (!move_ok(xs, y, dt, rows, s, m, k, n, dev_status) || (gates && !ok4(gates))) return MOE_ERR_INVALID_ARG;
+    return decode_sorted_launch(xs, dt, rows, gates, s, m, k, n, y, dev_status, as_stream(stream));
+}
+
+moe_status moe_decode_sorted_bwd(const void *dy, const void *xs, moe_dtype dt, const int32_t *rows,
+                                 const float *gates, int64_t s, int m, int k, int64_t n, void *d_xs, float *d_gates,
+                                 int32_t *dev_status, void *stream) {
+    if (!move_ok(dy, d_xs, dt, rows, s, m, k, n, dev_status) || !ok16(xs) || !ok4(gates) || !ok4(d_gates))
+        return MOE_ERR_INVALID_ARG;
+    return decode_sorted_bwd_launch(dy, xs, dt, rows, gates, s, m, k, n, d_xs, d_gates, dev_status,
+                                    as_stream(stream));
+}
+
+moe_status moe_expert_ffn_sorted(const void *x, moe_dtype dt, const int32_t *offsets, const void *w1, const void *b1,
+                                 const void *w3, const void *w2, const void *b2, moe_act act, int e, int64_t n, int m,
+                                 int h, void *hid, void *pre, void *out, int32_t *dev_status, void *stream) {
+    if (!valid_dt(dt) || !sorted_ffn_shape_ok(act, e, n, m, h) || !ok16(x) || !ok4(offsets) || !ok16(w1) ||
+        !ok16(w2) || !opt16(b1) || !opt16(b2) || !ok16(hid) || !opt16(pre) || !ok16(out) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (act == MOE_ACT_SWIGLU && (!ok16(w3) || b1 || b2)) return MOE_ERR_INVALID_ARG;
+    if (dt != MOE_BF16 || !sorted_ffn_supported(act, e, n, m, h)) return MOE_ERR_UNSUPPORTED;
+    return ffn_tc_launch(x, nullptr, nullptr, w1, b1, w3, w2, b2, act, e, n, m, h, hid, out, dev_status,
+                         as_stream(stream), 0, 0, pre, SortedRows{offsets, n});
+}
+
+size_t moe_expert_ffn_sorted_bwd_workspace_size(moe_act act, int e, int64_t n, int m, int h) {
+    if (!sorted_ffn_shape_ok(act, e, n, m, h) || !sorted_ffn_supported(act, e, n, m, h)) return 0;
+    return ffn_tc_sorted_bwd_workspace_bytes(act, e, n, m, h);
+}
+
+moe_status moe_expert_ffn_sorted_bwd(const void *x, const void *hid, const void *pre, moe_dtype dt,
+                                     const int32_t *offsets, const void *w1, const void *w3, const void *w2,
+                                     moe_act act, int e, int64_t n, int m, int h, const void *d_out, void *workspace,
+                                     size_t workspace_bytes, void *d_x, moe_dtype wgrad_dt, void *d_w1, void *d_w3,
+                                     void *d_w2, void *d_b1, void *d_b2, int32_t *dev_status, void *stream) {
+    if (!valid_dt(dt) || !valid_dt(wgrad_dt) || !sorted_ffn_shape_ok(act, e, n, m, h) || !ok16(x) || !ok16(hid) ||
+        !ok16(pre) || !ok4(offsets) || !ok16(w1) || !ok16(w2) || !ok16(d_out) || !ok16(workspace) || !ok16(d_x) ||
+        !ok16(d_w1) || !ok16(d_w2) || !opt16(d_b1) || !opt16(d_b2) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (act == MOE_ACT_SWIGLU && (!ok16(w3) || !ok16(d_w3) || d_b1 || d_b2)) return MOE_ERR_INVALID_ARG;
+    if (dt != MOE_BF16 || !sorted_ffn_supported(act, e, n, m, h)) return MOE_ERR_UNSUPPORTED;
+    if (workspace_bytes < ffn_tc_sorted_bwd_workspace_bytes(act, e, n, m, h)) return MOE_ERR_INVALID_ARG;
+    return ffn_tc_bwd_launch(x, hid, nullptr, nullptr, w1, nullptr, w3, w2, act, e, n, m, h, d_out, workspace, d_x,
+                             d_w1, d_w3, d_w2, d_b1, d_b2, dev_status, as_stream(stream), pre, wgrad_dt == MOE_F32,
+                             SortedRows{offsets, n});
 }
 
 size_t moe_layer_workspace_size(moe_dtype dt, moe_act act, int64_t s, int m, int e, int k,

@@ -200,6 +200,19 @@ template <> struct Elt<__nv_bfloat16> {
     }
 };
 
+// Rows sorted by expert: expert j has the rows offsets[j] .. offsets[j + 1] - 1 of n (offsets [e + 1] on
+// the device; null: not sorted).
+struct SortedRows {
+    const int32_t *offsets = nullptr;
+    int64_t n = 0;
+};
+
+// First row and number of rows of expert j, inside the buffer whatever the offsets hold.
+__device__ __forceinline__ void sorted_span(const SortedRows &so, int j, int64_t &first, int64_t &count) {
+    first = min((int64_t)max(so.offsets[j], 0), so.n);
+    count = max((int64_t)0, min((int64_t)max(so.offsets[j + 1], 0), so.n) - first);
+}
+
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 }  // namespace moe

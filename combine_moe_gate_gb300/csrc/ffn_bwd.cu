@@ -213,7 +213,7 @@ static_assert(CS_COLS == 32 * 8 && CS_WARPS * 32 >= CS_COLS, "8 columns a lane, 
 
 __global__ void __launch_bounds__(CS_WARPS * 32)
 colsum_kernel(ColsumOps ops, int64_t c_max, const int32_t *__restrict__ counts,
-              const int32_t *__restrict__ c_dev, int out_f32, int32_t *status) {
+              const int32_t *__restrict__ c_dev, int out_f32, int32_t *status, SortedRows so) {
     pdl_enter();
     if (status_bad(status)) return;
     __shared__ float part[CS_WARPS][CS_COLS];
@@ -227,12 +227,14 @@ colsum_kernel(ColsumOps ops, int64_t c_max, const int32_t *__restrict__ counts,
     const int cols = o.cols;
     const int64_t pitch = o.pitch;
     const int c0 = bx * CS_COLS + 8 * lane;
-    const int64_t kept = max(0, min(min(counts[j], *c_dev), (int)min(c_max, (int64_t)0x7fffffff)));
+    int64_t first = (int64_t)j * c_max, kept;
+    if (so.offsets) sorted_span(so, j, first, kept);
+    else kept = max(0, min(min(counts[j], *c_dev), (int)min(c_max, (int64_t)0x7fffffff)));
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) acc[i] = 0.0f;
     if (c0 < cols) {
-        const __nv_bfloat16 *sp = src + (int64_t)j * c_max * pitch + c0;
+        const __nv_bfloat16 *sp = src + first * pitch + c0;
         for (int64_t r0 = warp; r0 < kept; r0 += (int64_t)CS_WARPS * CS_U) {
             V16 v[CS_U];
 #pragma unroll
@@ -310,7 +312,7 @@ constexpr int TR_WARPS = 8;   // one warp per row, 64 / TR_WARPS CTAs per expert
 
 __global__ void __launch_bounds__(TR_WARPS * 32)
 tail_rows_kernel(TailOps ops, int64_t c_max, const int32_t *__restrict__ counts,
-                 const int32_t *__restrict__ c_dev, int32_t *status) {
+                 const int32_t *__restrict__ c_dev, int32_t *status, SortedRows so) {
     pdl_enter();
     if (status_bad(status)) return;
     const TailOp &o = ops.op[blockIdx.z];
@@ -319,11 +321,13 @@ tail_rows_kernel(TailOps ops, int64_t c_max, const int32_t *__restrict__ counts,
     const int64_t src_pitch = o.pitch;
     const int cols = o.cols;
     const int j = blockIdx.y;
-    const int64_t kept = min((int64_t)max(counts[j], 0), min((int64_t)*c_dev, c_max));
+    int64_t first = (int64_t)j * c_max, kept;
+    if (so.offsets) sorted_span(so, j, first, kept);
+    else kept = min((int64_t)max(counts[j], 0), min((int64_t)*c_dev, c_max));
     const int nvalid = (int)(kept & 63);
     if (nvalid == 0) return;
     const int r = blockIdx.x * TR_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const __nv_bfloat16 *srow = src + ((int64_t)j * c_max + (kept - nvalid) + r) * src_pitch;
+    const __nv_bfloat16 *srow = src + (first + (kept - nvalid) + r) * src_pitch;
     __nv_bfloat16 *drow = dst + ((int64_t)j * 64 + r) * cols;
     for (int c = lane * 8; c < cols; c += 32 * 8) {
         V16 v{};
@@ -336,7 +340,7 @@ tail_rows_kernel(TailOps ops, int64_t c_max, const int32_t *__restrict__ counts,
 
 moe_status tail_rows_launch(const TailOps &ops, int nops, int64_t c_max, int e,
                             const int32_t *counts, const int32_t *c_dev, int32_t *status,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, SortedRows so) {
     if (nops < 1 || nops > TAIL_MAX_OPS || e < 1 || e > 65535 || c_max < 1) return MOE_ERR_INVALID_ARG;
     for (int i = 0; i < nops; i++) {
         const TailOp &o = ops.op[i];
@@ -344,7 +348,7 @@ moe_status tail_rows_launch(const TailOps &ops, int nops, int64_t c_max, int e,
             return MOE_ERR_INVALID_ARG;
     }
     return launch_pdl(tail_rows_kernel, dim3(64 / TR_WARPS, (unsigned)e, (unsigned)nops),
-                      dim3(TR_WARPS * 32), 0, stream, ops, c_max, counts, c_dev, status);
+                      dim3(TR_WARPS * 32), 0, stream, ops, c_max, counts, c_dev, status, so);
 }
 
 // ------------------------------------------------------- zero empty experts
@@ -354,11 +358,13 @@ constexpr int ZE_THREADS = 256, ZE_BLOCKS = 64;   // CTAs per (expert, matrix)
 
 __global__ void __launch_bounds__(ZE_THREADS)
 zero_empty_experts_kernel(ZeroOps ops, int64_t c_max, const int32_t *__restrict__ counts,
-                          const int32_t *__restrict__ c_dev, int32_t *status) {
+                          const int32_t *__restrict__ c_dev, int32_t *status, SortedRows so) {
     pdl_enter();
     if (status_bad(status)) return;
     const int j = blockIdx.y;
-    const int64_t kept = min((int64_t)max(counts[j], 0), min((int64_t)*c_dev, c_max));
+    int64_t first, kept;
+    if (so.offsets) sorted_span(so, j, first, kept);
+    else kept = min((int64_t)max(counts[j], 0), min((int64_t)*c_dev, c_max));
     if (kept > 0) return;
     const ZeroOp &o = ops.op[blockIdx.z];
     V16 *dst = reinterpret_cast<V16 *>(static_cast<char *>(o.ptr) + (int64_t)j * o.bytes);
@@ -373,19 +379,20 @@ zero_empty_experts_kernel(ZeroOps ops, int64_t c_max, const int32_t *__restrict_
 
 moe_status zero_empty_experts_launch(const ZeroOps &ops, int nops, int64_t c_max, int e,
                                      const int32_t *counts, const int32_t *c_dev, int32_t *status,
-                                     cudaStream_t stream) {
+                                     cudaStream_t stream, SortedRows so) {
     if (nops < 1 || nops > 3 || e < 1 || e > 65535 || c_max < 1) return MOE_ERR_INVALID_ARG;
     for (int i = 0; i < nops; i++)
         if (!ops.op[i].ptr || ops.op[i].bytes < 16 || ops.op[i].bytes % 16 || !aligned16(ops.op[i].ptr))
             return MOE_ERR_INVALID_ARG;
     return launch_pdl(zero_empty_experts_kernel, dim3(ZE_BLOCKS, (unsigned)e, (unsigned)nops),
-                      dim3(ZE_THREADS), 0, stream, ops, c_max, counts, c_dev, status);
+                      dim3(ZE_THREADS), 0, stream, ops, c_max, counts, c_dev, status, so);
 }
 
 moe_status colsum_launch(const __nv_bfloat16 *src, int e, int64_t c_max, int cols,
                          int64_t src_pitch, const int32_t *counts, const int32_t *c_dev,
                          void *out, int32_t *status, cudaStream_t stream, bool out_f32,
-                         const __nv_bfloat16 *src2, int cols2, int64_t src2_pitch, void *out2) {
+                         const __nv_bfloat16 *src2, int cols2, int64_t src2_pitch, void *out2,
+                         SortedRows so) {
     // rows of whole 16-byte chunks
     if (e < 1 || e > 65535 || cols < 1 || cols % 8 || src_pitch % 8 || !aligned16(src))
         return MOE_ERR_INVALID_ARG;
@@ -396,7 +403,7 @@ moe_status colsum_launch(const __nv_bfloat16 *src, int e, int64_t c_max, int col
     ops.op[1] = src2 ? ColsumOp{src2, cols2, src2_pitch, out2} : ColsumOp{src, 0, src_pitch, out};
     const int nb = (cols + CS_COLS - 1) / CS_COLS + (src2 ? (cols2 + CS_COLS - 1) / CS_COLS : 0);
     return launch_pdl(colsum_kernel, dim3((unsigned)nb, (unsigned)e), dim3(CS_WARPS * 32), 0, stream,
-                      ops, c_max, counts, c_dev, out_f32 ? 1 : 0, status);
+                      ops, c_max, counts, c_dev, out_f32 ? 1 : 0, status, so);
 }
 
 }  // namespace moe

@@ -27,6 +27,10 @@ moe_status act_bwd_launch(const __nv_bfloat16 *pa, const __nv_bfloat16 *pb,
                           const int32_t *counts, const int32_t *c_dev, __nv_bfloat16 *d_pre,
                           int32_t *status, cudaStream_t stream);
 
+// The launchers below take the rows of an [e, c_max, ...] buffer (counts, c_dev), or, with `so`, rows
+// sorted by expert: then expert b's rows r are rows so.offsets[b] + r of the operands, counts, c_dev
+// and c_max unused.
+
 // out[b][c] = sum over the kept rows r of src[b][r][c] (fp32 sum in a fixed
 // order, one rounding to bf16); src rows of `cols` columns at row pitch
 // src_pitch, batch stride c_max * src_pitch.  With src2, the same for a
@@ -36,7 +40,7 @@ moe_status colsum_launch(const __nv_bfloat16 *src, int e, int64_t c_max, int col
                          int64_t src_pitch, const int32_t *counts, const int32_t *c_dev,
                          void *out, int32_t *status, cudaStream_t stream, bool out_f32 = false,
                          const __nv_bfloat16 *src2 = nullptr, int cols2 = 0,
-                         int64_t src2_pitch = 0, void *out2 = nullptr);
+                         int64_t src2_pitch = 0, void *out2 = nullptr, SortedRows so = {});
 
 // The partly kept last 64-row block of every expert, for the MN-major weight
 // gradients, for up to TAIL_MAX_OPS operands in one launch: with kept_b =
@@ -57,7 +61,7 @@ struct TailOps {
 };
 moe_status tail_rows_launch(const TailOps &ops, int nops, int64_t c_max, int e,
                             const int32_t *counts, const int32_t *c_dev, int32_t *status,
-                            cudaStream_t stream);
+                            cudaStream_t stream, SortedRows so = {});
 
 // Zero the `bytes` of slab b (of up to 3 matrices [e, ...], slab b of matrix i
 // at op[i].ptr + b * op[i].bytes) for every expert b without kept rows
@@ -72,6 +76,6 @@ struct ZeroOps {
 };
 moe_status zero_empty_experts_launch(const ZeroOps &ops, int nops, int64_t c_max, int e,
                                      const int32_t *counts, const int32_t *c_dev, int32_t *status,
-                                     cudaStream_t stream);
+                                     cudaStream_t stream, SortedRows so = {});
 
 }  // namespace moe

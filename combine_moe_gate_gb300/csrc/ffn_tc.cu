@@ -206,7 +206,16 @@ struct GemmArgs {
     // Error-path test: the producers issue no copies, so the MMA issuer's
     // bounded wait on the first stage runs out (MOE_ERR_TIMEOUT).
     int32_t stall;
+    // Rows sorted by expert: expert j has the rows offsets[j] .. offsets[j + 1] - 1 of n_rows, as its
+    // output rows or (k_counts set) as its contraction; counts, c_dev and k_cdev are not read then.
+    const int32_t *offsets;
+    int64_t n_rows;
 };
+
+// Entry j of the offsets, inside the buffer whatever it holds.
+__device__ __forceinline__ int sorted_at(const GemmArgs &a, int j) {
+    return (int)min((int64_t)max(a.offsets[j], 0), a.n_rows);
+}
 
 // ------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t su32(const void *p) {
@@ -676,21 +685,38 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int nk = (args.K + BK - 1) / BK;
     const bool kmode = args.k_counts != nullptr;           // K per expert
     const int urows = kmode ? (int)args.c_max : 0;
+    // first output row of expert j; first row of its contraction
+    auto row_base = [&](int j) {
+        return args.offsets && !kmode ? (int64_t)sorted_at(args, j) : (int64_t)j * args.c_max + args.row_lo;
+    };
 
     // ---- setup: per-expert row counts and tile prefix (warp 0), barriers,
     // TMEM allocation (warp 1)
     if (warp == 0) {
-        const int c_eff = kmode ? 0 : (int)min((int64_t)*args.c_dev, args.c_max);
-        const int k_eff = kmode ? (int)min((int64_t)*args.k_cdev, (int64_t)args.K) : 0;
+        const bool sorted = args.offsets != nullptr;
+        const int c_eff = kmode || sorted ? 0 : (int)min((int64_t)*args.c_dev, args.c_max);
+        const int k_eff = kmode && !sorted ? (int)min((int64_t)*args.k_cdev, (int64_t)args.K) : 0;
         int run = 0;
         for (int base = 0; base < e; base += 32) {
             int j = base + lane;
-            int rows = j >= e ? 0 : kmode ? urows : min(max(args.counts[j], 0), c_eff);
-            if (!kmode && j < e) {   // the kept rows inside [row_lo, row_hi)
-                const int hi = args.row_hi > 0 ? min(rows, args.row_hi) : rows;
-                rows = max(0, hi - args.row_lo);
+            int rows = 0;
+            if (sorted) {
+                int own_rows = 0;
+                if (j < e) {
+                    const int lo = args.offsets[j], hi = args.offsets[j + 1];
+                    if (lo < 0 || hi < lo || hi > args.n_rows) set_status(args.status, MOE_ERR_INVALID_ARG);
+                    own_rows = max(0, sorted_at(args, j + 1) - sorted_at(args, j));
+                    kept_rows[j] = own_rows;
+                    rows = kmode ? urows : own_rows;
+                }
+            } else {
+                rows = j >= e ? 0 : kmode ? urows : min(max(args.counts[j], 0), c_eff);
+                if (!kmode && j < e) {   // the kept rows inside [row_lo, row_hi)
+                    const int hi = args.row_hi > 0 ? min(rows, args.row_hi) : rows;
+                    rows = max(0, hi - args.row_lo);
+                }
+                if (j < e) kept_rows[j] = kmode ? min(max(args.k_counts[j], 0), k_eff) : rows;
             }
-            if (j < e) kept_rows[j] = kmode ? min(max(args.k_counts[j], 0), k_eff) : rows;
             // per-expert K: an expert without any K rows gets no tiles when asked
             // (its zero output is written elsewhere)
             if (kmode && args.skip_empty && j < e && kept_rows[j] == 0) rows = 0;
@@ -768,7 +794,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         for (int t = tile0; t < total && !args.stall; t += tile_step) {
             Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
             // A: this CTA's 128 rows, half of them per producer
-            const int a_row = (int)((int64_t)T.j * args.c_max + args.row_lo + (int64_t)T.mt * BMT +
+            const int a_row = (int)(row_base(T.j) + (int64_t)T.mt * BMT +
                                     (int64_t)prank * TL::A_ROWS + (int64_t)hh * TL::A_BOX_ROWS);
             // B rows of this CTA: its half of the (each) N = 256 sub-tile; with
             // TN = 2 producer hh loads N sub-tile hh
@@ -779,12 +805,13 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             // MN-major weight gradients: a last K block only partly kept
             // comes from the tail maps (rows j * BK ..)
             const bool part_tail = AMN && (kept_rows[T.j] % BK) != 0;
+            const int k_base = AMN && args.offsets ? sorted_at(args, T.j) : T.j * args.b_rows;
             for (int kb = 0; kb < T.nk; kb++) {
                 int ok = 1;
                 if (lane == 0) {
                     ok = mbar_wait<PAIR>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status);
                     const bool tail = part_tail && kb == T.nk - 1;
-                    const int k_row = tail ? T.j * BK : T.j * args.b_rows + kb * BK;
+                    const int k_row = tail ? T.j * BK : k_base + kb * BK;
                     if (ok && PAIR && AMN) {
                         const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
                         if (is_a) {
@@ -962,10 +989,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const int row = T.mt * BMT + row_in_tile;
             const bool valid = row < T.rows;
             const bool all_kept = row - lane + 31 < T.rows;  // the warp's 32 rows
-            const int64_t grow0 = (int64_t)T.j * args.c_max + args.row_lo + row - lane;
+            const int64_t grow0 = row_base(T.j) + row - lane;
             __nv_bfloat16 *orow =
-                args.out + ((int64_t)T.j * args.c_max + args.row_lo + row) *
-                               (args.out_pitch ? args.out_pitch : (int64_t)args.n_out);
+                args.out + (grow0 + lane) * (args.out_pitch ? args.out_pitch : (int64_t)args.n_out);
             const __nv_bfloat16 *brow = args.bias ? args.bias + (int64_t)T.j * args.n_out : nullptr;
             const uint32_t tbase = tmem + ((uint32_t)(sub * 32) << 16) +
                                    (uint32_t)(acc * TL::ACC_COLS + (TM == 2 ? half * BN : 0));
@@ -993,8 +1019,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out,
                                 orow);
                     if (EPI == EPI_SWIGLU_SAVE && valid) {   // this lane's row of a, then of b
-                        __nv_bfloat16 *arow = args.aux_out + ((int64_t)T.j * args.c_max + args.row_lo +
-                                                              row) * (2 * (int64_t)args.n_out);
+                        __nv_bfloat16 *arow = args.aux_out + (grow0 + lane) * (2 * (int64_t)args.n_out);
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
                             if (gcol + 8 * q < args.n_out) {
@@ -1032,11 +1057,10 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 const float sa = F8 && valid ? args.a_scale[grow0 + lane] : 0.0f;
                 const __nv_bfloat16 *drow =
                     DACT || DACTP
-                        ? args.aux + ((int64_t)T.j * args.c_max + args.row_lo + row) *
-                                         ((DSWI ? 2 : 1) * (int64_t)args.n_out)
+                        ? args.aux + (grow0 + lane) * ((DSWI ? 2 : 1) * (int64_t)args.n_out)
                         : nullptr;
                 __nv_bfloat16 *prow =
-                    SAVE ? args.aux_out + ((int64_t)T.j * args.c_max + args.row_lo + row) * (int64_t)args.n_out
+                    SAVE ? args.aux_out + (grow0 + lane) * (int64_t)args.n_out
                          : nullptr;
                 const float *bsc = F8 ? args.b_scale + (int64_t)T.j * args.n_out : nullptr;
 #pragma unroll 1
@@ -1323,6 +1347,8 @@ moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtenso
     constexpr int NOUT_TILE = is_swiglu(EPI) ? BN / 2 : BN * TN;
     const int64_t ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
     int64_t upper = (int64_t)args.e * ((args.c_max + TL::BMT - 1) / TL::BMT) * ntn;
+    if (args.offsets && !args.k_counts)   // a partly filled tile an expert that has rows
+        upper = (args.n_rows / TL::BMT + (args.n_rows < args.e ? args.n_rows : args.e)) * ntn;
     int64_t grid = upper < nunits ? upper : nunits;
     if (grid < 1) grid = 1;
     if (CL == 1)
@@ -1364,7 +1390,8 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
                          const void *w1, const void *b1, const void *w3, const void *w2,
                          const void *b2, moe_act act, int e, int64_t c_max, int m, int h,
                          void *hid, void *out, int32_t *st, cudaStream_t stream, int row_lo,
-                         int row_hi, void *pre) {
+                         int row_hi, void *pre, SortedRows so) {
+    const uint64_t rows = so.offsets ? (uint64_t)so.n : (uint64_t)e * c_max;
     // fc1: 256-row tiles on CTA pairs (2-SM MMA), two accumulators per CTA so
     // its activation epilogue overlaps the next tile's main loop.
     // fc2 (bias-only epilogue, long K, about one tile per pair): 256 x 512
@@ -1378,16 +1405,18 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
     // one CTA's B box: a pair CTA's half tile, or a 1-SM SwiGLU tile's W1/W3 half
     // one producer's B box: half of a CTA's B rows (1-SM SwiGLU: the W1 or W3 half)
     const uint32_t b1_box = T1::B_BOX_ROWS;
-    if (!make_map(&mA1, buf, (uint64_t)e * c_max, (uint64_t)m, T1::A_BOX_ROWS, BK1) ||
+    if (!make_map(&mA1, buf, rows, (uint64_t)m, T1::A_BOX_ROWS, BK1) ||
         !make_map(&mB1, w1, (uint64_t)e * h, (uint64_t)m, b1_box, BK1) ||
         !make_map(&mB3, swiglu ? w3 : w1, (uint64_t)e * h, (uint64_t)m, b1_box, BK1) ||
-        !make_map(&mA2, hid, (uint64_t)e * c_max, (uint64_t)h, T2::A_BOX_ROWS, BK2) ||
+        !make_map(&mA2, hid, rows, (uint64_t)h, T2::A_BOX_ROWS, BK2) ||
         !make_map(&mB2, w2, (uint64_t)e * m, (uint64_t)h, T2::B_BOX_ROWS, BK2) ||
-        !make_map(&mO1, hid, (uint64_t)e * c_max, (uint64_t)h, 32, 32) ||
-        !make_map(&mO2, out, (uint64_t)e * c_max, (uint64_t)m, 32, 32))
+        !make_map(&mO1, hid, rows, (uint64_t)h, 32, 32) ||
+        !make_map(&mO2, out, rows, (uint64_t)m, 32, 32))
         return MOE_ERR_CUDA;
     GemmArgs g1{counts, c_dev, st, (const __nv_bfloat16 *)b1, (__nv_bfloat16 *)hid, c_max, e, m, h, h,
                 nullptr, nullptr, row_lo, row_hi};
+    g1.offsets = so.offsets;
+    g1.n_rows = so.n;
     g1.aux_out = (__nv_bfloat16 *)pre;   // training: fc1 also keeps its pre-activation
     moe_status r;
     if (swiglu) {
@@ -1403,6 +1432,8 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
     if (r != MOE_OK) return r;
     GemmArgs g2{counts, c_dev, st, (const __nv_bfloat16 *)b2, (__nv_bfloat16 *)out, c_max, e, h, m, m,
                 nullptr, nullptr, row_lo, row_hi};
+    g2.offsets = so.offsets;
+    g2.n_rows = so.n;
     return launch_gemm<EPI_BIAS, TM2, BK2, CL2, TN2>(mA2, mB2, mB2, mO2, g2, stream);
 }
 
@@ -1487,17 +1518,19 @@ struct BwdLayout {
     int64_t pa, pb, dh, dpre, wT, tDo, tHid, tDp, tBuf, total;
 };
 
-BwdLayout bwd_layout(moe_act act, int e, int64_t c_max, int m, int h) {
+// rows: of the buffers (e * c_max, or the sorted rows); saved: only the backward that reads the
+// forward's pre-activation, which keeps no recomputed one.
+BwdLayout bwd_layout(moe_act act, int e, int64_t rows, int m, int h, bool saved = false) {
     const bool swiglu = act == MOE_ACT_SWIGLU;
     const int64_t E = e, H2 = swiglu ? 2 * (int64_t)h : h;
     BwdLayout L{};
     int64_t o = 0;
     auto take = [&](int64_t bytes) { const int64_t at = o; o += up256i(bytes); return at; };
-    L.pa = take(swiglu ? E * c_max * h * 2 : 0);   // SwiGLU's recomputed a and b
-    L.pb = take(swiglu ? E * c_max * h * 2 : 0);
-    L.dh = take(E * c_max * h * 2);
-    L.dpre = take(E * c_max * H2 * 2);
-    L.wT = take(swiglu ? E * m * H2 * 2 : 0);   // [W1 | W3] transposed (SwiGLU only)
+    L.pa = take(swiglu && !saved ? rows * h * 2 : 0);   // SwiGLU's recomputed a and b
+    L.pb = take(swiglu && !saved ? rows * h * 2 : 0);
+    L.dh = take(saved ? 0 : rows * h * 2);
+    L.dpre = take(rows * H2 * 2);
+    L.wT = take(swiglu && (!saved || h % 64) ? E * m * H2 * 2 : 0);   // [W1 | W3] transposed (SwiGLU only)
     // the partly kept last 64-row block of each expert's d_out, hid, d_pre, buf
     L.tDo = take(E * 64 * m * 2);
     L.tHid = take(E * 64 * h * 2);
@@ -1507,19 +1540,26 @@ BwdLayout bwd_layout(moe_act act, int e, int64_t c_max, int m, int h) {
     return L;
 }
 
+uint64_t rows_of(int e, int64_t c_max, const SortedRows &so) {
+    return so.offsets ? (uint64_t)so.n : (uint64_t)e * c_max;
+}
+
 // out[j] = A[j] B[j]^T (+ bias[j]) over the rows min(counts[j], *c_dev, c_max)
 // of every expert j: A [e * c_max, K], B [e * b_rows, K], out [e, c_max, n_out].
 moe_status gemm_bias(const void *a, const void *b, int b_rows, void *out, const void *bias,
                      const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int K,
-                     int n_out, int32_t *st, cudaStream_t stream) {
+                     int n_out, int32_t *st, cudaStream_t stream,
+                     SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
     CUtensorMap mA, mB, mO;
-    if (!make_map(&mA, a, (uint64_t)e * c_max, (uint64_t)K, T2::A_BOX_ROWS, 64) ||
+    if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)K, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, b, (uint64_t)e * b_rows, (uint64_t)K, T2::B_BOX_ROWS, 64) ||
-        !make_map(&mO, out, (uint64_t)e * c_max, (uint64_t)n_out, 32, 32))
+        !make_map(&mO, out, rows_of(e, c_max, so), (uint64_t)n_out, 32, 32))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, (const __nv_bfloat16 *)bias, (__nv_bfloat16 *)out, c_max, e, K,
                n_out, b_rows, nullptr, nullptr, 0, 0};
+    g.offsets = so.offsets;
+    g.n_rows = so.n;
     return launch_gemm<EPI_BIAS, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
 }
 
@@ -1527,15 +1567,18 @@ moe_status gemm_bias(const void *a, const void *b, int b_rows, void *out, const 
 // (K rows per expert; rows past an expert's K meet zero columns of A).
 moe_status gemm_bias_bmn(const void *a, const void *b, void *out, const int32_t *counts,
                          const int32_t *c_dev, int e, int64_t c_max, int K, int n_out, int32_t *st,
-                         cudaStream_t stream) {
+                         cudaStream_t stream,
+                     SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
     CUtensorMap mA, mB, mO;
-    if (!make_map(&mA, a, (uint64_t)e * c_max, (uint64_t)K, T2::A_BOX_ROWS, 64) ||
+    if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)K, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, b, (uint64_t)e * K, (uint64_t)n_out, 64, 64) ||
-        !make_map(&mO, out, (uint64_t)e * c_max, (uint64_t)n_out, 32, 32))
+        !make_map(&mO, out, rows_of(e, c_max, so), (uint64_t)n_out, 32, 32))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)out, c_max, e, K, n_out, K, nullptr,
                nullptr, 0, 0};
+    g.offsets = so.offsets;
+    g.n_rows = so.n;
     return launch_gemm<EPI_BIAS_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
 }
 
@@ -1544,17 +1587,20 @@ moe_status gemm_bias_bmn(const void *a, const void *b, void *out, const int32_t 
 // the 64-row K block, so no block straddles the two).
 moe_status gemm_bias_bmn2(const void *a, const void *b1, const void *b3, void *out,
                           const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int h,
-                          int n_out, int32_t *st, cudaStream_t stream) {
+                          int n_out, int32_t *st, cudaStream_t stream,
+                     SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
     CUtensorMap mA, mB, mB3, mO;
-    if (!make_map(&mA, a, (uint64_t)e * c_max, 2 * (uint64_t)h, T2::A_BOX_ROWS, 64) ||
+    if (!make_map(&mA, a, rows_of(e, c_max, so), 2 * (uint64_t)h, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, b1, (uint64_t)e * h, (uint64_t)n_out, 64, 64) ||
         !make_map(&mB3, b3, (uint64_t)e * h, (uint64_t)n_out, 64, 64) ||
-        !make_map(&mO, out, (uint64_t)e * c_max, (uint64_t)n_out, 32, 32))
+        !make_map(&mO, out, rows_of(e, c_max, so), (uint64_t)n_out, 32, 32))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)out, c_max, e, 2 * h, n_out, h, nullptr,
                nullptr, 0, 0};
     g.k_split = h;
+    g.offsets = so.offsets;
+    g.n_rows = so.n;
     return launch_gemm<EPI_BIAS_BMN, 1, 64, 2, 1>(mA, mB, mB3, mO, g, stream);
 }
 
@@ -1581,18 +1627,21 @@ moe_status gemm_dact(const void *buf, const void *w1, const void *b1, const void
 // MN-major and its epilogue applies the derivative; d_hid is never stored.
 moe_status gemm_dact_bmn(const void *d_out, const void *w2, const void *pre, moe_act act, void *d_pre,
                          const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int m,
-                         int h, int32_t *st, cudaStream_t stream) {
+                         int h, int32_t *st, cudaStream_t stream,
+                     SortedRows so = {}) {
     // 256 x 256 pair tiles with two accumulators: the derivative epilogue
     // (a load of the pre-activation and the GELU derivative per element)
     // overlaps the next tile's main loop
     using T2 = Tiling<1, 64, 2, 1>;
     CUtensorMap mA, mB, mO;
-    if (!make_map(&mA, d_out, (uint64_t)e * c_max, (uint64_t)m, T2::A_BOX_ROWS, 64) ||
+    if (!make_map(&mA, d_out, rows_of(e, c_max, so), (uint64_t)m, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64) ||
-        !make_map(&mO, d_pre, (uint64_t)e * c_max, (uint64_t)h, 32, 32))
+        !make_map(&mO, d_pre, rows_of(e, c_max, so), (uint64_t)h, 32, 32))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)d_pre, c_max, e, m, h, m, nullptr,
                nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)pre};
+    g.offsets = so.offsets;
+    g.n_rows = so.n;
     return act == MOE_ACT_GELU ? launch_gemm<EPI_DGELU_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream)
                                : launch_gemm<EPI_DRELU_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
 }
@@ -1602,18 +1651,21 @@ moe_status gemm_dact_bmn(const void *d_out, const void *w2, const void *pre, moe
 // silu(a)] ([e, c_max, 2h]); d_hid is never stored.
 moe_status gemm_dswiglu_bmn(const void *d_out, const void *w2, const void *ab, void *d_pre,
                             const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int m,
-                            int h, int32_t *st, cudaStream_t stream) {
+                            int h, int32_t *st, cudaStream_t stream,
+                     SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
     CUtensorMap mA, mB, mO;
-    if (!make_map(&mA, d_out, (uint64_t)e * c_max, (uint64_t)m, T2::A_BOX_ROWS, 64) ||
+    if (!make_map(&mA, d_out, rows_of(e, c_max, so), (uint64_t)m, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64) ||
         // d_a: the first h columns of each 2h-wide row (the map's extent clips a
         // box at h, so d_b's columns are never written by it)
-        !make_map(&mO, d_pre, (uint64_t)e * c_max, (uint64_t)h, 32, 32, 2 * (uint64_t)h))
+        !make_map(&mO, d_pre, rows_of(e, c_max, so), (uint64_t)h, 32, 32, 2 * (uint64_t)h))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)d_pre, c_max, e, m, h, m, nullptr,
                nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)ab};
     g.out_pitch = 2 * (int64_t)h;
+    g.offsets = so.offsets;
+    g.n_rows = so.n;
     return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
 }
 
@@ -1629,17 +1681,22 @@ moe_status gemm_wgrad_mn(const void *a, int64_t a_pitch, int a_cols, const void 
                          int64_t a_tpitch, const void *b, int64_t b_pitch, int b_cols,
                          const void *b_tail, int64_t b_tpitch, void *out, const int32_t *counts,
                          const int32_t *c_dev, int e, int64_t c_max, int32_t *st, cudaStream_t stream,
-                         bool out_f32 = false) {
+                         bool out_f32 = false, SortedRows so = {}) {
     CUtensorMap mA, mAt, mB, mBt, mO;
-    if (!make_map(&mA, a, (uint64_t)e * c_max, (uint64_t)a_cols, 64, 64, (uint64_t)a_pitch) ||
+    if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)a_cols, 64, 64, (uint64_t)a_pitch) ||
         !make_map(&mAt, a_tail, (uint64_t)e * 64, (uint64_t)a_cols, 64, 64, (uint64_t)a_tpitch) ||
-        !make_map(&mB, b, (uint64_t)e * c_max, (uint64_t)b_cols, 64, 64, (uint64_t)b_pitch) ||
+        !make_map(&mB, b, rows_of(e, c_max, so), (uint64_t)b_cols, 64, 64, (uint64_t)b_pitch) ||
         !make_map(&mBt, b_tail, (uint64_t)e * 64, (uint64_t)b_cols, 64, 64, (uint64_t)b_tpitch) ||
         !(out_f32 ? make_map_f32_out(&mO, out, (uint64_t)e * a_cols, (uint64_t)b_cols)
                   : make_map(&mO, out, (uint64_t)e * a_cols, (uint64_t)b_cols, 32, 32)))
         return MOE_ERR_CUDA;
     GemmArgs g{nullptr, nullptr, st, nullptr, (__nv_bfloat16 *)out, a_cols, e, (int)c_max, b_cols,
                (int)c_max, counts, c_dev, 0, 0};
+    if (so.offsets) {   // the sorted rows are the contraction
+        g.K = (int)so.n;
+        g.k_counts = g.offsets = so.offsets;
+        g.n_rows = so.n;
+    }
     g.skip_empty = 1;   // the zero gradients of experts without kept rows: zero_empty_experts_launch
     if (out_f32) {   // fp32 boxes of 32 rows x 16 columns
         g.out_f32 = (float *)out;
@@ -1651,7 +1708,11 @@ moe_status gemm_wgrad_mn(const void *a, int64_t a_pitch, int a_cols, const void 
 }  // namespace
 
 size_t ffn_tc_bwd_workspace_bytes(moe_act act, int e, int64_t c_max, int m, int h) {
-    return (size_t)bwd_layout(act, e, c_max, m, h).total;
+    return (size_t)bwd_layout(act, e, (int64_t)e * c_max, m, h).total;
+}
+
+size_t ffn_tc_sorted_bwd_workspace_bytes(moe_act act, int e, int64_t n, int m, int h) {
+    return (size_t)bwd_layout(act, e, n, m, h, true).total;
 }
 
 moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *counts,
@@ -1659,10 +1720,10 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
                              const void *w2, moe_act act, int e, int64_t c_max, int m, int h,
                              const void *d_out, void *ws, void *d_buf, void *d_w1, void *d_w3,
                              void *d_w2, void *d_b1, void *d_b2, int32_t *st, cudaStream_t stream,
-                             const void *pre, bool wgrad_f32) {
+                             const void *pre, bool wgrad_f32, SortedRows so) {
     using bf = __nv_bfloat16;
     const bool swiglu = act == MOE_ACT_SWIGLU;
-    const BwdLayout L = bwd_layout(act, e, c_max, m, h);
+    const BwdLayout L = bwd_layout(act, e, (int64_t)rows_of(e, c_max, so), m, h, so.offsets != nullptr);
     const int64_t H2 = swiglu ? 2 * (int64_t)h : h;
     if (c_max > 0x7fffffff || H2 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
     char *w = (char *)ws;
@@ -1691,10 +1752,10 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
     // activation backward); then d_buf
     if (pre && swiglu) {
         // the forward's saved [a | b]: one product, d_hid never stored
-        MOE_TRY(gemm_dswiglu_bmn(d_out, w2, pre, dpre, counts, c_dev, e, c_max, m, h, st, stream));
+        MOE_TRY(gemm_dswiglu_bmn(d_out, w2, pre, dpre, counts, c_dev, e, c_max, m, h, st, stream, so));
     } else if (pre) {
         // the forward's saved pre-activation: one product, d_hid never stored
-        MOE_TRY(gemm_dact_bmn(d_out, w2, pre, act, dpre, counts, c_dev, e, c_max, m, h, st, stream));
+        MOE_TRY(gemm_dact_bmn(d_out, w2, pre, act, dpre, counts, c_dev, e, c_max, m, h, st, stream, so));
     } else if (swiglu) {
         MOE_TRY(gemm_bias_bmn(d_out, w2, dh, counts, c_dev, e, c_max, m, h, st, stream));
         MOE_TRY(gemm_bias(buf, w1, h, pa, nullptr, counts, c_dev, e, c_max, m, h, st, stream));
@@ -1705,11 +1766,11 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
         MOE_TRY(gemm_dact(buf, w1, b1, dh, act, dpre, counts, c_dev, e, c_max, m, h, st, stream));
     }
     if (swiglu_mn)
-        MOE_TRY(gemm_bias_bmn2(dpre, w1, w3, d_buf, counts, c_dev, e, c_max, h, m, st, stream));
+        MOE_TRY(gemm_bias_bmn2(dpre, w1, w3, d_buf, counts, c_dev, e, c_max, h, m, st, stream, so));
     else if (swiglu)
-        MOE_TRY(gemm_bias(dpre, wT, m, d_buf, nullptr, counts, c_dev, e, c_max, (int)H2, m, st, stream));
+        MOE_TRY(gemm_bias(dpre, wT, m, d_buf, nullptr, counts, c_dev, e, c_max, (int)H2, m, st, stream, so));
     else
-        MOE_TRY(gemm_bias_bmn(dpre, w1, d_buf, counts, c_dev, e, c_max, h, m, st, stream));
+        MOE_TRY(gemm_bias_bmn(dpre, w1, d_buf, counts, c_dev, e, c_max, h, m, st, stream, so));
     // weight gradients: the kept rows are the contraction, each expert over
     // its own; both operands are read MN-major in place, the partly kept last
     // 64-row block of each expert from a zero-padded copy
@@ -1719,7 +1780,7 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
         tails.op[1] = TailOp{(const bf *)hid, h, h, tHid};
         tails.op[2] = TailOp{dpre, H2, (int)H2, tDp};
         tails.op[3] = TailOp{(const bf *)buf, m, m, tBuf};
-        MOE_TRY(tail_rows_launch(tails, 4, c_max, e, counts, c_dev, st, stream));
+        MOE_TRY(tail_rows_launch(tails, 4, c_max, e, counts, c_dev, st, stream, so));
         // the weight gradients of experts without kept rows are zero: plain
         // stores at the HBM rate instead of the products' zero tiles
         const int64_t gb = wgrad_f32 ? 4 : 2;
@@ -1727,24 +1788,25 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
         zo.op[0] = ZeroOp{d_w1, (int64_t)h * m * gb};
         zo.op[1] = ZeroOp{d_w2, (int64_t)m * h * gb};
         zo.op[2] = ZeroOp{d_w3, (int64_t)h * m * gb};
-        MOE_TRY(zero_empty_experts_launch(zo, swiglu ? 3 : 2, c_max, e, counts, c_dev, st, stream));
+        MOE_TRY(zero_empty_experts_launch(zo, swiglu ? 3 : 2, c_max, e, counts, c_dev, st, stream, so));
     }
     MOE_TRY(gemm_wgrad_mn(d_out, m, m, tDo, m, hid, h, h, tHid, h, d_w2, counts, c_dev, e, c_max, st,
-                          stream, wgrad_f32));
+                          stream, wgrad_f32, so));
     MOE_TRY(gemm_wgrad_mn(dpre, H2, h, tDp, H2, buf, m, m, tBuf, m, d_w1, counts, c_dev, e, c_max,
-                          st, stream, wgrad_f32));
+                          st, stream, wgrad_f32, so));
     if (swiglu)
         MOE_TRY(gemm_wgrad_mn(dpre + h, H2, h, tDp + h, H2, buf, m, m, tBuf, m, d_w3, counts, c_dev,
-                              e, c_max, st, stream, wgrad_f32));
+                              e, c_max, st, stream, wgrad_f32, so));
     // bias gradients (ReLU / GELU experts), both in one launch
     if (!swiglu && d_b1 && d_b2)
         MOE_TRY(colsum_launch(dpre, e, c_max, h, h, counts, c_dev, d_b1, st, stream, wgrad_f32,
-                              (const bf *)d_out, m, m, d_b2));
+                              (const bf *)d_out, m, m, d_b2, so));
     else if (!swiglu && d_b1)
-        MOE_TRY(colsum_launch(dpre, e, c_max, h, h, counts, c_dev, d_b1, st, stream, wgrad_f32));
+        MOE_TRY(colsum_launch(dpre, e, c_max, h, h, counts, c_dev, d_b1, st, stream, wgrad_f32,
+                              nullptr, 0, 0, nullptr, so));
     else if (!swiglu && d_b2)
         MOE_TRY(colsum_launch((const bf *)d_out, e, c_max, m, m, counts, c_dev, d_b2, st, stream,
-                              wgrad_f32));
+                              wgrad_f32, nullptr, 0, 0, nullptr, so));
 #undef MOE_TRY
     return MOE_OK;
 }

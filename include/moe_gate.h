@@ -532,6 +532,109 @@ moe_status moe_expert_ffn_fp4(const void *buf_q, const void *buf_scale, const fl
                               void *workspace, size_t workspace_bytes, void *out,
                               int32_t *dev_status, void *stream);
 
+/*
+ * Rows sorted by expert ("dropless"): instead of an [e, c_max, m] buffer with a
+ * capacity, one [n, m] buffer in which expert j has the rows offsets[j] ..
+ * offsets[j+1]-1.  No route is dropped and no row is padding.  n is the caller's
+ * (s*k always suffices) and at most 2^31 - 1024; rows from offsets[e] on belong
+ * to no expert: no call reads them as data or writes them.
+ *
+ * moe_sort_routes: the order of the routes of idx [k, s], which is stable: the
+ * rows of an expert are its routes in route-priority order (as
+ * moe_capacity_locations ranks them).
+ *   offsets [e+1]: offsets[0] = 0, offsets[j+1] - offsets[j] = routes of expert j;
+ *   rows [k, s]: rows[r, t] = the row of route r of token t;
+ *   source [k*s] or NULL: the route r*s + t of each row, -1 behind the last row.
+ * An idx of -1 is a route without an expert (a padded token, an expert that is
+ * not held here): it gets no row, rows = -1.  Any other idx outside [0, e)
+ * stores MOE_ERR_INVALID_ARG in dev_status.  Deterministic.  k may exceed e here
+ * (an expert may be named twice by a token: two rows).  workspace:
+ * moe_sort_workspace_size() bytes, scratch.
+ */
+size_t moe_sort_workspace_size(int64_t s, int e, int k);
+moe_status moe_sort_routes(const int32_t *idx, int64_t s, int e, int k, int32_t *rows,
+                           int32_t *offsets, int32_t *source, void *workspace,
+                           size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * The tokens' rows on their way in: out[rows[r,t], :] = x[t, :], or, with gates
+ * (NULL: none), gates[r,t] * x[t, :] (the exact product rounded once).
+ * x [s, m], out [n, m] in `dt`; rows [k, s] as moe_sort_routes writes them (each
+ * row at most once; -1: no row); gates [k, s] fp32.  In this call and the next
+ * three a rows entry outside [-1, n) stores MOE_ERR_INVALID_ARG in dev_status, the
+ * gate of a route without a row is not used, and 1 <= k <= 32.
+ */
+moe_status moe_encode_sorted(const void *x, moe_dtype dt, const int32_t *rows, const float *gates,
+                             int64_t s, int m, int k, int64_t n, void *out, int32_t *dev_status,
+                             void *stream);
+
+/*
+ * Gradient of moe_encode_sorted: d_x[t, :] = sum over the token's rows of
+ * gates[r,t] * d_out[rows[r,t], :] (gates NULL: the plain sum), in fp32 in
+ * ascending r from +0 with fused multiply-adds, rounded once; and, with d_gates
+ * (needs gates and x, else NULL), d_gates[r,t] = <x[t, :], d_out[rows[r,t], :]> in
+ * fp32 in an order fixed by the shape, 0 for a route without a row.
+ */
+moe_status moe_encode_sorted_bwd(const void *d_out, const void *x, moe_dtype dt,
+                                 const int32_t *rows, const float *gates, int64_t s, int m, int k,
+                                 int64_t n, void *d_x, float *d_gates, int32_t *dev_status,
+                                 void *stream);
+
+/*
+ * The way back: y[t, :] = sum over the token's rows of gates[r,t] *
+ * xs[rows[r,t], :] (gates NULL: the plain sum), in fp32 in ascending r from +0 with
+ * fused multiply-adds, rounded once; 0 for a token without rows.
+ */
+moe_status moe_decode_sorted(const void *xs, moe_dtype dt, const int32_t *rows, const float *gates,
+                             int64_t s, int m, int k, int64_t n, void *y, int32_t *dev_status,
+                             void *stream);
+
+/*
+ * Gradient of moe_decode_sorted with gates: d_xs[rows[r,t], :] = gates[r,t] *
+ * dy[t, :] (one rounding; rows of no route are not written), d_gates[r,t] =
+ * <dy[t, :], xs[rows[r,t], :]> in fp32, 0 for a route without a row.  (Without
+ * gates, d_xs is moe_encode_sorted of dy.)
+ */
+moe_status moe_decode_sorted_bwd(const void *dy, const void *xs, moe_dtype dt, const int32_t *rows,
+                                 const float *gates, int64_t s, int m, int k, int64_t n,
+                                 void *d_xs, float *d_gates, int32_t *dev_status, void *stream);
+
+/*
+ * The expert FFN (moe_expert_ffn, _train) on sorted rows: for every expert j and
+ * its rows i,
+ *   hid[i,:] = act(x[i,:] W1[j]^T + b1[j]), or silu(x W1^T) * (x W3^T) (SwiGLU);
+ *   out[i,:] = hid[i,:] W2[j]^T + b2[j],
+ * fp32 accumulation; hid [n, h] is an output, rounded to bf16, and what the second
+ * product reads.  pre (NULL: not kept): the pre-activation [n, h], SwiGLU's a and b
+ * [n, 2h], rounded to bf16, for moe_expert_ffn_sorted_bwd.  x, out [n, m]; offsets
+ * [e+1] int32 on the device, ascending from 0 to at most n (else, in every call on
+ * sorted rows, MOE_ERR_INVALID_ARG in dev_status and unspecified rows inside the
+ * buffers); weights and biases as moe_expert_ffn.  bf16 only.
+ */
+moe_status moe_expert_ffn_sorted(const void *x, moe_dtype dt, const int32_t *offsets,
+                                 const void *w1, const void *b1, const void *w3, const void *w2,
+                                 const void *b2, moe_act act, int e, int64_t n, int m, int h,
+                                 void *hid, void *pre, void *out, int32_t *dev_status,
+                                 void *stream);
+
+/* Bytes of device workspace moe_expert_ffn_sorted_bwd needs (0: bad shape). */
+size_t moe_expert_ffn_sorted_bwd_workspace_size(moe_act act, int e, int64_t n, int m, int h);
+
+/*
+ * Gradient of moe_expert_ffn_sorted from what it kept (hid, pre), as
+ * moe_expert_ffn_bwd_saved: d_x [n, m] (other rows not written) and the weights' and
+ * biases' gradients in wgrad_dt (MOE_BF16 or MOE_F32), zeros for an expert without
+ * rows.  d_pre = (d_out W2) * act'(pre) is rounded to bf16 as the operand of the
+ * products after it; sums in fp32.  d_b1, d_b2 may be NULL.
+ */
+moe_status moe_expert_ffn_sorted_bwd(const void *x, const void *hid, const void *pre, moe_dtype dt,
+                                     const int32_t *offsets, const void *w1, const void *w3,
+                                     const void *w2, moe_act act, int e, int64_t n, int m, int h,
+                                     const void *d_out, void *workspace, size_t workspace_bytes,
+                                     void *d_x, moe_dtype wgrad_dt, void *d_w1, void *d_w3,
+                                     void *d_w2, void *d_b1, void *d_b2, int32_t *dev_status,
+                                     void *stream);
+
 /* Bytes of device workspace moe_layer_forward needs. */
 size_t moe_layer_workspace_size(moe_dtype dt, moe_act act, int64_t s, int m, int e, int k,
                                 int64_t c_max, int h);
