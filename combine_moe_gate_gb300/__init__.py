@@ -12,7 +12,8 @@ Functions keep the C names:
     moe_route_topk, moe_route_bwd,
     moe_quantize_fp4, moe_dequantize_fp4, moe_product_fp4, moe_expert_ffn_fp4,
     moe_sort_routes, moe_encode_sorted, moe_encode_sorted_bwd, moe_decode_sorted,
-    moe_decode_sorted_bwd, moe_expert_ffn_sorted, moe_expert_ffn_sorted_bwd
+    moe_decode_sorted_bwd, moe_expert_ffn_sorted, moe_expert_ffn_sorted_bwd,
+    moe_quantize_rows_int8, moe_product_int8, moe_expert_ffn_int8
 plus the size queries and `MoEError`.
 """
 
@@ -103,6 +104,11 @@ def load():
         "moe_expert_ffn_sorted_bwd_workspace_size": (SZ, [I, I, I64, I, I]),
         "moe_expert_ffn_sorted_bwd": (I, [P, P, P, I, P, P, P, P, I, I, I64, I, I, P, P, SZ, P, I, P, P, P,
                                           P, P, P, P]),
+        "moe_quantize_rows_int8": (I, [P, I, P, I64, I, I, I64, P, P, P, P]),
+        "moe_product_int8_workspace_size": (SZ, [I, I64, I, I]),
+        "moe_product_int8": (I, [P, P, P, P, P, P, I, I64, I, I, P, SZ, P, I, P, P]),
+        "moe_expert_ffn_int8_workspace_size": (SZ, [I, I, I64, I, I]),
+        "moe_expert_ffn_int8": (I, [P, P, P, P, P, P, P, P, P, P, P, I, I, I64, I, I, P, SZ, P, P, P]),
         "moe_status_str": (ctypes.c_char_p, [I]),
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_debug_stall_gemms": (I, [I]),
@@ -484,6 +490,66 @@ def moe_expert_ffn_sorted_bwd(x, hid, pre, offsets, w1, w3, w2, act, d_out, work
         _dt(d_w1), _ptr(d_w1, "d_w1", gdt, (e, h, m)), _ptr(d_w3, "d_w3", gdt, (e, h, m)),
         _ptr(d_w2, "d_w2", gdt, (e, m, h)), _ptr(d_b1, "d_b1", gdt, (e, h)), _ptr(d_b2, "d_b2", gdt, (e, m)),
         _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_expert_ffn_sorted_bwd")
+
+
+# ----------------------------------------------------- 8-bit integer operands
+def moe_quantize_rows_int8(src, q, scale, dev_status, rows=None, stream=None):
+    """8-bit codes (int8) and a scale for each row of src [..., cols] (bf16 or
+    fp32); with rows [k, s] of src [s, cols], into the sorted rows of q [n, cols]
+    and scale [n]."""
+    cols = src.shape[-1]
+    s = src.numel() // cols if cols else 0
+    I, F = _i32(), _f32()
+    if rows is None:
+        k, n = 0, s
+        qs, ss = tuple(src.shape), tuple(src.shape[:-1])
+    else:
+        k, n = rows.shape[0], q.shape[0]
+        s, cols = src.shape
+        qs, ss = (n, cols), (n,)
+    _check(load().moe_quantize_rows_int8(
+        _ptr(src, "src"), _dt(src), _ptr(rows, "rows", I, (k, s)), s, cols, k, n, _ptr(q, "q", torch.int8, qs),
+        _ptr(scale, "scale", F, ss), _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_quantize_rows_int8")
+
+
+def moe_product_int8_workspace_size(e, n, k, n_out) -> int:
+    return int(load().moe_product_int8_workspace_size(int(e), int(n), int(k), int(n_out)))
+
+
+def moe_product_int8(a_q, a_scale, offsets, b_q, b_scale, bias, workspace, out, dev_status, stream=None):
+    """out [n, n_out] (bf16 or fp32) = the rows a_q [n, k] times their experts'
+    b_q [e, n_out, k] (int8, scales [n] and [e, n_out]) + bias [e, n_out] bf16 or
+    None; offsets [e + 1] or None (e = 1: all rows)."""
+    n, k = a_q.shape
+    e, n_out, _ = b_q.shape
+    I, F, I8 = _i32(), _f32(), torch.int8
+    _check(load().moe_product_int8(
+        _ptr(a_q, "a_q", I8), _ptr(a_scale, "a_scale", F, (n,)), _ptr(offsets, "offsets", I, (e + 1,)),
+        _ptr(b_q, "b_q", I8, (e, n_out, k)), _ptr(b_scale, "b_scale", F, (e, n_out)),
+        _ptr(bias, "bias", torch.bfloat16, (e, n_out)), e, n, k, n_out, _ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _ptr(out, "out", None, (n, n_out)), _dt(out),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_product_int8")
+
+
+def moe_expert_ffn_int8_workspace_size(act, e, n, m, h) -> int:
+    return int(load().moe_expert_ffn_int8_workspace_size(_act(act), int(e), int(n), int(m), int(h)))
+
+
+def moe_expert_ffn_int8(x_q, x_scale, offsets, w1_q, w1_scale, b1, w3_q, w3_scale, w2_q, w2_scale, b2, act, workspace,
+                        out, dev_status, stream=None):
+    """The expert FFN on 8-bit rows x_q [n, m] and weights (int8, a scale for each
+    row and output channel); out [n, m] bf16; w3 and its scales for SwiGLU only,
+    which takes no biases; offsets [e + 1] or None (e = 1)."""
+    n, m = x_q.shape
+    e, h, _ = w1_q.shape
+    I, F, I8, bf = _i32(), _f32(), torch.int8, torch.bfloat16
+    _check(load().moe_expert_ffn_int8(
+        _ptr(x_q, "x_q", I8), _ptr(x_scale, "x_scale", F, (n,)), _ptr(offsets, "offsets", I, (e + 1,)),
+        _ptr(w1_q, "w1_q", I8, (e, h, m)), _ptr(w1_scale, "w1_scale", F, (e, h)), _ptr(b1, "b1", bf, (e, h)),
+        _ptr(w3_q, "w3_q", I8, (e, h, m)), _ptr(w3_scale, "w3_scale", F, (e, h)), _ptr(w2_q, "w2_q", I8, (e, m, h)),
+        _ptr(w2_scale, "w2_scale", F, (e, m)), _ptr(b2, "b2", bf, (e, m)), _act(act), e, n, m, h,
+        _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), _ptr(out, "out", bf, (n, m)),
+        _ptr(dev_status, "dev_status", I), _stream(stream)), "moe_expert_ffn_int8")
 
 
 # ------------------------------------------------- microscaled 4-bit operands

@@ -102,6 +102,17 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
                              const void *pre = nullptr, bool wgrad_f32 = false,
                              SortedRows so = {});
 size_t ffn_tc_sorted_bwd_workspace_bytes(moe_act act, int e, int64_t n, int m, int h);
+moe_status quantize_rows_int8_launch(const void *src, moe_dtype sdt, const int32_t *rows, int64_t s, int cols, int k,
+                                     int64_t n, void *q, float *scale, int32_t *st, cudaStream_t stream);
+size_t product_int8_workspace_bytes(int64_t n, int k);
+moe_status product_int8_launch(const void *a_q, const float *a_scale, const SortedRows &so, const void *b_q,
+                               const float *b_scale, const void *bias, int e, int k, int n_out, void *ws, void *out,
+                               bool f32, int32_t *st, cudaStream_t stream);
+size_t ffn_int8_workspace_bytes(int64_t n, int m, int h);
+moe_status ffn_int8_launch(const void *x_q, const float *x_scale, const SortedRows &so, const void *w1_q,
+                           const float *w1_scale, const void *b1, const void *w3_q, const float *w3_scale,
+                           const void *w2_q, const float *w2_scale, const void *b2, moe_act act, int e, int m, int h,
+                           void *ws, void *out, int32_t *st, cudaStream_t stream);
 size_t sort_workspace_bytes(int64_t s, int e, int k);
 moe_status sort_routes_launch(const int32_t *idx, int64_t s, int e, int k, int32_t *rows, int32_t *offsets,
                               int32_t *source, void *ws, int32_t *st, cudaStream_t stream);
@@ -506,6 +517,73 @@ moe_status moe_expert_ffn_sorted_bwd(const void *x, const void *hid, const void 
     return ffn_tc_bwd_launch(x, hid, nullptr, nullptr, w1, nullptr, w3, w2, act, e, n, m, h, d_out, workspace, d_x,
                              d_w1, d_w3, d_w2, d_b1, d_b2, dev_status, as_stream(stream), pre, wgrad_dt == MOE_F32,
                              SortedRows{offsets, n});
+}
+
+// --------------------------------------------------- 8-bit integer experts
+namespace {
+
+bool int8_shape_ok(int e, int64_t n, int k, int n_out) {
+    return e >= 1 && e <= kMaxE && n >= 1 && k >= 16 && k % 16 == 0 && n_out >= 8 && n_out % 8 == 0;
+}
+
+// k: int32 holds any sum of 8-bit products; the rest within the grouped product's indexes
+bool int8_supported(int e, int64_t n, int k, int n_out) {
+    return k < 1 << 17 && n <= kMaxRows && (int64_t)e * n_out < (int64_t)1 << 31 &&
+           (n / 192 + e) * ((n_out + 127) / 128) < (int64_t)1 << 31;
+}
+
+}  // namespace
+
+moe_status moe_quantize_rows_int8(const void *src, moe_dtype sdt, const int32_t *rows, int64_t s, int cols, int k,
+                                  int64_t n, void *q, float *scale, int32_t *dev_status, void *stream) {
+    if (!valid_dt(sdt) || s < 1 || s > kMaxRows || cols < 16 || cols % 16 || n < 1 || n > kMaxRows || !ok16(src) ||
+        !ok16(q) || !ok4(scale) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (rows ? !ok4(rows) || k < 1 || k > kMaxK || s > kMaxRows / k : k != 0 || n != s) return MOE_ERR_INVALID_ARG;
+    return quantize_rows_int8_launch(src, sdt, rows, s, cols, k, n, q, scale, dev_status, as_stream(stream));
+}
+
+size_t moe_product_int8_workspace_size(int e, int64_t n, int k, int n_out) {
+    if (!int8_shape_ok(e, n, k, n_out) || !int8_supported(e, n, k, n_out)) return 0;
+    return product_int8_workspace_bytes(n, k);
+}
+
+moe_status moe_product_int8(const void *a_q, const float *a_scale, const int32_t *offsets, const void *b_q,
+                            const float *b_scale, const void *bias, int e, int64_t n, int k, int n_out,
+                            void *workspace, size_t workspace_bytes, void *out, moe_dtype odt, int32_t *dev_status,
+                            void *stream) {
+    if (!int8_shape_ok(e, n, k, n_out) || !valid_dt(odt) || !ok16(a_q) || !ok4(a_scale) ||
+        (offsets ? !ok4(offsets) : e != 1) || !ok16(b_q) || !ok4(b_scale) || !opt16(bias) || !ok16(workspace) ||
+        !ok16(out) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (!int8_supported(e, n, k, n_out)) return MOE_ERR_UNSUPPORTED;
+    if (workspace_bytes < product_int8_workspace_bytes(n, k)) return MOE_ERR_INVALID_ARG;
+    return product_int8_launch(a_q, a_scale, SortedRows{offsets, n}, b_q, b_scale, bias, e, k, n_out, workspace, out,
+                               odt == MOE_F32, dev_status, as_stream(stream));
+}
+
+size_t moe_expert_ffn_int8_workspace_size(moe_act act, int e, int64_t n, int m, int h) {
+    if (!act_ok(act) || m % 16 || !int8_shape_ok(e, n, m, h) || !int8_shape_ok(e, n, h, m) ||
+        !int8_supported(e, n, m, h) || !int8_supported(e, n, h, m))
+        return 0;
+    return ffn_int8_workspace_bytes(n, m, h);
+}
+
+moe_status moe_expert_ffn_int8(const void *x_q, const float *x_scale, const int32_t *offsets, const void *w1_q,
+                               const float *w1_scale, const void *b1, const void *w3_q, const float *w3_scale,
+                               const void *w2_q, const float *w2_scale, const void *b2, moe_act act, int e, int64_t n,
+                               int m, int h, void *workspace, size_t workspace_bytes, void *out, int32_t *dev_status,
+                               void *stream) {
+    if (!act_ok(act) || !int8_shape_ok(e, n, m, h) || !int8_shape_ok(e, n, h, m) || !ok16(x_q) || !ok4(x_scale) ||
+        (offsets ? !ok4(offsets) : e != 1) || !ok16(w1_q) || !ok4(w1_scale) || !opt16(b1) || !ok16(w2_q) ||
+        !ok4(w2_scale) || !opt16(b2) || !ok16(workspace) || !ok16(out) || !ok4(dev_status))
+        return MOE_ERR_INVALID_ARG;
+    if (act == MOE_ACT_SWIGLU ? !ok16(w3_q) || !ok4(w3_scale) || b1 || b2 : w3_q || w3_scale)
+        return MOE_ERR_INVALID_ARG;
+    if (!int8_supported(e, n, m, h) || !int8_supported(e, n, h, m)) return MOE_ERR_UNSUPPORTED;
+    if (workspace_bytes < ffn_int8_workspace_bytes(n, m, h)) return MOE_ERR_INVALID_ARG;
+    return ffn_int8_launch(x_q, x_scale, SortedRows{offsets, n}, w1_q, w1_scale, b1, w3_q, w3_scale, w2_q, w2_scale, b2,
+                           act, e, m, h, workspace, out, dev_status, as_stream(stream));
 }
 
 size_t moe_layer_workspace_size(moe_dtype dt, moe_act act, int64_t s, int m, int e, int k,

@@ -1,0 +1,508 @@
+// Grouped products of 8-bit integer rows and weights on the tensor cores.  Included by ffn_tc.cu,
+// whose barrier, copy and TMEM helpers it shares.
+//
+//   out[i, :] = act(s_x[i] s_w[j] (X[i] W[j]^T) + bias[j])   for the rows i of every expert j
+//
+// sm_103a has no integer tcgen05 (kind::i8), and its mma.sync integers run at a small part of the
+// 16-bit rate.  Every 8-bit integer is an fp16 number, and a product of two is exact in fp32, so the
+// products run as kind::f16 on fp16 operands with fp32 sums: exact while a partial sum is below
+// 2^24 (always for K <= 1024), otherwise with fp32's rounding.  The weights stay 8-bit in memory and
+// in shared memory and become fp16 on the way from there to TMEM, where the MMA reads them as its A
+// operand; the rows (few bytes beside the weights, or reused by many weight tiles) are widened once
+// before.  So a stage costs shared memory 8 KB of weights in and out and 12 KB of rows in and out per
+// 64 of K and SM, 320 clocks at 128 bytes a clock, against 384 clocks of MMA.
+//
+// One persistent kernel on CTA pairs, tiles of 256 output channels (M: 128 a CTA) by up to 192 rows
+// (N, a multiple of 32 that the expert's rows are cut into evenly), 512 threads a CTA:
+//   warp 0       weights: 128 x 128 bytes a stage
+//   warp 2       rows: this CTA's half of the tile's rows, boxes of 32 rows x 64 fp16
+//   warps 4-11   widen: two groups of four warps take the stage's two halves of 64 K; a lane reads its
+//                channel's 64 bytes and writes 32 TMEM columns
+//   warp 1       allocates TMEM; in the even CTA issues the pair's MMAs (A from TMEM, K = 16 each)
+//   warps 12-15  epilogue: TMEM holds channels by rows, so a lane has one channel's scale and bias;
+//                the block is turned in shared memory and stored as rows
+// TMEM: two accumulators of 192 columns, four stages of A of 32 columns.
+#pragma once
+
+#include "int8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int I8_NT = 192;                       // rows per tile at most
+constexpr int I8_BK = 128;                       // K per stage
+constexpr int I8_W_BYTES = UM * I8_BK;           // weights of a stage, one CTA
+constexpr int I8_BOX = 32;                       // rows of one row copy
+constexpr int I8_BOX_BYTES = I8_BOX * 128;       // 64 fp16 each
+constexpr int I8_XH_BYTES = I8_NT / 2 * 128;     // rows of half a stage, one CTA
+constexpr int I8_X_BYTES = 2 * I8_XH_BYTES;
+constexpr int I8_STAGES = 5;
+constexpr int I8_ASTAGES = 4;                    // halves of 64 K in TMEM
+constexpr uint32_t I8_A_COL = 2 * I8_NT;         // their first column
+constexpr int I8_CVT0 = 4, I8_EPI0 = 12;         // first warp of the two roles
+constexpr int I8_THREADS = 512;
+constexpr int I8_STG_BYTES = 32 * 32 * 4;        // output staging per epilogue warp
+static_assert(I8_A_COL + I8_ASTAGES * 32 <= TMEM_COLS, "TMEM");
+
+// A wait for a parity is sound while its barrier cannot get two phases ahead of the waiter; the
+// next phase of every barrier needs each of its waiters:
+//   wfull (copies): waited for by the CTA's 8 widening warps, each of which then arrives at wempty;
+//     wempty (8): waited for by the weights' producer, who issues the next copies.
+//   xfull (even CTA: its rows' producer, and the bytes of both CTAs): waited for by the MMA issuer, whose
+//     commit is xempty (per CTA): waited for by that CTA's producer, without whose bytes the next xfull
+//     does not come.  (A tile has N / 2 rows for each CTA, N at least 32, so both always copy.)
+//   afull (even CTA: the stage's 4 widening warps of both CTAs): waited for by the MMA issuer, whose
+//     commit is aempty (per CTA): waited for by those 4 warps (stage a always belongs to group a % 2).
+//   dfull (a commit, per CTA): waited for by its 4 epilogue warps, each of which then arrives at dempty
+//     (even CTA, 8): waited for by the MMA issuer.   drain: one phase.
+// All roles of both CTAs go through the same tiles.
+struct I8Ctl {
+    uint64_t wfull[I8_STAGES], wempty[I8_STAGES];
+    uint64_t xfull[I8_STAGES], xempty[I8_STAGES];
+    uint64_t afull[I8_ASTAGES], aempty[I8_ASTAGES];
+    uint64_t dfull[2], dempty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort;
+    int32_t total_tiles;
+    int32_t tile_start[MAX_E + 1];
+};
+
+constexpr size_t I8_SMEM = 1024 + (size_t)I8_STAGES * (I8_W_BYTES + I8_X_BYTES) + 4 * I8_STG_BYTES + sizeof(I8Ctl);
+static_assert(I8_SMEM <= 227 * 1024 - 1024, "shared memory");
+
+struct I8Args {
+    SortedRows so;               // offsets null: one expert has all n rows
+    int32_t *status;
+    const float *x_scale;        // [n]
+    const float *w_scale;        // [e, n_out]
+    const float *w3_scale;       // SwiGLU
+    const __nv_bfloat16 *bias;   // [e, n_out] or nullptr
+    void *out;                   // [n, n_out]
+    int e;
+    int K;
+    int n_out;
+    int32_t stall;               // tests: the producers issue no copies
+};
+
+struct I8Tile {
+    int j, ct, row0, rows, n;    // expert, channel tile, first row, live rows, N
+};
+
+__device__ __forceinline__ void i8_rows(const I8Args &a, int j, int64_t &first, int64_t &count) {
+    if (a.so.offsets) {
+        sorted_span(a.so, j, first, count);
+    } else {
+        first = 0;
+        count = a.so.n;
+    }
+}
+
+// Tile t; an expert's row tiles vary fastest, so neighbouring CTAs read the same weights.
+__device__ __forceinline__ I8Tile i8_tile(const I8Args &a, const int32_t *tile_start, int t) {
+    int lo = 0, hi = a.e;   // largest j with tile_start[j] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tile_start[mid] <= t) lo = mid; else hi = mid;
+    }
+    I8Tile T;
+    T.j = lo;
+    int64_t first, count;
+    i8_rows(a, lo, first, count);
+    const int rows = (int)count, tiles = (rows + I8_NT - 1) / I8_NT, local = t - tile_start[lo];
+    // even cuts: as rows > 192 (tiles - 1), none of the tiles is empty
+    const int per = ((rows + tiles - 1) / tiles + 31) & ~31;
+    T.ct = local / tiles;
+    const int rt = local - T.ct * tiles;
+    T.row0 = (int)first + rt * per;
+    T.rows = min(per, rows - rt * per);
+    T.n = (T.rows + 31) & ~31;
+    return T;
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 2-SM MMA with A (fp16, two a column, lane = row) in both CTAs' TMEM.
+__device__ __forceinline__ void umma_pair_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on the even CTA's mbarrier once this thread's TMEM stores are done (cluster scope: the
+// other CTA's MMA issuer reads behind it).
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ float i8_relu(float v) { return v < 0.0f ? 0.0f : v; }   // a NaN stays one
+
+template <int EPI, typename OUT>
+__global__ void __launch_bounds__(I8_THREADS, 1)
+i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW3,
+              const __grid_constant__ CUtensorMap tmX, const I8Args args) {
+    constexpr bool SWI = EPI == I8_SWIGLU;
+    constexpr int CH = SWI ? 64 : UM;             // output channels per CTA and tile
+    __shared__ int32_t s_bad;
+    pdl_enter();
+    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
+    __syncthreads();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sW = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sX = sW + I8_STAGES * I8_W_BYTES;
+    uint8_t *stg_all = sX + I8_STAGES * I8_X_BYTES;
+    I8Ctl *ctl = (I8Ctl *)(stg_all + 4 * I8_STG_BYTES);
+    __shared__ __align__(16) float s_scale[4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int tile0 = blockIdx.x / 2, tile_step = gridDim.x / 2;
+    const int nct = (args.n_out + 2 * CH - 1) / (2 * CH);
+    const int nk = (args.K + I8_BK - 1) / I8_BK;
+
+    if (warp == 0) {
+        int run = 0;
+        for (int base = 0; base < args.e; base += 32) {
+            const int j = base + lane;
+            int own = 0;
+            if (j < args.e) {
+                int64_t first, count;
+                i8_rows(args, j, first, count);
+                if (args.so.offsets) {
+                    const int lo = args.so.offsets[j], hi = args.so.offsets[j + 1];
+                    if (lo < 0 || hi < lo || hi > args.so.n) set_status(args.status, MOE_ERR_INVALID_ARG);
+                }
+                own = ((int)count + I8_NT - 1) / I8_NT * nct;
+            }
+            int v = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (j < args.e) ctl->tile_start[j] = run + v - own;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) {
+            ctl->tile_start[args.e] = run;
+            ctl->total_tiles = run;
+            ctl->abort = 0;
+            for (int s = 0; s < I8_STAGES; s++) {
+                mbar_init(&ctl->wfull[s], 1);
+                mbar_init(&ctl->wempty[s], 8);
+                mbar_init(&ctl->xfull[s], 1);
+                mbar_init(&ctl->xempty[s], 1);
+            }
+            for (int s = 0; s < I8_ASTAGES; s++) {
+                mbar_init(&ctl->afull[s], 8);
+                mbar_init(&ctl->aempty[s], 1);
+            }
+            for (int s = 0; s < 2; s++) {
+                mbar_init(&ctl->dfull[s], 1);
+                mbar_init(&ctl->dempty[s], 8);
+            }
+            mbar_init(&ctl->drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    int total = ctl->total_tiles;
+    {
+        int any_bad = 0;   // the same decision in both CTAs
+        for (uint32_t r = 0; r < 2; r++) {
+            int b;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(b) : "r"(map_to_rank(su32(&s_bad), r)));
+            any_bad |= b;
+        }
+        if (any_bad) total = 0;
+    }
+    int32_t *abort_flag = &ctl->abort;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
+                const I8Tile T = i8_tile(args, ctl->tile_start, t);
+                const int ch = T.j * args.n_out + T.ct * 2 * CH + (int)rank * CH;
+                for (int kb = 0; kb < nk; kb++) {
+                    if (!mbar_wait(&ctl->wempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
+                    mbar_expect_tx(&ctl->wfull[s], I8_W_BYTES);
+                    tma_load_2d(sW + s * I8_W_BYTES, &tmW, kb * I8_BK, ch, &ctl->wfull[s]);
+                    if (SWI)
+                        tma_load_2d(sW + s * I8_W_BYTES + I8_W_BYTES / 2, &tmW3, kb * I8_BK, ch, &ctl->wfull[s]);
+                    if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
+                const I8Tile T = i8_tile(args, ctl->tile_start, t);
+                const int half = T.n / 2, boxes = (half + I8_BOX - 1) / I8_BOX;
+                const int r0 = T.row0 + (int)rank * half;
+                for (int kb = 0; kb < nk; kb++) {
+                    if (!mbar_wait<true>(&ctl->xempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
+                    const uint32_t fb = map_to_rank(su32(&ctl->xfull[s]), 0);
+                    if (rank == 0) mbar_expect_tx(&ctl->xfull[s], 2 * 2 * boxes * I8_BOX_BYTES);
+                    for (int hf = 0; hf < 2; hf++)
+                        for (int b = 0; b < boxes; b++)
+                            tma_load_2d_pair(sX + s * I8_X_BYTES + hf * I8_XH_BYTES + b * I8_BOX_BYTES, &tmX,
+                                             kb * I8_BK + hf * 64, r0 + b * I8_BOX, fb);
+                    if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            if (rank == 0) {
+                int s = 0, acc = 0, a = 0;
+                uint32_t ph = 0, aph = 0, accph = 0;
+                bool ok = true;
+                for (int t = tile0; t < total && ok; t += tile_step) {
+                    const I8Tile T = i8_tile(args, ctl->tile_start, t);
+                    const uint32_t idesc = (1u << 4) | ((uint32_t)(T.n >> 3) << 17) | ((uint32_t)((2 * UM) >> 4) << 24);
+                    if (!mbar_wait<true>(&ctl->dempty[acc], accph ^ 1u, abort_flag, args.status)) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(acc * I8_NT);
+                    for (int kb = 0; kb < nk && ok; kb++) {
+                        if (!mbar_wait<true>(&ctl->xfull[s], ph, abort_flag, args.status)) { ok = false; break; }
+                        for (int hf = 0; hf < 2; hf++) {
+                            if (!mbar_wait<true>(&ctl->afull[a], aph, abort_flag, args.status)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint32_t b0 = su32(sX + s * I8_X_BYTES + hf * I8_XH_BYTES);
+                            const uint32_t a0 = tmem + I8_A_COL + (uint32_t)(a * 32);
+#pragma unroll
+                            for (int kk = 0; kk < 4; kk++)
+                                umma_pair_ts(d, a0 + kk * 8, sdesc<128>(b0 + kk * 32), idesc, (kb | hf | kk) != 0);
+                            umma_commit_pair(&ctl->aempty[a], (uint16_t)3u);
+                            if (++a == I8_ASTAGES) { a = 0; aph ^= 1u; }
+                        }
+                        if (!ok) break;
+                        umma_commit_pair(&ctl->xempty[s], (uint16_t)3u);
+                        if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair(&ctl->dfull[acc], (uint16_t)3u);
+                    if (++acc == 2) { acc = 0; accph ^= 1u; }
+                }
+                umma_commit_pair(&ctl->drain, (uint16_t)3u);
+            }
+            unsigned long long t0 = gtimer();
+            while (!mbar_try<true>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
+            }
+        }
+    } else if (warp >= I8_CVT0 && warp < I8_EPI0) {
+        // ------------------------------------------------------------- widen
+        const int g = (warp - I8_CVT0) >> 2, quarter = warp & 3;
+        const int row = SWI ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane) : quarter * 32 + lane;
+        const uint32_t ta = tmem + I8_A_COL + ((uint32_t)(quarter * 32) << 16);
+        int s = 0, a = g;                  // this group's TMEM stages: g, g + 2
+        uint32_t ph = 0, aph = 0;
+        bool ok = true;
+        for (int t = tile0; t < total && ok; t += tile_step) {
+            for (int kb = 0; kb < nk; kb++) {
+                ok = mbar_wait(&ctl->wfull[s], ph, abort_flag, args.status);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint8_t *src = sW + s * I8_W_BYTES + row * 128;
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + (((g * 4 + c) ^ (row & 7)) << 4));
+                    i8_widen(v.x, r[8 * c], r[8 * c + 1]);
+                    i8_widen(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    i8_widen(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    i8_widen(v.w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->wempty[s]);
+                ok = mbar_wait<true>(&ctl->aempty[a], aph ^ 1u, abort_flag, args.status);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                tmem_st32(ta + (uint32_t)(a * 32), r);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_release_cluster(map_to_rank(su32(&ctl->afull[a]), 0));
+                a += 2;
+                if (a >= I8_ASTAGES) { a = g; aph ^= 1u; }
+                if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+    } else if (warp >= I8_EPI0) {
+        // ---------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        uint8_t *stg = stg_all + quarter * I8_STG_BYTES;
+        float *ssc = s_scale[quarter];
+        int acc = 0;
+        uint32_t accph = 0;
+        for (int t = tile0; t < total; t += tile_step) {
+            const I8Tile T = i8_tile(args, ctl->tile_start, t);
+            // this warp's first output channel, and this lane's
+            const int ch0 = T.ct * 2 * CH + (int)rank * CH + quarter * (CH / 4);
+            const int ch = ch0 + (SWI ? lane & 15 : lane);
+            float sb = 0.0f, bias = 0.0f;
+            if (ch < args.n_out) {
+                const int64_t at = (int64_t)T.j * args.n_out + ch;
+                sb = SWI && lane >= 16 ? args.w3_scale[at] : args.w_scale[at];
+                if (!SWI && args.bias) bias = __bfloat162float(args.bias[at]);
+            }
+            const bool ok = mbar_wait<true>(&ctl->dfull[acc], accph, abort_flag, args.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * I8_NT);
+            for (int c0 = 0; c0 < T.n; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld32(tb + (uint32_t)c0, r);
+                const int left = T.rows - c0;          // live rows of this block (32 or fewer)
+                ssc[lane] = lane < left ? args.x_scale[(int64_t)T.row0 + c0 + lane] : 0.0f;
+                __syncwarp();
+                tmem_wait_ld(r);
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 sa = *reinterpret_cast<const float4 *>(ssc + i);
+                    v[i] = __fmaf_rn(__uint_as_float(r[i]), sa.x * sb, bias);
+                    v[i + 1] = __fmaf_rn(__uint_as_float(r[i + 1]), sa.y * sb, bias);
+                    v[i + 2] = __fmaf_rn(__uint_as_float(r[i + 2]), sa.z * sb, bias);
+                    v[i + 3] = __fmaf_rn(__uint_as_float(r[i + 3]), sa.w * sb, bias);
+                }
+                if constexpr (SWI) {
+                    // lane l < 16 holds a, lane l + 16 b of a channel: the first takes rows 0-15, the
+                    // second rows 16-31
+                    __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(stg);
+                    const bool up = lane >= 16;
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 16], 16);
+                        const float ga = up ? other : v[i], gb = up ? v[i + 16] : other;
+                        sp[(i + (lane & 16)) * 16 + (lane & 15)] = __float2bfloat16_rn(silu(ga) * gb);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int q = lane; q < 64; q += 32) {
+                        const int row = q >> 1, part = (q & 1) * 8;
+                        if (row < left && ch0 + part < args.n_out)
+                            *reinterpret_cast<uint4 *>((__nv_bfloat16 *)args.out +
+                                                       ((int64_t)T.row0 + c0 + row) * args.n_out + ch0 + part) =
+                                *reinterpret_cast<const uint4 *>(sp + row * 16 + part);
+                    }
+                } else {
+                    OUT *sp = reinterpret_cast<OUT *>(stg);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 a = make_float2(v[i], v[i + 1]);
+                        if (EPI == I8_GELU) a = gelu_erf2(a);
+                        if (EPI == I8_RELU) a = make_float2(i8_relu(a.x), i8_relu(a.y));
+                        if constexpr (sizeof(OUT) == 2) {
+                            sp[i * 32 + lane] = __float2bfloat16_rn(a.x);
+                            sp[(i + 1) * 32 + lane] = __float2bfloat16_rn(a.y);
+                        } else {
+                            sp[i * 32 + lane] = a.x;
+                            sp[(i + 1) * 32 + lane] = a.y;
+                        }
+                    }
+                    __syncwarp();
+                    constexpr int PER = 16 / sizeof(OUT), PARTS = 32 / PER;   // values and pieces of a row
+#pragma unroll
+                    for (int q = lane; q < 32 * PARTS; q += 32) {
+                        const int row = q / PARTS, part = (q % PARTS) * PER;
+                        if (row < left && ch0 + part < args.n_out)
+                            *reinterpret_cast<uint4 *>((OUT *)args.out + ((int64_t)T.row0 + c0 + row) * args.n_out +
+                                                       ch0 + part) =
+                                *reinterpret_cast<const uint4 *>(sp + row * 32 + part);
+                    }
+                }
+                __syncwarp();   // staging and scales are rewritten for the next block
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->dempty[acc]), 0));
+            if (++acc == 2) { acc = 0; accph ^= 1u; }
+        }
+    }
+
+    __syncwarp();   // the elected lanes are back
+    tc_fence_before();
+    if (*(volatile int32_t *)abort_flag) {   // copies may still be landing: they take microseconds
+        unsigned long long t0 = gtimer();
+        while (gtimer() - t0 < 1000000ull) {
+        }
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+template <int EPI, typename OUT>
+moe_status launch_i8(const void *x16, const void *w, const void *w3, I8Args args, cudaStream_t stream) {
+    args.stall = take_gemm_stall() ? 1 : 0;
+    constexpr bool SWI = EPI == I8_SWIGLU;
+    constexpr int CH = SWI ? 64 : UM;
+    CUtensorMap mW, mW3, mX;
+    if (!make_map_u8(&mW, w, (uint64_t)args.e * args.n_out, (uint64_t)args.K, CH) ||
+        !make_map_u8(&mW3, SWI ? w3 : w, (uint64_t)args.e * args.n_out, (uint64_t)args.K, CH) ||
+        !make_map(&mX, x16, (uint64_t)args.so.n, (uint64_t)args.K, I8_BOX, 64))   // fp16: 16-bit elements
+        return MOE_ERR_CUDA;
+    auto kern = i8_group_gemm<EPI, OUT>;
+    static int units[64] = {0};   // resident clusters per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    int nunits = dev >= 0 && dev < 64 ? units[dev] : 0;
+    if (!nunits) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)I8_SMEM) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        nunits = max_clusters(kern, I8_SMEM, 2, I8_THREADS);
+        if (dev >= 0 && dev < 64) units[dev] = nunits;
+    }
+    const int64_t nct = (args.n_out + 2 * CH - 1) / (2 * CH);
+    const int64_t upper = (args.so.n / I8_NT + (args.so.n < args.e ? args.so.n : args.e)) * nct;
+    const int64_t grid = upper < nunits ? upper : nunits;
+    return launch_cluster_pdl(kern, dim3((unsigned)(2 * grid)), dim3(I8_THREADS), I8_SMEM, 2, stream, mW, mW3, mX,
+                              args);
+}
+
+}  // namespace
+
+// out [n, n_out] (bf16, or fp32 when f32: the plain product only) from the rows' codes as fp16 numbers.
+moe_status i8_gemm_launch(const void *x16, const float *x_scale, const SortedRows &so, const void *w,
+                          const float *w_scale, const void *w3, const float *w3_scale, const void *bias, int epi,
+                          bool f32, int e, int K, int n_out, void *out, int32_t *st, cudaStream_t stream) {
+    I8Args g{so, st, x_scale, w_scale, w3_scale, (const __nv_bfloat16 *)bias, out, e, K, n_out, 0};
+    switch (epi) {
+        case I8_RELU: return launch_i8<I8_RELU, __nv_bfloat16>(x16, w, w3, g, stream);
+        case I8_GELU: return launch_i8<I8_GELU, __nv_bfloat16>(x16, w, w3, g, stream);
+        case I8_SWIGLU: return launch_i8<I8_SWIGLU, __nv_bfloat16>(x16, w, w3, g, stream);
+        default:
+            return f32 ? launch_i8<I8_BIAS, float>(x16, w, w3, g, stream)
+                       : launch_i8<I8_BIAS, __nv_bfloat16>(x16, w, w3, g, stream);
+    }
+}
+
+}  // namespace moe

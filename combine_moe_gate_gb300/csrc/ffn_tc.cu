@@ -1304,10 +1304,10 @@ int sm_count() {
 // Resident clusters of `cl` CTAs of a kernel with this configuration (the
 // GPCs bound how many clusters of ~200 KB-shared-memory CTAs fit at once).
 template <typename K>
-int max_clusters(K kern, size_t smem, int cl) {
+int max_clusters(K kern, size_t smem, int cl, int threads = NUM_THREADS) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cl);
-    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1815,3 +1815,4 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
 
 // The products of microscaled 4-bit operands (they share the helpers above).
 #include "ffn_fp4.cuh"
+#include "ffn_int8.cuh"   // and those of 8-bit integers

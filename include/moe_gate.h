@@ -635,6 +635,64 @@ moe_status moe_expert_ffn_sorted_bwd(const void *x, const void *hid, const void 
                                      void *d_w2, void *d_b1, void *d_b2, int32_t *dev_status,
                                      void *stream);
 
+/*
+ * 8-bit integer rows, one fp32 scale each: value = code * scale,
+ *   scale = amax / 127,  code = round(x * (127 / amax)) to nearest even,
+ * in fp32 (both quotients and the product rounded); codes 0 and scale 1 for a row
+ * whose largest magnitude amax is below 2^-100, codes 0 and a NaN scale for a row
+ * that holds an infinity or a NaN.
+ *
+ * moe_quantize_rows_int8: src [s, cols] in `sdt`, cols a multiple of 16.
+ *   rows NULL: q [s, cols] int8, scale [s]; k = 0 and n = s then;
+ *   rows [k, s] (moe_sort_routes): the codes and scale of token t go to the rows
+ *   rows[r, t] of q [n, cols], scale [n], as moe_encode_sorted moves rows (the
+ *   tokens are read once); other rows are not written.
+ * Weights [e, rows, cols] are quantised per output channel as e * rows rows.
+ */
+moe_status moe_quantize_rows_int8(const void *src, moe_dtype sdt, const int32_t *rows, int64_t s,
+                                  int cols, int k, int64_t n, void *q, float *scale,
+                                  int32_t *dev_status, void *stream);
+
+/* Bytes of device workspace moe_product_int8 needs (0: bad shape). */
+size_t moe_product_int8_workspace_size(int e, int64_t n, int k, int n_out);
+
+/*
+ * Grouped product of 8-bit integers on sorted rows: for every expert j and its
+ * rows i (offsets as moe_expert_ffn_sorted; NULL with e = 1: all n rows)
+ *   out[i,:] = a_scale[i] b_scale[j,:] (sum_k a_q[i,k] b_q[j,:,k]) + bias[j,:],
+ * rounded once to `odt`.  a_q [n, k] int8 with a_scale [n]; b_q [e, n_out, k] int8
+ * with b_scale [e, n_out] (one per output channel); bias [e, n_out] bf16 or NULL;
+ * out [n, n_out].  Codes may take all of -128 .. 127.  The sum is exact up to 8 rows
+ * in all, and otherwise while its partial sums stay below 2^24 (for k <= 1024
+ * always); beyond it is an fp32 sum.  k a multiple of 16 below 2^17, n_out a multiple
+ * of 8.
+ */
+moe_status moe_product_int8(const void *a_q, const float *a_scale, const int32_t *offsets,
+                            const void *b_q, const float *b_scale, const void *bias, int e,
+                            int64_t n, int k, int n_out, void *workspace, size_t workspace_bytes,
+                            void *out, moe_dtype odt, int32_t *dev_status, void *stream);
+
+/* Bytes of device workspace moe_expert_ffn_int8 needs (0: bad shape). */
+size_t moe_expert_ffn_int8_workspace_size(moe_act act, int e, int64_t n, int m, int h);
+
+/*
+ * The expert FFN on 8-bit integer operands and sorted rows: for every expert's rows
+ *   hid = bf16(act(x . w1^T + b1)), or bf16(silu(x . w1^T) * (x . w3^T)) (SwiGLU, no
+ *         biases), quantised by rows as moe_quantize_rows_int8 does;
+ *   out = bf16(hid . w2^T + b2),
+ * the products as moe_product_int8 forms them.  x_q [n, m], x_scale [n]; w1, w3
+ * [e, h, m], w2 [e, m, h] int8 with scales [e, h], [e, h], [e, m]; b1 [e, h], b2
+ * [e, m] bf16 or NULL; out [n, m] bf16.  m and h multiples of 16 below 2^17.
+ * Workspace: the hidden [n, h] bf16, then, from the next 256-byte boundary, its
+ * scales [n]; a caller may read them after the call.
+ */
+moe_status moe_expert_ffn_int8(const void *x_q, const float *x_scale, const int32_t *offsets,
+                               const void *w1_q, const float *w1_scale, const void *b1,
+                               const void *w3_q, const float *w3_scale, const void *w2_q,
+                               const float *w2_scale, const void *b2, moe_act act, int e, int64_t n,
+                               int m, int h, void *workspace, size_t workspace_bytes, void *out,
+                               int32_t *dev_status, void *stream);
+
 /* Bytes of device workspace moe_layer_forward needs. */
 size_t moe_layer_workspace_size(moe_dtype dt, moe_act act, int64_t s, int m, int e, int k,
                                 int64_t c_max, int h);
