@@ -16,12 +16,12 @@
 // (N, a multiple of 32 that the expert's rows are cut into evenly), 512 threads a CTA:
 //   warp 0       weights: 128 x 128 bytes a stage
 //   warp 2       rows: this CTA's half of the tile's rows, boxes of 32 rows x 64 fp16
-//   warps 4-11   widen: two groups of four warps take the stage's two halves of 64 K; a lane reads its
+//   warps 4-11   widen: two groups of four warps take a stage's two halves of 64 K; a lane reads its
 //                channel's 64 bytes and writes 32 TMEM columns
 //   warp 1       allocates TMEM; in the even CTA issues the pair's MMAs (A from TMEM, K = 16 each)
 //   warps 12-15  epilogue: TMEM holds channels by rows, so a lane has one channel's scale and bias;
 //                the block is turned in shared memory and stored as rows
-// TMEM: two accumulators of 192 columns, four stages of A of 32 columns.
+// TMEM: two accumulators of 192 columns, two stages of A of 64 columns.
 #pragma once
 
 #include "int8.cuh"
@@ -37,29 +37,29 @@ constexpr int I8_BOX_BYTES = I8_BOX * 128;       // 64 fp16 each
 constexpr int I8_XH_BYTES = I8_NT / 2 * 128;     // rows of half a stage, one CTA
 constexpr int I8_X_BYTES = 2 * I8_XH_BYTES;
 constexpr int I8_STAGES = 5;
-constexpr int I8_ASTAGES = 4;                    // halves of 64 K in TMEM
+constexpr int I8_SLOTS = 2;                      // stages of A in TMEM, 64 columns each
 constexpr uint32_t I8_A_COL = 2 * I8_NT;         // their first column
 constexpr int I8_CVT0 = 4, I8_EPI0 = 12;         // first warp of the two roles
 constexpr int I8_THREADS = 512;
 constexpr int I8_STG_BYTES = 32 * 32 * 4;        // output staging per epilogue warp
-static_assert(I8_A_COL + I8_ASTAGES * 32 <= TMEM_COLS, "TMEM");
+static_assert(I8_A_COL + I8_SLOTS * 64 <= TMEM_COLS && I8_SLOTS < I8_STAGES, "TMEM");
 
-// A wait for a parity is sound while its barrier cannot get two phases ahead of the waiter; the
-// next phase of every barrier needs each of its waiters:
+// Step i of the pair (a stage of K) uses the barriers i % STAGES and the TMEM slot i % SLOTS.  A wait
+// for a parity is sound while its barrier cannot get two phases ahead of the waiter; the next phase of
+// every barrier needs each of its waiters:
 //   wfull (copies): waited for by the CTA's 8 widening warps, each of which then arrives at wempty;
 //     wempty (8): waited for by the weights' producer, who issues the next copies.
-//   xfull (even CTA: its rows' producer, and the bytes of both CTAs): waited for by the MMA issuer, whose
-//     commit is xempty (per CTA): waited for by that CTA's producer, without whose bytes the next xfull
-//     does not come.  (A tile has N / 2 rows for each CTA, N at least 32, so both always copy.)
-//   afull (even CTA: the stage's 4 widening warps of both CTAs): waited for by the MMA issuer, whose
-//     commit is aempty (per CTA): waited for by those 4 warps (stage a always belongs to group a % 2).
+//   full (even CTA: 16 widening warps and the rows' producer, with the bytes of both CTAs): waited for by
+//     the MMA issuer.  (A tile has N / 2 rows for each CTA, N at least 32, so both always copy.)
+//   empty (per CTA, a commit after the step's MMAs): waited for by the rows' producer before step
+//     i + STAGES and by the 8 widening warps before they write the slot in step i + SLOTS; the barrier's
+//     next phase is that of the MMAs of step i + STAGES, whose full needs all of them.
 //   dfull (a commit, per CTA): waited for by its 4 epilogue warps, each of which then arrives at dempty
 //     (even CTA, 8): waited for by the MMA issuer.   drain: one phase.
 // All roles of both CTAs go through the same tiles.
 struct I8Ctl {
     uint64_t wfull[I8_STAGES], wempty[I8_STAGES];
-    uint64_t xfull[I8_STAGES], xempty[I8_STAGES];
-    uint64_t afull[I8_ASTAGES], aempty[I8_ASTAGES];
+    uint64_t full[I8_STAGES], empty[I8_STAGES];
     uint64_t dfull[2], dempty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -142,10 +142,36 @@ __device__ __forceinline__ void umma_pair_ts(uint32_t d, uint32_t a, uint64_t b,
         : "memory");
 }
 
-// Arrive on the even CTA's mbarrier once this thread's TMEM stores are done (cluster scope: the
-// other CTA's MMA issuer reads behind it).
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Whether the phase with `parity` is complete, without waiting.
+template <bool CL>
+__device__ __forceinline__ bool mbar_test(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    if (CL)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(b)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(b)), "r"(parity)
+            : "memory");
+    return ok != 0;
+}
+
+// mbar_wait for the waits on the way of every 64 of K: the clock is read only after some tries.
+template <bool CL>
+__device__ __forceinline__ bool i8_wait(uint64_t *b, uint32_t parity, int32_t *abort_flag, int32_t *status) {
+#pragma unroll 1
+    for (int i = 0; i < 64; i++)
+        if (mbar_try<CL>(b, parity)) return true;
+    return mbar_wait<CL>(b, parity, abort_flag, status);
 }
 
 __device__ __forceinline__ float i8_relu(float v) { return v < 0.0f ? 0.0f : v; }   // a NaN stays one
@@ -202,12 +228,8 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             for (int s = 0; s < I8_STAGES; s++) {
                 mbar_init(&ctl->wfull[s], 1);
                 mbar_init(&ctl->wempty[s], 8);
-                mbar_init(&ctl->xfull[s], 1);
-                mbar_init(&ctl->xempty[s], 1);
-            }
-            for (int s = 0; s < I8_ASTAGES; s++) {
-                mbar_init(&ctl->afull[s], 8);
-                mbar_init(&ctl->aempty[s], 1);
+                mbar_init(&ctl->full[s], 17);
+                mbar_init(&ctl->empty[s], 1);
             }
             for (int s = 0; s < 2; s++) {
                 mbar_init(&ctl->dfull[s], 1);
@@ -247,7 +269,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const I8Tile T = i8_tile(args, ctl->tile_start, t);
                 const int ch = T.j * args.n_out + T.ct * 2 * CH + (int)rank * CH;
                 for (int kb = 0; kb < nk; kb++) {
-                    if (!mbar_wait(&ctl->wempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
+                    if (!i8_wait<false>(&ctl->wempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
                     mbar_expect_tx(&ctl->wfull[s], I8_W_BYTES);
                     tma_load_2d(sW + s * I8_W_BYTES, &tmW, kb * I8_BK, ch, &ctl->wfull[s]);
                     if (SWI)
@@ -266,9 +288,9 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const int half = T.n / 2, boxes = (half + I8_BOX - 1) / I8_BOX;
                 const int r0 = T.row0 + (int)rank * half;
                 for (int kb = 0; kb < nk; kb++) {
-                    if (!mbar_wait<true>(&ctl->xempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
-                    const uint32_t fb = map_to_rank(su32(&ctl->xfull[s]), 0);
-                    if (rank == 0) mbar_expect_tx(&ctl->xfull[s], 2 * 2 * boxes * I8_BOX_BYTES);
+                    if (!i8_wait<true>(&ctl->empty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
+                    const uint32_t fb = map_to_rank(su32(&ctl->full[s]), 0);
+                    if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * 2 * boxes * I8_BOX_BYTES);
                     for (int hf = 0; hf < 2; hf++)
                         for (int b = 0; b < boxes; b++)
                             tma_load_2d_pair(sX + s * I8_X_BYTES + hf * I8_XH_BYTES + b * I8_BOX_BYTES, &tmX,
@@ -280,31 +302,30 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     } else if (warp == 1) {
         if (lane == 0) {
             if (rank == 0) {
-                int s = 0, acc = 0, a = 0;
-                uint32_t ph = 0, aph = 0, accph = 0;
-                bool ok = true;
+                int s = 0, acc = 0, slot = 0;
+                uint32_t ph = 0, accph = 0;
+                bool ok = true, ready = false;   // ready: the next step's full was seen
                 for (int t = tile0; t < total && ok; t += tile_step) {
                     const I8Tile T = i8_tile(args, ctl->tile_start, t);
                     const uint32_t idesc = (1u << 4) | ((uint32_t)(T.n >> 3) << 17) | ((uint32_t)((2 * UM) >> 4) << 24);
-                    if (!mbar_wait<true>(&ctl->dempty[acc], accph ^ 1u, abort_flag, args.status)) break;
-                    tc_fence_after();
+                    if (!i8_wait<true>(&ctl->dempty[acc], accph ^ 1u, abort_flag, args.status)) break;
                     const uint32_t d = tmem + (uint32_t)(acc * I8_NT);
-                    for (int kb = 0; kb < nk && ok; kb++) {
-                        if (!mbar_wait<true>(&ctl->xfull[s], ph, abort_flag, args.status)) { ok = false; break; }
-                        for (int hf = 0; hf < 2; hf++) {
-                            if (!mbar_wait<true>(&ctl->afull[a], aph, abort_flag, args.status)) { ok = false; break; }
-                            tc_fence_after();
-                            const uint32_t b0 = su32(sX + s * I8_X_BYTES + hf * I8_XH_BYTES);
-                            const uint32_t a0 = tmem + I8_A_COL + (uint32_t)(a * 32);
+                    for (int kb = 0; kb < nk; kb++) {
+                        if (!ready && !i8_wait<true>(&ctl->full[s], ph, abort_flag, args.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t b0 = sdesc<128>(su32(sX + s * I8_X_BYTES));
+                        const uint32_t a0 = tmem + I8_A_COL + (uint32_t)(slot * 64);
+                        // a look at the next step's barrier travels while this step's MMAs are issued
+                        const int sn = s + 1 == I8_STAGES ? 0 : s + 1;
+                        ready = mbar_test<true>(&ctl->full[sn], sn ? ph : ph ^ 1u);
 #pragma unroll
-                            for (int kk = 0; kk < 4; kk++)
-                                umma_pair_ts(d, a0 + kk * 8, sdesc<128>(b0 + kk * 32), idesc, (kb | hf | kk) != 0);
-                            umma_commit_pair(&ctl->aempty[a], (uint16_t)3u);
-                            if (++a == I8_ASTAGES) { a = 0; aph ^= 1u; }
-                        }
-                        if (!ok) break;
-                        umma_commit_pair(&ctl->xempty[s], (uint16_t)3u);
-                        if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                        for (int kk = 0; kk < 8; kk++)
+                            umma_pair_ts(d, a0 + kk * 8,
+                                         b0 + (((kk >> 2) * I8_XH_BYTES + (kk & 3) * 32) >> 4), idesc, (kb | kk) != 0);
+                        umma_commit_pair(&ctl->empty[s], (uint16_t)3u);
+                        if (++slot == I8_SLOTS) slot = 0;
+                        s = sn;
+                        if (s == 0) ph ^= 1u;
                     }
                     if (!ok) break;
                     umma_commit_pair(&ctl->dfull[acc], (uint16_t)3u);
@@ -321,12 +342,13 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         const int g = (warp - I8_CVT0) >> 2, quarter = warp & 3;
         const int row = SWI ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane) : quarter * 32 + lane;
         const uint32_t ta = tmem + I8_A_COL + ((uint32_t)(quarter * 32) << 16);
-        int s = 0, a = g;                  // this group's TMEM stages: g, g + 2
-        uint32_t ph = 0, aph = 0;
+        int s = 0, slot = 0, se = 0;      // se: the barrier of the step that last used the slot
+        uint32_t ph = 0, eph = 0;
+        int64_t step = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t += tile_step) {
-            for (int kb = 0; kb < nk; kb++) {
-                ok = mbar_wait(&ctl->wfull[s], ph, abort_flag, args.status);
+            for (int kb = 0; kb < nk; kb++, step++) {
+                ok = i8_wait<false>(&ctl->wfull[s], ph, abort_flag, args.status);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const uint8_t *src = sW + s * I8_W_BYTES + row * 128;
                 uint32_t r[32];
@@ -340,16 +362,18 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->wempty[s]);
-                ok = mbar_wait<true>(&ctl->aempty[a], aph ^ 1u, abort_flag, args.status);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (step >= I8_SLOTS) {
+                    ok = i8_wait<true>(&ctl->empty[se], eph, abort_flag, args.status);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    if (++se == I8_STAGES) { se = 0; eph ^= 1u; }
+                }
                 tc_fence_after();
-                tmem_st32(ta + (uint32_t)(a * 32), r);
+                tmem_st32(ta + (uint32_t)(slot * 64 + g * 32), r);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_release_cluster(map_to_rank(su32(&ctl->afull[a]), 0));
-                a += 2;
-                if (a >= I8_ASTAGES) { a = g; aph ^= 1u; }
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->full[s]), 0));
+                if (++slot == I8_SLOTS) slot = 0;
                 if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
             }
         }
@@ -371,7 +395,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 sb = SWI && lane >= 16 ? args.w3_scale[at] : args.w_scale[at];
                 if (!SWI && args.bias) bias = __bfloat162float(args.bias[at]);
             }
-            const bool ok = mbar_wait<true>(&ctl->dfull[acc], accph, abort_flag, args.status);
+            const bool ok = i8_wait<true>(&ctl->dfull[acc], accph, abort_flag, args.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * I8_NT);
