@@ -66,10 +66,11 @@ struct I8Ctl {
     int32_t abort;
     int32_t total_tiles;
     int32_t tile_start[MAX_E + 1];
+    int32_t first[MAX_E + 1];    // the offsets, inside the buffer and ascending
 };
 
 constexpr size_t I8_SMEM = 1024 + (size_t)I8_STAGES * (I8_W_BYTES + I8_X_BYTES) + 4 * I8_STG_BYTES + sizeof(I8Ctl);
-static_assert(I8_SMEM <= 227 * 1024 - 1024, "shared memory");
+static_assert(I8_SMEM <= 227 * 1024 - 600, "shared memory");   // and what is not dynamic
 
 struct I8Args {
     SortedRows so;               // offsets null: one expert has all n rows
@@ -89,32 +90,22 @@ struct I8Tile {
     int j, ct, row0, rows, n;    // expert, channel tile, first row, live rows, N
 };
 
-__device__ __forceinline__ void i8_rows(const I8Args &a, int j, int64_t &first, int64_t &count) {
-    if (a.so.offsets) {
-        sorted_span(a.so, j, first, count);
-    } else {
-        first = 0;
-        count = a.so.n;
-    }
-}
-
 // Tile t; an expert's row tiles vary fastest, so neighbouring CTAs read the same weights.
-__device__ __forceinline__ I8Tile i8_tile(const I8Args &a, const int32_t *tile_start, int t) {
-    int lo = 0, hi = a.e;   // largest j with tile_start[j] <= t
+__device__ __forceinline__ I8Tile i8_tile(const I8Ctl *ctl, int e, int t) {
+    int lo = 0, hi = e;   // largest j with tile_start[j] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tile_start[mid] <= t) lo = mid; else hi = mid;
+        if (ctl->tile_start[mid] <= t) lo = mid; else hi = mid;
     }
     I8Tile T;
     T.j = lo;
-    int64_t first, count;
-    i8_rows(a, lo, first, count);
-    const int rows = (int)count, tiles = (rows + I8_NT - 1) / I8_NT, local = t - tile_start[lo];
+    const int first = ctl->first[lo], rows = ctl->first[lo + 1] - first;
+    const int tiles = (rows + I8_NT - 1) / I8_NT, local = t - ctl->tile_start[lo];
     // even cuts: as rows > 192 (tiles - 1), none of the tiles is empty
     const int per = ((rows + tiles - 1) / tiles + 31) & ~31;
     T.ct = local / tiles;
     const int rt = local - T.ct * tiles;
-    T.row0 = (int)first + rt * per;
+    T.row0 = first + rt * per;
     T.rows = min(per, rows - rt * per);
     T.n = (T.rows + 31) & ~31;
     return T;
@@ -132,13 +123,36 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
-// 2-SM MMA with A (fp16, two a column, lane = row) in both CTAs' TMEM.
-__device__ __forceinline__ void umma_pair_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One lane of the warp (the same at each call): 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t i8_elect() {
+    uint32_t one;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one;
+}
+
+// 2-SM MMA with A (fp16, two a column, lane = row) in both CTAs' TMEM, by the lane with `one`.
+__device__ __forceinline__ void umma_pair_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                             uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_pair_one(uint64_t *bar, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            su32(bar)),
+        "h"((uint16_t)3u), "r"(one)
         : "memory");
 }
 
@@ -200,18 +214,21 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 
     if (warp == 0) {
         int run = 0;
+        bool bad = false;
+        for (int base = 0; base <= args.e; base += 32) {
+            const int j = base + lane;
+            if (j <= args.e) {
+                const int o = args.so.offsets ? args.so.offsets[j] : j ? (int)args.so.n : 0;
+                if (o < 0 || o > args.so.n || (args.so.offsets && j && o < args.so.offsets[j - 1])) bad = true;
+                ctl->first[j] = o;
+            }
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad) set_status(args.status, MOE_ERR_INVALID_ARG);   // and no tiles
+        __syncwarp();
         for (int base = 0; base < args.e; base += 32) {
             const int j = base + lane;
-            int own = 0;
-            if (j < args.e) {
-                int64_t first, count;
-                i8_rows(args, j, first, count);
-                if (args.so.offsets) {
-                    const int lo = args.so.offsets[j], hi = args.so.offsets[j + 1];
-                    if (lo < 0 || hi < lo || hi > args.so.n) set_status(args.status, MOE_ERR_INVALID_ARG);
-                }
-                own = ((int)count + I8_NT - 1) / I8_NT * nct;
-            }
+            const int own = j < args.e && !bad ? (ctl->first[j + 1] - ctl->first[j] + I8_NT - 1) / I8_NT * nct : 0;
             int v = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -266,7 +283,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             uint32_t ph = 0;
             bool ok = true;
             for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
-                const I8Tile T = i8_tile(args, ctl->tile_start, t);
+                const I8Tile T = i8_tile(ctl, args.e, t);
                 const int ch = T.j * args.n_out + T.ct * 2 * CH + (int)rank * CH;
                 for (int kb = 0; kb < nk; kb++) {
                     if (!i8_wait<false>(&ctl->wempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
@@ -284,7 +301,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             uint32_t ph = 0;
             bool ok = true;
             for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
-                const I8Tile T = i8_tile(args, ctl->tile_start, t);
+                const I8Tile T = i8_tile(ctl, args.e, t);
                 const int half = T.n / 2, boxes = (half + I8_BOX - 1) / I8_BOX;
                 const int r0 = T.row0 + (int)rank * half;
                 for (int kb = 0; kb < nk; kb++) {
@@ -300,42 +317,47 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            if (rank == 0) {
-                int s = 0, acc = 0, slot = 0;
-                uint32_t ph = 0, accph = 0;
-                bool ok = true, ready = false;   // ready: the next step's full was seen
-                for (int t = tile0; t < total && ok; t += tile_step) {
-                    const I8Tile T = i8_tile(args, ctl->tile_start, t);
-                    const uint32_t idesc = (1u << 4) | ((uint32_t)(T.n >> 3) << 17) | ((uint32_t)((2 * UM) >> 4) << 24);
-                    if (!i8_wait<true>(&ctl->dempty[acc], accph ^ 1u, abort_flag, args.status)) break;
-                    const uint32_t d = tmem + (uint32_t)(acc * I8_NT);
-                    for (int kb = 0; kb < nk; kb++) {
-                        if (!ready && !i8_wait<true>(&ctl->full[s], ph, abort_flag, args.status)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint64_t b0 = sdesc<128>(su32(sX + s * I8_X_BYTES));
-                        const uint32_t a0 = tmem + I8_A_COL + (uint32_t)(slot * 64);
-                        // a look at the next step's barrier travels while this step's MMAs are issued
-                        const int sn = s + 1 == I8_STAGES ? 0 : s + 1;
-                        ready = mbar_test<true>(&ctl->full[sn], sn ? ph : ph ^ 1u);
+        // The whole warp goes along and one lane's instructions count: in a branch of one lane the
+        // descriptors would be moved to uniform registers for every MMA (about 95 clocks each).
+        if (rank == 0) {
+            const uint32_t one = i8_elect();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t x0 = sdesc<128>(__shfl_sync(0xffffffffu, su32(sX), 0));
+            int s = 0, acc = 0, slot = 0;
+            uint32_t ph = 0, accph = 0;
+            bool ok = true, ready = false;   // ready: the next step's full was seen
+            for (int t = tile0; t < total && ok; t += tile_step) {
+                const int n = __shfl_sync(0xffffffffu, i8_tile(ctl, args.e, t).n, 0);
+                const uint32_t idesc = (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((2 * UM) >> 4) << 24);
+                ok = i8_wait<true>(&ctl->dempty[acc], accph ^ 1u, abort_flag, args.status);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint32_t d = tm + (uint32_t)(acc * I8_NT);
+                for (int kb = 0; kb < nk; kb++) {
+                    ok = ready || i8_wait<true>(&ctl->full[s], ph, abort_flag, args.status);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t b0 = x0 + (uint64_t)(s * (I8_X_BYTES >> 4));
+                    const uint32_t a0 = tm + I8_A_COL + (uint32_t)(slot * 64);
+                    // a look at the next step's barrier travels while this step's MMAs are issued
+                    const int sn = s + 1 == I8_STAGES ? 0 : s + 1;
+                    ready = mbar_test<true>(&ctl->full[sn], sn ? ph : ph ^ 1u);
 #pragma unroll
-                        for (int kk = 0; kk < 8; kk++)
-                            umma_pair_ts(d, a0 + kk * 8,
-                                         b0 + (((kk >> 2) * I8_XH_BYTES + (kk & 3) * 32) >> 4), idesc, (kb | kk) != 0);
-                        umma_commit_pair(&ctl->empty[s], (uint16_t)3u);
-                        if (++slot == I8_SLOTS) slot = 0;
-                        s = sn;
-                        if (s == 0) ph ^= 1u;
-                    }
-                    if (!ok) break;
-                    umma_commit_pair(&ctl->dfull[acc], (uint16_t)3u);
-                    if (++acc == 2) { acc = 0; accph ^= 1u; }
+                    for (int kk = 0; kk < 8; kk++)
+                        umma_pair_ts(d, a0 + kk * 8, b0 + (((kk >> 2) * I8_XH_BYTES + (kk & 3) * 32) >> 4), idesc,
+                                     (kb | kk) != 0, one);
+                    umma_commit_pair_one(&ctl->empty[s], one);
+                    if (++slot == I8_SLOTS) slot = 0;
+                    s = sn;
+                    if (s == 0) ph ^= 1u;
                 }
-                umma_commit_pair(&ctl->drain, (uint16_t)3u);
+                if (!ok) break;
+                umma_commit_pair_one(&ctl->dfull[acc], one);
+                if (++acc == 2) { acc = 0; accph ^= 1u; }
             }
-            unsigned long long t0 = gtimer();
-            while (!mbar_try<true>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
-            }
+            umma_commit_pair_one(&ctl->drain, one);
+        }
+        unsigned long long t0 = gtimer();
+        while (!mbar_try<true>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
         }
     } else if (warp >= I8_CVT0 && warp < I8_EPI0) {
         // ------------------------------------------------------------- widen
@@ -345,10 +367,10 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         int s = 0, slot = 0, se = 0;      // se: the barrier of the step that last used the slot
         uint32_t ph = 0, eph = 0;
         int64_t step = 0;
-        bool ok = true;
+        bool ok = true, ready = false;    // ready: the next step's weights were seen
         for (int t = tile0; t < total && ok; t += tile_step) {
             for (int kb = 0; kb < nk; kb++, step++) {
-                ok = i8_wait<false>(&ctl->wfull[s], ph, abort_flag, args.status);
+                ok = ready || i8_wait<false>(&ctl->wfull[s], ph, abort_flag, args.status);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const uint8_t *src = sW + s * I8_W_BYTES + row * 128;
                 uint32_t r[32];
@@ -362,6 +384,8 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->wempty[s]);
+                const int sn = s + 1 == I8_STAGES ? 0 : s + 1;
+                ready = mbar_test<false>(&ctl->wfull[sn], sn ? ph : ph ^ 1u);
                 if (step >= I8_SLOTS) {
                     ok = i8_wait<true>(&ctl->empty[se], eph, abort_flag, args.status);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -374,7 +398,8 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->full[s]), 0));
                 if (++slot == I8_SLOTS) slot = 0;
-                if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                s = sn;
+                if (s == 0) ph ^= 1u;
             }
         }
     } else if (warp >= I8_EPI0) {
@@ -385,7 +410,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         int acc = 0;
         uint32_t accph = 0;
         for (int t = tile0; t < total; t += tile_step) {
-            const I8Tile T = i8_tile(args, ctl->tile_start, t);
+            const I8Tile T = i8_tile(ctl, args.e, t);
             // this warp's first output channel, and this lane's
             const int ch0 = T.ct * 2 * CH + (int)rank * CH + quarter * (CH / 4);
             const int ch = ch0 + (SWI ? lane & 15 : lane);
