@@ -16,12 +16,18 @@
 // (N, a multiple of 32 that the expert's rows are cut into evenly), 512 threads a CTA:
 //   warp 0       weights: 128 x 128 bytes a stage
 //   warp 2       rows: this CTA's half of the tile's rows, boxes of 32 rows x 64 fp16
-//   warps 4-11   widen: two groups of four warps take a stage's two halves of 64 K; a lane reads its
-//                channel's 64 bytes and writes 32 TMEM columns
+//   warps 4-11   widen: two groups of four warps take the stages in turn; a lane reads its channel's
+//                128 bytes and writes 64 TMEM columns
 //   warp 1       allocates TMEM; in the even CTA issues the pair's MMAs (A from TMEM, K = 16 each)
 //   warps 12-15  epilogue: TMEM holds channels by rows, so a lane has one channel's scale and bias;
 //                the block is turned in shared memory and stored as rows
-// TMEM: two accumulators of 192 columns, two stages of A of 64 columns.
+// TMEM (512 columns), by the largest N of the launch's tiles: the way from a stage's MMAs over the widening
+// warps to the MMAs that read what they wrote takes about 2000 clocks (two barriers across the pair), so
+// three or four stages of A (64 columns each) have to be under way:
+//   N <= 64    accumulators at 0 and 64,   4 stages from 128
+//   N <= 128   accumulators at 0 and 128,  4 stages from 256
+//   N <= 192   accumulators at 0 and 128,  3 stages from 320: they share columns 128 .. 191, so the next
+//              tile's MMAs wait until the epilogue has read those
 #pragma once
 
 #include "int8.cuh"
@@ -36,40 +42,58 @@ constexpr int I8_BOX = 32;                       // rows of one row copy
 constexpr int I8_BOX_BYTES = I8_BOX * 128;       // 64 fp16 each
 constexpr int I8_XH_BYTES = I8_NT / 2 * 128;     // rows of half a stage, one CTA
 constexpr int I8_X_BYTES = 2 * I8_XH_BYTES;
-constexpr int I8_STAGES = 5;
-constexpr int I8_SLOTS = 2;                      // stages of A in TMEM, 64 columns each
-constexpr uint32_t I8_A_COL = 2 * I8_NT;         // their first column
+constexpr int I8_WST = 6, I8_XST = 4;            // stages of weights, of rows
+static_assert(I8_WST % 2 == 0 && (I8_XST & (I8_XST - 1)) == 0, "the widening groups take the stages in turn");
 constexpr int I8_CVT0 = 4, I8_EPI0 = 12;         // first warp of the two roles
 constexpr int I8_THREADS = 512;
 constexpr int I8_STG_BYTES = 32 * 32 * 4;        // output staging per epilogue warp
-static_assert(I8_A_COL + I8_SLOTS * 64 <= TMEM_COLS && I8_SLOTS < I8_STAGES, "TMEM");
 
-// Step i of the pair (a stage of K) uses the barriers i % STAGES and the TMEM slot i % SLOTS.  A wait
-// for a parity is sound while its barrier cannot get two phases ahead of the waiter; the next phase of
-// every barrier needs each of its waiters:
-//   wfull (copies): waited for by the CTA's 8 widening warps, each of which then arrives at wempty;
-//     wempty (8): waited for by the weights' producer, who issues the next copies.
-//   full (even CTA: 16 widening warps and the rows' producer, with the bytes of both CTAs): waited for by
-//     the MMA issuer.  (A tile has N / 2 rows for each CTA, N at least 32, so both always copy.)
+struct I8Layout {
+    uint32_t acc1, slot0;        // first column of the second accumulator, of the stages of A
+    int slots;                   // I8_XST or one fewer
+    bool shared;                 // the accumulators share columns [128, 192)
+};
+
+__device__ __forceinline__ I8Layout i8_layout(int max_n) {
+    if (max_n <= 64) return I8Layout{64, 128, 4, false};
+    if (max_n <= 128) return I8Layout{128, 256, 4, false};
+    return I8Layout{128, 320, 3, true};
+}
+
+// Step i of the pair (a stage of K) uses the weights' barriers i % WST, the rows' i % XST and the TMEM
+// slot i % slots.  A wait for a parity is sound while its barrier is neither two phases ahead of the
+// waiter (the next phase needs the waiter) nor one behind (the waiter has seen the phase before, or what
+// follows from it):
+//   wfull (copies): waited for by the 4 widening warps of the CTA that take step i (they took step i - WST
+//     as well), each of which then arrives at wempty; wempty (4): waited for by the weights' producer, who
+//     issues the next copies.
+//   full (even CTA: 4 widening warps of each CTA, and the rows' producer with the bytes of both):
+//     waited for by the MMA issuer.  (A tile has N / 2 rows for each CTA, N at least 32: both always copy.)
+//     A widening warp arrives for step i after the MMAs of step i - slots, so that of i - XST is complete.
 //   empty (per CTA, a commit after the step's MMAs): waited for by the rows' producer before step
-//     i + STAGES and by the 8 widening warps before they write the slot in step i + SLOTS; the barrier's
-//     next phase is that of the MMAs of step i + STAGES, whose full needs all of them.
+//     i + XST, whose MMAs are its next phase and need that producer; and by the widening warps of step
+//     i + slots before they write the slot.  With slots = XST a warp meets the same barrier every other turn
+//     and its next phase is that of the warp's own step.  With slots = XST - 1 it meets all of them: it
+//     looks at step i - 1's in passing, whose next phase is that of the warp's own step i + slots, so that
+//     it has seen every phase in order.
 //   dfull (a commit, per CTA): waited for by its 4 epilogue warps, each of which then arrives at dempty
-//     (even CTA, 8): waited for by the MMA issuer.   drain: one phase.
+//     (even CTA, 8), waited for by the MMA issuer, who commits the next dfull: two of each, by the tile's
+//     number.  drain: one phase.
 // All roles of both CTAs go through the same tiles.
 struct I8Ctl {
-    uint64_t wfull[I8_STAGES], wempty[I8_STAGES];
-    uint64_t full[I8_STAGES], empty[I8_STAGES];
+    uint64_t wfull[I8_WST], wempty[I8_WST];
+    uint64_t full[I8_XST], empty[I8_XST];
     uint64_t dfull[2], dempty[2];
     uint64_t drain;
     uint32_t tmem_base;
     int32_t abort;
     int32_t total_tiles;
+    int32_t max_n;               // largest N of any tile
     int32_t tile_start[MAX_E + 1];
     int32_t first[MAX_E + 1];    // the offsets, inside the buffer and ascending
 };
 
-constexpr size_t I8_SMEM = 1024 + (size_t)I8_STAGES * (I8_W_BYTES + I8_X_BYTES) + 4 * I8_STG_BYTES + sizeof(I8Ctl);
+constexpr size_t I8_SMEM = 1024 + (size_t)I8_WST * I8_W_BYTES + (size_t)I8_XST * I8_X_BYTES + 4 * I8_STG_BYTES + sizeof(I8Ctl);
 static_assert(I8_SMEM <= 227 * 1024 - 600, "shared memory");   // and what is not dynamic
 
 struct I8Args {
@@ -90,6 +114,9 @@ struct I8Tile {
     int j, ct, row0, rows, n;    // expert, channel tile, first row, live rows, N
 };
 
+// Rows of a tile: even cuts, a multiple of 32.  (As rows > 192 (tiles - 1), none of the tiles is empty.)
+__device__ __forceinline__ int i8_cut(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) & ~31; }
+
 // Tile t; an expert's row tiles vary fastest, so neighbouring CTAs read the same weights.
 __device__ __forceinline__ I8Tile i8_tile(const I8Ctl *ctl, int e, int t) {
     int lo = 0, hi = e;   // largest j with tile_start[j] <= t
@@ -101,8 +128,7 @@ __device__ __forceinline__ I8Tile i8_tile(const I8Ctl *ctl, int e, int t) {
     T.j = lo;
     const int first = ctl->first[lo], rows = ctl->first[lo + 1] - first;
     const int tiles = (rows + I8_NT - 1) / I8_NT, local = t - ctl->tile_start[lo];
-    // even cuts: as rows > 192 (tiles - 1), none of the tiles is empty
-    const int per = ((rows + tiles - 1) / tiles + 31) & ~31;
+    const int per = i8_cut(rows, tiles);
     T.ct = local / tiles;
     const int rt = local - T.ct * tiles;
     T.row0 = first + rt * per;
@@ -202,8 +228,8 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     __syncthreads();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sW = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *sX = sW + I8_STAGES * I8_W_BYTES;
-    uint8_t *stg_all = sX + I8_STAGES * I8_X_BYTES;
+    uint8_t *sX = sW + I8_WST * I8_W_BYTES;
+    uint8_t *stg_all = sX + I8_XST * I8_X_BYTES;
     I8Ctl *ctl = (I8Ctl *)(stg_all + 4 * I8_STG_BYTES);
     __shared__ __align__(16) float s_scale[4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -213,7 +239,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     const int nk = (args.K + I8_BK - 1) / I8_BK;
 
     if (warp == 0) {
-        int run = 0;
+        int run = 0, max_n = 0;
         bool bad = false;
         for (int base = 0; base <= args.e; base += 32) {
             const int j = base + lane;
@@ -228,7 +254,9 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         __syncwarp();
         for (int base = 0; base < args.e; base += 32) {
             const int j = base + lane;
-            const int own = j < args.e && !bad ? (ctl->first[j + 1] - ctl->first[j] + I8_NT - 1) / I8_NT * nct : 0;
+            const int rows = j < args.e && !bad ? ctl->first[j + 1] - ctl->first[j] : 0;
+            const int cuts = (rows + I8_NT - 1) / I8_NT, own = cuts * nct;
+            if (rows) max_n = max(max_n, i8_cut(rows, cuts));
             int v = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -238,14 +266,18 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             if (j < args.e) ctl->tile_start[j] = run + v - own;
             run += __shfl_sync(0xffffffffu, v, 31);
         }
+        max_n = __reduce_max_sync(0xffffffffu, max_n);
         if (lane == 0) {
+            ctl->max_n = max_n;
             ctl->tile_start[args.e] = run;
             ctl->total_tiles = run;
             ctl->abort = 0;
-            for (int s = 0; s < I8_STAGES; s++) {
+            for (int s = 0; s < I8_WST; s++) {
                 mbar_init(&ctl->wfull[s], 1);
-                mbar_init(&ctl->wempty[s], 8);
-                mbar_init(&ctl->full[s], 17);
+                mbar_init(&ctl->wempty[s], 4);
+            }
+            for (int s = 0; s < I8_XST; s++) {
+                mbar_init(&ctl->full[s], 9);
                 mbar_init(&ctl->empty[s], 1);
             }
             for (int s = 0; s < 2; s++) {
@@ -276,6 +308,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         if (any_bad) total = 0;
     }
     int32_t *abort_flag = &ctl->abort;
+    const I8Layout L = i8_layout(ctl->max_n);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -291,7 +324,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     tma_load_2d(sW + s * I8_W_BYTES, &tmW, kb * I8_BK, ch, &ctl->wfull[s]);
                     if (SWI)
                         tma_load_2d(sW + s * I8_W_BYTES + I8_W_BYTES / 2, &tmW3, kb * I8_BK, ch, &ctl->wfull[s]);
-                    if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                    if (++s == I8_WST) { s = 0; ph ^= 1u; }
                 }
             }
         }
@@ -312,7 +345,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                         for (int b = 0; b < boxes; b++)
                             tma_load_2d_pair(sX + s * I8_X_BYTES + hf * I8_XH_BYTES + b * I8_BOX_BYTES, &tmX,
                                              kb * I8_BK + hf * 64, r0 + b * I8_BOX, fb);
-                    if (++s == I8_STAGES) { s = 0; ph ^= 1u; }
+                    if (++s == I8_XST) { s = 0; ph ^= 1u; }
                 }
             }
         }
@@ -323,36 +356,39 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             const uint32_t one = i8_elect();
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint64_t x0 = sdesc<128>(__shfl_sync(0xffffffffu, su32(sX), 0));
-            int s = 0, acc = 0, slot = 0;
-            uint32_t ph = 0, accph = 0;
+            const uint32_t slot0 = __shfl_sync(0xffffffffu, L.slot0, 0), acc1 = __shfl_sync(0xffffffffu, L.acc1, 0);
+            const int slots = __shfl_sync(0xffffffffu, L.slots, 0);
+            int s = 0, slot = 0, i = 0;      // i: the pair's tiles so far
+            uint32_t ph = 0;
             bool ok = true, ready = false;   // ready: the next step's full was seen
-            for (int t = tile0; t < total && ok; t += tile_step) {
+            for (int t = tile0; t < total && ok; t += tile_step, i++) {
                 const int n = __shfl_sync(0xffffffffu, i8_tile(ctl, args.e, t).n, 0);
                 const uint32_t idesc = (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((2 * UM) >> 4) << 24);
-                ok = i8_wait<true>(&ctl->dempty[acc], accph ^ 1u, abort_flag, args.status);
+                // the accumulator's last tile is read, or (shared) the columns that the one before holds too
+                const int last = L.shared ? i - 1 : i - 2;
+                if (last >= 0) ok = i8_wait<true>(&ctl->dempty[last & 1], (last >> 1) & 1, abort_flag, args.status);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                const uint32_t d = tm + (uint32_t)(acc * I8_NT);
+                const uint32_t d = tm + (i & 1 ? acc1 : 0);
                 for (int kb = 0; kb < nk; kb++) {
                     ok = ready || i8_wait<true>(&ctl->full[s], ph, abort_flag, args.status);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t b0 = x0 + (uint64_t)(s * (I8_X_BYTES >> 4));
-                    const uint32_t a0 = tm + I8_A_COL + (uint32_t)(slot * 64);
+                    const uint32_t a0 = tm + slot0 + (uint32_t)(slot * 64);
                     // a look at the next step's barrier travels while this step's MMAs are issued
-                    const int sn = s + 1 == I8_STAGES ? 0 : s + 1;
+                    const int sn = (s + 1) & (I8_XST - 1);
                     ready = mbar_test<true>(&ctl->full[sn], sn ? ph : ph ^ 1u);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
                         umma_pair_ts(d, a0 + kk * 8, b0 + (((kk >> 2) * I8_XH_BYTES + (kk & 3) * 32) >> 4), idesc,
                                      (kb | kk) != 0, one);
                     umma_commit_pair_one(&ctl->empty[s], one);
-                    if (++slot == I8_SLOTS) slot = 0;
+                    if (++slot == slots) slot = 0;
                     s = sn;
                     if (s == 0) ph ^= 1u;
                 }
                 if (!ok) break;
-                umma_commit_pair_one(&ctl->dfull[acc], one);
-                if (++acc == 2) { acc = 0; accph ^= 1u; }
+                umma_commit_pair_one(&ctl->dfull[i & 1], one);
             }
             umma_commit_pair_one(&ctl->drain, one);
         }
@@ -363,53 +399,66 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         // ------------------------------------------------------------- widen
         const int g = (warp - I8_CVT0) >> 2, quarter = warp & 3;
         const int row = SWI ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane) : quarter * 32 + lane;
-        const uint32_t ta = tmem + I8_A_COL + ((uint32_t)(quarter * 32) << 16);
-        int s = 0, slot = 0, se = 0;      // se: the barrier of the step that last used the slot
-        uint32_t ph = 0, eph = 0;
-        int64_t step = 0;
-        bool ok = true, ready = false;    // ready: the next step's weights were seen
-        for (int t = tile0; t < total && ok; t += tile_step) {
-            for (int kb = 0; kb < nk; kb++, step++) {
-                ok = ready || i8_wait<false>(&ctl->wfull[s], ph, abort_flag, args.status);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                const uint8_t *src = sW + s * I8_W_BYTES + row * 128;
+        const uint32_t ta = tmem + L.slot0 + ((uint32_t)(quarter * 32) << 16);
+        const int tiles = total > tile0 ? (total - tile0 + tile_step - 1) / tile_step : 0;
+        const uint32_t steps = (uint32_t)tiles * (uint32_t)nk;
+        int s = g, slot = g;
+        uint32_t ph = 0;
+        bool ready = false;                                   // the next step's weights were seen
+        const uint32_t slots = (uint32_t)L.slots;
+        auto emptied = [&](uint32_t q, bool wait) {           // the MMAs of step q are done
+            uint64_t *b = &ctl->empty[q & (I8_XST - 1)];
+            const uint32_t parity = q / I8_XST & 1u;
+            return wait ? i8_wait<true>(b, parity, abort_flag, args.status) : mbar_test<true>(b, parity);
+        };
+        for (uint32_t step = g; step < steps; step += 2) {
+            bool ok = ready || i8_wait<false>(&ctl->wfull[s], ph, abort_flag, args.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const uint8_t *src = sW + s * I8_W_BYTES + row * 128;
+            const int sn = s + 2 >= I8_WST ? s + 2 - I8_WST : s + 2;
+            // the step before the slot's last (see empty): the look travels during the arithmetic
+            bool seen = slots == I8_XST || step <= slots || emptied(step - slots - 1, false);
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
                 uint32_t r[32];
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + (((g * 4 + c) ^ (row & 7)) << 4));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + (((hf * 4 + c) ^ (row & 7)) << 4));
                     i8_widen(v.x, r[8 * c], r[8 * c + 1]);
                     i8_widen(v.y, r[8 * c + 2], r[8 * c + 3]);
                     i8_widen(v.z, r[8 * c + 4], r[8 * c + 5]);
                     i8_widen(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->wempty[s]);
-                const int sn = s + 1 == I8_STAGES ? 0 : s + 1;
-                ready = mbar_test<false>(&ctl->wfull[sn], sn ? ph : ph ^ 1u);
-                if (step >= I8_SLOTS) {
-                    ok = i8_wait<true>(&ctl->empty[se], eph, abort_flag, args.status);
+                if (hf == 0 && step >= slots) {
+                    if (!seen) seen = emptied(step - slots - 1, true);
+                    ok = seen && emptied(step - slots, true);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    if (++se == I8_STAGES) { se = 0; eph ^= 1u; }
+                    tc_fence_after();
                 }
-                tc_fence_after();
-                tmem_st32(ta + (uint32_t)(slot * 64 + g * 32), r);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->full[s]), 0));
-                if (++slot == I8_SLOTS) slot = 0;
-                s = sn;
-                if (s == 0) ph ^= 1u;
+                if (hf == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->wempty[s]);
+                    ready = mbar_test<false>(&ctl->wfull[sn], sn > s ? ph : ph ^ 1u);
+                }
+                tmem_st32(ta + (uint32_t)(slot * 64 + hf * 32), r);
             }
+            if (!ok) break;
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->full[step & (I8_XST - 1)]), 0));
+            slot += 2;
+            if (slot >= L.slots) slot -= L.slots;
+            if (sn < s) ph ^= 1u;
+            s = sn;
         }
     } else if (warp >= I8_EPI0) {
         // ---------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         uint8_t *stg = stg_all + quarter * I8_STG_BYTES;
         float *ssc = s_scale[quarter];
-        int acc = 0;
-        uint32_t accph = 0;
-        for (int t = tile0; t < total; t += tile_step) {
+        int i = 0;
+        for (int t = tile0; t < total; t += tile_step, i++) {
             const I8Tile T = i8_tile(ctl, args.e, t);
             // this warp's first output channel, and this lane's
             const int ch0 = T.ct * 2 * CH + (int)rank * CH + quarter * (CH / 4);
@@ -420,17 +469,29 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 sb = SWI && lane >= 16 ? args.w3_scale[at] : args.w_scale[at];
                 if (!SWI && args.bias) bias = __bfloat162float(args.bias[at]);
             }
-            const bool ok = i8_wait<true>(&ctl->dfull[acc], accph, abort_flag, args.status);
+            const bool ok = i8_wait<true>(&ctl->dfull[i & 1], (i >> 1) & 1, abort_flag, args.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * I8_NT);
-            for (int c0 = 0; c0 < T.n; c0 += 32) {
+            const uint32_t tb = tmem + ((uint32_t)(quarter * 32) << 16) + (i & 1 ? L.acc1 : 0);
+            // shared accumulators: the blocks that the next tile's accumulator holds too come first (of an
+            // even tile columns 128 .., of an odd one 0 .. 63), then the issuer may go on
+            const int blocks = T.n / 32, begin = L.shared && !(i & 1) && blocks > 4 ? 4 : 0;
+            const int both = !L.shared ? 0 : i & 1 ? min(2, blocks) : blocks - begin < blocks ? blocks - begin : 0;
+            auto next_tile = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->dempty[i & 1]), 0));
+            };
+            if (L.shared && both == 0) next_tile();
+            for (int q = 0; q < blocks; q++) {
+                const int at = begin + q, c0 = 32 * (at < blocks ? at : at - blocks);
                 uint32_t r[32];
                 tmem_ld32(tb + (uint32_t)c0, r);
                 const int left = T.rows - c0;          // live rows of this block (32 or fewer)
                 ssc[lane] = lane < left ? args.x_scale[(int64_t)T.row0 + c0 + lane] : 0.0f;
                 __syncwarp();
                 tmem_wait_ld(r);
+                if (q + 1 == both) next_tile();
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
@@ -488,10 +549,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 }
                 __syncwarp();   // staging and scales are rewritten for the next block
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(su32(&ctl->dempty[acc]), 0));
-            if (++acc == 2) { acc = 0; accph ^= 1u; }
+            if (!L.shared) next_tile();
         }
     }
 

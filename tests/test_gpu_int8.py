@@ -171,6 +171,20 @@ def test_product_position_of_every_code():
     assert torch.equal(out, w[0].t()[5:11].float())
 
 
+@pytest.mark.parametrize("rows,experts", [(2, 96), (33, 64), (64, 48), (100, 48), (128, 40), (150, 40), (192, 40), (500, 12)])
+def test_product_of_many_tiles_a_pair(rows, experts):
+    """Several tiles of many stages for each pair of multiprocessors, in every layout of tensor memory; fp32
+    sums of small codes are exact, so the result is."""
+    k, n_out = 1920, 2056
+    n = rows * experts
+    a, w = codes((n, k), 1, -15, 16), codes((experts, n_out, k), 2, -15, 16)     # sums below 2^19
+    sa, sw = torch.full((n,), 0.5, device="cuda"), torch.full((experts, n_out), 0.25, device="cuda")
+    out = product(a, sa, offsets([rows] * experts), w, sw, None, F32)
+    for j in range(experts):
+        want = (a[j * rows:(j + 1) * rows].float() @ w[j].float().t()) * 0.125
+        assert torch.equal(out[j * rows:(j + 1) * rows], want), j
+
+
 def test_product_nan_scale_stays_in_its_row():
     a, w = codes((50, 64), 1), codes((1, 64, 64), 2)
     sa = torch.ones(50, device="cuda")
