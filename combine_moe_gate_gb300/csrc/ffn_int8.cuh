@@ -15,7 +15,8 @@
 // One persistent kernel on CTA pairs, tiles of 256 output channels (M: 128 a CTA) by up to 192 rows
 // (N, a multiple of 32 that the expert's rows are cut into evenly), 512 threads a CTA:
 //   warp 0       weights: 128 x 128 bytes a stage
-//   warp 2       rows: this CTA's half of the tile's rows, boxes of 32 rows x 64 fp16
+//   warps 2, 3   rows: this CTA's half of the tile's rows, each one half of the stage's K, in boxes of
+//                32 rows x 64 fp16
 //   warps 4-11   widen: two groups of four warps take the stages in turn; a lane reads its channel's
 //                128 bytes and writes 64 TMEM columns
 //   warp 1       allocates TMEM; in the even CTA issues the pair's MMAs (A from TMEM, K = 16 each)
@@ -50,7 +51,7 @@ constexpr int I8_STG_BYTES = 32 * 32 * 4;        // output staging per epilogue 
 
 struct I8Layout {
     uint32_t acc1, slot0;        // first column of the second accumulator, of the stages of A
-    int slots;                   // I8_XST or one fewer
+    int slots;                   // at most I8_XST
     bool shared;                 // the accumulators share columns [128, 192)
 };
 
@@ -67,15 +68,13 @@ __device__ __forceinline__ I8Layout i8_layout(int max_n) {
 //   wfull (copies): waited for by the 4 widening warps of the CTA that take step i (they took step i - WST
 //     as well), each of which then arrives at wempty; wempty (4): waited for by the weights' producer, who
 //     issues the next copies.
-//   full (even CTA: 4 widening warps of each CTA, and the rows' producer with the bytes of both):
-//     waited for by the MMA issuer.  (A tile has N / 2 rows for each CTA, N at least 32: both always copy.)
+//   full (even CTA: 4 widening warps of each CTA, and its two rows' producers with the bytes of both CTAs):
+//     waited for by the MMA issuer.  (A tile has N / 2 rows for each CTA, N at least 32: all always copy.)
 //     A widening warp arrives for step i after the MMAs of step i - slots, so that of i - XST is complete.
-//   empty (per CTA, a commit after the step's MMAs): waited for by the rows' producer before step
-//     i + XST, whose MMAs are its next phase and need that producer; and by the widening warps of step
-//     i + slots before they write the slot.  With slots = XST a warp meets the same barrier every other turn
-//     and its next phase is that of the warp's own step.  With slots = XST - 1 it meets all of them: it
-//     looks at step i - 1's in passing, whose next phase is that of the warp's own step i + slots, so that
-//     it has seen every phase in order.
+//   empty (per CTA, a commit after the step's MMAs): waited for by the rows' producers before step
+//     i + XST, whose MMAs are its next phase and need their bytes; and by the widening warps of step
+//     i + slots before they write the slot: as XST is even, a barrier is always met by the same group, at
+//     each of its phases, and the next phase comes after or with the MMAs of step i + slots.
 //   dfull (a commit, per CTA): waited for by its 4 epilogue warps, each of which then arrives at dempty
 //     (even CTA, 8), waited for by the MMA issuer, who commits the next dfull: two of each, by the tile's
 //     number.  drain: one phase.
@@ -147,17 +146,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
-}
-
-// One lane of the warp (the same at each call): 1 there, 0 elsewhere.
-__device__ __forceinline__ uint32_t i8_elect() {
-    uint32_t one;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(one));
-    return one;
 }
 
 // 2-SM MMA with A (fp16, two a column, lane = row) in both CTAs' TMEM, by the lane with `one`.
@@ -277,7 +265,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 mbar_init(&ctl->wempty[s], 4);
             }
             for (int s = 0; s < I8_XST; s++) {
-                mbar_init(&ctl->full[s], 9);
+                mbar_init(&ctl->full[s], 10);
                 mbar_init(&ctl->empty[s], 1);
             }
             for (int s = 0; s < 2; s++) {
@@ -311,41 +299,52 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     const I8Layout L = i8_layout(ctl->max_n);
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
+            uint32_t ph = 1;
+            bool ok = true, ready = false;   // ready: the next stage was seen free
             for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
                 const I8Tile T = i8_tile(ctl, args.e, t);
                 const int ch = T.j * args.n_out + T.ct * 2 * CH + (int)rank * CH;
                 for (int kb = 0; kb < nk; kb++) {
-                    if (!i8_wait<false>(&ctl->wempty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
+                    ok = ready || i8_wait<false>(&ctl->wempty[s], ph, abort_flag, args.status);
+                    if (!ok) break;
+                    const int sn = s + 1 == I8_WST ? 0 : s + 1;
+                    ready = mbar_test<false>(&ctl->wempty[sn], sn ? ph : ph ^ 1u);
                     mbar_expect_tx(&ctl->wfull[s], I8_W_BYTES);
                     tma_load_2d(sW + s * I8_W_BYTES, &tmW, kb * I8_BK, ch, &ctl->wfull[s]);
                     if (SWI)
                         tma_load_2d(sW + s * I8_W_BYTES + I8_W_BYTES / 2, &tmW3, kb * I8_BK, ch, &ctl->wfull[s]);
-                    if (++s == I8_WST) { s = 0; ph ^= 1u; }
+                    s = sn;
+                    if (s == 0) ph ^= 1u;
                 }
             }
         }
-    } else if (warp == 2) {
-        if (lane == 0) {
+    } else if (warp == 2 || warp == 3) {
+        // (elected lanes issue copies faster than a branch on the lane number, as they do MMAs: six copies
+        // took 730 clocks of a stage's 768)
+        if (elect_one()) {
+            const int hf = warp - 2;
+            const uint32_t fb0 = map_to_rank(su32(&ctl->full[0]), 0);
+            uint8_t *sh = sX + hf * I8_XH_BYTES;
             int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
+            uint32_t ph = 1;
+            bool ok = true, ready = false;
             for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
                 const I8Tile T = i8_tile(ctl, args.e, t);
                 const int half = T.n / 2, boxes = (half + I8_BOX - 1) / I8_BOX;
                 const int r0 = T.row0 + (int)rank * half;
                 for (int kb = 0; kb < nk; kb++) {
-                    if (!i8_wait<true>(&ctl->empty[s], ph ^ 1u, abort_flag, args.status)) { ok = false; break; }
-                    const uint32_t fb = map_to_rank(su32(&ctl->full[s]), 0);
-                    if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * 2 * boxes * I8_BOX_BYTES);
-                    for (int hf = 0; hf < 2; hf++)
-                        for (int b = 0; b < boxes; b++)
-                            tma_load_2d_pair(sX + s * I8_X_BYTES + hf * I8_XH_BYTES + b * I8_BOX_BYTES, &tmX,
-                                             kb * I8_BK + hf * 64, r0 + b * I8_BOX, fb);
-                    if (++s == I8_XST) { s = 0; ph ^= 1u; }
+                    ok = ready || i8_wait<true>(&ctl->empty[s], ph, abort_flag, args.status);
+                    if (!ok) break;
+                    const int sn = (s + 1) & (I8_XST - 1);
+                    ready = mbar_test<true>(&ctl->empty[sn], sn ? ph : ph ^ 1u);
+                    if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * boxes * I8_BOX_BYTES);
+                    for (int b = 0; b < boxes; b++)
+                        tma_load_2d_pair(sh + s * I8_X_BYTES + b * I8_BOX_BYTES, &tmX, kb * I8_BK + hf * 64,
+                                         r0 + b * I8_BOX, fb0 + 8 * s);
+                    s = sn;
+                    if (s == 0) ph ^= 1u;
                 }
             }
         }
@@ -353,7 +352,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         // The whole warp goes along and one lane's instructions count: in a branch of one lane the
         // descriptors would be moved to uniform registers for every MMA (about 95 clocks each).
         if (rank == 0) {
-            const uint32_t one = i8_elect();
+            const uint32_t one = elect_one();
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint64_t x0 = sdesc<128>(__shfl_sync(0xffffffffu, su32(sX), 0));
             const uint32_t slot0 = __shfl_sync(0xffffffffu, L.slot0, 0), acc1 = __shfl_sync(0xffffffffu, L.acc1, 0);
@@ -406,18 +405,11 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         uint32_t ph = 0;
         bool ready = false;                                   // the next step's weights were seen
         const uint32_t slots = (uint32_t)L.slots;
-        auto emptied = [&](uint32_t q, bool wait) {           // the MMAs of step q are done
-            uint64_t *b = &ctl->empty[q & (I8_XST - 1)];
-            const uint32_t parity = q / I8_XST & 1u;
-            return wait ? i8_wait<true>(b, parity, abort_flag, args.status) : mbar_test<true>(b, parity);
-        };
         for (uint32_t step = g; step < steps; step += 2) {
             bool ok = ready || i8_wait<false>(&ctl->wfull[s], ph, abort_flag, args.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint8_t *src = sW + s * I8_W_BYTES + row * 128;
             const int sn = s + 2 >= I8_WST ? s + 2 - I8_WST : s + 2;
-            // the step before the slot's last (see empty): the look travels during the arithmetic
-            bool seen = slots == I8_XST || step <= slots || emptied(step - slots - 1, false);
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
                 uint32_t r[32];
@@ -430,8 +422,8 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     i8_widen(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
                 if (hf == 0 && step >= slots) {
-                    if (!seen) seen = emptied(step - slots - 1, true);
-                    ok = seen && emptied(step - slots, true);
+                    const uint32_t last = step - slots;   // of the slot
+                    ok = i8_wait<true>(&ctl->empty[last & (I8_XST - 1)], last / I8_XST & 1u, abort_flag, args.status);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     tc_fence_after();
                 }
