@@ -354,25 +354,56 @@ moe_status tail_rows_launch(const TailOps &ops, int nops, int64_t c_max, int e,
 // ------------------------------------------------------- zero empty experts
 namespace {
 
-constexpr int ZE_THREADS = 256, ZE_BLOCKS = 64;   // CTAs per (expert, matrix)
+// One resident wave of CTAs; each lists the experts without rows (usually none: then there is nothing else to
+// do; a CTA for every expert, matrix and slice took 43 us for 64 experts that all had rows) and takes its share
+// of their 64 KB pieces.
+constexpr int ZE_THREADS = 256, ZE_CTAS = 4, ZE_PIECE = 65536, ZE_MAX_E = 1024;
 
 __global__ void __launch_bounds__(ZE_THREADS)
-zero_empty_experts_kernel(ZeroOps ops, int64_t c_max, const int32_t *__restrict__ counts,
+zero_empty_experts_kernel(ZeroOps ops, int nops, int e, int64_t c_max, const int32_t *__restrict__ counts,
                           const int32_t *__restrict__ c_dev, int32_t *status, SortedRows so) {
     pdl_enter();
     if (status_bad(status)) return;
-    const int j = blockIdx.y;
-    int64_t first, kept;
-    if (so.offsets) sorted_span(so, j, first, kept);
-    else kept = min((int64_t)max(counts[j], 0), min((int64_t)*c_dev, c_max));
-    if (kept > 0) return;
-    const ZeroOp &o = ops.op[blockIdx.z];
-    V16 *dst = reinterpret_cast<V16 *>(static_cast<char *>(o.ptr) + (int64_t)j * o.bytes);
-    const int64_t n = o.bytes / 16;
-    V16 z{};
-    for (int64_t i = (int64_t)blockIdx.x * ZE_THREADS + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * ZE_THREADS)
-        st_v16(dst + i, z);
+    constexpr int PER = ZE_MAX_E / ZE_THREADS, NW = ZE_THREADS / 32;
+    __shared__ int32_t order[ZE_MAX_E], count[PER * NW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned empty[PER];   // the same ascending list in every CTA
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const int j = i * ZE_THREADS + threadIdx.x;
+        int64_t first, kept = 1;
+        if (j < e) {
+            if (so.offsets) sorted_span(so, j, first, kept);
+            else kept = min((int64_t)max(counts[j], 0), min((int64_t)*c_dev, c_max));
+        }
+        empty[i] = __ballot_sync(0xffffffffu, kept <= 0);
+        if (lane == 0) count[i * NW + warp] = __popc(empty[i]);
+    }
+    __syncthreads();
+    int n = 0, at[PER] = {};
+#pragma unroll
+    for (int q = 0; q < PER * NW; q++) {
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+            if (q == i * NW + warp) at[i] = n;
+        n += count[q];
+    }
+    if (n == 0) return;
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        if ((empty[i] >> lane) & 1u) order[at[i] + __popc(empty[i] & ((1u << lane) - 1u))] = i * ZE_THREADS + threadIdx.x;
+    __syncthreads();
+    const V16 z{};
+    for (int x = 0; x < nops; x++) {
+        const ZeroOp &o = ops.op[x];
+        const int64_t pieces = (o.bytes + ZE_PIECE - 1) / ZE_PIECE;
+        for (int64_t it = blockIdx.x; it < n * pieces; it += gridDim.x) {
+            const int64_t j = it / pieces, off = (it - j * pieces) * ZE_PIECE;
+            char *dst = static_cast<char *>(o.ptr) + (int64_t)order[j] * o.bytes + off;
+            const int len = (int)min((int64_t)ZE_PIECE, o.bytes - off);
+            for (int i = threadIdx.x * 16; i < len; i += ZE_THREADS * 16) st_v16(dst + i, z);
+        }
+    }
 }
 
 }  // namespace
@@ -384,8 +415,13 @@ moe_status zero_empty_experts_launch(const ZeroOps &ops, int nops, int64_t c_max
     for (int i = 0; i < nops; i++)
         if (!ops.op[i].ptr || ops.op[i].bytes < 16 || ops.op[i].bytes % 16 || !aligned16(ops.op[i].ptr))
             return MOE_ERR_INVALID_ARG;
-    return launch_pdl(zero_empty_experts_kernel, dim3(ZE_BLOCKS, (unsigned)e, (unsigned)nops),
-                      dim3(ZE_THREADS), 0, stream, ops, c_max, counts, c_dev, status, so);
+    if (e > ZE_MAX_E) return MOE_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+        return MOE_ERR_CUDA;
+    return launch_pdl(zero_empty_experts_kernel, dim3((unsigned)(sms * ZE_CTAS)), dim3(ZE_THREADS), 0, stream, ops, nops,
+                      e, c_max, counts, c_dev, status, so);
 }
 
 moe_status colsum_launch(const __nv_bfloat16 *src, int e, int64_t c_max, int cols,

@@ -67,15 +67,15 @@ constexpr int SMEM_RING = 192 * 1024;   // operand ring per CTA
 // pre-activation: out = d_hid * act'(acc + bias) with d_hid (GemmArgs::aux)
 // laid out like out; the pre-activation itself is never stored.
 // EPI_GELU_SAVE / EPI_RELU_SAVE: fc1 that also stores the pre-activation
-// acc + bias (bf16) to GemmArgs::aux_out, laid out like out.
+// acc + bias (bf16) to GemmArgs::aux_out, laid out like out (map tmAt).
 // EPI_DGELU_BMN / EPI_DRELU_BMN: d_hid = acc (B MN-major) times act'(pre)
 // with the saved pre-activation (GemmArgs::aux) laid out like out.
 // EPI_WGRAD_MN_F32: EPI_WGRAD_MN writing fp32 to GemmArgs::out_f32.
 // EPI_SWIGLU_SAVE: the SwiGLU fc1 that also stores a = buf W1^T and
-// b = buf W3^T (bf16) to GemmArgs::aux_out, rows of 2 * n_out: a, then b.
+// b = buf W3^T (bf16) to GemmArgs::aux_out, rows of 2 * n_out: a (map tmAt), then b (tmBt).
 // EPI_DSWIGLU_BMN: d_hid = acc (B MN-major) and the saved [a | b] rows
 // (GemmArgs::aux, 2 * n_out a row) give d_a = d_hid * b * silu'(a) into out
-// and d_b = d_hid * silu(a) into out + n_out, out rows of GemmArgs::out_pitch.
+// and d_b = d_hid * silu(a) into out + n_out (map tmB3), out rows of GemmArgs::out_pitch.
 enum Epi { EPI_GELU = 0, EPI_RELU = 1, EPI_SWIGLU = 2, EPI_BIAS = 3, EPI_BIAS_BMN = 4,
            EPI_WGRAD_MN = 5, EPI_DGELU = 6, EPI_DRELU = 7, EPI_GELU_SAVE = 8, EPI_RELU_SAVE = 9,
            EPI_DGELU_BMN = 10, EPI_DRELU_BMN = 11, EPI_WGRAD_MN_F32 = 12, EPI_SWIGLU_SAVE = 13,
@@ -358,6 +358,37 @@ __device__ __forceinline__ void epi_store32(const CUtensorMap *map, uint8_t *stg
             }
         }
     }
+}
+
+// A warp's block of 32 rows x 32 bf16 columns of another matrix (row 0, column 0 of the block at p, rows
+// `pitch` elements apart), read as 64-byte pieces of eight rows at a time: a lane's own row in one go
+// would touch 32 lines a load.  Rows from `rows` on and columns from `cols` on are zeros.
+__device__ __forceinline__ void blk_fetch(V16 (&v)[4], const __nv_bfloat16 *p, int64_t pitch, int rows, int cols,
+                                          int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int row = 8 * i + (lane >> 2), col = (lane & 3) * 8;
+        v[i] = V16{};
+        if (row < rows && col < cols) v[i] = ld_v16(p + row * pitch + col);
+    }
+}
+
+// The fetched block turned through the warp's staging buffer: o[] = this lane's row, 16 pairs.
+__device__ __forceinline__ void blk_turn(uint8_t *stg, const V16 (&v)[4], uint32_t (&o)[16], int lane) {
+    if (lane == 0) bulk_wait_read<0>();   // the previous store has read the buffer
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int row = 8 * i + (lane >> 2);
+        st_shared_v4(stg + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), v[i].w[0], v[i].w[1], v[i].w[2], v[i].w[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+        o[4 * c] = q.x; o[4 * c + 1] = q.y; o[4 * c + 2] = q.z; o[4 * c + 3] = q.w;
+    }
+    __syncwarp();
 }
 
 // The same for 16 fp32 columns (64-byte rows: the same staging pattern and
@@ -982,8 +1013,18 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         uint8_t *stg = stg_all + ew * STG_WARP_BYTES;
         int acc = 0;
         uint32_t acc_phase = 0;
+        // derivative epilogues: this warp's next 32 x 32 block of aux (SwiGLU: of a and of b)
+        V16 fa[4], fb[4];
+        auto fetch = [&](const Tile &T, int c0) {
+            const int row0 = T.mt * BMT + row_in_tile - lane, gcol = T.nt * NOUT_TILE + col0 + c0;
+            const int64_t pitch = (DSWI ? 2 : 1) * (int64_t)args.n_out;
+            const __nv_bfloat16 *p = args.aux + (row_base(T.j) + row0) * pitch + gcol;
+            blk_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
+            if (DSWI) blk_fetch(fb, p + args.n_out, pitch, T.rows - row0, args.n_out - gcol, lane);
+        };
         for (int t = tile0; t < total; t += tile_step) {
             Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
+            if constexpr (DACT || DACTP) fetch(T, 0);   // on its way while the main loop ends
             if (!mbar_wait<PAIR>(&ctl->tfull[acc], acc_phase, abort_flag, args.status)) break;
             tc_fence_after();
             const int row = T.mt * BMT + row_in_tile;
@@ -1018,23 +1059,17 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                               __uint_as_float(u[2 * i + 1]));
                     epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out,
                                 orow);
-                    if (EPI == EPI_SWIGLU_SAVE && valid) {   // this lane's row of a, then of b
+                    if (EPI == EPI_SWIGLU_SAVE) {   // a, then b
                         __nv_bfloat16 *arow = args.aux_out + (grow0 + lane) * (2 * (int64_t)args.n_out);
 #pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            if (gcol + 8 * q < args.n_out) {
-                                V16 oa, ob;
+                        for (int i = 0; i < 16; i++)
+                            pk[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                        epi_store32(&tmAt, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out, arow);
 #pragma unroll
-                                for (int i = 0; i < 4; i++) {
-                                    oa.w[i] = pack_bf16(__uint_as_float(r[8 * q + 2 * i]),
-                                                        __uint_as_float(r[8 * q + 2 * i + 1]));
-                                    ob.w[i] = pack_bf16(__uint_as_float(u[8 * q + 2 * i]),
-                                                        __uint_as_float(u[8 * q + 2 * i + 1]));
-                                }
-                                st_v16(arow + gcol + 8 * q, oa);
-                                st_v16(arow + args.n_out + gcol + 8 * q, ob);
-                            }
-                        }
+                        for (int i = 0; i < 16; i++)
+                            pk[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+                        epi_store32(&tmBt, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out,
+                                    arow + args.n_out);
                     }
                 }
             } else {
@@ -1055,14 +1090,58 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 __syncwarp();
                 // e4m3: this lane's row scale (its output row)
                 const float sa = F8 && valid ? args.a_scale[grow0 + lane] : 0.0f;
-                const __nv_bfloat16 *drow =
-                    DACT || DACTP
-                        ? args.aux + (grow0 + lane) * ((DSWI ? 2 : 1) * (int64_t)args.n_out)
-                        : nullptr;
                 __nv_bfloat16 *prow =
                     SAVE ? args.aux_out + (grow0 + lane) * (int64_t)args.n_out
                          : nullptr;
                 const float *bsc = F8 ? args.b_scale + (int64_t)T.j * args.n_out : nullptr;
+                if constexpr (DACT || DACTP) {
+                    // the derivative of an activation: a block of 32 columns at a time, the next one's
+                    // rows of aux on their way meanwhile
+#pragma unroll 1
+                    for (int c0 = 0; c0 < COLS; c0 += 32) {
+                        const int gcol = T.nt * NOUT_TILE + col0 + c0;
+                        uint32_t r[32], dv[16], db[16];
+                        if (T.nk > 0) {
+                            tmem_ld32(tbase + (uint32_t)(col0 + c0), r);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i++) r[i] = 0u;   // empty contraction
+                        }
+                        blk_turn(stg, fa, dv, lane);
+                        if (DSWI) blk_turn(stg, fb, db, lane);
+                        if (c0 + 32 < COLS) fetch(T, c0 + 32);
+                        if (T.nk > 0) tmem_wait_ld(r);
+                        uint32_t pk[16], pb[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            const float2 acc2 = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                            const float2 bias2 = *reinterpret_cast<const float2 *>(bsl + c0 + 2 * i);
+                            float2 a = __fadd2_rn(acc2, bias2);
+                            const float2 u = make_float2(bf16lo(dv[i]), bf16hi(dv[i]));
+                            if constexpr (DSWI) {
+                                // a = d_hid; u and bv: the saved a and b of these two columns
+                                const float2 bv = make_float2(bf16lo(db[i]), bf16hi(db[i]));
+                                const float sx = 1.0f / (1.0f + expf(-u.x));
+                                const float sy = 1.0f / (1.0f + expf(-u.y));
+                                pb[i] = pack_bf16(a.x * u.x * sx, a.y * u.y * sy);   // d_b
+                                a = make_float2(a.x * bv.x * sx * (1.0f + u.x * (1.0f - sx)),
+                                                a.y * bv.y * sy * (1.0f + u.y * (1.0f - sy)));   // d_a
+                            } else {
+                                // DACT: aux is d_hid, a the pre-activation; DACTP: aux is the saved
+                                // pre-activation, a = d_hid
+                                const float2 z = DACT ? a : u, g = DACT ? u : a;
+                                const float2 da = DGELU ? gelu_grad2(z)
+                                                        : make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+                                a = __fmul2_rn(g, da);
+                            }
+                            pk[i] = pack_bf16(a.x, a.y);
+                        }
+                        epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out, orow);
+                        if (DSWI)   // the second half of the output rows
+                            epi_store32(&tmB3, stg, pb, all_kept, valid, lane, grow0, gcol, args.n_out,
+                                        orow + args.n_out);
+                    }
+                } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < COLS; c0 += 64) {
                     uint32_t r[2][32];
@@ -1080,27 +1159,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         const int gcol = T.nt * NOUT_TILE + col0 + c0 + 32 * h2;
                         uint32_t pk[16];
                         float of[32];   // weight gradients in fp32: this row's 32 columns
-                        uint32_t dv[16];   // activation backward: this row's d_hid or pre (SwiGLU: a), 32 columns
-                        uint32_t db[16];   // SwiGLU backward: this row's b, 32 columns
-                        if (DACT || DACTP) {
-#pragma unroll
-                            for (int q = 0; q < 4; q++) {
-                                V16 v{}, w{};
-                                if (valid && gcol + q * 8 < args.n_out) {
-                                    v = ld_v16(drow + gcol + q * 8);
-                                    if (DSWI) w = ld_v16(drow + args.n_out + gcol + q * 8);
-                                }
-#pragma unroll
-                                for (int i = 0; i < 4; i++) {
-                                    dv[q * 4 + i] = v.w[i];
-                                    db[q * 4 + i] = w.w[i];
-                                }
-                            }
-                        }
+                        uint32_t pp[16];   // fc1 keeping its pre-activation: this row's 32 columns
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
-                            uint32_t pp[4];   // fc1 keeping its pre-activation: 8 packed columns
-                            uint32_t pb[4];   // SwiGLU backward: d_b, 8 packed columns
                             const float4 *bp = reinterpret_cast<const float4 *>(bsl + c0 + 32 * h2 + q * 8);
                             const float4 bl = bp[0], bh = bp[1];
                             const float2 bb[4] = {make_float2(bl.x, bl.y), make_float2(bl.z, bl.w),
@@ -1122,51 +1183,14 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                                                 __uint_as_float(r[h2][q * 8 + 2 * i + 1]));
                                 float2 a = F8 ? __ffma2_rn(acc2, make_float2(sc[2 * i], sc[2 * i + 1]), bb[i])
                                               : __fadd2_rn(acc2, bb[i]);
-                                if (SAVE) pp[i] = pack_bf16(a.x, a.y);
+                                if (SAVE) pp[q * 4 + i] = pack_bf16(a.x, a.y);
                                 if (GELU) a = gelu_erf2(a);
                                 else if (RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
-                                if constexpr (DSWI) {
-                                    // a = d_hid; the saved a and b of these two columns
-                                    const float2 av = make_float2(__uint_as_float(dv[q * 4 + i] << 16),
-                                                                  __uint_as_float(dv[q * 4 + i] & 0xFFFF0000u));
-                                    const float2 bv = make_float2(__uint_as_float(db[q * 4 + i] << 16),
-                                                                  __uint_as_float(db[q * 4 + i] & 0xFFFF0000u));
-                                    const float sx = 1.0f / (1.0f + expf(-av.x));
-                                    const float sy = 1.0f / (1.0f + expf(-av.y));
-                                    pb[i] = pack_bf16(a.x * av.x * sx, a.y * av.y * sy);   // d_b
-                                    a = make_float2(a.x * bv.x * sx * (1.0f + av.x * (1.0f - sx)),
-                                                    a.y * bv.y * sy * (1.0f + av.y * (1.0f - sy)));   // d_a
-                                } else if (DACT || DACTP) {
-                                    // DACT: aux is d_hid, a the pre-activation; DACTP: aux is
-                                    // the saved pre-activation, a = d_hid
-                                    const uint32_t u2 = dv[q * 4 + i];
-                                    const float2 u = make_float2(__uint_as_float(u2 << 16),
-                                                                 __uint_as_float(u2 & 0xFFFF0000u));
-                                    const float2 z = DACT ? a : u, g = DACT ? u : a;
-                                    const float2 da = DGELU ? gelu_grad2(z)
-                                                            : make_float2(z.x > 0.0f ? 1.0f : 0.0f,
-                                                                          z.y > 0.0f ? 1.0f : 0.0f);
-                                    a = __fmul2_rn(g, da);
-                                }
                                 if constexpr (F32OUT) {
                                     of[q * 8 + 2 * i] = a.x;
                                     of[q * 8 + 2 * i + 1] = a.y;
                                 } else {
                                     pk[q * 4 + i] = pack_bf16(a.x, a.y);
-                                }
-                            }
-                            if (SAVE && valid && gcol + q * 8 < args.n_out) {
-                                // this lane's row of the pre-activation, 8 columns
-                                V16 o;
-                                o.w[0] = pp[0]; o.w[1] = pp[1]; o.w[2] = pp[2]; o.w[3] = pp[3];
-                                st_v16(prow + gcol + q * 8, o);
-                            }
-                            if constexpr (DSWI) {
-                                if (valid && gcol + q * 8 < args.n_out) {
-                                    // d_b: the second half of this lane's output row, 8 columns
-                                    V16 o;
-                                    o.w[0] = pb[0]; o.w[1] = pb[1]; o.w[2] = pb[2]; o.w[3] = pb[3];
-                                    st_v16(orow + args.n_out + gcol + q * 8, o);
                                 }
                             }
                         }
@@ -1179,8 +1203,11 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         } else {
                             epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol,
                                         args.n_out, orow);
+                            if (SAVE)
+                                epi_store32(&tmAt, stg, pp, all_kept, valid, lane, grow0, gcol, args.n_out, prow);
                         }
                     }
+                }
                 }
                 __syncwarp();   // slice reused for the next tile
             }
@@ -1417,16 +1444,22 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
                 nullptr, nullptr, row_lo, row_hi};
     g1.offsets = so.offsets;
     g1.n_rows = so.n;
+    // the kept pre-activation's output maps (SwiGLU: a and b, the halves of 2h-wide rows)
+    CUtensorMap mPa, mPb;
+    const uint64_t pw = swiglu ? 2 * (uint64_t)h : (uint64_t)h;
+    if (pre && (!make_map(&mPa, pre, rows, (uint64_t)h, 32, 32, pw) ||
+                (swiglu && !make_map(&mPb, (const __nv_bfloat16 *)pre + h, rows, (uint64_t)h, 32, 32, pw))))
+        return MOE_ERR_CUDA;
     g1.aux_out = (__nv_bfloat16 *)pre;   // training: fc1 also keeps its pre-activation
     moe_status r;
     if (swiglu) {
-        r = pre ? launch_gemm<EPI_SWIGLU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB3, mO1, g1, stream)
+        r = pre ? launch_gemm<EPI_SWIGLU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB3, mO1, g1, stream, &mPa, &mPb)
                 : launch_gemm<EPI_SWIGLU, TM1, BK1, CL1, 1>(mA1, mB1, mB3, mO1, g1, stream);
     } else if (act == MOE_ACT_GELU) {
-        r = pre ? launch_gemm<EPI_GELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream)
+        r = pre ? launch_gemm<EPI_GELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream, &mPa)
                 : launch_gemm<EPI_GELU, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream);
     } else {
-        r = pre ? launch_gemm<EPI_RELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream)
+        r = pre ? launch_gemm<EPI_RELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream, &mPa)
                 : launch_gemm<EPI_RELU, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream);
     }
     if (r != MOE_OK) return r;
@@ -1654,19 +1687,21 @@ moe_status gemm_dswiglu_bmn(const void *d_out, const void *w2, const void *ab, v
                             int h, int32_t *st, cudaStream_t stream,
                      SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mO;
+    CUtensorMap mA, mB, mO, mOb;
     if (!make_map(&mA, d_out, rows_of(e, c_max, so), (uint64_t)m, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64) ||
         // d_a: the first h columns of each 2h-wide row (the map's extent clips a
         // box at h, so d_b's columns are never written by it)
-        !make_map(&mO, d_pre, rows_of(e, c_max, so), (uint64_t)h, 32, 32, 2 * (uint64_t)h))
+        !make_map(&mO, d_pre, rows_of(e, c_max, so), (uint64_t)h, 32, 32, 2 * (uint64_t)h) ||
+        // d_b: the other h columns
+        !make_map(&mOb, (const __nv_bfloat16 *)d_pre + h, rows_of(e, c_max, so), (uint64_t)h, 32, 32, 2 * (uint64_t)h))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)d_pre, c_max, e, m, h, m, nullptr,
                nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)ab};
     g.out_pitch = 2 * (int64_t)h;
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
+    return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mOb, mO, g, stream);
 }
 
 // Weight gradients out[j] = A[j]^T B[j] over the first min(counts[j], *c_dev,

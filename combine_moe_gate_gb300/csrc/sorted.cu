@@ -15,6 +15,7 @@ namespace {
 // last row, so they are ranked like the others).
 constexpr int SS_NT = 1024, SS_NW = SS_NT / 32, SS_MAXE = 256, SS_MAXN = 16384;   // one launch
 constexpr int ST_NT = 256, ST_NW = ST_NT / 32, ST_BLK = 256;                      // two launches
+constexpr int ST_HELD = 8;                                                        // rounds kept in registers
 constexpr int SORT_MAXB = 1025;                                                   // buckets
 
 __device__ __forceinline__ int bucket_of(int v, int e, int32_t *status) {
@@ -133,18 +134,26 @@ sort_hist_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds, 
     for (int q = threadIdx.x; q < nb; q += ST_NT) cnt[q] = 0;
     __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * rounds * ST_NT;
-#pragma unroll 4
-    for (int r = 0; r < rounds; r++) {
-        const int64_t j = base + r * ST_NT + threadIdx.x;
-        count_warp(cnt, j < n ? bucket_of(__ldg(idx + j), e, status) : -1, lt);
+    for (int r0 = 0; r0 < rounds; r0 += ST_HELD) {
+        int b[ST_HELD];   // all loads in flight first
+#pragma unroll
+        for (int r = 0; r < ST_HELD; r++) {
+            const int64_t j = base + (r0 + r) * ST_NT + threadIdx.x;
+            b[r] = r0 + r < rounds && j < n ? bucket_of(__ldg(idx + j), e, status) : -1;
+        }
+#pragma unroll
+        for (int r = 0; r < ST_HELD; r++)
+            if (r0 + r < rounds) count_warp(cnt, b[r], lt);
     }
     __syncthreads();
     for (int q = threadIdx.x; q < nb; q += ST_NT) hist[(int64_t)q * gridDim.x + blockIdx.x] = cnt[q];
 }
 
 // ... and places them: a warp adds up a bucket's counts, those of the chunks before (all of the at
-// most 256 chunks are read by every CTA: a third launch to sum them once costs more), then takes
-// `rounds` x 32 consecutive routes.
+// most 256 chunks are read by every CTA: a third launch to sum them once costs more), and takes
+// `rounds` x 32 consecutive routes.  HELD: at most ST_HELD rounds, kept in registers with their ranks in the
+// warp; otherwise the routes are counted first and read again to be placed.
+template <bool HELD>
 __global__ void __launch_bounds__(ST_NT)
 sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds, const int32_t *__restrict__ hist,
                   int32_t *__restrict__ rows, int32_t *__restrict__ offsets, int32_t *__restrict__ source,
@@ -154,33 +163,61 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
     extern __shared__ int32_t sm[];
     __shared__ int32_t part[ST_NW];
     const int nb = e + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nblk = gridDim.x;
-    int32_t *start = sm, *before = start + nb + 1, *cnt = before + nb;   // cnt [8][nb]; its first row also holds the totals
+    int32_t *start = sm, *before = start + nb + 1, *tot = before + nb, *cnt = tot + nb;   // cnt [8][nb]
     const unsigned lt = (1u << lane) - 1u;
-    for (int b = warp; b < nb; b += ST_NW) {
-        int32_t all = 0, pre = 0;
+    const int64_t at = ((int64_t)blockIdx.x * ST_NW + warp) * rounds * 32;
+    int bucket[ST_HELD], rank[ST_HELD];
+    if (HELD) {
 #pragma unroll
-        for (int q = 0; q < ST_BLK; q += 32) {
-            if (q < nblk) {
-                const int32_t c = q + lane < nblk ? hist[(int64_t)b * nblk + q + lane] : 0;
-                all += c;
-                pre += q + lane < (int)blockIdx.x ? c : 0;
+        for (int r = 0; r < ST_HELD; r++) {
+            const int64_t j = at + r * 32 + lane;
+            bucket[r] = r < rounds && j < n ? bucket_of(__ldg(idx + j), e, status) : -1;
+        }
+    }
+    for (int q = tid; q < ST_NW * nb; q += ST_NT) cnt[q] = 0;
+    // four buckets a turn: up to 32 loads under way
+    for (int b0 = warp; b0 < nb; b0 += 4 * ST_NW) {
+        int32_t all[4] = {0, 0, 0, 0}, pre[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int b = b0 + i * ST_NW;
+#pragma unroll
+            for (int q = 0; q < ST_BLK; q += 32) {
+                if (q >= nblk) break;
+                const int32_t c = b < nb && q + lane < nblk ? hist[(int64_t)b * nblk + q + lane] : 0;
+                all[i] += c;
+                pre[i] += q + lane < (int)blockIdx.x ? c : 0;
             }
         }
-        all = __reduce_add_sync(0xffffffffu, all);
-        pre = __reduce_add_sync(0xffffffffu, pre);
-        if (lane == 0) { cnt[b] = all; before[b] = pre; }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int b = b0 + i * ST_NW;
+            all[i] = __reduce_add_sync(0xffffffffu, all[i]);
+            pre[i] = __reduce_add_sync(0xffffffffu, pre[i]);
+            if (lane == 0 && b < nb) { tot[b] = all[i]; before[b] = pre[i]; }
+        }
     }
     __syncthreads();
-    exclusive_scan<ST_NT>(cnt, start, nb, part);
-    for (int q = tid; q < ST_NW * nb; q += ST_NT) cnt[q] = 0;
-    __syncthreads();
-    const int64_t at = ((int64_t)blockIdx.x * ST_NW + warp) * rounds * 32;
-#pragma unroll 4
-    for (int r = 0; r < rounds; r++) {
-        const int64_t j = at + r * 32 + lane;
-        count_warp(cnt + warp * nb, j < n ? bucket_of(__ldg(idx + j), e, status) : -1, lt);
+    int32_t *mine = cnt + warp * nb;
+    if (HELD) {
+#pragma unroll
+        for (int r = 0; r < ST_HELD; r++) {
+            if (r >= rounds) break;
+            const int b = bucket[r];
+            const unsigned peers = __match_any_sync(0xffffffffu, b);
+            const int32_t first = b >= 0 ? mine[b] : 0;
+            __syncwarp();
+            if (b >= 0 && (peers & lt) == 0) mine[b] = first + __popc(peers);
+            __syncwarp();
+            rank[r] = first + __popc(peers & lt);
+        }
+    } else {
+        for (int r = 0; r < rounds; r++) {
+            const int64_t j = at + r * 32 + lane;
+            count_warp(mine, j < n ? bucket_of(__ldg(idx + j), e, status) : -1, lt);
+        }
     }
-    __syncthreads();
+    exclusive_scan<ST_NT>(tot, start, nb, part);
     for (int b = tid; b < nb; b += ST_NT) {
         int32_t run = start[b] + before[b];
         for (int w = 0; w < ST_NW; w++) {
@@ -192,7 +229,21 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
     if (blockIdx.x == 0)
         for (int b = tid; b < nb; b += ST_NT) offsets[b] = start[b];
     __syncthreads();
-    place_segment(idx, at, rounds, n, e, cnt + warp * nb, rows, source, status, lt);
+    if (HELD) {
+#pragma unroll
+        for (int r = 0; r < ST_HELD; r++) {
+            if (r >= rounds) break;
+            const int b = bucket[r];
+            const int64_t j = at + r * 32 + lane;
+            if (b >= 0) {
+                const int32_t pos = mine[b] + rank[r];
+                rows[j] = b < e ? pos : -1;
+                if (source) source[pos] = b < e ? (int32_t)j : -1;
+            }
+        }
+    } else {
+        place_segment(idx, at, rounds, n, e, mine, rows, source, status, lt);
+    }
 }
 
 // ------------------------------------------------------------ rows in and back
@@ -242,7 +293,8 @@ constexpr int mv_ctas() {
     return KG * U >= 8 ? 2 : MODE & DOTS ? 3 : 4;
 }
 
-template <typename T, int MODE, int KG, int U>
+// KT: routes whose dot products are summed in one pass over the row (DOTS; a multiple of KG).
+template <typename T, int MODE, int KT, int KG, int U>
 __global__ void __launch_bounds__(MV_NT, (mv_ctas<MODE, KG, U>()))
 move_rows_kernel(const MoveArgs g) {
     pdl_enter();
@@ -250,7 +302,7 @@ move_rows_kernel(const MoveArgs g) {
     constexpr bool in = MODE & IN, back = MODE & BACK, dots = MODE & DOTS, gated = MODE & GATES;
     constexpr bool read_a = in || dots, read_b = back || dots;
     constexpr int VEC = Elt<T>::VEC;
-    __shared__ float part[MV_NW][32];
+    __shared__ float part[MV_NW][KT];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tpc = MV_NW / g.wpt;                   // tokens a CTA holds at a time
     const int sub = warp % g.wpt;                    // this warp's share of its token
@@ -284,11 +336,14 @@ move_rows_kernel(const MoveArgs g) {
         V16 *ao = reinterpret_cast<V16 *>(static_cast<T *>(g.a_out) + (mine ? t : 0) * g.m);
         const V16 *bp = static_cast<const V16 *>(g.b);
         V16 *bo = static_cast<V16 *>(g.b_out);
-        const int64_t at = (int64_t)row * nch;       // lane r: route r's row, in chunks
-        for (int rg = 0; rg < (dots ? k : 1); rg += KG) {   // with dot products: a group of routes at a time
-            float dot[KG];
+        // this lane's 16-byte piece of route r's row
+        auto piece = [&](int r, int c) {
+            return (int64_t)__shfl_sync(0xffffffffu, row, r & 31) * nch + c;
+        };
+        for (int rg = 0; rg < (dots ? k : 1); rg += KT) {
+            float dot[KT];
 #pragma unroll
-            for (int i = 0; i < KG; i++) dot[i] = 0.0f;
+            for (int i = 0; i < KT; i++) dot[i] = 0.0f;
             if (mine) {
                 for (int c0 = sub * 32 * U; c0 < nch; c0 += g.wpt * 32 * U) {
                     const int c = c0 + lane;
@@ -296,7 +351,7 @@ move_rows_kernel(const MoveArgs g) {
                     if (read_a) {
 #pragma unroll
                         for (int u = 0; u < U; u++)
-                            if (c + 32 * u < nch) av[u] = k > KG ? ld_v16(ap + c + 32 * u) : ld_stream(ap + c + 32 * u);
+                            if (c + 32 * u < nch) av[u] = k > KT ? ld_v16(ap + c + 32 * u) : ld_stream(ap + c + 32 * u);
                     }
                     float acc[U][VEC];
                     if (back) {
@@ -305,28 +360,30 @@ move_rows_kernel(const MoveArgs g) {
 #pragma unroll
                             for (int i = 0; i < VEC; i++) acc[u][i] = 0.0f;
                     }
-                    for (int r0 = dots ? rg : 0; r0 < (dots ? rg + 1 : k); r0 += KG) {
+                    // KG routes from r0 on; their dot products are dot[d0 ..]
+                    auto group = [&](int r0, float *dt) {
                         V16 bv[KG][U];
                         if (read_b) {
 #pragma unroll
                             for (int i = 0; i < KG; i++) {
-                                const int64_t o = __shfl_sync(0xffffffffu, at, (r0 + i) & 31);
+                                const int64_t o = piece(r0 + i, c);
                                 if (r0 + i < k && ((live >> (r0 + i)) & 1u)) {
 #pragma unroll
                                     for (int u = 0; u < U; u++)
-                                        if (c + 32 * u < nch) bv[i][u] = ld_stream(bp + o + c + 32 * u);
+                                        if (c + 32 * u < nch) bv[i][u] = ld_stream(bp + o + 32 * u);
                                 }
                             }
                         }
 #pragma unroll
                         for (int i = 0; i < KG; i++) {
-                            const int64_t o = __shfl_sync(0xffffffffu, at, (r0 + i) & 31);
+                            int64_t o = 0;
+                            if (in) o = piece(r0 + i, c);
                             const float w = gated ? __shfl_sync(0xffffffffu, wt, (r0 + i) & 31) : 1.0f;
                             if (r0 + i < k && ((live >> (r0 + i)) & 1u)) {
 #pragma unroll
                                 for (int u = 0; u < U; u++) {
                                     if (c + 32 * u >= nch) continue;
-                                    if (in) st_v16(bo + o + c + 32 * u, gated ? ScaleRound<T>::apply(w, av[u]) : av[u]);
+                                    if (in) st_v16(bo + o + 32 * u, gated ? ScaleRound<T>::apply(w, av[u]) : av[u]);
                                     if (!read_b) continue;
                                     float f[VEC];
                                     Elt<T>::unpack(bv[i][u], f);
@@ -339,11 +396,17 @@ move_rows_kernel(const MoveArgs g) {
                                         float x[VEC];
                                         Elt<T>::unpack(av[u], x);
 #pragma unroll
-                                        for (int q = 0; q < VEC; q++) dot[i] = __fmaf_rn(x[q], f[q], dot[i]);
+                                        for (int q = 0; q < VEC; q++) dt[i] = __fmaf_rn(x[q], f[q], dt[i]);
                                     }
                                 }
                             }
                         }
+                    };
+                    if constexpr (dots) {
+#pragma unroll
+                        for (int d0 = 0; d0 < KT; d0 += KG) group(rg + d0, dot + d0);
+                    } else {
+                        for (int r0 = 0; r0 < k; r0 += KG) group(r0, dot);
                     }
                     if (back) {
 #pragma unroll
@@ -352,18 +415,18 @@ move_rows_kernel(const MoveArgs g) {
                     }
                 }
             }
-            if (dots) {   // lane i < KG: route rg + i
-                float sum = reduce_many<KG>(dot, lane);
+            if (dots) {   // lane i < KT: route rg + i
+                float sum = reduce_many<KT>(dot, lane);
                 if (g.wpt > 1) {
-                    if (lane < KG) part[warp][lane] = sum;
+                    if (lane < KT) part[warp][lane] = sum;
                     __syncthreads();
-                    if (sub == 0 && lane < KG) {
+                    if (sub == 0 && lane < KT) {
                         sum = part[warp][lane];
                         for (int w = 1; w < g.wpt; w++) sum += part[warp + w][lane];
                     }
                     __syncthreads();
                 }
-                if (mine && sub == 0 && lane < KG && rg + lane < k)
+                if (mine && sub == 0 && lane < KT && rg + lane < k)
                     g.dots[(int64_t)(rg + lane) * g.s + t] = (live >> (rg + lane)) & 1u ? sum : 0.0f;
             }
         }
@@ -382,7 +445,7 @@ int sm_count() {
     return cached[dev];
 }
 
-template <typename T, int MODE, int KG, int U>
+template <typename T, int MODE, int KT, int KG, int U>
 moe_status move_launch(MoveArgs g, cudaStream_t stream) {
     // as many warps a token as there are turns of 32 U chunks for, while the tokens alone leave warps idle
     const int sms = sm_count(), turns = (g.m / Elt<T>::VEC + 32 * U - 1) / (32 * U);
@@ -390,20 +453,22 @@ moe_status move_launch(MoveArgs g, cudaStream_t stream) {
     while (g.wpt < MV_NW && g.wpt < turns && g.s * g.wpt < (int64_t)sms * 24) g.wpt *= 2;
     const int64_t ctas = (g.s * g.wpt + MV_NW - 1) / MV_NW;
     const int64_t cap = (int64_t)sms * mv_ctas<MODE, KG, U>();   // resident at once
-    return launch_pdl(move_rows_kernel<T, MODE, KG, U>, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(MV_NT), 0,
+    return launch_pdl(move_rows_kernel<T, MODE, KT, KG, U>, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(MV_NT), 0,
                       stream, g);
 }
 
-// Routes in flight by k, so that a lane has about eight 16-byte loads under way.
+// Eight or more 16-byte loads a lane under way, of at least two neighbouring chunks of a row: with one (512
+// bytes a row and turn) the way back of 8191 x 8 rows of 4 KB took 111 us, with two 54; the way in's gradient
+// with dot products 112 and 57.
 template <typename T, int MODE>
 moe_status move_typed(const MoveArgs &g, cudaStream_t stream) {
     if constexpr (!(MODE & (BACK | DOTS))) {
-        return move_launch<T, MODE, 1, 4>(g, stream);
+        return move_launch<T, MODE, 1, 1, 4>(g, stream);
     } else {
-        if (g.k == 1) return move_launch<T, MODE, 1, 4>(g, stream);
-        if (g.k == 2) return move_launch<T, MODE, 2, 4>(g, stream);
-        if (g.k <= 4) return move_launch<T, MODE, 4, 2>(g, stream);
-        return move_launch<T, MODE, 8, 1>(g, stream);
+        if (g.k == 1) return move_launch<T, MODE, 1, 1, 4>(g, stream);
+        if (g.k == 2) return move_launch<T, MODE, 2, 2, 4>(g, stream);
+        if (g.k <= 4 || !(MODE & DOTS)) return move_launch<T, MODE, 4, 4, 2>(g, stream);
+        return move_launch<T, MODE, 8, 8, 2>(g, stream);
     }
 }
 
@@ -436,8 +501,9 @@ moe_status sort_routes_launch(const int32_t *idx, int64_t s, int e, int k, int32
     moe_status r = launch_pdl(sort_hist_kernel, dim3(nblk), dim3(ST_NT), 0, stream, idx, n, e, rounds, (int32_t *)ws,
                               st);
     if (r != MOE_OK) return r;
-    return launch_pdl(sort_place_kernel, dim3(nblk), dim3(ST_NT), (size_t)(2 * nb + 1 + ST_NW * nb) * 4, stream, idx,
-                      n, e, rounds, (const int32_t *)ws, rows, offsets, source, st);
+    return launch_pdl(rounds <= ST_HELD ? sort_place_kernel<true> : sort_place_kernel<false>, dim3(nblk), dim3(ST_NT),
+                      (size_t)(3 * nb + 1 + ST_NW * nb) * 4, stream, idx, n, e, rounds, (const int32_t *)ws, rows,
+                      offsets, source, st);
 }
 
 moe_status encode_sorted_launch(const void *x, moe_dtype dt, const int32_t *rows, const float *gates, int64_t s, int m,
@@ -468,8 +534,8 @@ moe_status encode_sorted_bwd_launch(const void *d_out, const void *x, moe_dtype 
     if (k <= 8) return move<BACK | DOTS | GATES>(dt, g, stream);   // all routes of a token in one group
     const moe_status r = move<BACK | GATES>(dt, g, stream);
     if (r != MOE_OK) return r;
-    return dt == MOE_BF16 ? move_launch<__nv_bfloat16, DOTS, 8, 1>(g, stream)
-                          : move_launch<float, DOTS, 8, 1>(g, stream);
+    return dt == MOE_BF16 ? move_launch<__nv_bfloat16, DOTS, 8, 8, 2>(g, stream)
+                          : move_launch<float, DOTS, 8, 8, 2>(g, stream);
 }
 
 }  // namespace moe
