@@ -498,11 +498,23 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     // second rows 16-31
                     __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(stg);
                     const bool up = lane >= 16;
+                    bool mid = true;
 #pragma unroll
                     for (int i = 0; i < 16; i++) {
                         const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 16], 16);
                         const float ga = up ? other : v[i], gb = up ? v[i + 16] : other;
-                        sp[(i + (lane & 16)) * 16 + (lane & 15)] = __float2bfloat16_rn(silu(ga) * gb);
+                        v[i] = ga;
+                        v[i + 16] = gb;
+                        mid &= i + (lane & 16) >= left || silu_mid_ok(ga);
+                    }
+                    if (__all_sync(0xffffffffu, mid)) {
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            sp[(i + (lane & 16)) * 16 + (lane & 15)] = __float2bfloat16_rn(silu_mid(v[i]) * v[i + 16]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            sp[(i + (lane & 16)) * 16 + (lane & 15)] = __float2bfloat16_rn(silu(v[i]) * v[i + 16]);
                     }
                     __syncwarp();
 #pragma unroll

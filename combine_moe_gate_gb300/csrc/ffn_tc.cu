@@ -35,7 +35,10 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "common.cuh"
+#include "exact.cuh"
 
 namespace moe {
 namespace {
@@ -637,6 +640,21 @@ __device__ __forceinline__ float2 gelu_grad2(float2 z) {
 
 __device__ __forceinline__ float silu(float a) { return a / (1.0f + expf(-a)); }
 
+// The same bits without the general division, whose range checks end in branches that keep the
+// elements of a block from overlapping (a 32 x 32 block took 7 us): for |a| <= 80 the divisor is in
+// [1, 2^116] and, for a = +0 or |a| >= 2^-100, the quotient within div_mid's range.
+__device__ __forceinline__ bool silu_mid_ok(float a) {
+    const uint32_t u = __float_as_uint(a);
+    return ((u & 0x7FFFFFFFu) - 0x0D800000u) <= 0x42A00000u - 0x0D800000u || u == 0u;   // 2^-100 .. 80, or +0
+}
+__device__ __forceinline__ float silu_mid(float a) {
+    const float b = 1.0f + expf(-a);
+    return div_mid(a, b, rcp_mid(b));
+}
+// 1 / (1 + e^-a), for |a| <= 80.
+__device__ __forceinline__ bool sigmoid_mid_ok(float a) { return fabsf(a) <= 80.0f; }
+__device__ __forceinline__ float sigmoid_mid(float a) { return rcp_mid(1.0f + expf(-a)); }
+
 // Tile t -> (expert j, m-tile, n-tile); m-tile varies fastest.  rows: the
 // expert's output rows; nk: its K blocks.  kept_rows[] holds the output rows
 // per expert, or (uniform_rows > 0: every expert has that many output rows)
@@ -1052,11 +1070,20 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         for (int i = 0; i < 32; i++) r[i] = u[i] = 0u;   // empty contraction
                     }
                     uint32_t pk[16];
+                    bool mid = true;
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        pk[i] = pack_bf16(silu(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
-                                          silu(__uint_as_float(r[2 * i + 1])) *
-                                              __uint_as_float(u[2 * i + 1]));
+                    for (int i = 0; i < 32; i++) mid &= silu_mid_ok(__uint_as_float(r[i]));
+                    if (!__any_sync(0xffffffffu, valid && !mid)) {
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            pk[i] = pack_bf16(silu_mid(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
+                                              silu_mid(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            pk[i] = pack_bf16(silu(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
+                                              silu(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+                    }
                     epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out,
                                 orow);
                     if (EPI == EPI_SWIGLU_SAVE) {   // a, then b
@@ -1112,6 +1139,14 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         if (c0 + 32 < COLS) fetch(T, c0 + 32);
                         if (T.nk > 0) tmem_wait_ld(r);
                         uint32_t pk[16], pb[16];
+                        bool mid = true;
+                        if (DSWI) {
+#pragma unroll
+                            for (int i = 0; i < 16; i++)
+                                mid &= sigmoid_mid_ok(bf16lo(dv[i])) && sigmoid_mid_ok(bf16hi(dv[i]));
+                            mid = !__any_sync(0xffffffffu, valid && !mid);
+                        }
+                        auto columns = [&](auto general) {
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
                             const float2 acc2 = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
@@ -1121,8 +1156,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             if constexpr (DSWI) {
                                 // a = d_hid; u and bv: the saved a and b of these two columns
                                 const float2 bv = make_float2(bf16lo(db[i]), bf16hi(db[i]));
-                                const float sx = 1.0f / (1.0f + expf(-u.x));
-                                const float sy = 1.0f / (1.0f + expf(-u.y));
+                                const float sx = general.value ? 1.0f / (1.0f + expf(-u.x)) : sigmoid_mid(u.x);
+                                const float sy = general.value ? 1.0f / (1.0f + expf(-u.y)) : sigmoid_mid(u.y);
                                 pb[i] = pack_bf16(a.x * u.x * sx, a.y * u.y * sy);   // d_b
                                 a = make_float2(a.x * bv.x * sx * (1.0f + u.x * (1.0f - sx)),
                                                 a.y * bv.y * sy * (1.0f + u.y * (1.0f - sy)));   // d_a
@@ -1136,6 +1171,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             }
                             pk[i] = pack_bf16(a.x, a.y);
                         }
+                        };
+                        if (DSWI && !mid) columns(std::true_type{});
+                        else columns(std::false_type{});
                         epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out, orow);
                         if (DSWI)   // the second half of the output rows
                             epi_store32(&tmB3, stg, pb, all_kept, valid, lane, grow0, gcol, args.n_out,
