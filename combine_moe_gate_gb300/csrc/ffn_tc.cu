@@ -325,42 +325,26 @@ __device__ __forceinline__ void st_shared_v4(uint8_t *p, uint32_t a, uint32_t b,
                  : "memory");
 }
 
-// One lane's 32 output columns (pk: 16 packed bf16 pairs, column order) of a
-// warp's 32 consecutive rows starting at global row grow0, columns gcol...
-// When all 32 rows are kept: through the warp's staging buffer (row = lane,
-// 16-byte chunk c of a 64-byte row at c ^ ((row >> 1) & 3), the 64-byte
-// swizzle pattern) and one TMA store, which clips columns >= n_out.
-// Otherwise direct stores of this lane's row if it is kept.
-__device__ __forceinline__ void epi_store32(const CUtensorMap *map, uint8_t *stg,
-                                            const uint32_t (&pk)[16], bool all_kept, bool kept,
-                                            int lane, int64_t grow0, int gcol, int n_out,
-                                            __nv_bfloat16 *orow) {
-    if (all_kept) {
-        if (gcol >= n_out) return;  // warp-uniform
-        if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
-        __syncwarp();
-        const int sw = (lane >> 1) & 3;
+// A warp's block of 32 rows of 64 bytes (a lane's row: 16 words), turned in the warp's staging buffer (row
+// = lane, 16-byte chunk c at c ^ ((row >> 1) & 3)) and stored as whole 64-byte pieces of eight rows at a time
+// from `out` on (row 0, first byte of the block; rows `pitch` bytes apart).  Rows from `rows` on and bytes from
+// `bytes` on are left out.  (TMA stores of the same boxes, with the wait until the last one has read the
+// buffer, held up every block by some 1500 clocks.)
+__device__ __forceinline__ void epi_store64(uint8_t *stg, const uint32_t (&w)[16], void *out, int64_t pitch, int rows,
+                                            int bytes, int lane) {
+    const int sw = (lane >> 1) & 3;
 #pragma unroll
-        for (int c = 0; c < 4; c++)
-            st_shared_v4(stg + lane * 64 + ((c ^ sw) << 4), pk[c * 4 + 0], pk[c * 4 + 1],
-                         pk[c * 4 + 2], pk[c * 4 + 3]);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(map, gcol, (int)grow0, stg);
-            bulk_commit();
-        }
-    } else if (kept) {
+    for (int c = 0; c < 4; c++)
+        st_shared_v4(stg + lane * 64 + ((c ^ sw) << 4), w[c * 4 + 0], w[c * 4 + 1], w[c * 4 + 2], w[c * 4 + 3]);
+    __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            if (gcol + q * 8 < n_out) {
-                V16 o;
-                o.w[0] = pk[q * 4 + 0]; o.w[1] = pk[q * 4 + 1];
-                o.w[2] = pk[q * 4 + 2]; o.w[3] = pk[q * 4 + 3];
-                st_v16(orow + gcol + q * 8, o);
-            }
-        }
+    for (int i = 0; i < 4; i++) {
+        const int row = 8 * i + (lane >> 2), c = lane & 3;
+        const uint4 q = *reinterpret_cast<const uint4 *>(stg + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+        if (row < rows && c * 16 < bytes)
+            *reinterpret_cast<uint4 *>(static_cast<char *>(out) + row * pitch + c * 16) = q;
     }
+    __syncwarp();
 }
 
 // A warp's block of 32 rows x 32 bf16 columns of another matrix (row 0, column 0 of the block at p, rows
@@ -378,8 +362,6 @@ __device__ __forceinline__ void blk_fetch(V16 (&v)[4], const __nv_bfloat16 *p, i
 
 // The fetched block turned through the warp's staging buffer: o[] = this lane's row, 16 pairs.
 __device__ __forceinline__ void blk_turn(uint8_t *stg, const V16 (&v)[4], uint32_t (&o)[16], int lane) {
-    if (lane == 0) bulk_wait_read<0>();   // the previous store has read the buffer
-    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int row = 8 * i + (lane >> 2);
@@ -392,37 +374,6 @@ __device__ __forceinline__ void blk_turn(uint8_t *stg, const V16 (&v)[4], uint32
         o[4 * c] = q.x; o[4 * c + 1] = q.y; o[4 * c + 2] = q.z; o[4 * c + 3] = q.w;
     }
     __syncwarp();
-}
-
-// The same for 16 fp32 columns (64-byte rows: the same staging pattern and
-// swizzle), with a 16 x 32 fp32 output map; the fallback stores this lane's
-// row directly.
-__device__ __forceinline__ void epi_store16f(const CUtensorMap *map, uint8_t *stg, const float *v,
-                                             bool all_kept, bool kept, int lane, int64_t grow0,
-                                             int gcol, int n_out, float *frow) {
-    if (all_kept) {
-        if (gcol >= n_out) return;  // warp-uniform
-        if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
-        __syncwarp();
-        const int sw = (lane >> 1) & 3;
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-            st_shared_v4(stg + lane * 64 + ((c ^ sw) << 4), __float_as_uint(v[4 * c]),
-                         __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-                         __float_as_uint(v[4 * c + 3]));
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(map, gcol, (int)grow0, stg);
-            bulk_commit();
-        }
-    } else if (kept) {
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (gcol + 4 * q < n_out)
-                *reinterpret_cast<float4 *>(frow + gcol + 4 * q) =
-                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    }
 }
 
 // ------------------------------------------------------- CTA-pair helpers
@@ -1047,10 +998,13 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             tc_fence_after();
             const int row = T.mt * BMT + row_in_tile;
             const bool valid = row < T.rows;
-            const bool all_kept = row - lane + 31 < T.rows;  // the warp's 32 rows
             const int64_t grow0 = row_base(T.j) + row - lane;
-            __nv_bfloat16 *orow =
-                args.out + (grow0 + lane) * (args.out_pitch ? args.out_pitch : (int64_t)args.n_out);
+            const int live = T.rows - (row - lane);          // live rows from the warp's first on
+            // a block of 32 bf16 columns from gcol on, of `out` with rows of `pitch` elements
+            auto store32 = [&](const uint32_t (&pk)[16], __nv_bfloat16 *out, int64_t pitch, int gcol) {
+                epi_store64(stg, pk, out + grow0 * pitch + gcol, 2 * pitch, live, 2 * (args.n_out - gcol), lane);
+            };
+            const int64_t opitch = args.out_pitch ? args.out_pitch : (int64_t)args.n_out;
             const __nv_bfloat16 *brow = args.bias ? args.bias + (int64_t)T.j * args.n_out : nullptr;
             const uint32_t tbase = tmem + ((uint32_t)(sub * 32) << 16) +
                                    (uint32_t)(acc * TL::ACC_COLS + (TM == 2 ? half * BN : 0));
@@ -1084,19 +1038,16 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             pk[i] = pack_bf16(silu(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
                                               silu(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
                     }
-                    epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out,
-                                orow);
+                    store32(pk, args.out, opitch, gcol);
                     if (EPI == EPI_SWIGLU_SAVE) {   // a, then b
-                        __nv_bfloat16 *arow = args.aux_out + (grow0 + lane) * (2 * (int64_t)args.n_out);
 #pragma unroll
                         for (int i = 0; i < 16; i++)
                             pk[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        epi_store32(&tmAt, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out, arow);
+                        store32(pk, args.aux_out, 2 * (int64_t)args.n_out, gcol);
 #pragma unroll
                         for (int i = 0; i < 16; i++)
                             pk[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-                        epi_store32(&tmBt, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out,
-                                    arow + args.n_out);
+                        store32(pk, args.aux_out + args.n_out, 2 * (int64_t)args.n_out, gcol);
                     }
                 }
             } else {
@@ -1117,9 +1068,6 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 __syncwarp();
                 // e4m3: this lane's row scale (its output row)
                 const float sa = F8 && valid ? args.a_scale[grow0 + lane] : 0.0f;
-                __nv_bfloat16 *prow =
-                    SAVE ? args.aux_out + (grow0 + lane) * (int64_t)args.n_out
-                         : nullptr;
                 const float *bsc = F8 ? args.b_scale + (int64_t)T.j * args.n_out : nullptr;
                 if constexpr (DACT || DACTP) {
                     // the derivative of an activation: a block of 32 columns at a time, the next one's
@@ -1174,10 +1122,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         };
                         if (DSWI && !mid) columns(std::true_type{});
                         else columns(std::false_type{});
-                        epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol, args.n_out, orow);
-                        if (DSWI)   // the second half of the output rows
-                            epi_store32(&tmB3, stg, pb, all_kept, valid, lane, grow0, gcol, args.n_out,
-                                        orow + args.n_out);
+                        store32(pk, args.out, opitch, gcol);
+                        if (DSWI) store32(pb, args.out + args.n_out, opitch, gcol);   // the second half of the rows
                     }
                 } else {
 #pragma unroll 1
@@ -1232,17 +1178,18 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                 }
                             }
                         }
-                        if constexpr (F32OUT) {   // fp32 weight gradients: two 16-column boxes
-                            float *frow = args.out_f32 + (grow0 + lane) * (int64_t)args.n_out;
-                            epi_store16f(&tmO, stg, of, all_kept, valid, lane, grow0, gcol, args.n_out,
-                                         frow);
-                            epi_store16f(&tmO, stg, of + 16, all_kept, valid, lane, grow0, gcol + 16,
-                                         args.n_out, frow);
+                        if constexpr (F32OUT) {   // fp32 weight gradients: 16 columns at a time
+#pragma unroll
+                            for (int hc = 0; hc < 2; hc++) {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int i = 0; i < 16; i++) w[i] = __float_as_uint(of[16 * hc + i]);
+                                epi_store64(stg, w, args.out_f32 + grow0 * args.n_out + gcol + 16 * hc,
+                                            4 * (int64_t)args.n_out, live, 4 * (args.n_out - gcol - 16 * hc), lane);
+                            }
                         } else {
-                            epi_store32(&tmO, stg, pk, all_kept, valid, lane, grow0, gcol,
-                                        args.n_out, orow);
-                            if (SAVE)
-                                epi_store32(&tmAt, stg, pp, all_kept, valid, lane, grow0, gcol, args.n_out, prow);
+                            store32(pk, args.out, opitch, gcol);
+                            if (SAVE) store32(pp, args.aux_out, (int64_t)args.n_out, gcol);
                         }
                     }
                 }
@@ -1258,8 +1205,6 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if (++acc == TL::NACC) { acc = 0; acc_phase ^= 1u; }
         }
-        if (lane == 0) bulk_wait_all();  // output stores complete before the CTA exits
-        __syncwarp();
     }
 
     tc_fence_before();

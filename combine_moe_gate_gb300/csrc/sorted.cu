@@ -13,10 +13,12 @@ namespace {
 // ------------------------------------------------------------------- the sort
 // Buckets 0 .. e-1 are the experts, bucket e the routes without one (source[] says -1 behind the
 // last row, so they are ranked like the others).
-constexpr int SS_NT = 1024, SS_NW = SS_NT / 32, SS_MAXE = 256, SS_MAXN = 16384;   // one launch
+constexpr int SS_NT = 1024, SS_NW = SS_NT / 32, SS_MAXE = 256, SS_MAXN = 2048;   // one launch
 constexpr int ST_NT = 256, ST_NW = ST_NT / 32, ST_BLK = 256;                      // two launches
 constexpr int ST_HELD = 8;                                                        // rounds kept in registers
 constexpr int SORT_MAXB = 1025;                                                   // buckets
+
+constexpr int NO_ROUTE = (int)0x80000000;   // past the table's end (as an entry of it: an error like any other)
 
 __device__ __forceinline__ int bucket_of(int v, int e, int32_t *status) {
     if ((unsigned)v < (unsigned)e) return v;
@@ -83,8 +85,9 @@ __device__ __forceinline__ void place_segment(const int32_t *__restrict__ idx, i
     }
 }
 
-// Up to 16384 routes of up to 256 experts: one launch, a CTA of 32 warps for 1024 routes.  Every
-// CTA counts all routes (at most 16 a thread) and those before its own, so none waits for another.
+// Up to 2048 routes of up to 256 experts: one launch, a CTA of 32 warps for 1024 routes.  Every
+// CTA counts all routes and those before its own, so none waits for another.  (16384 routes this way: 29 us;
+// a match of a warp's buckets costs about 50 clocks of the multiprocessor.)
 __global__ void __launch_bounds__(SS_NT)
 sort_small_kernel(const int32_t *__restrict__ idx, int n, int e, int32_t *__restrict__ rows,
                   int32_t *__restrict__ offsets, int32_t *__restrict__ source, int32_t *status) {
@@ -135,15 +138,15 @@ sort_hist_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds, 
     __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * rounds * ST_NT;
     for (int r0 = 0; r0 < rounds; r0 += ST_HELD) {
-        int b[ST_HELD];   // all loads in flight first
+        int v[ST_HELD];   // all loads in flight before the first is looked at
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++) {
             const int64_t j = base + (r0 + r) * ST_NT + threadIdx.x;
-            b[r] = r0 + r < rounds && j < n ? bucket_of(__ldg(idx + j), e, status) : -1;
+            v[r] = r0 + r < rounds && j < n ? __ldg(idx + j) : NO_ROUTE;
         }
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++)
-            if (r0 + r < rounds) count_warp(cnt, b[r], lt);
+            if (r0 + r < rounds) count_warp(cnt, v[r] != NO_ROUTE ? bucket_of(v[r], e, status) : -1, lt);
     }
     __syncthreads();
     for (int q = threadIdx.x; q < nb; q += ST_NT) hist[(int64_t)q * gridDim.x + blockIdx.x] = cnt[q];
@@ -171,22 +174,27 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++) {
             const int64_t j = at + r * 32 + lane;
-            bucket[r] = r < rounds && j < n ? bucket_of(__ldg(idx + j), e, status) : -1;
+            bucket[r] = r < rounds && j < n ? __ldg(idx + j) : NO_ROUTE;
         }
     }
     for (int q = tid; q < ST_NW * nb; q += ST_NT) cnt[q] = 0;
-    // four buckets a turn: up to 32 loads under way
+    // four buckets a turn: up to 32 loads under way before the first is added
     for (int b0 = warp; b0 < nb; b0 += 4 * ST_NW) {
-        int32_t all[4] = {0, 0, 0, 0}, pre[4] = {0, 0, 0, 0};
+        int32_t c[4][ST_BLK / 32], all[4], pre[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int q = 0; q < ST_BLK / 32; q++) {
+                const int b = b0 + i * ST_NW, k = 32 * q + lane;
+                c[i][q] = b < nb && k < nblk ? hist[(int64_t)b * nblk + k] : 0;
+            }
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const int b = b0 + i * ST_NW;
+            all[i] = pre[i] = 0;
 #pragma unroll
-            for (int q = 0; q < ST_BLK; q += 32) {
-                if (q >= nblk) break;
-                const int32_t c = b < nb && q + lane < nblk ? hist[(int64_t)b * nblk + q + lane] : 0;
-                all[i] += c;
-                pre[i] += q + lane < (int)blockIdx.x ? c : 0;
+            for (int q = 0; q < ST_BLK / 32; q++) {
+                all[i] += c[i][q];
+                pre[i] += 32 * q + lane < (int)blockIdx.x ? c[i][q] : 0;
             }
         }
 #pragma unroll
@@ -200,6 +208,9 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
     __syncthreads();
     int32_t *mine = cnt + warp * nb;
     if (HELD) {
+#pragma unroll
+        for (int r = 0; r < ST_HELD; r++)
+            bucket[r] = bucket[r] != NO_ROUTE ? bucket_of(bucket[r], e, status) : -1;
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++) {
             if (r >= rounds) break;
