@@ -152,15 +152,6 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
-// One lane of a converged warp.  The compiler knows that a single thread runs
-// what this guards and issues its tcgen05 instructions back to back: a row of
-// tcgen05.cp takes 17 cycles each, against 59 behind a comparison of the lane
-// number (4096 x 4096 x 8192, NV: 93 us with the comparison, 48 us with this).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 
 // mbar_wait by a whole warp: the same answer in every lane (what follows is
 // warp-wide).

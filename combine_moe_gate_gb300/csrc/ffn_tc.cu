@@ -296,28 +296,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// TMA store of a box from this CTA's shared memory (bulk async-group).
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, const void *src) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     (uint64_t)map),
-                 "r"(x), "r"(y), "r"(su32(src))
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Wait until at most N of this thread's store groups still read shared memory.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-// Wait until all of this thread's store groups have completed.
-__device__ __forceinline__ void bulk_wait_all() {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-__device__ __forceinline__ void fence_proxy_async() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 __device__ __forceinline__ void st_shared_v4(uint8_t *p, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(su32(p)), "r"(a), "r"(b), "r"(c),
@@ -528,6 +506,16 @@ __device__ __forceinline__ void tmem_tie(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31]));
 }
 
+// One lane of a converged warp.  The compiler knows that a single thread runs
+// what this guards and issues its tcgen05 instructions back to back: a row of
+// tcgen05.cp takes 17 cycles each, against 59 behind a comparison of the lane
+// number (4096 x 4096 x 8192, NV: 93 us with the comparison, 48 us with this).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // GELU, exact erf form: a * Phi(a) with Phi(a) = 0.5 (1 + erf(a / sqrt 2)),
 // evaluated as 1 - erfc/2 for a >= 0 and erfc(|a| / sqrt 2) / 2 for a < 0 so
 // that the negative tail does not cancel.  erfc(x) for x >= 0 by Abramowitz &
@@ -602,9 +590,14 @@ __device__ __forceinline__ float silu_mid(float a) {
     const float b = 1.0f + expf(-a);
     return div_mid(a, b, rcp_mid(b));
 }
-// 1 / (1 + e^-a), for |a| <= 80.
+// 1 / (1 + e^-a) as rcp_mid of the divisor, for |a| <= 80; two at a time.
 __device__ __forceinline__ bool sigmoid_mid_ok(float a) { return fabsf(a) <= 80.0f; }
-__device__ __forceinline__ float sigmoid_mid(float a) { return rcp_mid(1.0f + expf(-a)); }
+__device__ __forceinline__ float2 rcp_mid2(float2 x) {
+    float2 y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+    return __ffma2_rn(__ffma2_rn(make_float2(-x.x, -x.y), y, make_float2(1.0f, 1.0f)), y, y);
+}
 
 // Tile t -> (expert j, m-tile, n-tile); m-tile varies fastest.  rows: the
 // expert's output rows; nk: its K blocks.  kept_rows[] holds the output rows
@@ -788,10 +781,12 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         const bool is_a = (prod & 1) == 0;
         const int hh = prod >> 1;   // row half of this producer's boxes
         constexpr int A_BOX_BYTES = TL::A_BOX_ROWS * ROWB, B_BOX_BYTES = TL::B_BOX_ROWS * ROWB;
+        if (elect_one()) {
         int stage = 0;
         uint32_t phase = 0;
         int issued = 0;
-        for (int t = tile0; t < total && !args.stall; t += tile_step) {
+        bool ok = true;
+        for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
             Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
             // A: this CTA's 128 rows, half of them per producer
             const int a_row = (int)(row_base(T.j) + (int64_t)T.mt * BMT +
@@ -807,12 +802,12 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const bool part_tail = AMN && (kept_rows[T.j] % BK) != 0;
             const int k_base = AMN && args.offsets ? sorted_at(args, T.j) : T.j * args.b_rows;
             for (int kb = 0; kb < T.nk; kb++) {
-                int ok = 1;
-                if (lane == 0) {
-                    ok = mbar_wait<PAIR>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status);
+                ok = mbar_wait<PAIR>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status);
+                if (!ok) break;
+                {
                     const bool tail = part_tail && kb == T.nk - 1;
                     const int k_row = tail ? T.j * BK : k_base + kb * BK;
-                    if (ok && PAIR && AMN) {
+                    if (PAIR && AMN) {
                         const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
                         if (is_a) {
                             // this CTA's 128 output rows = A columns, block hh of 64
@@ -829,7 +824,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                                      i * (B_BOX_BYTES / TN),
                                                  tail ? &tmBt : &tmB, n_col + 64 * i, k_row, fb);
                         }
-                    } else if (ok && PAIR) {
+                    } else if (PAIR) {
                         const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
                         if (is_a) {
                             if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * A_BOX_BYTES);
@@ -853,32 +848,30 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES,
                                              is_swiglu(EPI) && prank ? &tmB3 : &tmB, kb * BK, b_row, fb);
                         }
-                    } else if (ok && is_a) {
+                    } else if (is_a) {
                         mbar_expect_tx(&ctl->full[stage], A_BOX_BYTES);
                         tma_load_2d(sA + stage * A_BYTES + hh * A_BOX_BYTES, &tmA, kb * BK, a_row,
                                     &ctl->full[stage]);
-                    } else if (ok && is_swiglu(EPI)) {
+                    } else if (is_swiglu(EPI)) {
                         // W1 rows in the first half of the B tile, W3 rows in the second
                         mbar_expect_tx(&ctl->full[stage], B_BOX_BYTES);
                         tma_load_2d(sB + stage * B_BYTES + hh * B_BOX_BYTES, hh ? &tmB3 : &tmB, kb * BK,
                                     b_row - hh * TL::B_BOX_ROWS, &ctl->full[stage]);
-                    } else if (ok) {
+                    } else {
                         mbar_expect_tx(&ctl->full[stage], B_BOX_BYTES);
                         tma_load_2d(sB + stage * B_BYTES + hh * B_BOX_BYTES, &tmB, kb * BK, b_row,
                                     &ctl->full[stage]);
                     }
                 }
-                if (!__shfl_sync(0xffffffffu, ok, 0)) goto producer_done;
                 issued++;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-    producer_done:
         // wait (bounded) for this thread's copies still in flight before the CTA
         // can exit (a pair's second CTA cannot observe the first CTA's barriers:
         // its copies are covered by the MMAs that consume them, or on an abort
         // by the delay before the final cluster barrier)
-        if (lane == 0 && (!PAIR || prank == 0)) {
+        if (!PAIR || prank == 0) {
             for (int i = max(0, issued - STAGES); i < issued; i++) {
                 int s = i % STAGES;
                 uint32_t ph = (uint32_t)((i / STAGES) & 1);
@@ -887,8 +880,11 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 }
             }
         }
-    } else if (warp == 1 && lane == 0) {
+        }
+        __syncwarp();
+    } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
+        if (elect_one()) {
         if (!PAIR || prank == 0) {
             // both CTAs of the pair
             const uint16_t pair_mask = (uint16_t)3u;
@@ -968,6 +964,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         unsigned long long t0 = gtimer();
         while (!mbar_try<PAIR>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
         }
+        }
+        __syncwarp();
     } else if (warp >= 2 && warp < PROD_WARP0) {
         // ------------------------------------------------------------- epilogue
         // TM = 1: warp (sub, half) owns rows sub*32.. and half of the columns.
@@ -1088,10 +1086,12 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         if (T.nk > 0) tmem_wait_ld(r);
                         uint32_t pk[16], pb[16];
                         bool mid = true;
-                        if (DSWI) {
+                        if (DSWI) {   // the largest magnitude of the row's a, two at a time
+                            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
 #pragma unroll
                             for (int i = 0; i < 16; i++)
-                                mid &= sigmoid_mid_ok(bf16lo(dv[i])) && sigmoid_mid_ok(bf16hi(dv[i]));
+                                top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&dv[i])));
+                            mid = sigmoid_mid_ok(__low2float(top)) && sigmoid_mid_ok(__high2float(top));
                             mid = !__any_sync(0xffffffffu, valid && !mid);
                         }
                         auto columns = [&](auto general) {
@@ -1104,11 +1104,15 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             if constexpr (DSWI) {
                                 // a = d_hid; u and bv: the saved a and b of these two columns
                                 const float2 bv = make_float2(bf16lo(db[i]), bf16hi(db[i]));
-                                const float sx = general.value ? 1.0f / (1.0f + expf(-u.x)) : sigmoid_mid(u.x);
-                                const float sy = general.value ? 1.0f / (1.0f + expf(-u.y)) : sigmoid_mid(u.y);
-                                pb[i] = pack_bf16(a.x * u.x * sx, a.y * u.y * sy);   // d_b
-                                a = make_float2(a.x * bv.x * sx * (1.0f + u.x * (1.0f - sx)),
-                                                a.y * bv.y * sy * (1.0f + u.y * (1.0f - sy)));   // d_a
+                                const float2 one = make_float2(1.0f, 1.0f);
+                                const float2 den = __fadd2_rn(one, make_float2(expf(-u.x), expf(-u.y)));
+                                float2 sg;
+                                if (general.value) sg = make_float2(1.0f / den.x, 1.0f / den.y);
+                                else sg = rcp_mid2(den);
+                                const float2 db2 = __fmul2_rn(__fmul2_rn(a, u), sg);
+                                pb[i] = pack_bf16(db2.x, db2.y);   // d_b
+                                const float2 rest = __fadd2_rn(one, make_float2(-sg.x, -sg.y));
+                                a = __fmul2_rn(__fmul2_rn(__fmul2_rn(a, bv), sg), __ffma2_rn(u, rest, one));   // d_a
                             } else {
                                 // DACT: aux is d_hid, a the pre-activation; DACTP: aux is the saved
                                 // pre-activation, a = d_hid
