@@ -354,6 +354,64 @@ __device__ __forceinline__ void blk_turn(uint8_t *stg, const V16 (&v)[4], uint32
     __syncwarp();
 }
 
+// The same for two matrices' blocks of 32 rows x 16 columns (32-byte rows; in the staging buffer the first at
+// 0, the second at 1024, 16-byte chunk c of row r at c ^ ((r >> 2) & 1)): fetched or stored by pieces of 16
+// rows, held as this lane's rows.
+__device__ __forceinline__ void half_fetch(V16 (&v)[2], const __nv_bfloat16 *p, int64_t pitch, int rows, int cols,
+                                           int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int row = 16 * i + (lane >> 1), col = (lane & 1) * 8;
+        v[i] = V16{};
+        if (row < rows && col < cols) v[i] = ld_v16(p + row * pitch + col);
+    }
+}
+__device__ __forceinline__ uint8_t *half_at(uint8_t *stg, int row, int c) {
+    return stg + row * 32 + ((c ^ ((row >> 2) & 1)) << 4);
+}
+__device__ __forceinline__ void half_put(uint8_t *stg, const V16 (&a)[2], const V16 (&b)[2], int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        uint8_t *p = half_at(stg, 16 * i + (lane >> 1), lane & 1);
+        st_shared_v4(p, a[i].w[0], a[i].w[1], a[i].w[2], a[i].w[3]);
+        st_shared_v4(p + 1024, b[i].w[0], b[i].w[1], b[i].w[2], b[i].w[3]);
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void half_row(uint8_t *stg, uint32_t (&a)[8], uint32_t (&b)[8], int lane) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        const uint8_t *p = half_at(stg, lane, c);
+        const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 1024);
+        a[4 * c] = x.x; a[4 * c + 1] = x.y; a[4 * c + 2] = x.z; a[4 * c + 3] = x.w;
+        b[4 * c] = y.x; b[4 * c + 1] = y.y; b[4 * c + 2] = y.z; b[4 * c + 3] = y.w;
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void half_row_put(uint8_t *stg, const uint32_t (&a)[8], const uint32_t (&b)[8], int lane) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+        uint8_t *p = half_at(stg, lane, c);
+        st_shared_v4(p, a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
+        st_shared_v4(p + 1024, b[4 * c], b[4 * c + 1], b[4 * c + 2], b[4 * c + 3]);
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void half_store(uint8_t *stg, __nv_bfloat16 *pa, __nv_bfloat16 *pb, int64_t pitch, int rows,
+                                           int cols, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int row = 16 * i + (lane >> 1), col = (lane & 1) * 8;
+        const uint8_t *p = half_at(stg, row, lane & 1);
+        const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 1024);
+        if (row < rows && col < cols) {
+            *reinterpret_cast<uint4 *>(pa + row * pitch + col) = x;
+            *reinterpret_cast<uint4 *>(pb + row * pitch + col) = y;
+        }
+    }
+    __syncwarp();
+}
+
 // ------------------------------------------------------- CTA-pair helpers
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -493,6 +551,22 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
           "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
         :
         : "memory");
+}
+
+// 16 columns: the load, and the wait tied to its registers.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 
 // Ties further registers to an already completed wait (emits nothing).
@@ -980,14 +1054,18 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         uint8_t *stg = stg_all + ew * STG_WARP_BYTES;
         int acc = 0;
         uint32_t acc_phase = 0;
-        // derivative epilogues: this warp's next 32 x 32 block of aux (SwiGLU: of a and of b)
-        V16 fa[4], fb[4];
+        // derivative epilogues: this warp's next block of aux, 32 rows x 32 columns (SwiGLU: 16 of a and of b)
+        V16 fa[DSWI ? 2 : 4], fb[2];
         auto fetch = [&](const Tile &T, int c0) {
             const int row0 = T.mt * BMT + row_in_tile - lane, gcol = T.nt * NOUT_TILE + col0 + c0;
             const int64_t pitch = (DSWI ? 2 : 1) * (int64_t)args.n_out;
             const __nv_bfloat16 *p = args.aux + (row_base(T.j) + row0) * pitch + gcol;
-            blk_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
-            if (DSWI) blk_fetch(fb, p + args.n_out, pitch, T.rows - row0, args.n_out - gcol, lane);
+            if constexpr (DSWI) {
+                half_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
+                half_fetch(fb, p + args.n_out, pitch, T.rows - row0, args.n_out - gcol, lane);
+            } else if constexpr (DACT || DACTP) {
+                blk_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
+            }
         };
         for (int t = tile0; t < total; t += tile_step) {
             Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
@@ -1067,13 +1145,62 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 // e4m3: this lane's row scale (its output row)
                 const float sa = F8 && valid ? args.a_scale[grow0 + lane] : 0.0f;
                 const float *bsc = F8 ? args.b_scale + (int64_t)T.j * args.n_out : nullptr;
-                if constexpr (DACT || DACTP) {
+                if constexpr (DSWI) {
+                    // SwiGLU's derivative, 16 columns at a time: with 32, and the next block's rows of a
+                    // and b on their way, no registers are left for elements to overlap (a block of
+                    // 32 columns took 7000 clocks at a fifth of the issue slots)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < COLS; c0 += 16) {
+                        const int gcol = T.nt * NOUT_TILE + col0 + c0;
+                        uint32_t r[16], ua[8], ub[8];
+                        if (T.nk > 0) {
+                            tmem_ld16(tbase + (uint32_t)(col0 + c0), r);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i++) r[i] = 0u;   // empty contraction
+                        }
+                        half_put(stg, fa, fb, lane);
+                        half_row(stg, ua, ub, lane);
+                        if (c0 + 16 < COLS) fetch(T, c0 + 16);
+                        __nv_bfloat162 top = __float2bfloat162_rn(0.0f);   // the largest magnitude of a
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&ua[i])));
+                        const bool mid = sigmoid_mid_ok(__low2float(top)) && sigmoid_mid_ok(__high2float(top));
+                        if (T.nk > 0) tmem_wait_ld16(r);
+                        uint32_t da[8], db[8];
+                        auto columns = [&](auto general) {
+                            const float2 one = make_float2(1.0f, 1.0f);
+#pragma unroll
+                            for (int i = 0; i < 8; i++) {
+                                const float2 dh = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                const float2 u = make_float2(bf16lo(ua[i]), bf16hi(ua[i]));
+                                const float2 v = make_float2(bf16lo(ub[i]), bf16hi(ub[i]));
+                                const float2 den = __fadd2_rn(one, make_float2(expf(-u.x), expf(-u.y)));
+                                float2 sg;
+                                if (general.value) sg = make_float2(1.0f / den.x, 1.0f / den.y);
+                                else sg = rcp_mid2(den);
+                                const float2 y = __fmul2_rn(__fmul2_rn(dh, u), sg);
+                                const float2 rest = __fadd2_rn(one, make_float2(-sg.x, -sg.y));
+                                const float2 x = __fmul2_rn(__fmul2_rn(__fmul2_rn(dh, v), sg), __ffma2_rn(u, rest, one));
+                                da[i] = pack_bf16(x.x, x.y);
+                                db[i] = pack_bf16(y.x, y.y);
+                            }
+                        };
+                        if (__any_sync(0xffffffffu, valid && !mid)) columns(std::true_type{});
+                        else columns(std::false_type{});
+                        // d_a, and d_b in the second half of the rows
+                        half_row_put(stg, da, db, lane);
+                        half_store(stg, args.out + grow0 * opitch + gcol, args.out + grow0 * opitch + args.n_out + gcol,
+                                   opitch, live, args.n_out - gcol, lane);
+                    }
+                } else if constexpr (DACT || DACTP) {
                     // the derivative of an activation: a block of 32 columns at a time, the next one's
                     // rows of aux on their way meanwhile
 #pragma unroll 1
                     for (int c0 = 0; c0 < COLS; c0 += 32) {
                         const int gcol = T.nt * NOUT_TILE + col0 + c0;
-                        uint32_t r[32], dv[16], db[16];
+                        uint32_t r[32], dv[16];
                         if (T.nk > 0) {
                             tmem_ld32(tbase + (uint32_t)(col0 + c0), r);
                         } else {
@@ -1081,53 +1208,24 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             for (int i = 0; i < 32; i++) r[i] = 0u;   // empty contraction
                         }
                         blk_turn(stg, fa, dv, lane);
-                        if (DSWI) blk_turn(stg, fb, db, lane);
                         if (c0 + 32 < COLS) fetch(T, c0 + 32);
                         if (T.nk > 0) tmem_wait_ld(r);
-                        uint32_t pk[16], pb[16];
-                        bool mid = true;
-                        if (DSWI) {   // the largest magnitude of the row's a, two at a time
-                            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
-#pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&dv[i])));
-                            mid = sigmoid_mid_ok(__low2float(top)) && sigmoid_mid_ok(__high2float(top));
-                            mid = !__any_sync(0xffffffffu, valid && !mid);
-                        }
-                        auto columns = [&](auto general) {
+                        uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
                             const float2 acc2 = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
                             const float2 bias2 = *reinterpret_cast<const float2 *>(bsl + c0 + 2 * i);
-                            float2 a = __fadd2_rn(acc2, bias2);
+                            const float2 a = __fadd2_rn(acc2, bias2);
                             const float2 u = make_float2(bf16lo(dv[i]), bf16hi(dv[i]));
-                            if constexpr (DSWI) {
-                                // a = d_hid; u and bv: the saved a and b of these two columns
-                                const float2 bv = make_float2(bf16lo(db[i]), bf16hi(db[i]));
-                                const float2 one = make_float2(1.0f, 1.0f);
-                                const float2 den = __fadd2_rn(one, make_float2(expf(-u.x), expf(-u.y)));
-                                float2 sg;
-                                if (general.value) sg = make_float2(1.0f / den.x, 1.0f / den.y);
-                                else sg = rcp_mid2(den);
-                                const float2 db2 = __fmul2_rn(__fmul2_rn(a, u), sg);
-                                pb[i] = pack_bf16(db2.x, db2.y);   // d_b
-                                const float2 rest = __fadd2_rn(one, make_float2(-sg.x, -sg.y));
-                                a = __fmul2_rn(__fmul2_rn(__fmul2_rn(a, bv), sg), __ffma2_rn(u, rest, one));   // d_a
-                            } else {
-                                // DACT: aux is d_hid, a the pre-activation; DACTP: aux is the saved
-                                // pre-activation, a = d_hid
-                                const float2 z = DACT ? a : u, g = DACT ? u : a;
-                                const float2 da = DGELU ? gelu_grad2(z)
-                                                        : make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
-                                a = __fmul2_rn(g, da);
-                            }
-                            pk[i] = pack_bf16(a.x, a.y);
+                            // DACT: aux is d_hid, a the pre-activation; DACTP: aux is the saved
+                            // pre-activation, a = d_hid
+                            const float2 z = DACT ? a : u, g = DACT ? u : a;
+                            const float2 da = DGELU ? gelu_grad2(z)
+                                                    : make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+                            const float2 d = __fmul2_rn(g, da);
+                            pk[i] = pack_bf16(d.x, d.y);
                         }
-                        };
-                        if (DSWI && !mid) columns(std::true_type{});
-                        else columns(std::false_type{});
                         store32(pk, args.out, opitch, gcol);
-                        if (DSWI) store32(pb, args.out + args.n_out, opitch, gcol);   // the second half of the rows
                     }
                 } else {
 #pragma unroll 1
