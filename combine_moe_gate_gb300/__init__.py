@@ -831,5 +831,8 @@ def moe_probe_fp32_fma(packed, blocks, iters, out, stream=None):
                                      _ptr(out, "out", _f32()), _stream(stream)), "moe_probe_fp32_fma")
 
 
-from .layer import (Fp4Operand, MoELayerBuffers, MoELayerFp4Buffers, alloc_layer,  # noqa: E402,F401
-                    alloc_layer_fp4, quantize_weights_fp4, run_layer, run_layer_fp4, run_layer_host)
+from .layer import (Fp4Operand, Int8Operand, MoELayerBuffers, MoELayerFp4Buffers,  # noqa: E402,F401
+                    MoESortedBuffers, MoESortedGrads, alloc_grads_sorted, alloc_layer,
+                    alloc_layer_fp4, alloc_layer_sorted, quantize_weights_fp4, quantize_weights_int8,
+                    run_layer, run_layer_fp4, run_layer_host, run_layer_int8, run_layer_sorted,
+                    run_layer_sorted_bwd)

@@ -104,15 +104,19 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
 size_t ffn_tc_sorted_bwd_workspace_bytes(moe_act act, int e, int64_t n, int m, int h);
 moe_status quantize_rows_int8_launch(const void *src, moe_dtype sdt, const int32_t *rows, int64_t s, int cols, int k,
                                      int64_t n, void *q, float *scale, int32_t *st, cudaStream_t stream);
-size_t product_int8_workspace_bytes(int64_t n, int k);
+size_t product_int8_workspace_bytes(int e, int64_t n, int k);
 moe_status product_int8_launch(const void *a_q, const float *a_scale, const SortedRows &so, const void *b_q,
                                const float *b_scale, const void *bias, int e, int k, int n_out, void *ws, void *out,
                                bool f32, int32_t *st, cudaStream_t stream);
-size_t ffn_int8_workspace_bytes(int64_t n, int m, int h);
+size_t ffn_int8_workspace_bytes(int e, int64_t n, int m, int h);
 moe_status ffn_int8_launch(const void *x_q, const float *x_scale, const SortedRows &so, const void *w1_q,
                            const float *w1_scale, const void *b1, const void *w3_q, const float *w3_scale,
                            const void *w2_q, const float *w2_scale, const void *b2, moe_act act, int e, int m, int h,
                            void *ws, void *out, int32_t *st, cudaStream_t stream);
+bool few_rows(int64_t n, int e);
+moe_status ffn_few_launch(const void *x, const SortedRows &so, const void *w1, const void *b1, const void *w3,
+                          const void *w2, const void *b2, moe_act act, int e, int m, int h, void *hid, void *pre,
+                          void *out, int32_t *st, cudaStream_t stream);
 size_t sort_workspace_bytes(int64_t s, int e, int k);
 moe_status sort_routes_launch(const int32_t *idx, int64_t s, int e, int k, int32_t *rows, int32_t *offsets,
                               int32_t *source, void *ws, int32_t *st, cudaStream_t stream);
@@ -493,6 +497,9 @@ moe_status moe_expert_ffn_sorted(const void *x, moe_dtype dt, const int32_t *off
         return MOE_ERR_INVALID_ARG;
     if (act == MOE_ACT_SWIGLU && (!ok16(w3) || b1 || b2)) return MOE_ERR_INVALID_ARG;
     if (dt != MOE_BF16 || !sorted_ffn_supported(act, e, n, m, h)) return MOE_ERR_UNSUPPORTED;
+    if (few_rows(n, e))
+        return ffn_few_launch(x, SortedRows{offsets, n}, w1, b1, w3, w2, b2, act, e, m, h, hid, pre, out, dev_status,
+                              as_stream(stream));
     return ffn_tc_launch(x, nullptr, nullptr, w1, b1, w3, w2, b2, act, e, n, m, h, hid, out, dev_status,
                          as_stream(stream), 0, 0, pre, SortedRows{offsets, n});
 }
@@ -545,7 +552,7 @@ moe_status moe_quantize_rows_int8(const void *src, moe_dtype sdt, const int32_t 
 
 size_t moe_product_int8_workspace_size(int e, int64_t n, int k, int n_out) {
     if (!int8_shape_ok(e, n, k, n_out) || !int8_supported(e, n, k, n_out)) return 0;
-    return product_int8_workspace_bytes(n, k);
+    return product_int8_workspace_bytes(e, n, k);
 }
 
 moe_status moe_product_int8(const void *a_q, const float *a_scale, const int32_t *offsets, const void *b_q,
@@ -557,7 +564,7 @@ moe_status moe_product_int8(const void *a_q, const float *a_scale, const int32_t
         !ok16(out) || !ok4(dev_status))
         return MOE_ERR_INVALID_ARG;
     if (!int8_supported(e, n, k, n_out)) return MOE_ERR_UNSUPPORTED;
-    if (workspace_bytes < product_int8_workspace_bytes(n, k)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < product_int8_workspace_bytes(e, n, k)) return MOE_ERR_INVALID_ARG;
     return product_int8_launch(a_q, a_scale, SortedRows{offsets, n}, b_q, b_scale, bias, e, k, n_out, workspace, out,
                                odt == MOE_F32, dev_status, as_stream(stream));
 }
@@ -566,7 +573,7 @@ size_t moe_expert_ffn_int8_workspace_size(moe_act act, int e, int64_t n, int m, 
     if (!act_ok(act) || m % 16 || !int8_shape_ok(e, n, m, h) || !int8_shape_ok(e, n, h, m) ||
         !int8_supported(e, n, m, h) || !int8_supported(e, n, h, m))
         return 0;
-    return ffn_int8_workspace_bytes(n, m, h);
+    return ffn_int8_workspace_bytes(e, n, m, h);
 }
 
 moe_status moe_expert_ffn_int8(const void *x_q, const float *x_scale, const int32_t *offsets, const void *w1_q,
@@ -581,7 +588,7 @@ moe_status moe_expert_ffn_int8(const void *x_q, const float *x_scale, const int3
     if (act == MOE_ACT_SWIGLU ? !ok16(w3_q) || !ok4(w3_scale) || b1 || b2 : w3_q || w3_scale)
         return MOE_ERR_INVALID_ARG;
     if (!int8_supported(e, n, m, h) || !int8_supported(e, n, h, m)) return MOE_ERR_UNSUPPORTED;
-    if (workspace_bytes < ffn_int8_workspace_bytes(n, m, h)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < ffn_int8_workspace_bytes(e, n, m, h)) return MOE_ERR_INVALID_ARG;
     return ffn_int8_launch(x_q, x_scale, SortedRows{offsets, n}, w1_q, w1_scale, b1, w3_q, w3_scale, w2_q, w2_scale, b2,
                            act, e, m, h, workspace, out, dev_status, as_stream(stream));
 }

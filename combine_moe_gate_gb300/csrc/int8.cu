@@ -1,4 +1,4 @@
-// 8-bit integer rows: the quantiser, the products of few rows, and the order of the launches.
+// 8-bit integer rows: the quantiser, and the order of the launches.
 //
 //   scale = amax / 127, code = rn(x * (127 / amax))   per row, in fp32
 #include "int8.cuh"
@@ -202,11 +202,13 @@ widen_rows_kernel(const uint4 *__restrict__ src, uint4 *__restrict__ dst, const 
 }
 
 // ---------------------------------------------------------- products of few rows
-// Up to FEW_ROWS rows in all: a warp forms CPW = 2 output channels (SwiGLU: one of W1 and the same of
+// A warp forms CPW = 2 output channels (SwiGLU: one of W1 and the same of
 // W3) with every row of the channel's expert, R at a time; its lanes walk along K in 16-byte pieces
 // with dp4a, so the sums are exact integers.  Bound by the weights' bytes: FU pieces of both channels are
 // in flight a lane.  CTA (x, y): channels, and the expert whose first row is row y (others leave).
-constexpr int FEW_ROWS = 8, FU = 4, CPW = 2;
+// (mma.sync on 8-bit integers, 8 rows at a time, was slower here already at one row: 18 us against 13 for the FFN of
+// a row of 64 experts, 1024 x 704.)
+constexpr int FU = 4, CPW = 2;
 
 struct FewArgs {
     const int8_t *x, *w, *w3;
@@ -339,6 +341,12 @@ moe_status few(int act, bool f32, const FewArgs &g, cudaStream_t stream) {
     }
 }
 
+// Whether n rows in all go by dot products.  Each row costs them time, the tiles hardly any, so that the rows an
+// expert has decide, of which the host knows only the average (FFN, cold, dot products | tiles, us): 1 expert
+// 4096 x 8192, 2 rows 34 | 52, 4 rows 53 | 52; 8 experts of that size, 4 rows 56 | 56, 8 rows 83 | 74; 64 experts
+// 1024 x 704, 32 rows 32 | 39, 64 rows 48 | 48; 256 experts 2048 x 512, 64 rows 70 | 75.
+bool few_rows8(int64_t n, int e) { return n <= (e <= 4 ? 2 : e < 128 ? e / 2 : 64); }
+
 constexpr int64_t up256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 
 const int32_t *rows_end(const SortedRows &so, int e) { return so.offsets ? so.offsets + e : nullptr; }
@@ -362,14 +370,14 @@ moe_status quantize_rows_int8_launch(const void *src, moe_dtype sdt, const int32
 }
 
 // The rows as fp16 numbers, for the tensor-core form.
-size_t product_int8_workspace_bytes(int64_t n, int k) {
-    return (size_t)(n <= FEW_ROWS ? 256 : up256(n * k * 2));
+size_t product_int8_workspace_bytes(int e, int64_t n, int k) {
+    return (size_t)(few_rows8(n, e) ? 256 : up256(n * k * 2));
 }
 
 moe_status product_int8_launch(const void *a_q, const float *a_scale, const SortedRows &so, const void *b_q,
                                const float *b_scale, const void *bias, int e, int k, int n_out, void *ws, void *out,
                                bool f32, int32_t *st, cudaStream_t stream) {
-    if (so.n <= FEW_ROWS) {
+    if (few_rows8(so.n, e)) {
         const FewArgs g{(const int8_t *)a_q, (const int8_t *)b_q, nullptr, a_scale, b_scale, nullptr,
                         (const __nv_bfloat16 *)bias, out, so, e, k, n_out, st};
         return few(I8_BIAS, f32, g, stream);
@@ -385,28 +393,28 @@ struct FfnInt8Layout {
     int64_t hid, scale, code, x16, total;
 };
 
-FfnInt8Layout ffn_int8_layout(int64_t n, int m, int h) {
+FfnInt8Layout ffn_int8_layout(int e, int64_t n, int m, int h) {
     FfnInt8Layout L{};
     L.scale = up256(n * h * 2);
     L.code = L.scale + up256(n * 4);
-    L.x16 = L.code + up256(n * h * (n <= FEW_ROWS ? 1 : 2));
-    L.total = L.x16 + (n <= FEW_ROWS ? 0 : up256(n * m * 2));
+    L.x16 = L.code + up256(n * h * (few_rows8(n, e) ? 1 : 2));
+    L.total = L.x16 + (few_rows8(n, e) ? 0 : up256(n * m * 2));
     return L;
 }
 
-size_t ffn_int8_workspace_bytes(int64_t n, int m, int h) { return (size_t)ffn_int8_layout(n, m, h).total; }
+size_t ffn_int8_workspace_bytes(int e, int64_t n, int m, int h) { return (size_t)ffn_int8_layout(e, n, m, h).total; }
 
 moe_status ffn_int8_launch(const void *x_q, const float *x_scale, const SortedRows &so, const void *w1_q,
                            const float *w1_scale, const void *b1, const void *w3_q, const float *w3_scale,
                            const void *w2_q, const float *w2_scale, const void *b2, moe_act act, int e, int m, int h,
                            void *ws, void *out, int32_t *st, cudaStream_t stream) {
-    const FfnInt8Layout L = ffn_int8_layout(so.n, m, h);
+    const FfnInt8Layout L = ffn_int8_layout(e, so.n, m, h);
     char *w = (char *)ws;
     const int a = act == MOE_ACT_RELU ? I8_RELU : act == MOE_ACT_GELU ? I8_GELU : I8_SWIGLU;
     float *hs = (float *)(w + L.scale);
     const QuantArgs hq{w + L.hid, nullptr, rows_end(so, e), w + L.code, hs, so.n, so.n, h, 0, st};
     moe_status r;
-    if (so.n <= FEW_ROWS) {
+    if (few_rows8(so.n, e)) {
         const FewArgs g1{(const int8_t *)x_q, (const int8_t *)w1_q, (const int8_t *)w3_q, x_scale, w1_scale, w3_scale,
                          (const __nv_bfloat16 *)b1, w + L.hid, so, e, m, h, st};
         if ((r = few(a, false, g1, stream)) != MOE_OK) return r;

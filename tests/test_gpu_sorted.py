@@ -251,7 +251,7 @@ def forward(p, act, train=True):
     return hid, pre, out
 
 
-SHAPES = [([1], 8, 8), ([3, 0, 1], 64, 40), ([0, 0, 65], 72, 136), ([64, 128, 256, 1, 0, 255, 257], 128, 256),
+SHAPES = [([1], 8, 8), ([33], 520, 24), ([64], 264, 40), ([2, 0, 40, 11], 1032, 88), ([50, 15], 264, 40), ([3, 0, 1], 64, 40), ([0, 0, 65], 72, 136), ([64, 128, 256, 1, 0, 255, 257], 128, 256),
           ([500, 2, 700], 264, 520), ([0, 33, 31, 32, 97], 1024, 704), ([1] * 40 + [0] * 20, 256, 96),
           ([1300, 0, 300, 64], 520, 1040)]
 
