@@ -93,7 +93,7 @@ struct I8Ctl {
 };
 
 constexpr size_t I8_SMEM = 1024 + (size_t)I8_WST * I8_W_BYTES + (size_t)I8_XST * I8_X_BYTES + 4 * I8_STG_BYTES + sizeof(I8Ctl);
-static_assert(I8_SMEM <= 227 * 1024 - 600, "shared memory");   // and what is not dynamic
+static_assert(I8_SMEM + 4 * I8_NT * 4 + 64 <= 227 * 1024, "shared memory");   // with what is not dynamic
 
 struct I8Args {
     SortedRows so;               // offsets null: one expert has all n rows
@@ -211,21 +211,44 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     constexpr bool SWI = EPI == I8_SWIGLU;
     constexpr int CH = SWI ? 64 : UM;             // output channels per CTA and tile
     __shared__ int32_t s_bad;
-    pdl_enter();
-    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
-    __syncthreads();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sW = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sX = sW + I8_WST * I8_W_BYTES;
     uint8_t *stg_all = sX + I8_XST * I8_X_BYTES;
     I8Ctl *ctl = (I8Ctl *)(stg_all + 4 * I8_STG_BYTES);
-    __shared__ __align__(16) float s_scale[4][32];
+    __shared__ __align__(16) float s_scale[4][I8_NT];   // per epilogue warp: the tile's row scales
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int tile0 = blockIdx.x / 2, tile_step = gridDim.x / 2;
     const int nct = (args.n_out + 2 * CH - 1) / (2 * CH);
     const int nk = (args.K + I8_BK - 1) / I8_BK;
 
+    // barriers and TMEM before the wait for the kernel before, what the offsets say after it
+    if (warp == 0 && lane == 0) {
+        ctl->abort = 0;
+        for (int s = 0; s < I8_WST; s++) {
+            mbar_init(&ctl->wfull[s], 1);
+            mbar_init(&ctl->wempty[s], 4);
+        }
+        for (int s = 0; s < I8_XST; s++) {
+            mbar_init(&ctl->full[s], 10);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(&ctl->dfull[s], 1);
+            mbar_init(&ctl->dempty[s], 8);
+        }
+        mbar_init(&ctl->drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    pdl_enter();
+    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
     if (warp == 0) {
         int run = 0, max_n = 0;
         bool bad = false;
@@ -259,27 +282,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             ctl->max_n = max_n;
             ctl->tile_start[args.e] = run;
             ctl->total_tiles = run;
-            ctl->abort = 0;
-            for (int s = 0; s < I8_WST; s++) {
-                mbar_init(&ctl->wfull[s], 1);
-                mbar_init(&ctl->wempty[s], 4);
-            }
-            for (int s = 0; s < I8_XST; s++) {
-                mbar_init(&ctl->full[s], 10);
-                mbar_init(&ctl->empty[s], 1);
-            }
-            for (int s = 0; s < 2; s++) {
-                mbar_init(&ctl->dfull[s], 1);
-                mbar_init(&ctl->dempty[s], 8);
-            }
-            mbar_init(&ctl->drain, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-    } else if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ctl->tmem_base)),
-                     "r"(TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     cluster_sync();
@@ -461,6 +464,8 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 sb = SWI && lane >= 16 ? args.w3_scale[at] : args.w_scale[at];
                 if (!SWI && args.bias) bias = __bfloat162float(args.bias[at]);
             }
+            for (int r = lane; r < T.n; r += 32) ssc[r] = r < T.rows ? args.x_scale[(int64_t)T.row0 + r] : 0.0f;
+            __syncwarp();
             const bool ok = i8_wait<true>(&ctl->dfull[i & 1], (i >> 1) & 1, abort_flag, args.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -480,14 +485,12 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 uint32_t r[32];
                 tmem_ld32(tb + (uint32_t)c0, r);
                 const int left = T.rows - c0;          // live rows of this block (32 or fewer)
-                ssc[lane] = lane < left ? args.x_scale[(int64_t)T.row0 + c0 + lane] : 0.0f;
-                __syncwarp();
                 tmem_wait_ld(r);
                 if (q + 1 == both) next_tile();
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
-                    const float4 sa = *reinterpret_cast<const float4 *>(ssc + i);
+                    const float4 sa = *reinterpret_cast<const float4 *>(ssc + c0 + i);
                     v[i] = __fmaf_rn(__uint_as_float(r[i]), sa.x * sb, bias);
                     v[i + 1] = __fmaf_rn(__uint_as_float(r[i + 1]), sa.y * sb, bias);
                     v[i + 2] = __fmaf_rn(__uint_as_float(r[i + 2]), sa.z * sb, bias);
@@ -551,7 +554,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                                 *reinterpret_cast<const uint4 *>(sp + row * 32 + part);
                     }
                 }
-                __syncwarp();   // staging and scales are rewritten for the next block
+                __syncwarp();   // staging is rewritten for the next block, the scales for the next tile
             }
             if (!L.shared) next_tile();
         }

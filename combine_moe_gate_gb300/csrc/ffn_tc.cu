@@ -723,12 +723,6 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     constexpr int STAGES = TL::STAGES, BMT = TL::BMT, A_BYTES = TL::A_BYTES;
     constexpr int B_BYTES = TL::B_BYTES, ROWB = TL::ROWB;
     __shared__ int32_t s_bad;
-    pdl_enter();
-    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
-    __syncthreads();
-    // A single CTA may leave now (nothing allocated yet); a cluster decides
-    // together after its first cluster barrier.
-    if (!PAIR && s_bad) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = smem;
@@ -757,8 +751,38 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         return args.offsets && !kmode ? (int64_t)sorted_at(args, j) : (int64_t)j * args.c_max + args.row_lo;
     };
 
-    // ---- setup: per-expert row counts and tile prefix (warp 0), barriers,
-    // TMEM allocation (warp 1)
+    // ---- setup.  What needs nothing of the kernel before, the barriers (warp 0) and the TMEM (warp 1), comes
+    // before the wait for its end; then the per-expert row counts and the tile prefix (warp 0)
+    if (warp == 0 && lane == 0) {
+        ctl->abort = 0;
+        // full: one arrival (with its transaction bytes, for a pair those of
+        // both CTAs) from each of the four producers of the MMA-issuing CTA
+        // empty: released by the MMAs of every pair whose copies write the stage
+        for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 4); mbar_init(&ctl->empty[s], 1); }
+        for (int a = 0; a < 2; a++) {
+            mbar_init(&ctl->tfull[a], 1);
+            mbar_init(&ctl->tempty[a], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
+        }
+        mbar_init(&ctl->drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 1) {
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             su32(&ctl->tmem_base)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             su32(&ctl->tmem_base)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    __syncwarp();
+    pdl_enter();
+    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
     if (warp == 0) {
         const bool sorted = args.offsets != nullptr;
         const int c_eff = kmode || sorted ? 0 : (int)min((int64_t)*args.c_dev, args.c_max);
@@ -800,31 +824,6 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         if (lane == 0) {
             ctl->tile_start[e] = run;
             ctl->total_tiles = run;
-            ctl->abort = 0;
-            // full: one arrival (with its transaction bytes, for a pair those of
-            // both CTAs) from each of the four producers of the MMA-issuing CTA
-            // empty: released by the MMAs of every pair whose copies write the stage
-            for (int s = 0; s < STAGES; s++) { mbar_init(&ctl->full[s], 4); mbar_init(&ctl->empty[s], 1); }
-            for (int a = 0; a < 2; a++) {
-                mbar_init(&ctl->tfull[a], 1);
-                mbar_init(&ctl->tempty[a], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
-            }
-            mbar_init(&ctl->drain, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        }
-    } else if (warp == 1) {
-        if (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             su32(&ctl->tmem_base)),
-                         "r"(TMEM_COLS)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                             su32(&ctl->tmem_base)),
-                         "r"(TMEM_COLS)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
     tc_fence_before();
@@ -841,6 +840,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             any_bad |= b;
         }
         if (any_bad) total = 0;  // the same decision in every CTA of the cluster
+    } else if (s_bad) {
+        total = 0;
     }
     int32_t *abort_flag = &ctl->abort;
 
@@ -1067,9 +1068,27 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 blk_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
             }
         };
+        // a tile's part of aux into L2, a whole epilogue ahead: a block ahead does not cover DRAM's latency
+        auto to_l2 = [&](int t) {
+            const Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
+            const int row = T.mt * BMT + row_in_tile, gcol = T.nt * NOUT_TILE + col0;
+            if (row >= T.rows) return;
+            const __nv_bfloat16 *p = args.aux + (row_base(T.j) + row) * ((DSWI ? 2 : 1) * (int64_t)args.n_out) + gcol;
+#pragma unroll
+            for (int c = 0; c < COLS; c += 64)
+                if (gcol + c < args.n_out) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+                    if (DSWI) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + args.n_out + c));
+                }
+        };
+        if constexpr (DACT || DACTP)
+            if (tile0 < total) to_l2(tile0);
         for (int t = tile0; t < total; t += tile_step) {
             Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
-            if constexpr (DACT || DACTP) fetch(T, 0);   // on its way while the main loop ends
+            if constexpr (DACT || DACTP) {
+                fetch(T, 0);   // on its way while the main loop ends
+                if (t + tile_step < total) to_l2(t + tile_step);
+            }
             if (!mbar_wait<PAIR>(&ctl->tfull[acc], acc_phase, abort_flag, args.status)) break;
             tc_fence_after();
             const int row = T.mt * BMT + row_in_tile;

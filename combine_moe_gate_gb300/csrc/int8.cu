@@ -174,29 +174,28 @@ moe_status quantize_typed(const QuantArgs &g, cudaStream_t stream) {
     }
 }
 
-// Codes as fp16 numbers: dst[i] = src[i] over the first *end rows of `chunks` x 16 codes.
-constexpr int WN_U = 4;   // 16-byte loads under way a thread
+// Codes as fp16 numbers: dst[i] = src[i] over the first *end rows of `chunks` x 8 codes.  A thread takes 8
+// codes at a time, so that its warp writes 512 bytes in a row.
+constexpr int WN_U = 8;   // loads under way a thread
 
 __global__ void __launch_bounds__(256)
-widen_rows_kernel(const uint4 *__restrict__ src, uint4 *__restrict__ dst, const int32_t *end, int64_t n, int chunks,
+widen_rows_kernel(const uint2 *__restrict__ src, uint4 *__restrict__ dst, const int32_t *end, int64_t n, int chunks,
                   int32_t *status) {
     pdl_enter();
     if (status_bad(status)) return;
     const int64_t total = (end ? min((int64_t)max(*end, 0), n) : n) * chunks;
     for (int64_t i0 = (int64_t)blockIdx.x * 256 * WN_U + threadIdx.x; i0 < total; i0 += (int64_t)gridDim.x * 256 * WN_U) {
-        V16 v[WN_U];
+        uint2 v[WN_U];
 #pragma unroll
         for (int u = 0; u < WN_U; u++)
-            if (i0 + 256 * u < total) v[u] = ld_stream(src + i0 + 256 * u);
+            if (i0 + 256 * u < total) v[u] = __ldg(src + i0 + 256 * u);
 #pragma unroll
         for (int u = 0; u < WN_U; u++) {
             if (i0 + 256 * u >= total) continue;
-            uint32_t o[8];
-#pragma unroll
-            for (int q = 0; q < 4; q++) i8_widen(v[u].w[q], o[2 * q], o[2 * q + 1]);
-            uint4 *d = dst + 2 * (i0 + 256 * u);
-            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            uint4 o;
+            i8_widen(v[u].x, o.x, o.y);
+            i8_widen(v[u].y, o.z, o.w);
+            dst[i0 + 256 * u] = o;
         }
     }
 }
@@ -352,9 +351,9 @@ constexpr int64_t up256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 const int32_t *rows_end(const SortedRows &so, int e) { return so.offsets ? so.offsets + e : nullptr; }
 
 moe_status widen(const void *q, void *dst, const SortedRows &so, int e, int cols, int32_t *st, cudaStream_t stream) {
-    const int64_t per = 256 * WN_U, want = (so.n * (cols / 16) + per - 1) / per, cap = (int64_t)sm_count() * 8;
+    const int64_t per = 256 * WN_U, want = (so.n * (cols / 8) + per - 1) / per, cap = (int64_t)sm_count() * 8;
     return launch_pdl(widen_rows_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, stream,
-                      (const uint4 *)q, (uint4 *)dst, rows_end(so, e), so.n, cols / 16, st);
+                      (const uint2 *)q, (uint4 *)dst, rows_end(so, e), so.n, cols / 8, st);
 }
 
 }  // namespace
