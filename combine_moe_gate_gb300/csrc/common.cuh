@@ -124,6 +124,26 @@ __device__ __forceinline__ V16 ld_v16(const void *p) {
     return v;
 }
 
+// The same loads where `ok`, else zeros.  The predicate is the load's own: behind a branch the zeros and
+// the loaded value meet in a move, and the move waits for the load.
+__device__ __forceinline__ V16 ld_stream_if(const void *p, bool ok) {
+    V16 v{};
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(v.w[0]), "+r"(v.w[1]), "+r"(v.w[2]), "+r"(v.w[3]) : "l"(p), "r"((int)ok));
+    return v;
+}
+
+__device__ __forceinline__ V16 ld_v16_if(const void *p, bool ok) {
+    V16 v{};
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@p ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(v.w[0]), "+r"(v.w[1]), "+r"(v.w[2]), "+r"(v.w[3]) : "l"(p), "r"((int)ok));
+    return v;
+}
+
 __device__ __forceinline__ void st_v16(void *p, const V16 &v) {
     asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};"
                  :: "l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]) : "memory");

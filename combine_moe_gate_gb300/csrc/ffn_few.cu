@@ -76,17 +76,14 @@ ffn_few_kernel(const FewArgs g) {
 #pragma unroll
                 for (int q = 0; q < M; q++)
 #pragma unroll
-                    for (int hf = 0; hf < 2; hf++) {
-                        wv[u][q][hf] = V16{};
-                        if (p0 + 4 * u + t < pieces && (!hf || upper)) wv[u][q][hf] = ld_stream(wp[q][hf] + p0 + 4 * u);
-                    }
+                    for (int hf = 0; hf < 2; hf++)
+                        wv[u][q][hf] = ld_stream_if(wp[q][hf] + p0 + 4 * u, p0 + 4 * u + t < pieces && (!hf || upper));
 #pragma unroll
             for (int u = 0; u < FU; u++)
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     const int64_t row = r0 + 8 * b + gr;
-                    V16 xv{};
-                    if (p0 + 4 * u + t < pieces && row < lo + count) xv = ld_v16(xp + row * pieces + p0 + 4 * u);
+                    const V16 xv = ld_v16_if(xp + row * pieces + p0 + 4 * u, p0 + 4 * u + t < pieces && row < lo + count);
 #pragma unroll
                     for (int q = 0; q < M; q++) {
                         const V16 &a = wv[u][q][0], &c = wv[u][q][1];

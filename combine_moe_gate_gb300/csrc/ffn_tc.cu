@@ -333,8 +333,7 @@ __device__ __forceinline__ void blk_fetch(V16 (&v)[4], const __nv_bfloat16 *p, i
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int row = 8 * i + (lane >> 2), col = (lane & 3) * 8;
-        v[i] = V16{};
-        if (row < rows && col < cols) v[i] = ld_v16(p + row * pitch + col);
+        v[i] = ld_v16_if(p + row * pitch + col, row < rows && col < cols);
     }
 }
 
@@ -362,8 +361,7 @@ __device__ __forceinline__ void half_fetch(V16 (&v)[2], const __nv_bfloat16 *p, 
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         const int row = 16 * i + (lane >> 1), col = (lane & 1) * 8;
-        v[i] = V16{};
-        if (row < rows && col < cols) v[i] = ld_v16(p + row * pitch + col);
+        v[i] = ld_v16_if(p + row * pitch + col, row < rows && col < cols);
     }
 }
 __device__ __forceinline__ uint8_t *half_at(uint8_t *stg, int row, int c) {
@@ -1057,10 +1055,10 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         uint32_t acc_phase = 0;
         // derivative epilogues: this warp's next block of aux, 32 rows x 32 columns (SwiGLU: 16 of a and of b)
         V16 fa[DSWI ? 2 : 4], fb[2];
-        auto fetch = [&](const Tile &T, int c0) {
+        auto fetch = [&](const Tile &T, int64_t base, int c0) {   // base: row_base(T.j), once a tile (a load)
             const int row0 = T.mt * BMT + row_in_tile - lane, gcol = T.nt * NOUT_TILE + col0 + c0;
             const int64_t pitch = (DSWI ? 2 : 1) * (int64_t)args.n_out;
-            const __nv_bfloat16 *p = args.aux + (row_base(T.j) + row0) * pitch + gcol;
+            const __nv_bfloat16 *p = args.aux + (base + row0) * pitch + gcol;
             if constexpr (DSWI) {
                 half_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
                 half_fetch(fb, p + args.n_out, pitch, T.rows - row0, args.n_out - gcol, lane);
@@ -1085,15 +1083,16 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             if (tile0 < total) to_l2(tile0);
         for (int t = tile0; t < total; t += tile_step) {
             Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
+            const int64_t base = row_base(T.j);
             if constexpr (DACT || DACTP) {
-                fetch(T, 0);   // on its way while the main loop ends
+                fetch(T, base, 0);   // on its way while the main loop ends
                 if (t + tile_step < total) to_l2(t + tile_step);
             }
             if (!mbar_wait<PAIR>(&ctl->tfull[acc], acc_phase, abort_flag, args.status)) break;
             tc_fence_after();
             const int row = T.mt * BMT + row_in_tile;
             const bool valid = row < T.rows;
-            const int64_t grow0 = row_base(T.j) + row - lane;
+            const int64_t grow0 = base + row - lane;
             const int live = T.rows - (row - lane);          // live rows from the warp's first on
             // a block of 32 bf16 columns from gcol on, of `out` with rows of `pitch` elements
             auto store32 = [&](const uint32_t (&pk)[16], __nv_bfloat16 *out, int64_t pitch, int gcol) {
@@ -1180,7 +1179,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         }
                         half_put(stg, fa, fb, lane);
                         half_row(stg, ua, ub, lane);
-                        if (c0 + 16 < COLS) fetch(T, c0 + 16);
+                        if (c0 + 16 < COLS) fetch(T, base, c0 + 16);
                         __nv_bfloat162 top = __float2bfloat162_rn(0.0f);   // the largest magnitude of a
 #pragma unroll
                         for (int i = 0; i < 8; i++)
@@ -1227,7 +1226,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             for (int i = 0; i < 32; i++) r[i] = 0u;   // empty contraction
                         }
                         blk_turn(stg, fa, dv, lane);
-                        if (c0 + 32 < COLS) fetch(T, c0 + 32);
+                        if (c0 + 32 < COLS) fetch(T, base, c0 + 32);
                         if (T.nk > 0) tmem_wait_ld(r);
                         uint32_t pk[16];
 #pragma unroll

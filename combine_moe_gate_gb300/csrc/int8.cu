@@ -268,11 +268,8 @@ int8_few_kernel(const FewArgs g) {
             for (int u = 0; u < FU; u++)
 #pragma unroll
                 for (int c = 0; c < CPW; c++) {
-                    wv[u][c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (p0 + 32 * u < pieces) {
-                        const V16 q = ld_stream(wp[c] + p0 + 32 * u);
-                        wv[u][c] = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
-                    }
+                    const V16 q = ld_stream_if(wp[c] + p0 + 32 * u, p0 + 32 * u < pieces);
+                    wv[u][c] = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
                 }
 #pragma unroll
             for (int u = 0; u < FU; u++) {
