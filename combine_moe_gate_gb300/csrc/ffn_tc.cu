@@ -22,8 +22,8 @@
 //               tcgen05.commit to release stages and publish accumulators;
 //   warps 2-9   epilogue: tcgen05.ld 32 lanes x 32 columns, then the mode's
 //               arithmetic in fp32 (bias, activation, e4m3 scales, or an
-//               activation derivative), one rounding, and TMA stores of 32 x 32
-//               bf16 (or 32 x 16 fp32) boxes staged in shared memory.
+//               activation derivative), one rounding, and stores of 32 x 32
+//               bf16 (or 32 x 16 fp32) blocks turned in shared memory.
 // Tiles are 256 x 256 with two accumulators (a tile's epilogue overlaps the
 // next tile's main loop) or 256 x 512 with one (TN = 2: two N = 256 MMAs
 // share each A tile).  Operands are K-major, or MN-major (row-major [K, N]
@@ -70,15 +70,15 @@ constexpr int SMEM_RING = 192 * 1024;   // operand ring per CTA
 // pre-activation: out = d_hid * act'(acc + bias) with d_hid (GemmArgs::aux)
 // laid out like out; the pre-activation itself is never stored.
 // EPI_GELU_SAVE / EPI_RELU_SAVE: fc1 that also stores the pre-activation
-// acc + bias (bf16) to GemmArgs::aux_out, laid out like out (map tmAt).
+// acc + bias (bf16) to GemmArgs::aux_out, laid out like out.
 // EPI_DGELU_BMN / EPI_DRELU_BMN: d_hid = acc (B MN-major) times act'(pre)
 // with the saved pre-activation (GemmArgs::aux) laid out like out.
 // EPI_WGRAD_MN_F32: EPI_WGRAD_MN writing fp32 to GemmArgs::out_f32.
 // EPI_SWIGLU_SAVE: the SwiGLU fc1 that also stores a = buf W1^T and
-// b = buf W3^T (bf16) to GemmArgs::aux_out, rows of 2 * n_out: a (map tmAt), then b (tmBt).
+// b = buf W3^T (bf16) to GemmArgs::aux_out, rows of 2 * n_out: a, then b.
 // EPI_DSWIGLU_BMN: d_hid = acc (B MN-major) and the saved [a | b] rows
 // (GemmArgs::aux, 2 * n_out a row) give d_a = d_hid * b * silu'(a) into out
-// and d_b = d_hid * silu(a) into out + n_out (map tmB3), out rows of GemmArgs::out_pitch.
+// and d_b = d_hid * silu(a) into out + n_out, out rows of GemmArgs::out_pitch.
 enum Epi { EPI_GELU = 0, EPI_RELU = 1, EPI_SWIGLU = 2, EPI_BIAS = 3, EPI_BIAS_BMN = 4,
            EPI_WGRAD_MN = 5, EPI_DGELU = 6, EPI_DRELU = 7, EPI_GELU_SAVE = 8, EPI_RELU_SAVE = 9,
            EPI_DGELU_BMN = 10, EPI_DRELU_BMN = 11, EPI_WGRAD_MN_F32 = 12, EPI_SWIGLU_SAVE = 13,
@@ -155,8 +155,8 @@ struct Ctl {  // control block in shared memory
     int32_t tile_start[MAX_E + 1];
 };
 
-// Output staging per epilogue warp: 32 rows x 32 bf16 (64-byte swizzle),
-// written by the warp and stored to global memory by TMA.
+// Staging per epilogue warp: 32 rows x 32 bf16, turned between a lane's row
+// and pieces of several rows.
 constexpr int STG_WARP_BYTES = 2048;
 
 template <class TL>
@@ -699,7 +699,7 @@ __device__ __forceinline__ Tile decode_tile(const int32_t *tile_start, int e, in
 template <int EPI, int TM, int BK, int CL, int TN, int EB = 2>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap tmB3, const __grid_constant__ CUtensorMap tmO,
+              const __grid_constant__ CUtensorMap tmB3,
               const __grid_constant__ CUtensorMap tmAt, const __grid_constant__ CUtensorMap tmBt,
               const GemmArgs args) {
     using TL = Tiling<TM, BK, CL, TN, EB>;
@@ -855,188 +855,188 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         const int hh = prod >> 1;   // row half of this producer's boxes
         constexpr int A_BOX_BYTES = TL::A_BOX_ROWS * ROWB, B_BOX_BYTES = TL::B_BOX_ROWS * ROWB;
         if (elect_one()) {
-        int stage = 0;
-        uint32_t phase = 0;
-        int issued = 0;
-        bool ok = true;
-        for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
-            Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
-            // A: this CTA's 128 rows, half of them per producer
-            const int a_row = (int)(row_base(T.j) + (int64_t)T.mt * BMT +
-                                    (int64_t)prank * TL::A_ROWS + (int64_t)hh * TL::A_BOX_ROWS);
-            // B rows of this CTA: its half of the (each) N = 256 sub-tile; with
-            // TN = 2 producer hh loads N sub-tile hh
-            const int b_row = T.j * args.b_rows + T.nt * NOUT_TILE +
-                              (TN == 2 ? hh * BN + (int)prank * (BN / 2)
-                                       : (PAIR && !is_swiglu(EPI) ? (int)prank * TL::B_ROWS : 0) +
-                                             hh * TL::B_BOX_ROWS);
-            // MN-major weight gradients: a last K block only partly kept
-            // comes from the tail maps (rows j * BK ..)
-            const bool part_tail = AMN && (kept_rows[T.j] % BK) != 0;
-            const int k_base = AMN && args.offsets ? sorted_at(args, T.j) : T.j * args.b_rows;
-            for (int kb = 0; kb < T.nk; kb++) {
-                ok = mbar_wait<PAIR>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status);
-                if (!ok) break;
-                {
-                    const bool tail = part_tail && kb == T.nk - 1;
-                    const int k_row = tail ? T.j * BK : k_base + kb * BK;
-                    if (PAIR && AMN) {
-                        const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
-                        if (is_a) {
-                            // this CTA's 128 output rows = A columns, block hh of 64
-                            if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * A_BOX_BYTES);
-                            tma_load_2d_pair(sA + stage * A_BYTES + hh * A_BOX_BYTES,
-                                             tail ? &tmAt : &tmA,
-                                             T.mt * BMT + (int)prank * TL::A_ROWS + hh * 64, k_row, fb);
-                        } else {
-                            if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
-                            const int n_col = b_row - T.j * args.b_rows;
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            bool ok = true;
+            for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
+                Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
+                // A: this CTA's 128 rows, half of them per producer
+                const int a_row = (int)(row_base(T.j) + (int64_t)T.mt * BMT +
+                                        (int64_t)prank * TL::A_ROWS + (int64_t)hh * TL::A_BOX_ROWS);
+                // B rows of this CTA: its half of the (each) N = 256 sub-tile; with
+                // TN = 2 producer hh loads N sub-tile hh
+                const int b_row = T.j * args.b_rows + T.nt * NOUT_TILE +
+                                  (TN == 2 ? hh * BN + (int)prank * (BN / 2)
+                                           : (PAIR && !is_swiglu(EPI) ? (int)prank * TL::B_ROWS : 0) +
+                                                 hh * TL::B_BOX_ROWS);
+                // MN-major weight gradients: a last K block only partly kept
+                // comes from the tail maps (rows j * BK ..)
+                const bool part_tail = AMN && (kept_rows[T.j] % BK) != 0;
+                const int k_base = AMN && args.offsets ? sorted_at(args, T.j) : T.j * args.b_rows;
+                for (int kb = 0; kb < T.nk; kb++) {
+                    ok = mbar_wait<PAIR>(&ctl->empty[stage], phase ^ 1u, abort_flag, args.status);
+                    if (!ok) break;
+                    {
+                        const bool tail = part_tail && kb == T.nk - 1;
+                        const int k_row = tail ? T.j * BK : k_base + kb * BK;
+                        if (PAIR && AMN) {
+                            const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
+                            if (is_a) {
+                                // this CTA's 128 output rows = A columns, block hh of 64
+                                if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * A_BOX_BYTES);
+                                tma_load_2d_pair(sA + stage * A_BYTES + hh * A_BOX_BYTES,
+                                                 tail ? &tmAt : &tmA,
+                                                 T.mt * BMT + (int)prank * TL::A_ROWS + hh * 64, k_row, fb);
+                            } else {
+                                if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
+                                const int n_col = b_row - T.j * args.b_rows;
 #pragma unroll
-                            for (int i = 0; i < TN; i++)   // TN boxes of 64 columns
-                                tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES +
-                                                     i * (B_BOX_BYTES / TN),
-                                                 tail ? &tmBt : &tmB, n_col + 64 * i, k_row, fb);
-                        }
-                    } else if (PAIR) {
-                        const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
-                        if (is_a) {
-                            if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * A_BOX_BYTES);
-                            tma_load_2d_pair(sA + stage * A_BYTES + hh * A_BOX_BYTES, &tmA, kb * BK,
-                                             a_row, fb);
-                        } else if (BMN) {
-                            // this CTA's 128 columns of N sub-tile hh, K rows kb*BK ..:
-                            // two boxes of 64 columns (b_row - j * b_rows is the column)
-                            if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
-                            const int n_col = b_row - T.j * args.b_rows;
-                            const bool second = args.k_split > 0 && kb * BK >= args.k_split;
+                                for (int i = 0; i < TN; i++)   // TN boxes of 64 columns
+                                    tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES +
+                                                         i * (B_BOX_BYTES / TN),
+                                                     tail ? &tmBt : &tmB, n_col + 64 * i, k_row, fb);
+                            }
+                        } else if (PAIR) {
+                            const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
+                            if (is_a) {
+                                if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * A_BOX_BYTES);
+                                tma_load_2d_pair(sA + stage * A_BYTES + hh * A_BOX_BYTES, &tmA, kb * BK,
+                                                 a_row, fb);
+                            } else if (BMN) {
+                                // this CTA's 128 columns of N sub-tile hh, K rows kb*BK ..:
+                                // two boxes of 64 columns (b_row - j * b_rows is the column)
+                                if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
+                                const int n_col = b_row - T.j * args.b_rows;
+                                const bool second = args.k_split > 0 && kb * BK >= args.k_split;
 #pragma unroll
-                            for (int i = 0; i < TN; i++)   // TN boxes of 64 columns
-                                tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES +
-                                                     i * (B_BOX_BYTES / TN),
-                                                 second ? &tmB3 : &tmB, n_col + 64 * i,
-                                                 second ? k_row - args.k_split : k_row, fb);
+                                for (int i = 0; i < TN; i++)   // TN boxes of 64 columns
+                                    tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES +
+                                                         i * (B_BOX_BYTES / TN),
+                                                     second ? &tmB3 : &tmB, n_col + 64 * i,
+                                                     second ? k_row - args.k_split : k_row, fb);
+                            } else {
+                                // SwiGLU: the first CTA's half of B is W1, the second's W3
+                                if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
+                                tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES,
+                                                 is_swiglu(EPI) && prank ? &tmB3 : &tmB, kb * BK, b_row, fb);
+                            }
+                        } else if (is_a) {
+                            mbar_expect_tx(&ctl->full[stage], A_BOX_BYTES);
+                            tma_load_2d(sA + stage * A_BYTES + hh * A_BOX_BYTES, &tmA, kb * BK, a_row,
+                                        &ctl->full[stage]);
+                        } else if (is_swiglu(EPI)) {
+                            // W1 rows in the first half of the B tile, W3 rows in the second
+                            mbar_expect_tx(&ctl->full[stage], B_BOX_BYTES);
+                            tma_load_2d(sB + stage * B_BYTES + hh * B_BOX_BYTES, hh ? &tmB3 : &tmB, kb * BK,
+                                        b_row - hh * TL::B_BOX_ROWS, &ctl->full[stage]);
                         } else {
-                            // SwiGLU: the first CTA's half of B is W1, the second's W3
-                            if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
-                            tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES,
-                                             is_swiglu(EPI) && prank ? &tmB3 : &tmB, kb * BK, b_row, fb);
+                            mbar_expect_tx(&ctl->full[stage], B_BOX_BYTES);
+                            tma_load_2d(sB + stage * B_BYTES + hh * B_BOX_BYTES, &tmB, kb * BK, b_row,
+                                        &ctl->full[stage]);
                         }
-                    } else if (is_a) {
-                        mbar_expect_tx(&ctl->full[stage], A_BOX_BYTES);
-                        tma_load_2d(sA + stage * A_BYTES + hh * A_BOX_BYTES, &tmA, kb * BK, a_row,
-                                    &ctl->full[stage]);
-                    } else if (is_swiglu(EPI)) {
-                        // W1 rows in the first half of the B tile, W3 rows in the second
-                        mbar_expect_tx(&ctl->full[stage], B_BOX_BYTES);
-                        tma_load_2d(sB + stage * B_BYTES + hh * B_BOX_BYTES, hh ? &tmB3 : &tmB, kb * BK,
-                                    b_row - hh * TL::B_BOX_ROWS, &ctl->full[stage]);
-                    } else {
-                        mbar_expect_tx(&ctl->full[stage], B_BOX_BYTES);
-                        tma_load_2d(sB + stage * B_BYTES + hh * B_BOX_BYTES, &tmB, kb * BK, b_row,
-                                    &ctl->full[stage]);
+                    }
+                    issued++;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // wait (bounded) for this thread's copies still in flight before the CTA
+            // can exit (a pair's second CTA cannot observe the first CTA's barriers:
+            // its copies are covered by the MMAs that consume them, or on an abort
+            // by the delay before the final cluster barrier)
+            if (!PAIR || prank == 0) {
+                for (int i = max(0, issued - STAGES); i < issued; i++) {
+                    int s = i % STAGES;
+                    uint32_t ph = (uint32_t)((i / STAGES) & 1);
+                    unsigned long long t0 = gtimer();
+                    while (!mbar_try<PAIR>(&ctl->full[s], ph) && gtimer() - t0 < WAIT_NS) {
                     }
                 }
-                issued++;
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
-        }
-        // wait (bounded) for this thread's copies still in flight before the CTA
-        // can exit (a pair's second CTA cannot observe the first CTA's barriers:
-        // its copies are covered by the MMAs that consume them, or on an abort
-        // by the delay before the final cluster barrier)
-        if (!PAIR || prank == 0) {
-            for (int i = max(0, issued - STAGES); i < issued; i++) {
-                int s = i % STAGES;
-                uint32_t ph = (uint32_t)((i / STAGES) & 1);
-                unsigned long long t0 = gtimer();
-                while (!mbar_try<PAIR>(&ctl->full[s], ph) && gtimer() - t0 < WAIT_NS) {
-                }
-            }
-        }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (elect_one()) {
-        if (!PAIR || prank == 0) {
-            // both CTAs of the pair
-            const uint16_t pair_mask = (uint16_t)3u;
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
-            uint32_t acc_phase = 0;
-            for (int t = tile0; t < total; t += tile_step) {
-                const int tnk = kmode ? decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK).nk : nk;
-                if (!mbar_wait<PAIR>(&ctl->tempty[acc], acc_phase ^ 1u, abort_flag, args.status)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * TL::ACC_COLS);
-                bool ok = true;
-                for (int kb = 0; kb < tnk; kb++) {
-                    if (!mbar_wait<PAIR>(&ctl->full[stage], phase, abort_flag, args.status)) { ok = false; break; }
+            if (!PAIR || prank == 0) {
+                // both CTAs of the pair
+                const uint16_t pair_mask = (uint16_t)3u;
+                int stage = 0;
+                uint32_t phase = 0;
+                int acc = 0;
+                uint32_t acc_phase = 0;
+                for (int t = tile0; t < total; t += tile_step) {
+                    const int tnk = kmode ? decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK).nk : nk;
+                    if (!mbar_wait<PAIR>(&ctl->tempty[acc], acc_phase ^ 1u, abort_flag, args.status)) break;
                     tc_fence_after();
-                    const uint32_t a0 = su32(sA + stage * A_BYTES);
-                    const uint32_t b0 = su32(sB + stage * B_BYTES);
+                    const uint32_t d = tmem + (uint32_t)(acc * TL::ACC_COLS);
+                    bool ok = true;
+                    for (int kb = 0; kb < tnk; kb++) {
+                        if (!mbar_wait<PAIR>(&ctl->full[stage], phase, abort_flag, args.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t a0 = su32(sA + stage * A_BYTES);
+                        const uint32_t b0 = su32(sB + stage * B_BYTES);
 #pragma unroll
-                    for (int kk = 0; kk < ROWB / 32; kk++) {   // one MMA per 32 bytes of K
-                        if (F8) {
+                        for (int kk = 0; kk < ROWB / 32; kk++) {   // one MMA per 32 bytes of K
+                            if (F8) {
 #pragma unroll
-                            for (int tn = 0; tn < TN; tn++)
-                                umma_pair_f8(d + (uint32_t)(tn * BN), sdesc<ROWB>(a0 + kk * 32),
-                                             sdesc<ROWB>(b0 + tn * (B_BYTES / TN) + kk * 32),
-                                             (kb | kk) != 0);
-                        } else if (AMN) {
-                            // A and B: K rows of 128 bytes, kk * UK rows in; A's two
-                            // 64-column blocks A_BYTES / 2 apart, B's as below
+                                for (int tn = 0; tn < TN; tn++)
+                                    umma_pair_f8(d + (uint32_t)(tn * BN), sdesc<ROWB>(a0 + kk * 32),
+                                                 sdesc<ROWB>(b0 + tn * (B_BYTES / TN) + kk * 32),
+                                                 (kb | kk) != 0);
+                            } else if (AMN) {
+                                // A and B: K rows of 128 bytes, kk * UK rows in; A's two
+                                // 64-column blocks A_BYTES / 2 apart, B's as below
 #pragma unroll
-                            for (int tn = 0; tn < TN; tn++)
-                                umma_pair<IDESC_PAIR_MN>(
-                                    d + (uint32_t)(tn * BN), sdesc_mn(a0 + kk * UK * 128, A_BYTES / 2),
-                                    sdesc_mn(b0 + tn * (B_BYTES / TN) + kk * UK * 128,
-                                             B_BYTES / TN / 2),
-                                    (kb | kk) != 0);
-                        } else if (BMN) {
-                            // B: K rows of 128 bytes, kk * UK rows in; blocks of 64
-                            // columns (B_BYTES / TN / 2 bytes) apart
+                                for (int tn = 0; tn < TN; tn++)
+                                    umma_pair<IDESC_PAIR_MN>(
+                                        d + (uint32_t)(tn * BN), sdesc_mn(a0 + kk * UK * 128, A_BYTES / 2),
+                                        sdesc_mn(b0 + tn * (B_BYTES / TN) + kk * UK * 128,
+                                                 B_BYTES / TN / 2),
+                                        (kb | kk) != 0);
+                            } else if (BMN) {
+                                // B: K rows of 128 bytes, kk * UK rows in; blocks of 64
+                                // columns (B_BYTES / TN / 2 bytes) apart
 #pragma unroll
-                            for (int tn = 0; tn < TN; tn++)
-                                umma_pair<IDESC_PAIR_BMN>(
-                                    d + (uint32_t)(tn * BN), sdesc<ROWB>(a0 + kk * UK * 2),
-                                    sdesc_mn(b0 + tn * (B_BYTES / TN) + kk * UK * 128,
-                                             B_BYTES / TN / 2),
-                                    (kb | kk) != 0);
-                        } else if (PAIR) {
+                                for (int tn = 0; tn < TN; tn++)
+                                    umma_pair<IDESC_PAIR_BMN>(
+                                        d + (uint32_t)(tn * BN), sdesc<ROWB>(a0 + kk * UK * 2),
+                                        sdesc_mn(b0 + tn * (B_BYTES / TN) + kk * UK * 128,
+                                                 B_BYTES / TN / 2),
+                                        (kb | kk) != 0);
+                            } else if (PAIR) {
 #pragma unroll
-                            for (int tn = 0; tn < TN; tn++)  // N sub-tiles share the A tile
-                                umma_pair(d + (uint32_t)(tn * BN), sdesc<ROWB>(a0 + kk * UK * 2),
-                                          sdesc<ROWB>(b0 + tn * (B_BYTES / TN) + kk * UK * 2),
-                                          (kb | kk) != 0);
-                        } else {
+                                for (int tn = 0; tn < TN; tn++)  // N sub-tiles share the A tile
+                                    umma_pair(d + (uint32_t)(tn * BN), sdesc<ROWB>(a0 + kk * UK * 2),
+                                              sdesc<ROWB>(b0 + tn * (B_BYTES / TN) + kk * UK * 2),
+                                              (kb | kk) != 0);
+                            } else {
 #pragma unroll
-                            for (int hm = 0; hm < TM; hm++)  // M halves share the B tile
-                                umma(d + (uint32_t)(hm * BN),
-                                     sdesc<ROWB>(a0 + hm * UM * ROWB + kk * UK * 2),
-                                     sdesc<ROWB>(b0 + kk * UK * 2), (kb | kk) != 0);
+                                for (int hm = 0; hm < TM; hm++)  // M halves share the B tile
+                                    umma(d + (uint32_t)(hm * BN),
+                                         sdesc<ROWB>(a0 + hm * UM * ROWB + kk * UK * 2),
+                                         sdesc<ROWB>(b0 + kk * UK * 2), (kb | kk) != 0);
+                            }
                         }
+                        // stage reusable (in both CTAs of a pair) once these MMAs read it
+                        if (PAIR) umma_commit_pair(&ctl->empty[stage], pair_mask);
+                        else umma_commit(&ctl->empty[stage]);
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     }
-                    // stage reusable (in both CTAs of a pair) once these MMAs read it
-                    if (PAIR) umma_commit_pair(&ctl->empty[stage], pair_mask);
-                    else umma_commit(&ctl->empty[stage]);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (!ok) break;
+                    // accumulator ready when all MMAs finish (a tile without K
+                    // blocks is published at once; its epilogue writes zeros)
+                    if (PAIR) umma_commit_pair(&ctl->tfull[acc], pair_mask);
+                    else umma_commit(&ctl->tfull[acc]);
+                    if (++acc == TL::NACC) { acc = 0; acc_phase ^= 1u; }
                 }
-                if (!ok) break;
-                // accumulator ready when all MMAs finish (a tile without K
-                // blocks is published at once; its epilogue writes zeros)
-                if (PAIR) umma_commit_pair(&ctl->tfull[acc], pair_mask);
-                else umma_commit(&ctl->tfull[acc]);
-                if (++acc == TL::NACC) { acc = 0; acc_phase ^= 1u; }
+                // all MMAs issued by this thread complete before TMEM is released
+                if (PAIR) umma_commit_pair(&ctl->drain, pair_mask);
+                else umma_commit(&ctl->drain);
             }
-            // all MMAs issued by this thread complete before TMEM is released
-            if (PAIR) umma_commit_pair(&ctl->drain, pair_mask);
-            else umma_commit(&ctl->drain);
-        }
-        unsigned long long t0 = gtimer();
-        while (!mbar_try<PAIR>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
-        }
+            unsigned long long t0 = gtimer();
+            while (!mbar_try<PAIR>(&ctl->drain, 0) && gtimer() - t0 < WAIT_NS) {
+            }
         }
         __syncwarp();
     } else if (warp >= 2 && warp < PROD_WARP0) {
@@ -1247,72 +1247,72 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     }
                 } else {
 #pragma unroll 1
-                for (int c0 = 0; c0 < COLS; c0 += 64) {
-                    uint32_t r[2][32];
-                    if (T.nk > 0) {
-                        tmem_ld32(tbase + (uint32_t)(col0 + c0), r[0]);
-                        tmem_ld32(tbase + (uint32_t)(col0 + c0 + 32), r[1]);
-                        tmem_wait_ld(r[0]);
-                        tmem_tie(r[1]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i++) r[0][i] = r[1][i] = 0u;   // empty contraction
-                    }
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; h2++) {
-                        const int gcol = T.nt * NOUT_TILE + col0 + c0 + 32 * h2;
-                        uint32_t pk[16];
-                        float of[32];   // weight gradients in fp32: this row's 32 columns
-                        uint32_t pp[16];   // fc1 keeping its pre-activation: this row's 32 columns
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            const float4 *bp = reinterpret_cast<const float4 *>(bsl + c0 + 32 * h2 + q * 8);
-                            const float4 bl = bp[0], bh = bp[1];
-                            const float2 bb[4] = {make_float2(bl.x, bl.y), make_float2(bl.z, bl.w),
-                                                  make_float2(bh.x, bh.y), make_float2(bh.z, bh.w)};
-                            float sc[8];   // e4m3: a_scale * b_scale of the 8 columns
-                            if (F8) {
-                                const int g8 = gcol + q * 8;
-                                float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-                                if (g8 < args.n_out) {   // n_out is a multiple of 16
-                                    lo = reinterpret_cast<const float4 *>(bsc + g8)[0];
-                                    hi = reinterpret_cast<const float4 *>(bsc + g8)[1];
-                                }
-                                sc[0] = sa * lo.x; sc[1] = sa * lo.y; sc[2] = sa * lo.z; sc[3] = sa * lo.w;
-                                sc[4] = sa * hi.x; sc[5] = sa * hi.y; sc[6] = sa * hi.z; sc[7] = sa * hi.w;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const float2 acc2 = make_float2(__uint_as_float(r[h2][q * 8 + 2 * i]),
-                                                                __uint_as_float(r[h2][q * 8 + 2 * i + 1]));
-                                float2 a = F8 ? __ffma2_rn(acc2, make_float2(sc[2 * i], sc[2 * i + 1]), bb[i])
-                                              : __fadd2_rn(acc2, bb[i]);
-                                if (SAVE) pp[q * 4 + i] = pack_bf16(a.x, a.y);
-                                if (GELU) a = gelu_erf2(a);
-                                else if (RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
-                                if constexpr (F32OUT) {
-                                    of[q * 8 + 2 * i] = a.x;
-                                    of[q * 8 + 2 * i + 1] = a.y;
-                                } else {
-                                    pk[q * 4 + i] = pack_bf16(a.x, a.y);
-                                }
-                            }
-                        }
-                        if constexpr (F32OUT) {   // fp32 weight gradients: 16 columns at a time
-#pragma unroll
-                            for (int hc = 0; hc < 2; hc++) {
-                                uint32_t w[16];
-#pragma unroll
-                                for (int i = 0; i < 16; i++) w[i] = __float_as_uint(of[16 * hc + i]);
-                                epi_store64(stg, w, args.out_f32 + grow0 * args.n_out + gcol + 16 * hc,
-                                            4 * (int64_t)args.n_out, live, 4 * (args.n_out - gcol - 16 * hc), lane);
-                            }
+                    for (int c0 = 0; c0 < COLS; c0 += 64) {
+                        uint32_t r[2][32];
+                        if (T.nk > 0) {
+                            tmem_ld32(tbase + (uint32_t)(col0 + c0), r[0]);
+                            tmem_ld32(tbase + (uint32_t)(col0 + c0 + 32), r[1]);
+                            tmem_wait_ld(r[0]);
+                            tmem_tie(r[1]);
                         } else {
-                            store32(pk, args.out, opitch, gcol);
-                            if (SAVE) store32(pp, args.aux_out, (int64_t)args.n_out, gcol);
+#pragma unroll
+                            for (int i = 0; i < 32; i++) r[0][i] = r[1][i] = 0u;   // empty contraction
+                        }
+#pragma unroll
+                        for (int h2 = 0; h2 < 2; h2++) {
+                            const int gcol = T.nt * NOUT_TILE + col0 + c0 + 32 * h2;
+                            uint32_t pk[16];
+                            float of[32];   // weight gradients in fp32: this row's 32 columns
+                            uint32_t pp[16];   // fc1 keeping its pre-activation: this row's 32 columns
+#pragma unroll
+                            for (int q = 0; q < 4; q++) {
+                                const float4 *bp = reinterpret_cast<const float4 *>(bsl + c0 + 32 * h2 + q * 8);
+                                const float4 bl = bp[0], bh = bp[1];
+                                const float2 bb[4] = {make_float2(bl.x, bl.y), make_float2(bl.z, bl.w),
+                                                      make_float2(bh.x, bh.y), make_float2(bh.z, bh.w)};
+                                float sc[8];   // e4m3: a_scale * b_scale of the 8 columns
+                                if (F8) {
+                                    const int g8 = gcol + q * 8;
+                                    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+                                    if (g8 < args.n_out) {   // n_out is a multiple of 16
+                                        lo = reinterpret_cast<const float4 *>(bsc + g8)[0];
+                                        hi = reinterpret_cast<const float4 *>(bsc + g8)[1];
+                                    }
+                                    sc[0] = sa * lo.x; sc[1] = sa * lo.y; sc[2] = sa * lo.z; sc[3] = sa * lo.w;
+                                    sc[4] = sa * hi.x; sc[5] = sa * hi.y; sc[6] = sa * hi.z; sc[7] = sa * hi.w;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; i++) {
+                                    const float2 acc2 = make_float2(__uint_as_float(r[h2][q * 8 + 2 * i]),
+                                                                    __uint_as_float(r[h2][q * 8 + 2 * i + 1]));
+                                    float2 a = F8 ? __ffma2_rn(acc2, make_float2(sc[2 * i], sc[2 * i + 1]), bb[i])
+                                                  : __fadd2_rn(acc2, bb[i]);
+                                    if (SAVE) pp[q * 4 + i] = pack_bf16(a.x, a.y);
+                                    if (GELU) a = gelu_erf2(a);
+                                    else if (RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                                    if constexpr (F32OUT) {
+                                        of[q * 8 + 2 * i] = a.x;
+                                        of[q * 8 + 2 * i + 1] = a.y;
+                                    } else {
+                                        pk[q * 4 + i] = pack_bf16(a.x, a.y);
+                                    }
+                                }
+                            }
+                            if constexpr (F32OUT) {   // fp32 weight gradients: 16 columns at a time
+#pragma unroll
+                                for (int hc = 0; hc < 2; hc++) {
+                                    uint32_t w[16];
+#pragma unroll
+                                    for (int i = 0; i < 16; i++) w[i] = __float_as_uint(of[16 * hc + i]);
+                                    epi_store64(stg, w, args.out_f32 + grow0 * args.n_out + gcol + 16 * hc,
+                                                4 * (int64_t)args.n_out, live, 4 * (args.n_out - gcol - 16 * hc), lane);
+                                }
+                            } else {
+                                store32(pk, args.out, opitch, gcol);
+                                if (SAVE) store32(pp, args.aux_out, (int64_t)args.n_out, gcol);
+                            }
                         }
                     }
-                }
                 }
                 __syncwarp();   // slice reused for the next tile
             }
@@ -1370,8 +1370,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 2-D bf16 tensor map over a row-major [rows, cols] matrix, box box_rows x bk
-// (bk = 64: 128-byte swizzle; bk = 32: 64-byte swizzle, also the epilogue's
-// output staging; bk = 16: 32-byte swizzle).
+// (bk = 64: 128-byte swizzle; bk = 32: 64-byte swizzle; bk = 16: 32-byte swizzle).
 bool make_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
               int bk, uint64_t pitch = 0) {
     auto fn = encode_fn();
@@ -1385,21 +1384,6 @@ bool make_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, 
                     bk == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
                     : bk == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                : CU_TENSOR_MAP_SWIZZLE_32B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-// An fp32 output map over a row-major [rows, cols] matrix, boxes of 32 rows
-// x 16 columns (64-byte swizzle, the epilogue's staging pattern).
-bool make_map_f32_out(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * 4};
-    cuuint32_t box[2] = {16, 32};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -1456,7 +1440,7 @@ int max_clusters(K kern, size_t smem, int cl, int threads = NUM_THREADS) {
 
 template <int EPI, int TM, int BK, int CL, int TN, int EB = 2>
 moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b3,
-                       const CUtensorMap &o, const GemmArgs &args_in, cudaStream_t stream,
+                       const GemmArgs &args_in, cudaStream_t stream,
                        const CUtensorMap *a_tail = nullptr, const CUtensorMap *b_tail = nullptr) {
     using TL = Tiling<TM, BK, CL, TN, EB>;
     GemmArgs args = args_in;
@@ -1482,7 +1466,7 @@ moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtenso
     int64_t grid = upper < nunits ? upper : nunits;
     if (grid < 1) grid = 1;
     if (CL == 1)
-        return launch_pdl(kern, dim3((unsigned)grid), dim3(NUM_THREADS), SMEM, stream, a, b, b3, o,
+        return launch_pdl(kern, dim3((unsigned)grid), dim3(NUM_THREADS), SMEM, stream, a, b, b3,
                           a_tail ? *a_tail : a, b_tail ? *b_tail : b, args);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(CL * grid));
@@ -1498,7 +1482,7 @@ moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtenso
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, b, b3, o, a_tail ? *a_tail : a,
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, b, b3, a_tail ? *a_tail : a,
                                          b_tail ? *b_tail : b, args);
     note_launch();
     if (err != cudaSuccess) {
@@ -1530,7 +1514,7 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
     constexpr int CL1 = 2, CL2 = 2, TN2 = 2;
     using T1 = Tiling<TM1, BK1, CL1>;
     using T2 = Tiling<TM2, BK2, CL2, TN2>;
-    CUtensorMap mA1, mB1, mB3, mA2, mB2, mO1, mO2;
+    CUtensorMap mA1, mB1, mB3, mA2, mB2;
     const bool swiglu = act == MOE_ACT_SWIGLU;
     // one CTA's B box: a pair CTA's half tile, or a 1-SM SwiGLU tile's W1/W3 half
     // one producer's B box: half of a CTA's B rows (1-SM SwiGLU: the W1 or W3 half)
@@ -1539,38 +1523,30 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
         !make_map(&mB1, w1, (uint64_t)e * h, (uint64_t)m, b1_box, BK1) ||
         !make_map(&mB3, swiglu ? w3 : w1, (uint64_t)e * h, (uint64_t)m, b1_box, BK1) ||
         !make_map(&mA2, hid, rows, (uint64_t)h, T2::A_BOX_ROWS, BK2) ||
-        !make_map(&mB2, w2, (uint64_t)e * m, (uint64_t)h, T2::B_BOX_ROWS, BK2) ||
-        !make_map(&mO1, hid, rows, (uint64_t)h, 32, 32) ||
-        !make_map(&mO2, out, rows, (uint64_t)m, 32, 32))
+        !make_map(&mB2, w2, (uint64_t)e * m, (uint64_t)h, T2::B_BOX_ROWS, BK2))
         return MOE_ERR_CUDA;
     GemmArgs g1{counts, c_dev, st, (const __nv_bfloat16 *)b1, (__nv_bfloat16 *)hid, c_max, e, m, h, h,
                 nullptr, nullptr, row_lo, row_hi};
     g1.offsets = so.offsets;
     g1.n_rows = so.n;
-    // the kept pre-activation's output maps (SwiGLU: a and b, the halves of 2h-wide rows)
-    CUtensorMap mPa, mPb;
-    const uint64_t pw = swiglu ? 2 * (uint64_t)h : (uint64_t)h;
-    if (pre && (!make_map(&mPa, pre, rows, (uint64_t)h, 32, 32, pw) ||
-                (swiglu && !make_map(&mPb, (const __nv_bfloat16 *)pre + h, rows, (uint64_t)h, 32, 32, pw))))
-        return MOE_ERR_CUDA;
     g1.aux_out = (__nv_bfloat16 *)pre;   // training: fc1 also keeps its pre-activation
     moe_status r;
     if (swiglu) {
-        r = pre ? launch_gemm<EPI_SWIGLU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB3, mO1, g1, stream, &mPa, &mPb)
-                : launch_gemm<EPI_SWIGLU, TM1, BK1, CL1, 1>(mA1, mB1, mB3, mO1, g1, stream);
+        r = pre ? launch_gemm<EPI_SWIGLU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB3, g1, stream)
+                : launch_gemm<EPI_SWIGLU, TM1, BK1, CL1, 1>(mA1, mB1, mB3, g1, stream);
     } else if (act == MOE_ACT_GELU) {
-        r = pre ? launch_gemm<EPI_GELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream, &mPa)
-                : launch_gemm<EPI_GELU, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream);
+        r = pre ? launch_gemm<EPI_GELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, g1, stream)
+                : launch_gemm<EPI_GELU, TM1, BK1, CL1, 1>(mA1, mB1, mB1, g1, stream);
     } else {
-        r = pre ? launch_gemm<EPI_RELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream, &mPa)
-                : launch_gemm<EPI_RELU, TM1, BK1, CL1, 1>(mA1, mB1, mB1, mO1, g1, stream);
+        r = pre ? launch_gemm<EPI_RELU_SAVE, TM1, BK1, CL1, 1>(mA1, mB1, mB1, g1, stream)
+                : launch_gemm<EPI_RELU, TM1, BK1, CL1, 1>(mA1, mB1, mB1, g1, stream);
     }
     if (r != MOE_OK) return r;
     GemmArgs g2{counts, c_dev, st, (const __nv_bfloat16 *)b2, (__nv_bfloat16 *)out, c_max, e, h, m, m,
                 nullptr, nullptr, row_lo, row_hi};
     g2.offsets = so.offsets;
     g2.n_rows = so.n;
-    return launch_gemm<EPI_BIAS, TM2, BK2, CL2, TN2>(mA2, mB2, mB2, mO2, g2, stream);
+    return launch_gemm<EPI_BIAS, TM2, BK2, CL2, TN2>(mA2, mB2, mB2, g2, stream);
 }
 
 // ------------------------------------------------------------ e4m3 forward
@@ -1594,25 +1570,23 @@ moe_status ffn_tc_fp8_launch(const void *buf_q, const float *buf_scale, const in
     constexpr int BKF = 128;   // e4m3 elements per K block (128 bytes)
     using T1 = Tiling<1, BKF, 2, 1, 1>;
     using T2 = Tiling<1, BKF, 2, 1, 1>;
-    CUtensorMap mA1, mB1, mO1, mA2, mB2, mO2;
+    CUtensorMap mA1, mB1, mA2, mB2;
     if (!make_map_u8(&mA1, buf_q, (uint64_t)e * c_max, (uint64_t)m, T1::A_BOX_ROWS) ||
         !make_map_u8(&mB1, w1_q, (uint64_t)e * h, (uint64_t)m, T1::B_BOX_ROWS) ||
-        !make_map(&mO1, hid, (uint64_t)e * c_max, (uint64_t)h, 32, 32) ||
         !make_map_u8(&mA2, hid_q, (uint64_t)e * c_max, (uint64_t)h, T2::A_BOX_ROWS) ||
-        !make_map_u8(&mB2, w2_q, (uint64_t)e * m, (uint64_t)h, T2::B_BOX_ROWS) ||
-        !make_map(&mO2, out, (uint64_t)e * c_max, (uint64_t)m, 32, 32))
+        !make_map_u8(&mB2, w2_q, (uint64_t)e * m, (uint64_t)h, T2::B_BOX_ROWS))
         return MOE_ERR_CUDA;
     GemmArgs g1{counts, c_dev, st, (const __nv_bfloat16 *)b1, (__nv_bfloat16 *)hid, c_max, e, m, h, h,
                 nullptr, nullptr, 0, 0, buf_scale, w1_scale};
     moe_status r = act == MOE_ACT_GELU
-                       ? launch_gemm<EPI_GELU, 1, BKF, 2, 1, 1>(mA1, mB1, mB1, mO1, g1, stream)
-                       : launch_gemm<EPI_RELU, 1, BKF, 2, 1, 1>(mA1, mB1, mB1, mO1, g1, stream);
+                       ? launch_gemm<EPI_GELU, 1, BKF, 2, 1, 1>(mA1, mB1, mB1, g1, stream)
+                       : launch_gemm<EPI_RELU, 1, BKF, 2, 1, 1>(mA1, mB1, mB1, g1, stream);
     if (r != MOE_OK) return r;
     r = quantize_rows_fp8_launch(hid, e, c_max, h, counts, c_dev, hid_q, hid_scale, st, stream);
     if (r != MOE_OK) return r;
     GemmArgs g2{counts, c_dev, st, (const __nv_bfloat16 *)b2, (__nv_bfloat16 *)out, c_max, e, h, m, m,
                 nullptr, nullptr, 0, 0, hid_scale, w2_scale};
-    return launch_gemm<EPI_BIAS, 1, BKF, 2, 1, 1>(mA2, mB2, mB2, mO2, g2, stream);
+    return launch_gemm<EPI_BIAS, 1, BKF, 2, 1, 1>(mA2, mB2, mB2, g2, stream);
 }
 
 }  // namespace moe
@@ -1684,38 +1658,34 @@ uint64_t rows_of(int e, int64_t c_max, const SortedRows &so) {
 // of every expert j: A [e * c_max, K], B [e * b_rows, K], out [e, c_max, n_out].
 moe_status gemm_bias(const void *a, const void *b, int b_rows, void *out, const void *bias,
                      const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int K,
-                     int n_out, int32_t *st, cudaStream_t stream,
-                     SortedRows so = {}) {
+                     int n_out, int32_t *st, cudaStream_t stream, SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mO;
+    CUtensorMap mA, mB;
     if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)K, T2::A_BOX_ROWS, 64) ||
-        !make_map(&mB, b, (uint64_t)e * b_rows, (uint64_t)K, T2::B_BOX_ROWS, 64) ||
-        !make_map(&mO, out, rows_of(e, c_max, so), (uint64_t)n_out, 32, 32))
+        !make_map(&mB, b, (uint64_t)e * b_rows, (uint64_t)K, T2::B_BOX_ROWS, 64))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, (const __nv_bfloat16 *)bias, (__nv_bfloat16 *)out, c_max, e, K,
                n_out, b_rows, nullptr, nullptr, 0, 0};
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return launch_gemm<EPI_BIAS, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
+    return launch_gemm<EPI_BIAS, 1, 64, 2, 1>(mA, mB, mB, g, stream);
 }
 
 // The same with B MN-major: out[j] = A[j] B[j] with B [e * K, n_out] row-major
 // (K rows per expert; rows past an expert's K meet zero columns of A).
 moe_status gemm_bias_bmn(const void *a, const void *b, void *out, const int32_t *counts,
                          const int32_t *c_dev, int e, int64_t c_max, int K, int n_out, int32_t *st,
-                         cudaStream_t stream,
-                     SortedRows so = {}) {
+                         cudaStream_t stream, SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mO;
+    CUtensorMap mA, mB;
     if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)K, T2::A_BOX_ROWS, 64) ||
-        !make_map(&mB, b, (uint64_t)e * K, (uint64_t)n_out, 64, 64) ||
-        !make_map(&mO, out, rows_of(e, c_max, so), (uint64_t)n_out, 32, 32))
+        !make_map(&mB, b, (uint64_t)e * K, (uint64_t)n_out, 64, 64))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)out, c_max, e, K, n_out, K, nullptr,
                nullptr, 0, 0};
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return launch_gemm<EPI_BIAS_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
+    return launch_gemm<EPI_BIAS_BMN, 1, 64, 2, 1>(mA, mB, mB, g, stream);
 }
 
 // SwiGLU's d_buf = [d_a | d_b] [w1; w3]: A [e * c_max, 2h], B read MN-major
@@ -1723,21 +1693,19 @@ moe_status gemm_bias_bmn(const void *a, const void *b, void *out, const int32_t 
 // the 64-row K block, so no block straddles the two).
 moe_status gemm_bias_bmn2(const void *a, const void *b1, const void *b3, void *out,
                           const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int h,
-                          int n_out, int32_t *st, cudaStream_t stream,
-                     SortedRows so = {}) {
+                          int n_out, int32_t *st, cudaStream_t stream, SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mB3, mO;
+    CUtensorMap mA, mB, mB3;
     if (!make_map(&mA, a, rows_of(e, c_max, so), 2 * (uint64_t)h, T2::A_BOX_ROWS, 64) ||
         !make_map(&mB, b1, (uint64_t)e * h, (uint64_t)n_out, 64, 64) ||
-        !make_map(&mB3, b3, (uint64_t)e * h, (uint64_t)n_out, 64, 64) ||
-        !make_map(&mO, out, rows_of(e, c_max, so), (uint64_t)n_out, 32, 32))
+        !make_map(&mB3, b3, (uint64_t)e * h, (uint64_t)n_out, 64, 64))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)out, c_max, e, 2 * h, n_out, h, nullptr,
                nullptr, 0, 0};
     g.k_split = h;
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return launch_gemm<EPI_BIAS_BMN, 1, 64, 2, 1>(mA, mB, mB3, mO, g, stream);
+    return launch_gemm<EPI_BIAS_BMN, 1, 64, 2, 1>(mA, mB, mB3, g, stream);
 }
 
 // d_pre = d_hid * act'(buf w1^T + b1) over the kept rows (ReLU / GELU): the
@@ -1747,15 +1715,14 @@ moe_status gemm_dact(const void *buf, const void *w1, const void *b1, const void
                      void *d_pre, const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max,
                      int m, int h, int32_t *st, cudaStream_t stream) {
     using T1 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mO;
+    CUtensorMap mA, mB;
     if (!make_map(&mA, buf, (uint64_t)e * c_max, (uint64_t)m, T1::A_BOX_ROWS, 64) ||
-        !make_map(&mB, w1, (uint64_t)e * h, (uint64_t)m, T1::B_BOX_ROWS, 64) ||
-        !make_map(&mO, d_pre, (uint64_t)e * c_max, (uint64_t)h, 32, 32))
+        !make_map(&mB, w1, (uint64_t)e * h, (uint64_t)m, T1::B_BOX_ROWS, 64))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, (const __nv_bfloat16 *)b1, (__nv_bfloat16 *)d_pre, c_max, e, m, h, h,
                nullptr, nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)d_hid};
-    return act == MOE_ACT_GELU ? launch_gemm<EPI_DGELU, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream)
-                               : launch_gemm<EPI_DRELU, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
+    return act == MOE_ACT_GELU ? launch_gemm<EPI_DGELU, 1, 64, 2, 1>(mA, mB, mB, g, stream)
+                               : launch_gemm<EPI_DRELU, 1, 64, 2, 1>(mA, mB, mB, g, stream);
 }
 
 // d_pre = (d_out w2) * act'(pre) over the kept rows (ReLU / GELU) with the
@@ -1763,23 +1730,21 @@ moe_status gemm_dact(const void *buf, const void *w1, const void *b1, const void
 // MN-major and its epilogue applies the derivative; d_hid is never stored.
 moe_status gemm_dact_bmn(const void *d_out, const void *w2, const void *pre, moe_act act, void *d_pre,
                          const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int m,
-                         int h, int32_t *st, cudaStream_t stream,
-                     SortedRows so = {}) {
+                         int h, int32_t *st, cudaStream_t stream, SortedRows so = {}) {
     // 256 x 256 pair tiles with two accumulators: the derivative epilogue
     // (a load of the pre-activation and the GELU derivative per element)
     // overlaps the next tile's main loop
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mO;
+    CUtensorMap mA, mB;
     if (!make_map(&mA, d_out, rows_of(e, c_max, so), (uint64_t)m, T2::A_BOX_ROWS, 64) ||
-        !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64) ||
-        !make_map(&mO, d_pre, rows_of(e, c_max, so), (uint64_t)h, 32, 32))
+        !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)d_pre, c_max, e, m, h, m, nullptr,
                nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)pre};
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return act == MOE_ACT_GELU ? launch_gemm<EPI_DGELU_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream)
-                               : launch_gemm<EPI_DRELU_BMN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream);
+    return act == MOE_ACT_GELU ? launch_gemm<EPI_DGELU_BMN, 1, 64, 2, 1>(mA, mB, mB, g, stream)
+                               : launch_gemm<EPI_DRELU_BMN, 1, 64, 2, 1>(mA, mB, mB, g, stream);
 }
 
 // SwiGLU with the forward's saved [a | b] rows: d_hid = d_out w2 (w2 read
@@ -1787,24 +1752,18 @@ moe_status gemm_dact_bmn(const void *d_out, const void *w2, const void *pre, moe
 // silu(a)] ([e, c_max, 2h]); d_hid is never stored.
 moe_status gemm_dswiglu_bmn(const void *d_out, const void *w2, const void *ab, void *d_pre,
                             const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int m,
-                            int h, int32_t *st, cudaStream_t stream,
-                     SortedRows so = {}) {
+                            int h, int32_t *st, cudaStream_t stream, SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB, mO, mOb;
+    CUtensorMap mA, mB;
     if (!make_map(&mA, d_out, rows_of(e, c_max, so), (uint64_t)m, T2::A_BOX_ROWS, 64) ||
-        !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64) ||
-        // d_a: the first h columns of each 2h-wide row (the map's extent clips a
-        // box at h, so d_b's columns are never written by it)
-        !make_map(&mO, d_pre, rows_of(e, c_max, so), (uint64_t)h, 32, 32, 2 * (uint64_t)h) ||
-        // d_b: the other h columns
-        !make_map(&mOb, (const __nv_bfloat16 *)d_pre + h, rows_of(e, c_max, so), (uint64_t)h, 32, 32, 2 * (uint64_t)h))
+        !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64))
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)d_pre, c_max, e, m, h, m, nullptr,
                nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)ab};
     g.out_pitch = 2 * (int64_t)h;
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mOb, mO, g, stream);
+    return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mB, g, stream);
 }
 
 // Weight gradients out[j] = A[j]^T B[j] over the first min(counts[j], *c_dev,
@@ -1820,13 +1779,11 @@ moe_status gemm_wgrad_mn(const void *a, int64_t a_pitch, int a_cols, const void 
                          const void *b_tail, int64_t b_tpitch, void *out, const int32_t *counts,
                          const int32_t *c_dev, int e, int64_t c_max, int32_t *st, cudaStream_t stream,
                          bool out_f32 = false, SortedRows so = {}) {
-    CUtensorMap mA, mAt, mB, mBt, mO;
+    CUtensorMap mA, mAt, mB, mBt;
     if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)a_cols, 64, 64, (uint64_t)a_pitch) ||
         !make_map(&mAt, a_tail, (uint64_t)e * 64, (uint64_t)a_cols, 64, 64, (uint64_t)a_tpitch) ||
         !make_map(&mB, b, rows_of(e, c_max, so), (uint64_t)b_cols, 64, 64, (uint64_t)b_pitch) ||
-        !make_map(&mBt, b_tail, (uint64_t)e * 64, (uint64_t)b_cols, 64, 64, (uint64_t)b_tpitch) ||
-        !(out_f32 ? make_map_f32_out(&mO, out, (uint64_t)e * a_cols, (uint64_t)b_cols)
-                  : make_map(&mO, out, (uint64_t)e * a_cols, (uint64_t)b_cols, 32, 32)))
+        !make_map(&mBt, b_tail, (uint64_t)e * 64, (uint64_t)b_cols, 64, 64, (uint64_t)b_tpitch))
         return MOE_ERR_CUDA;
     GemmArgs g{nullptr, nullptr, st, nullptr, (__nv_bfloat16 *)out, a_cols, e, (int)c_max, b_cols,
                (int)c_max, counts, c_dev, 0, 0};
@@ -1836,11 +1793,11 @@ moe_status gemm_wgrad_mn(const void *a, int64_t a_pitch, int a_cols, const void 
         g.n_rows = so.n;
     }
     g.skip_empty = 1;   // the zero gradients of experts without kept rows: zero_empty_experts_launch
-    if (out_f32) {   // fp32 boxes of 32 rows x 16 columns
+    if (out_f32) {
         g.out_f32 = (float *)out;
-        return launch_gemm<EPI_WGRAD_MN_F32, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream, &mAt, &mBt);
+        return launch_gemm<EPI_WGRAD_MN_F32, 1, 64, 2, 1>(mA, mB, mB, g, stream, &mAt, &mBt);
     }
-    return launch_gemm<EPI_WGRAD_MN, 1, 64, 2, 1>(mA, mB, mB, mO, g, stream, &mAt, &mBt);
+    return launch_gemm<EPI_WGRAD_MN, 1, 64, 2, 1>(mA, mB, mB, g, stream, &mAt, &mBt);
 }
 
 }  // namespace
