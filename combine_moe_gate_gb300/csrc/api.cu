@@ -533,9 +533,10 @@ bool int8_shape_ok(int e, int64_t n, int k, int n_out) {
     return e >= 1 && e <= kMaxE && n >= 1 && k >= 16 && k % 16 == 0 && n_out >= 8 && n_out % 8 == 0;
 }
 
-// k: int32 holds any sum of 8-bit products; the rest within the grouped product's indexes
+// k: int32 holds any sum of 8-bit products; the rest within the grouped product's indexes (the
+// last tile of channels may reach past the end)
 bool int8_supported(int e, int64_t n, int k, int n_out) {
-    return k < 1 << 17 && n <= kMaxRows && (int64_t)e * n_out < (int64_t)1 << 31 &&
+    return k < 1 << 17 && n <= kMaxRows && (int64_t)e * n_out <= kMaxRows &&
            (n / 192 + e) * ((n_out + 127) / 128) < (int64_t)1 << 31;
 }
 

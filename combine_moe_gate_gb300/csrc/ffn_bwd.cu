@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(ZE_THREADS)
 zero_empty_experts_kernel(ZeroOps ops, int nops, int e, int64_t c_max, const int32_t *__restrict__ counts,
                           const int32_t *__restrict__ c_dev, int32_t *status, SortedRows so) {
     pdl_enter();
-    if (status_bad(status)) return;
+    if (__syncthreads_or(status_bad(status))) return;   // all of the CTA or none: the list is made together
     constexpr int PER = ZE_MAX_E / ZE_THREADS, NW = ZE_THREADS / 32;
     __shared__ int32_t order[ZE_MAX_E], count[PER * NW];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

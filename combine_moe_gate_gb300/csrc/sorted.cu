@@ -63,6 +63,14 @@ __device__ __forceinline__ void exclusive_scan(const int32_t *tot, int32_t *star
     __syncthreads();
 }
 
+// A route's row, and its route back.  A position is inside the table whenever every count was made; warps that
+// found dev_status set (by another CTA or stream) while the others went on have made none of theirs.
+__device__ __forceinline__ void put_route(int64_t j, int b, int32_t pos, int64_t n, int e, int32_t *__restrict__ rows,
+                                          int32_t *__restrict__ source) {
+    rows[j] = b < e ? pos : -1;
+    if (source && pos >= 0 && pos < n) source[pos] = b < e ? (int32_t)j : -1;
+}
+
 // The positions of `rounds` x 32 consecutive routes from `at` on, the warp's next free position of
 // each bucket in next[].
 __device__ __forceinline__ void place_segment(const int32_t *__restrict__ idx, int64_t at, int rounds, int64_t n,
@@ -77,11 +85,7 @@ __device__ __forceinline__ void place_segment(const int32_t *__restrict__ idx, i
         __syncwarp();
         if (b >= 0 && (peers & lt) == 0) next[b] = first + __popc(peers);
         __syncwarp();
-        if (b >= 0) {
-            const int32_t pos = first + __popc(peers & lt);
-            rows[j] = b < e ? pos : -1;
-            if (source) source[pos] = b < e ? (int32_t)j : -1;
-        }
+        if (b >= 0) put_route(j, b, first + __popc(peers & lt), n, e, rows, source);
     }
 }
 
@@ -246,11 +250,7 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
             if (r >= rounds) break;
             const int b = bucket[r];
             const int64_t j = at + r * 32 + lane;
-            if (b >= 0) {
-                const int32_t pos = mine[b] + rank[r];
-                rows[j] = b < e ? pos : -1;
-                if (source) source[pos] = b < e ? (int32_t)j : -1;
-            }
+            if (b >= 0) put_route(j, b, mine[b] + rank[r], n, e, rows, source);
         }
     } else {
         place_segment(idx, at, rounds, n, e, mine, rows, source, status, lt);
