@@ -5,6 +5,7 @@ calls that `run_layer_fp4` makes); this module sizes and allocates the tensors
 the C ABI writes into.
 """
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional
 
@@ -236,7 +237,7 @@ def _route_sorted(B, logits, bias, k, score, groups, topk_groups, group_top, sca
                    group_top=group_top, scale=scale, flags=MOE_FLAG_NORMALIZE_GATES if normalize_gates else 0,
                    stream=stream)
     if padding is not None:
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
+        with torch.cuda.stream(stream) if stream is not None else nullcontext():
             B.idx.masked_fill_(padding, -1)
     moe_sort_routes(B.idx, e, B.rows, B.offsets, B.sort_ws, B.status, stream=stream)
 
@@ -297,12 +298,16 @@ def run_layer_sorted_bwd(dy, logits, w1, w3, w2, act, bufs: MoESortedBuffers, gr
                               G.d_w2, G.d_b1, G.d_b2, B.status, stream=stream)
     moe_encode_sorted_bwd(G.d_xs, B.rows, G.d_x, B.status, stream=stream)
     idx = B.idx
-    if padding is not None:   # d_gates is 0 there, so that any k different experts' logits get 0
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
+    on = torch.cuda.stream(stream) if stream is not None else nullcontext()
+    if padding is not None:   # any k different experts: these tokens' gradient is set to 0 below
+        with on:
             first = torch.arange(idx.shape[0], dtype=torch.int32, device=idx.device)[:, None]
             idx = torch.where(padding, first, idx)
     moe_route_bwd(logits, idx, G.d_gates, G.d_logits, B.status, score=score, scale=scale,
                   flags=MOE_FLAG_NORMALIZE_GATES if normalize_gates else 0, stream=stream)
+    if padding is not None:   # whatever their logits hold
+        with on:
+            G.d_logits.masked_fill_(padding[:, None], 0.0)
     return G
 
 

@@ -162,3 +162,26 @@ def test_two_layers_on_two_streams():
     for bufs, want in zip(out, alone):
         for B in bufs:
             assert torch.equal(B.y, want) and B.status.item() == 0
+
+
+def test_what_padded_tokens_hold_does_not_matter():
+    """NaN in the padded tokens' x, logits and dy: the bits of zeros there."""
+    s, m, e, k, h, act = 90, 64, 6, 3, 96, "swiglu"
+    padding = torch.arange(s, device="cuda") % 5 == 2
+    got = []
+    for fill in (0.0, float("nan")):
+        p = inputs(s, m, e, h, act, 3)
+        for n in ("x", "logits", "dy"):
+            p[n][padding] = fill
+        args = (p["x"], p["logits"], None, p["w1"], None, p["w3"], p["w2"], None, act, k)
+        B, G = M.alloc_layer_sorted(s, m, e, k, h, act, train=True), M.alloc_grads_sorted(s, k, p["w1"], p["w3"], p["w2"], act)
+        M.run_layer_sorted(*args, B, padding=padding, **OPT)
+        M.run_layer_sorted_bwd(p["dy"], p["logits"], p["w1"], p["w3"], p["w2"], act, B, G, padding=padding, **OPT)
+        B8 = M.alloc_layer_sorted(s, m, e, k, h, act, int8=True)
+        q = {n: M.quantize_weights_int8(p[n]) for n in ("w1", "w3", "w2")}
+        M.run_layer_int8(p["x"], p["logits"], None, q["w1"], None, q["w3"], q["w2"], None, act, k, B8, padding=padding, **OPT)
+        assert B.status.item() == 0 and B8.status.item() == 0
+        assert (G.d_x[padding] == 0).all() and (G.d_logits[padding] == 0).all() and (B.y[padding] == 0).all()
+        got.append([B.y, B8.y, G.d_x, G.d_logits, G.d_w1, G.d_w3, G.d_w2])
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
