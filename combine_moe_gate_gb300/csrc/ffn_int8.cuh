@@ -248,21 +248,22 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     }
     __syncwarp();
     pdl_enter();
-    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
-    if (warp == 0) {
-        int run = 0, max_n = 0;
-        bool bad = false;
-        for (int base = 0; base <= args.e; base += 32) {
-            const int j = base + lane;
-            if (j <= args.e) {
-                const int o = args.so.offsets ? args.so.offsets[j] : j ? (int)args.so.n : 0;
-                if (o < 0 || o > args.so.n || (args.so.offsets && j && o < args.so.offsets[j - 1])) bad = true;
-                ctl->first[j] = o;
-            }
+    // one thread an expert, so that the loads travel together; the status by a warp that has none of the first 32
+    if (threadIdx.x == I8_THREADS - 1) s_bad = status_bad(args.status) ? 1 : 0;
+    bool bad = false;
+    for (int j = threadIdx.x; j <= args.e; j += I8_THREADS) {
+        int o = j ? (int)args.so.n : 0;
+        if (args.so.offsets) {
+            const int before = args.so.offsets[max(j - 1, 0)];
+            o = args.so.offsets[j];
+            bad |= o < 0 || o > args.so.n || before > o;
         }
-        bad = __any_sync(0xffffffffu, bad);
-        if (bad) set_status(args.status, MOE_ERR_INVALID_ARG);   // and no tiles
-        __syncwarp();
+        ctl->first[j] = o;
+    }
+    bad = __syncthreads_or(bad);
+    if (warp == 0) {
+        if (bad && lane == 0) set_status(args.status, MOE_ERR_INVALID_ARG);   // and no tiles
+        int run = 0, max_n = 0;
         for (int base = 0; base < args.e; base += 32) {
             const int j = base + lane;
             const int rows = j < args.e && !bad ? ctl->first[j + 1] - ctl->first[j] : 0;

@@ -215,10 +215,9 @@ struct GemmArgs {
     int64_t n_rows;
 };
 
-// Entry j of the offsets, inside the buffer whatever it holds.
-__device__ __forceinline__ int sorted_at(const GemmArgs &a, int j) {
-    return (int)min((int64_t)max(a.offsets[j], 0), a.n_rows);
-}
+// An offset, inside the buffer whatever it holds; entry j of the offsets so.
+__device__ __forceinline__ int in_rows(const GemmArgs &a, int o) { return (int)min((int64_t)max(o, 0), a.n_rows); }
+__device__ __forceinline__ int sorted_at(const GemmArgs &a, int j) { return in_rows(a, a.offsets[j]); }
 
 // ------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t su32(const void *p) {
@@ -780,35 +779,31 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     __syncwarp();
     pdl_enter();
-    if (threadIdx.x == 0) s_bad = status_bad(args.status) ? 1 : 0;
+    // one thread an expert, so that the loads travel together; the status by a warp that has none of the first 32
+    if (threadIdx.x == NUM_THREADS - 1) s_bad = status_bad(args.status) ? 1 : 0;
+    for (int j = threadIdx.x; j < e; j += NUM_THREADS) {
+        int kept;
+        if (args.offsets) {
+            const int lo = args.offsets[j], hi = args.offsets[j + 1];
+            if (lo < 0 || hi < lo || hi > args.n_rows) set_status(args.status, MOE_ERR_INVALID_ARG);
+            kept = max(0, in_rows(args, hi) - in_rows(args, lo));
+        } else if (kmode) {
+            kept = min(max(args.k_counts[j], 0), (int)min((int64_t)*args.k_cdev, (int64_t)args.K));
+        } else {   // the kept rows inside [row_lo, row_hi)
+            const int rows = min(max(args.counts[j], 0), (int)min((int64_t)*args.c_dev, args.c_max));
+            kept = max(0, (args.row_hi > 0 ? min(rows, args.row_hi) : rows) - args.row_lo);
+        }
+        kept_rows[j] = kept;
+    }
+    __syncthreads();
     if (warp == 0) {
-        const bool sorted = args.offsets != nullptr;
-        const int c_eff = kmode || sorted ? 0 : (int)min((int64_t)*args.c_dev, args.c_max);
-        const int k_eff = kmode && !sorted ? (int)min((int64_t)*args.k_cdev, (int64_t)args.K) : 0;
         int run = 0;
         for (int base = 0; base < e; base += 32) {
-            int j = base + lane;
-            int rows = 0;
-            if (sorted) {
-                int own_rows = 0;
-                if (j < e) {
-                    const int lo = args.offsets[j], hi = args.offsets[j + 1];
-                    if (lo < 0 || hi < lo || hi > args.n_rows) set_status(args.status, MOE_ERR_INVALID_ARG);
-                    own_rows = max(0, sorted_at(args, j + 1) - sorted_at(args, j));
-                    kept_rows[j] = own_rows;
-                    rows = kmode ? urows : own_rows;
-                }
-            } else {
-                rows = j >= e ? 0 : kmode ? urows : min(max(args.counts[j], 0), c_eff);
-                if (!kmode && j < e) {   // the kept rows inside [row_lo, row_hi)
-                    const int hi = args.row_hi > 0 ? min(rows, args.row_hi) : rows;
-                    rows = max(0, hi - args.row_lo);
-                }
-                if (j < e) kept_rows[j] = kmode ? min(max(args.k_counts[j], 0), k_eff) : rows;
-            }
+            const int j = base + lane;
             // per-expert K: an expert without any K rows gets no tiles when asked
             // (its zero output is written elsewhere)
-            if (kmode && args.skip_empty && j < e && kept_rows[j] == 0) rows = 0;
+            int rows = j < e ? kept_rows[j] : 0;
+            if (kmode && j < e) rows = args.skip_empty && rows == 0 ? 0 : urows;
             const int own = ((rows + BMT - 1) / BMT) * ntn;
             int v = own;
 #pragma unroll
