@@ -57,6 +57,9 @@ constexpr uint32_t TMEM_COLS = 512;     // all of TMEM
 constexpr int MAX_E = 1024;
 constexpr unsigned long long WAIT_NS = 1000000000ull;  // 1 s per wait
 constexpr int SMEM_RING = 192 * 1024;   // operand ring per CTA
+// Staging per epilogue warp: 32 rows x 32 bf16, turned between a lane's row
+// and pieces of several rows.
+constexpr int STG_WARP_BYTES = 2048;
 
 // EPI_BIAS_BMN: the bias epilogue with B read MN-major, straight from a
 // row-major [K, N] tensor (the weights of the data-gradient products).
@@ -78,7 +81,7 @@ constexpr int SMEM_RING = 192 * 1024;   // operand ring per CTA
 // b = buf W3^T (bf16) to GemmArgs::aux_out, rows of 2 * n_out: a, then b.
 // EPI_DSWIGLU_BMN: d_hid = acc (B MN-major) and the saved [a | b] rows
 // (GemmArgs::aux, 2 * n_out a row) give d_a = d_hid * b * silu'(a) into out
-// and d_b = d_hid * silu(a) into out + n_out, out rows of GemmArgs::out_pitch.
+// and d_b = d_hid * silu(a) into out + n_out, out laid out like aux.
 enum Epi { EPI_GELU = 0, EPI_RELU = 1, EPI_SWIGLU = 2, EPI_BIAS = 3, EPI_BIAS_BMN = 4,
            EPI_WGRAD_MN = 5, EPI_DGELU = 6, EPI_DRELU = 7, EPI_GELU_SAVE = 8, EPI_RELU_SAVE = 9,
            EPI_DGELU_BMN = 10, EPI_DRELU_BMN = 11, EPI_WGRAD_MN_F32 = 12, EPI_SWIGLU_SAVE = 13,
@@ -101,8 +104,9 @@ __host__ __device__ constexpr bool is_swiglu(int epi) { return epi == EPI_SWIGLU
 // or 32 (64-byte swizzle); the smaller stage doubles the number of stages in
 // the same shared memory, i.e. more operand bytes in flight to cover L2/HBM
 // latency.
-template <int TM, int BK_, int CL_ = 1, int TN_ = 1, int EB_ = 2>
+template <int TM, int BK_, int CL_ = 1, int TN_ = 1, int EB_ = 2, int RING_ = SMEM_RING, int STG_ = STG_WARP_BYTES>
 struct Tiling {
+    static constexpr int STG = STG_;                      // staging bytes of an epilogue warp
     static constexpr int EB = EB_;                        // bytes per operand element (2 bf16, 1 e4m3)
     static constexpr int TN = TN_;                        // N = 256 MMAs per K step (pairs)
     static constexpr int CL = CL_;                        // CTAs per cluster: 1 or 2
@@ -117,7 +121,7 @@ struct Tiling {
     static constexpr int A_BYTES = A_ROWS * ROWB;
     static constexpr int B_BYTES = B_ROWS * ROWB;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = SMEM_RING / STAGE_BYTES;
+    static constexpr int STAGES = RING_ / STAGE_BYTES;
     static constexpr int NACC = TM == 1 && TN == 1 ? 2 : 1;  // accumulator buffers
     static constexpr int ACC_COLS = BN * TM * TN;         // TMEM columns per buffer
     static_assert(ROWB == 128 || ROWB == 64, "BK");
@@ -149,19 +153,16 @@ struct Ctl {  // control block in shared memory
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
+    uint64_t aux[EPI_WARPS][2];   // SwiGLU's derivative: a warp's blocks of the saved rows
     uint32_t tmem_base;
     int32_t abort;
     int32_t total_tiles;
     int32_t tile_start[MAX_E + 1];
 };
 
-// Staging per epilogue warp: 32 rows x 32 bf16, turned between a lane's row
-// and pieces of several rows.
-constexpr int STG_WARP_BYTES = 2048;
-
 template <class TL>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)TL::STAGES * TL::STAGE_BYTES + (size_t)EPI_WARPS * STG_WARP_BYTES +
+    return 1024 + (size_t)TL::STAGES * TL::STAGE_BYTES + (size_t)EPI_WARPS * TL::STG +
            sizeof(Ctl<TL::STAGES>);
 }
 
@@ -199,8 +200,6 @@ struct GemmArgs {
     __nv_bfloat16 *aux_out;
     // EPI_WGRAD_MN_F32: the result in fp32 [e * c_max, n_out] (out unused).
     float *out_f32;
-    // Elements between rows of out (0: n_out).
-    int64_t out_pitch;
     // MN-major B stacked along K from two maps (SwiGLU's [W1; W3]): K rows from
     // k_split on come from tmB3, k_split rows earlier (0: tmB only).
     int32_t k_split;
@@ -324,19 +323,9 @@ __device__ __forceinline__ void epi_store64(uint8_t *stg, const uint32_t (&w)[16
     __syncwarp();
 }
 
-// A warp's block of 32 rows x 32 bf16 columns of another matrix (row 0, column 0 of the block at p, rows
-// `pitch` elements apart), read as 64-byte pieces of eight rows at a time: a lane's own row in one go
-// would touch 32 lines a load.  Rows from `rows` on and columns from `cols` on are zeros.
-__device__ __forceinline__ void blk_fetch(V16 (&v)[4], const __nv_bfloat16 *p, int64_t pitch, int rows, int cols,
-                                          int lane) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int row = 8 * i + (lane >> 2), col = (lane & 3) * 8;
-        v[i] = ld_v16_if(p + row * pitch + col, row < rows && col < cols);
-    }
-}
-
-// The fetched block turned through the warp's staging buffer: o[] = this lane's row, 16 pairs.
+// A block of 32 rows x 32 bf16 columns of another matrix, fetched as 64-byte pieces of eight rows at a time
+// (row 8 i + lane / 4, chunk lane % 4: a lane's own row in one go would touch 32 lines a load), turned
+// through the warp's staging buffer: o[] = this lane's row, 16 pairs.
 __device__ __forceinline__ void blk_turn(uint8_t *stg, const V16 (&v)[4], uint32_t (&o)[16], int lane) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -348,63 +337,6 @@ __device__ __forceinline__ void blk_turn(uint8_t *stg, const V16 (&v)[4], uint32
     for (int c = 0; c < 4; c++) {
         const uint4 q = *reinterpret_cast<const uint4 *>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
         o[4 * c] = q.x; o[4 * c + 1] = q.y; o[4 * c + 2] = q.z; o[4 * c + 3] = q.w;
-    }
-    __syncwarp();
-}
-
-// The same for two matrices' blocks of 32 rows x 16 columns (32-byte rows; in the staging buffer the first at
-// 0, the second at 1024, 16-byte chunk c of row r at c ^ ((r >> 2) & 1)): fetched or stored by pieces of 16
-// rows, held as this lane's rows.
-__device__ __forceinline__ void half_fetch(V16 (&v)[2], const __nv_bfloat16 *p, int64_t pitch, int rows, int cols,
-                                           int lane) {
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int row = 16 * i + (lane >> 1), col = (lane & 1) * 8;
-        v[i] = ld_v16_if(p + row * pitch + col, row < rows && col < cols);
-    }
-}
-__device__ __forceinline__ uint8_t *half_at(uint8_t *stg, int row, int c) {
-    return stg + row * 32 + ((c ^ ((row >> 2) & 1)) << 4);
-}
-__device__ __forceinline__ void half_put(uint8_t *stg, const V16 (&a)[2], const V16 (&b)[2], int lane) {
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        uint8_t *p = half_at(stg, 16 * i + (lane >> 1), lane & 1);
-        st_shared_v4(p, a[i].w[0], a[i].w[1], a[i].w[2], a[i].w[3]);
-        st_shared_v4(p + 1024, b[i].w[0], b[i].w[1], b[i].w[2], b[i].w[3]);
-    }
-    __syncwarp();
-}
-__device__ __forceinline__ void half_row(uint8_t *stg, uint32_t (&a)[8], uint32_t (&b)[8], int lane) {
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-        const uint8_t *p = half_at(stg, lane, c);
-        const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 1024);
-        a[4 * c] = x.x; a[4 * c + 1] = x.y; a[4 * c + 2] = x.z; a[4 * c + 3] = x.w;
-        b[4 * c] = y.x; b[4 * c + 1] = y.y; b[4 * c + 2] = y.z; b[4 * c + 3] = y.w;
-    }
-    __syncwarp();
-}
-__device__ __forceinline__ void half_row_put(uint8_t *stg, const uint32_t (&a)[8], const uint32_t (&b)[8], int lane) {
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-        uint8_t *p = half_at(stg, lane, c);
-        st_shared_v4(p, a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
-        st_shared_v4(p + 1024, b[4 * c], b[4 * c + 1], b[4 * c + 2], b[4 * c + 3]);
-    }
-    __syncwarp();
-}
-__device__ __forceinline__ void half_store(uint8_t *stg, __nv_bfloat16 *pa, __nv_bfloat16 *pb, int64_t pitch, int rows,
-                                           int cols, int lane) {
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int row = 16 * i + (lane >> 1), col = (lane & 1) * 8;
-        const uint8_t *p = half_at(stg, row, lane & 1);
-        const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 1024);
-        if (row < rows && col < cols) {
-            *reinterpret_cast<uint4 *>(pa + row * pitch + col) = x;
-            *reinterpret_cast<uint4 *>(pb + row * pitch + col) = y;
-        }
     }
     __syncwarp();
 }
@@ -695,13 +627,19 @@ __device__ __forceinline__ Tile decode_tile(const int32_t *tile_start, int e, in
     return T;
 }
 
+// SwiGLU's derivative gives two stages of the ring to the blocks of the saved rows: two of 32 rows x 32
+// columns of a and of b for each epilogue warp.
+template <int EPI, int TM, int BK, int CL, int TN, int EB>
+using TilingOf = Tiling<TM, BK, CL, TN, EB, EPI == EPI_DSWIGLU_BMN ? SMEM_RING - 64 * 1024 : SMEM_RING,
+                        EPI == EPI_DSWIGLU_BMN ? 8192 : STG_WARP_BYTES>;
+
 template <int EPI, int TM, int BK, int CL, int TN, int EB = 2>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmB3,
               const __grid_constant__ CUtensorMap tmAt, const __grid_constant__ CUtensorMap tmBt,
               const GemmArgs args) {
-    using TL = Tiling<TM, BK, CL, TN, EB>;
+    using TL = TilingOf<EPI, TM, BK, CL, TN, EB>;
     static_assert(TN == 1 || !is_swiglu(EPI), "SwiGLU tiles pair W1 and W3 in one N = 256 MMA");
     constexpr bool F8 = EB == 1;   // e4m3 operands (kind::f8f6f4), scaled epilogue
     static_assert(!F8 || (CL == 2 && !is_swiglu(EPI) && EPI != EPI_BIAS_BMN), "e4m3 pair tiles");
@@ -725,9 +663,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     uint8_t *sA = smem;
     uint8_t *sB = smem + STAGES * A_BYTES;
     uint8_t *stg_all = smem + STAGES * TL::STAGE_BYTES;  // output staging
-    Ctl<STAGES> *ctl = (Ctl<STAGES> *)(stg_all + EPI_WARPS * STG_WARP_BYTES);
+    Ctl<STAGES> *ctl = (Ctl<STAGES> *)(stg_all + EPI_WARPS * TL::STG);
     __shared__ int32_t kept_rows[MAX_E];
-    __shared__ __align__(16) float epi_bias[EPI_WARPS][256];  // per epilogue warp
+    __shared__ __align__(16) float epi_bias[EPI_WARPS][DSWI ? 4 : 256];  // per epilogue warp
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = args.e;
@@ -761,6 +699,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             mbar_init(&ctl->tempty[a], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
         }
         mbar_init(&ctl->drain, 1);
+        if (DSWI)
+            for (int w = 0; w < 2 * EPI_WARPS; w++) mbar_init(&ctl->aux[w >> 1][w & 1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     } else if (warp == 1) {
         if (PAIR) {
@@ -1045,43 +985,90 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         const int row_in_tile = (int)prank * UM + (TM == 2 ? half * UM : 0) + sub * 32 + lane;
         constexpr int COLS = TM == 2 ? NOUT_TILE : NOUT_TILE / 2;  // output columns per warp
         const int col0 = TM == 2 ? 0 : half * COLS;                // first output column
-        uint8_t *stg = stg_all + ew * STG_WARP_BYTES;
+        uint8_t *stg = stg_all + ew * TL::STG;
         int acc = 0;
         uint32_t acc_phase = 0;
-        // derivative epilogues: this warp's next block of aux, 32 rows x 32 columns (SwiGLU: 16 of a and of b)
-        V16 fa[DSWI ? 2 : 4], fb[2];
-        auto fetch = [&](const Tile &T, int64_t base, int c0) {   // base: row_base(T.j), once a tile (a load)
-            const int row0 = T.mt * BMT + row_in_tile - lane, gcol = T.nt * NOUT_TILE + col0 + c0;
-            const int64_t pitch = (DSWI ? 2 : 1) * (int64_t)args.n_out;
-            const __nv_bfloat16 *p = args.aux + (base + row0) * pitch + gcol;
-            if constexpr (DSWI) {
-                half_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
-                half_fetch(fb, p + args.n_out, pitch, T.rows - row0, args.n_out - gcol, lane);
-            } else if constexpr (DACT || DACTP) {
-                blk_fetch(fa, p, pitch, T.rows - row0, args.n_out - gcol, lane);
-            }
+        const int64_t opitch = (DSWI ? 2 : 1) * (int64_t)args.n_out;   // rows of out and aux
+        // a tile's columns that this warp has: none if all its rows are past the end
+        auto columns_of = [&](const Tile &T) {
+            return T.rows > T.mt * BMT + row_in_tile - lane ? min(COLS, args.n_out - T.nt * NOUT_TILE - col0) : 0;
+        };
+        // derivative epilogues: this warp's next block of aux, 32 rows x 32 columns
+        V16 fa[4];
+        // this lane's first piece of a tile's part of aux, and the rows and columns from it on (negative: none).
+        // No branch leads to the loads: where paths meet, the moves would wait for them.
+        int64_t at = 0;
+        int prow = 0, pcol = 0;
+        auto place = [&](const Tile &T, int64_t base) {
+            const int row0 = T.mt * BMT + row_in_tile - lane, gcol = T.nt * NOUT_TILE + col0;
+            at = (base + row0 + (lane >> 2)) * opitch + gcol + (lane & 3) * 8;
+            prow = T.rows - row0 - (lane >> 2);
+            pcol = args.n_out - gcol - (lane & 3) * 8;
+        };
+        auto fetch = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                fa[i] = ld_v16_if(args.aux + at + c0 + 8 * i * opitch, c0 < pcol && prow > 8 * i);
         };
         // a tile's part of aux into L2, a whole epilogue ahead: a block ahead does not cover DRAM's latency
-        auto to_l2 = [&](int t) {
-            const Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
+        auto to_l2 = [&](const Tile &T, int64_t base) {
             const int row = T.mt * BMT + row_in_tile, gcol = T.nt * NOUT_TILE + col0;
             if (row >= T.rows) return;
-            const __nv_bfloat16 *p = args.aux + (row_base(T.j) + row) * ((DSWI ? 2 : 1) * (int64_t)args.n_out) + gcol;
+            const __nv_bfloat16 *p = args.aux + (base + row) * opitch + gcol;
 #pragma unroll
             for (int c = 0; c < COLS; c += 64)
-                if (gcol + c < args.n_out) {
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
-                    if (DSWI) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + args.n_out + c));
-                }
+                if (gcol + c < args.n_out) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
         };
-        if constexpr (DACT || DACTP)
-            if (tile0 < total) to_l2(tile0);
+        // SwiGLU: blocks of 32 rows x 32 columns of a and of b come by TMA into two buffers of 4 KB in turn, over
+        // the tiles that the warp has columns of (loads of pieces of 16 rows at a time, a block ahead, held
+        // the kernel up by a quarter: every row is another line of the small L1 beside the ring).  Block q's
+        // barrier is aux[q & 1]; its next phase is asked for by the warp itself, after block q.
+        int ti = tile0 - tile_step, ci = 0, ce = 0;
+        Tile Ti{};
+        auto issue = [&](int q) {
+            ci += 32;
+            while (ci >= ce) {
+                ti += tile_step;
+                if (ti >= total) return;
+                Ti = decode_tile(ctl->tile_start, e, ti, BMT, kept_rows, urows, nk, BK);
+                ce = columns_of(Ti);
+                ci = 0;
+            }
+            if (elect_one()) {
+                uint64_t *bar = &ctl->aux[ew][q & 1];
+                uint8_t *dst = stg + (q & 1) * 4096;
+                const int y = (int)(row_base(Ti.j) + Ti.mt * BMT + row_in_tile - lane);
+                const int x = Ti.nt * NOUT_TILE + col0 + ci;
+                mbar_expect_tx(bar, 4096);
+                tma_load_2d(dst, &tmB3, x, y, bar);
+                tma_load_2d(dst + 2048, &tmB3, args.n_out + x, y, bar);
+            }
+            __syncwarp();
+        };
+        int q = 0;   // the warp's blocks so far
+        if constexpr (DSWI) {
+            issue(0);
+            issue(1);
+        }
+        // the next tile is looked up, and its first block of aux fetched, while this one is worked on
+        Tile Tn{};
+        int64_t base_n = 0;
+        if (tile0 < total) {
+            Tn = decode_tile(ctl->tile_start, e, tile0, BMT, kept_rows, urows, nk, BK);
+            base_n = row_base(Tn.j);
+            if constexpr ((DACT || DACTP) && !DSWI) {
+                place(Tn, base_n);
+                fetch(0);
+                to_l2(Tn, base_n);
+            }
+        }
         for (int t = tile0; t < total; t += tile_step) {
-            Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
-            const int64_t base = row_base(T.j);
-            if constexpr (DACT || DACTP) {
-                fetch(T, base, 0);   // on its way while the main loop ends
-                if (t + tile_step < total) to_l2(t + tile_step);
+            const Tile T = Tn;
+            const int64_t base = base_n;
+            const bool more = t + tile_step < total;
+            if (more) {
+                Tn = decode_tile(ctl->tile_start, e, t + tile_step, BMT, kept_rows, urows, nk, BK);
+                base_n = row_base(Tn.j);
             }
             if (!mbar_wait<PAIR>(&ctl->tfull[acc], acc_phase, abort_flag, args.status)) break;
             tc_fence_after();
@@ -1093,13 +1080,25 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             auto store32 = [&](const uint32_t (&pk)[16], __nv_bfloat16 *out, int64_t pitch, int gcol) {
                 epi_store64(stg, pk, out + grow0 * pitch + gcol, 2 * pitch, live, 2 * (args.n_out - gcol), lane);
             };
-            const int64_t opitch = args.out_pitch ? args.out_pitch : (int64_t)args.n_out;
+            const int cend = columns_of(T);
+            // after block c0: the block after it, or the next tile's first, whose other blocks come into L2
+            auto fetch_next = [&](int c0, int step) {
+                const bool last = c0 + step >= cend;
+                if (last) {
+                    place(Tn, base_n);
+                    if (!more) prow = 0;
+                }
+                fetch(last ? 0 : c0 + step);
+                if (c0 == 0 && more) to_l2(Tn, base_n);
+            };
+            if constexpr ((DACT || DACTP) && !DSWI)
+                if (cend <= 0) fetch_next(0, COLS);
             const __nv_bfloat16 *brow = args.bias ? args.bias + (int64_t)T.j * args.n_out : nullptr;
             const uint32_t tbase = tmem + ((uint32_t)(sub * 32) << 16) +
                                    (uint32_t)(acc * TL::ACC_COLS + (TM == 2 ? half * BN : 0));
             if (is_swiglu(EPI)) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < COLS; c0 += 32) {
+                for (int c0 = 0; c0 < cend; c0 += 32) {
                     const int ocol = col0 + c0;               // column within the tile's output
                     const int gcol = T.nt * NOUT_TILE + ocol; // column within the expert
                     uint32_t r[32], u[32];
@@ -1142,7 +1141,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             } else {
                 // this warp's bias columns, widened to fp32 in shared memory once per tile
                 float *bsl = epi_bias[ew];
-                if (lane * 8 < COLS) {
+                if (!DSWI && lane * 8 < COLS) {
                     const int g8 = T.nt * NOUT_TILE + col0 + lane * 8;
                     float b8[8];
                     if (brow && g8 < args.n_out) {
@@ -1159,59 +1158,92 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 const float sa = F8 && valid ? args.a_scale[grow0 + lane] : 0.0f;
                 const float *bsc = F8 ? args.b_scale + (int64_t)T.j * args.n_out : nullptr;
                 if constexpr (DSWI) {
-                    // SwiGLU's derivative, 16 columns at a time: with 32, and the next block's rows of a
-                    // and b on their way, no registers are left for elements to overlap (a block of
-                    // 32 columns took 7000 clocks at a fifth of the issue slots)
+                    // SwiGLU's derivative, 16 columns at a time: with 32 no registers are left for elements to
+                    // overlap (a block of 32 columns took 7000 clocks at a fifth of the issue slots)
+                    __nv_bfloat16 *const o = args.out + (grow0 + (lane >> 2)) * opitch + T.nt * NOUT_TILE + col0 + (lane & 3) * 8;
+                    const int ocols = args.n_out - T.nt * NOUT_TILE - col0 - (lane & 3) * 8;
+                    bool ok = true;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < COLS; c0 += 16) {
-                        const int gcol = T.nt * NOUT_TILE + col0 + c0;
-                        uint32_t r[16], ua[8], ub[8];
-                        if (T.nk > 0) {
-                            tmem_ld16(tbase + (uint32_t)(col0 + c0), r);
-                        } else {
+                    for (int c0 = 0; c0 < cend; c0 += 32, q++) {
+                        uint8_t *blk = stg + (q & 1) * 4096;
+                        ok = mbar_wait<false>(&ctl->aux[ew][q & 1], (q >> 1) & 1, abort_flag, args.status);
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+#pragma unroll 1
+                        for (int hf = 0; hf < 2; hf++) {
+                            uint32_t r[16], ua[8], ub[8];
+                            if (T.nk > 0) {
+                                tmem_ld16(tbase + (uint32_t)(col0 + c0 + 16 * hf), r);
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < 16; i++) r[i] = 0u;   // empty contraction
-                        }
-                        half_put(stg, fa, fb, lane);
-                        half_row(stg, ua, ub, lane);
-                        if (c0 + 16 < COLS) fetch(T, base, c0 + 16);
-                        __nv_bfloat162 top = __float2bfloat162_rn(0.0f);   // the largest magnitude of a
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&ua[i])));
-                        const bool mid = sigmoid_mid_ok(__low2float(top)) && sigmoid_mid_ok(__high2float(top));
-                        if (T.nk > 0) tmem_wait_ld16(r);
-                        uint32_t da[8], db[8];
-                        auto columns = [&](auto general) {
-                            const float2 one = make_float2(1.0f, 1.0f);
-#pragma unroll
-                            for (int i = 0; i < 8; i++) {
-                                const float2 dh = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                                const float2 u = make_float2(bf16lo(ua[i]), bf16hi(ua[i]));
-                                const float2 v = make_float2(bf16lo(ub[i]), bf16hi(ub[i]));
-                                const float2 den = __fadd2_rn(one, make_float2(expf(-u.x), expf(-u.y)));
-                                float2 sg;
-                                if (general.value) sg = make_float2(1.0f / den.x, 1.0f / den.y);
-                                else sg = rcp_mid2(den);
-                                const float2 y = __fmul2_rn(__fmul2_rn(dh, u), sg);
-                                const float2 rest = __fadd2_rn(one, make_float2(-sg.x, -sg.y));
-                                const float2 x = __fmul2_rn(__fmul2_rn(__fmul2_rn(dh, v), sg), __ffma2_rn(u, rest, one));
-                                da[i] = pack_bf16(x.x, x.y);
-                                db[i] = pack_bf16(y.x, y.y);
+                                for (int i = 0; i < 16; i++) r[i] = 0u;   // empty contraction
                             }
-                        };
-                        if (__any_sync(0xffffffffu, valid && !mid)) columns(std::true_type{});
-                        else columns(std::false_type{});
-                        // d_a, and d_b in the second half of the rows
-                        half_row_put(stg, da, db, lane);
-                        half_store(stg, args.out + grow0 * opitch + gcol, args.out + grow0 * opitch + args.n_out + gcol,
-                                   opitch, live, args.n_out - gcol, lane);
+                            // this lane's row, in place: read here, d_a and d_b written below (16-byte chunk c at
+                            // c ^ ((row >> 1) & 3))
+                            uint8_t *rp[2];
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                rp[c] = blk + lane * 64 + (((2 * hf + c) ^ ((lane >> 1) & 3)) << 4);
+                                const uint4 x = *reinterpret_cast<const uint4 *>(rp[c]);
+                                const uint4 y = *reinterpret_cast<const uint4 *>(rp[c] + 2048);
+                                ua[4 * c] = x.x; ua[4 * c + 1] = x.y; ua[4 * c + 2] = x.z; ua[4 * c + 3] = x.w;
+                                ub[4 * c] = y.x; ub[4 * c + 1] = y.y; ub[4 * c + 2] = y.z; ub[4 * c + 3] = y.w;
+                            }
+                            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);   // the largest magnitude of a
+#pragma unroll
+                            for (int i = 0; i < 8; i++)
+                                top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&ua[i])));
+                            const bool mid = sigmoid_mid_ok(__low2float(top)) && sigmoid_mid_ok(__high2float(top));
+                            if (T.nk > 0) tmem_wait_ld16(r);
+                            uint32_t da[8], db[8];
+                            auto columns = [&](auto general) {
+                                const float2 one = make_float2(1.0f, 1.0f);
+#pragma unroll
+                                for (int i = 0; i < 8; i++) {
+                                    const float2 dh = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                                    const float2 u = make_float2(bf16lo(ua[i]), bf16hi(ua[i]));
+                                    const float2 v = make_float2(bf16lo(ub[i]), bf16hi(ub[i]));
+                                    const float2 den = __fadd2_rn(one, make_float2(expf(-u.x), expf(-u.y)));
+                                    float2 sg;
+                                    if (general.value) sg = make_float2(1.0f / den.x, 1.0f / den.y);
+                                    else sg = rcp_mid2(den);
+                                    const float2 y = __fmul2_rn(__fmul2_rn(dh, u), sg);
+                                    const float2 rest = __fadd2_rn(one, make_float2(-sg.x, -sg.y));
+                                    const float2 x = __fmul2_rn(__fmul2_rn(__fmul2_rn(dh, v), sg), __ffma2_rn(u, rest, one));
+                                    da[i] = pack_bf16(x.x, x.y);
+                                    db[i] = pack_bf16(y.x, y.y);
+                                }
+                            };
+                            if (__any_sync(0xffffffffu, valid && !mid)) columns(std::true_type{});
+                            else columns(std::false_type{});
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                st_shared_v4(rp[c], da[4 * c], da[4 * c + 1], da[4 * c + 2], da[4 * c + 3]);
+                                st_shared_v4(rp[c] + 2048, db[4 * c], db[4 * c + 1], db[4 * c + 2], db[4 * c + 3]);
+                            }
+                        }
+                        __syncwarp();
+                        // d_a, and d_b in the second half of the rows, as whole 64-byte pieces of eight rows
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int row = 8 * i + (lane >> 2);
+                            const uint8_t *p = blk + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4);
+                            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(p + 2048);
+                            if (row < live && c0 < ocols) {
+                                *reinterpret_cast<uint4 *>(o + 8 * i * opitch + c0) = x;
+                                *reinterpret_cast<uint4 *>(o + 8 * i * opitch + c0 + args.n_out) = y;
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies write there next
+                        __syncwarp();
+                        issue(q + 2);
                     }
+                    if (!ok) break;
                 } else if constexpr (DACT || DACTP) {
                     // the derivative of an activation: a block of 32 columns at a time, the next one's
                     // rows of aux on their way meanwhile
 #pragma unroll 1
-                    for (int c0 = 0; c0 < COLS; c0 += 32) {
+                    for (int c0 = 0; c0 < cend; c0 += 32) {
                         const int gcol = T.nt * NOUT_TILE + col0 + c0;
                         uint32_t r[32], dv[16];
                         if (T.nk > 0) {
@@ -1221,7 +1253,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             for (int i = 0; i < 32; i++) r[i] = 0u;   // empty contraction
                         }
                         blk_turn(stg, fa, dv, lane);
-                        if (c0 + 32 < COLS) fetch(T, base, c0 + 32);
+                        fetch_next(c0, 32);
                         if (T.nk > 0) tmem_wait_ld(r);
                         uint32_t pk[16];
 #pragma unroll
@@ -1242,7 +1274,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     }
                 } else {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < COLS; c0 += 64) {
+                    for (int c0 = 0; c0 < cend; c0 += 64) {
                         uint32_t r[2][32];
                         if (T.nk > 0) {
                             tmem_ld32(tbase + (uint32_t)(col0 + c0), r[0]);
@@ -1437,7 +1469,7 @@ template <int EPI, int TM, int BK, int CL, int TN, int EB = 2>
 moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b3,
                        const GemmArgs &args_in, cudaStream_t stream,
                        const CUtensorMap *a_tail = nullptr, const CUtensorMap *b_tail = nullptr) {
-    using TL = Tiling<TM, BK, CL, TN, EB>;
+    using TL = TilingOf<EPI, TM, BK, CL, TN, EB>;
     GemmArgs args = args_in;
     args.stall = take_gemm_stall() ? 1 : 0;
     auto kern = tc_group_gemm<EPI, TM, BK, CL, TN, EB>;
@@ -1749,16 +1781,16 @@ moe_status gemm_dswiglu_bmn(const void *d_out, const void *w2, const void *ab, v
                             const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max, int m,
                             int h, int32_t *st, cudaStream_t stream, SortedRows so = {}) {
     using T2 = Tiling<1, 64, 2, 1>;
-    CUtensorMap mA, mB;
+    CUtensorMap mA, mB, mP;
     if (!make_map(&mA, d_out, rows_of(e, c_max, so), (uint64_t)m, T2::A_BOX_ROWS, 64) ||
-        !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64))
+        !make_map(&mB, w2, (uint64_t)e * m, (uint64_t)h, 64, 64) ||
+        !make_map(&mP, ab, rows_of(e, c_max, so), 2 * (uint64_t)h, 32, 32))   // blocks of the saved rows
         return MOE_ERR_CUDA;
     GemmArgs g{counts, c_dev, st, nullptr, (__nv_bfloat16 *)d_pre, c_max, e, m, h, m, nullptr,
                nullptr, 0, 0, nullptr, nullptr, (const __nv_bfloat16 *)ab};
-    g.out_pitch = 2 * (int64_t)h;
     g.offsets = so.offsets;
     g.n_rows = so.n;
-    return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mB, g, stream);
+    return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mP, g, stream);
 }
 
 // Weight gradients out[j] = A[j]^T B[j] over the first min(counts[j], *c_dev,
