@@ -362,7 +362,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         uint32_t phase = 0;
         if (elect_one()) {
             for (int t = tile0; t < total && !args.stall; t += tile_step) {
-                const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
+                const Tile T = decode_tile<2 * UM, 1, 1>(ctl->tile_start, e, t, kept_rows, nk, NoOps{});
                 // this CTA's boxes of A, and the bytes of both CTAs' copies
                 const int left = T.rows - T.mt * 2 * UM - hh * 64;
                 const int n0 = min(max((left + 31) / 32, 0), 2), n1 = min(max((left - UM + 31) / 32, 0), 2);
@@ -463,7 +463,7 @@ fp4_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         uint2 *bsl = epi_bias[ew];
         int done = 0;
         for (int t = tile0; t < total; t += tile_step, done++) {
-            const Tile T = decode_tile(ctl->tile_start, e, t, 2 * UM, kept_rows, 0, nk, F4_BK);
+            const Tile T = decode_tile<2 * UM, 1, 1>(ctl->tile_start, e, t, kept_rows, nk, NoOps{});
             const int row = T.mt * 2 * UM + (int)prank * UM + sub * 32 + lane;
             const bool any = row - lane < T.rows;   // of the warp's rows
             const bool valid = row < T.rows, all_kept = row - lane + 31 < T.rows;

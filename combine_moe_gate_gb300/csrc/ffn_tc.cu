@@ -63,12 +63,12 @@ constexpr int STG_WARP_BYTES = 2048;
 
 // EPI_BIAS_BMN: the bias epilogue with B read MN-major, straight from a
 // row-major [K, N] tensor (the weights of the data-gradient products).
-// EPI_WGRAD_MN: the weight-gradient products out[j] = A[j]^T B[j] with both
-// operands read MN-major from row-major activations [e * b_rows, M or N]
-// (b_rows rows per expert): expert j contracts over its first k_counts[j]
-// rows; a last K block that is only partly kept is read from the tail maps
-// instead ([e * BK, M or N]: those rows copied, zeros after them), so no
-// row past an expert's kept rows is ever read.
+// EPI_WGRAD_MN: the weight-gradient products out[j] = A[j]^T B[j], up to three
+// of them in one launch (WgradOps), with both operands read MN-major from
+// row-major activations [e * b_rows, M or N] (b_rows rows per expert): expert j
+// contracts over its first k_counts[j] rows; a last K block that is only
+// partly kept is read from the tail maps instead ([e * BK, M or N]: those rows
+// copied, zeros after them), so no row past an expert's kept rows is ever read.
 // EPI_DGELU / EPI_DRELU: the activation backward fused into the recomputed
 // pre-activation: out = d_hid * act'(acc + bias) with d_hid (GemmArgs::aux)
 // laid out like out; the pre-activation itself is never stored.
@@ -177,11 +177,9 @@ struct GemmArgs {
     int K;             // contraction length
     int n_out;         // output columns per expert
     int b_rows;        // rows of each B tensor map per expert
-    // Contraction per expert (weight gradients): when set, every expert has
-    // c_max output rows (counts / c_dev unused) and expert j contracts over
-    // its first min(k_counts[j], *k_cdev, K) K columns only; the operands must
-    // be zero from there to the next multiple of BK.  An expert with none
-    // gets a zero output tile and no MMA.
+    // Contraction per expert (weight gradients): expert j contracts over its
+    // first min(k_counts[j], *k_cdev, K) rows only (counts, c_dev, c_max and
+    // n_out unused); an expert with none gets no tile and nothing is written.
     const int32_t *k_counts;
     const int32_t *k_cdev;
     // Row range (forward only): expert rows [row_lo, row_hi) of the kept rows
@@ -198,21 +196,33 @@ struct GemmArgs {
     const __nv_bfloat16 *aux;
     // EPI_GELU_SAVE / EPI_RELU_SAVE: where the pre-activation goes, likewise.
     __nv_bfloat16 *aux_out;
-    // EPI_WGRAD_MN_F32: the result in fp32 [e * c_max, n_out] (out unused).
-    float *out_f32;
     // MN-major B stacked along K from two maps (SwiGLU's [W1; W3]): K rows from
     // k_split on come from tmB3, k_split rows earlier (0: tmB only).
     int32_t k_split;
-    // Per-expert K: experts without K rows get no tiles (nothing written).
-    int32_t skip_empty;
     // Error-path test: the producers issue no copies, so the MMA issuer's
     // bounded wait on the first stage runs out (MOE_ERR_TIMEOUT).
     int32_t stall;
     // Rows sorted by expert: expert j has the rows offsets[j] .. offsets[j + 1] - 1 of n_rows, as its
-    // output rows or (k_counts set) as its contraction; counts, c_dev and k_cdev are not read then.
+    // output rows or (weight gradients) as its contraction; counts, c_dev, k_counts and k_cdev are not read then.
     const int32_t *offsets;
     int64_t n_rows;
 };
+
+// The weight-gradient products of a launch: out [e, rows, cols] (bf16, or fp32) from the operands' maps and
+// those of their tails.  An expert's tiles of all of them come one after another: they share operands.
+struct WgradOp {
+    CUtensorMap a, b, a_tail, b_tail;
+    void *out;
+    int rows, cols;
+};
+struct WgradOps {
+    WgradOp op[3];
+    int n;
+};
+struct NoOps {};
+constexpr bool is_wgrad(int epi) { return epi == EPI_WGRAD_MN || epi == EPI_WGRAD_MN_F32; }
+template <int EPI>
+using OpsOf = std::conditional_t<is_wgrad(EPI), WgradOps, NoOps>;
 
 // An offset, inside the buffer whatever it holds; entry j of the offsets so.
 __device__ __forceinline__ int in_rows(const GemmArgs &a, int o) { return (int)min((int64_t)max(o, 0), a.n_rows); }
@@ -603,14 +613,13 @@ __device__ __forceinline__ float2 rcp_mid2(float2 x) {
 }
 
 // Tile t -> (expert j, m-tile, n-tile); m-tile varies fastest.  rows: the
-// expert's output rows; nk: its K blocks.  kept_rows[] holds the output rows
-// per expert, or (uniform_rows > 0: every expert has that many output rows)
-// the K columns per expert.
-struct Tile { int j, mt, nt, rows, nk; };
+// expert's output rows; nk: its K blocks (weight gradients: kept_rows[j] are
+// the rows of the contraction, op the product).
+struct Tile { int j, mt, nt, rows, nk, op; };
 
-__device__ __forceinline__ Tile decode_tile(const int32_t *tile_start, int e, int t, int bmt,
-                                            const int32_t *kept_rows, int uniform_rows,
-                                            int nk_all, int bk) {
+template <int BMT, int BK, int NT, typename Ops>
+__device__ __forceinline__ Tile decode_tile(const int32_t *tile_start, int e, int t, const int32_t *kept_rows,
+                                            int nk_all, const Ops &ops) {
     int lo = 0, hi = e;  // largest j with tile_start[j] <= t
     while (hi - lo > 1) {
         int mid = (lo + hi) >> 1;
@@ -618,10 +627,20 @@ __device__ __forceinline__ Tile decode_tile(const int32_t *tile_start, int e, in
     }
     Tile T;
     T.j = lo;
+    T.op = 0;
+    T.rows = kept_rows[lo];
+    T.nk = nk_all;
     int local = t - tile_start[lo];
-    T.rows = uniform_rows > 0 ? uniform_rows : kept_rows[lo];
-    T.nk = uniform_rows > 0 ? (kept_rows[lo] + bk - 1) / bk : nk_all;
-    int mtiles = (T.rows + bmt - 1) / bmt;
+    if constexpr (std::is_same_v<Ops, WgradOps>) {
+        T.nk = (T.rows + BK - 1) / BK;
+        for (;; T.op++) {
+            T.rows = ops.op[T.op].rows;
+            const int n = (T.rows + BMT - 1) / BMT * ((ops.op[T.op].cols + NT - 1) / NT);
+            if (local < n || T.op + 1 >= ops.n) break;
+            local -= n;
+        }
+    }
+    const int mtiles = (T.rows + BMT - 1) / BMT;
     T.nt = local / mtiles;
     T.mt = local % mtiles;
     return T;
@@ -637,14 +656,14 @@ template <int EPI, int TM, int BK, int CL, int TN, int EB = 2>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmB3,
-              const __grid_constant__ CUtensorMap tmAt, const __grid_constant__ CUtensorMap tmBt,
+              const __grid_constant__ OpsOf<EPI> ops,
               const GemmArgs args) {
     using TL = TilingOf<EPI, TM, BK, CL, TN, EB>;
     static_assert(TN == 1 || !is_swiglu(EPI), "SwiGLU tiles pair W1 and W3 in one N = 256 MMA");
     constexpr bool F8 = EB == 1;   // e4m3 operands (kind::f8f6f4), scaled epilogue
     static_assert(!F8 || (CL == 2 && !is_swiglu(EPI) && EPI != EPI_BIAS_BMN), "e4m3 pair tiles");
     constexpr bool F32OUT = EPI == EPI_WGRAD_MN_F32;   // fp32 result, stored from registers
-    constexpr bool AMN = EPI == EPI_WGRAD_MN || F32OUT;   // A MN-major as well, tail blocks from tmAt / tmBt
+    constexpr bool AMN = EPI == EPI_WGRAD_MN || F32OUT;   // A MN-major as well, products of `ops`
     constexpr bool DACT = EPI == EPI_DGELU || EPI == EPI_DRELU;   // activation backward epilogue
     constexpr bool DSWI = EPI == EPI_DSWIGLU_BMN;   // SwiGLU derivative of a saved [a | b]
     constexpr bool DACTP = EPI == EPI_DGELU_BMN || EPI == EPI_DRELU_BMN || DSWI;   // act' of a saved pre
@@ -677,13 +696,21 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int tile0 = (int)(blockIdx.x / CL);
     const int tile_step = (int)(gridDim.x / CL);
     constexpr int NOUT_TILE = is_swiglu(EPI) ? BN / 2 : BN * TN;  // output columns per tile
-    const int ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
     const int nk = (args.K + BK - 1) / BK;
-    const bool kmode = args.k_counts != nullptr;           // K per expert
-    const int urows = kmode ? (int)args.c_max : 0;
-    // first output row of expert j; first row of its contraction
-    auto row_base = [&](int j) {
-        return args.offsets && !kmode ? (int64_t)sorted_at(args, j) : (int64_t)j * args.c_max + args.row_lo;
+    // tiles of one tile of rows, or (weight gradients) of an expert
+    int ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
+    if constexpr (AMN) {
+        ntn = 0;
+        for (int o = 0; o < ops.n; o++)
+            ntn += (ops.op[o].rows + BMT - 1) / BMT * ((ops.op[o].cols + NOUT_TILE - 1) / NOUT_TILE);
+    }
+    // first output row of a tile's expert
+    auto row_base = [&](const Tile &T) {
+        return AMN ? (int64_t)T.j * T.rows
+               : args.offsets ? (int64_t)sorted_at(args, T.j) : (int64_t)T.j * args.c_max + args.row_lo;
+    };
+    auto tile_at = [&](int t) {
+        return decode_tile<BMT, BK, NOUT_TILE>(ctl->tile_start, e, t, kept_rows, nk, ops);
     };
 
     // ---- setup.  What needs nothing of the kernel before, the barriers (warp 0) and the TMEM (warp 1), comes
@@ -727,7 +754,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const int lo = args.offsets[j], hi = args.offsets[j + 1];
             if (lo < 0 || hi < lo || hi > args.n_rows) set_status(args.status, MOE_ERR_INVALID_ARG);
             kept = max(0, in_rows(args, hi) - in_rows(args, lo));
-        } else if (kmode) {
+        } else if (AMN) {
             kept = min(max(args.k_counts[j], 0), (int)min((int64_t)*args.k_cdev, (int64_t)args.K));
         } else {   // the kept rows inside [row_lo, row_hi)
             const int rows = min(max(args.counts[j], 0), (int)min((int64_t)*args.c_dev, args.c_max));
@@ -740,11 +767,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         int run = 0;
         for (int base = 0; base < e; base += 32) {
             const int j = base + lane;
-            // per-expert K: an expert without any K rows gets no tiles when asked
-            // (its zero output is written elsewhere)
-            int rows = j < e ? kept_rows[j] : 0;
-            if (kmode && j < e) rows = args.skip_empty && rows == 0 ? 0 : urows;
-            const int own = ((rows + BMT - 1) / BMT) * ntn;
+            // (an expert without rows of a contraction gets no tiles: its zero output is written elsewhere)
+            const int rows = j < e ? kept_rows[j] : 0;
+            const int own = AMN ? (rows > 0 ? ntn : 0) : (rows + BMT - 1) / BMT * ntn;
             int v = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -795,9 +820,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             int issued = 0;
             bool ok = true;
             for (int t = tile0; t < total && !args.stall && ok; t += tile_step) {
-                Tile T = decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK);
+                Tile T = tile_at(t);
                 // A: this CTA's 128 rows, half of them per producer
-                const int a_row = (int)(row_base(T.j) + (int64_t)T.mt * BMT +
+                const int a_row = (int)(row_base(T) + (int64_t)T.mt * BMT +
                                         (int64_t)prank * TL::A_ROWS + (int64_t)hh * TL::A_BOX_ROWS);
                 // B rows of this CTA: its half of the (each) N = 256 sub-tile; with
                 // TN = 2 producer hh loads N sub-tile hh
@@ -815,22 +840,19 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                     {
                         const bool tail = part_tail && kb == T.nk - 1;
                         const int k_row = tail ? T.j * BK : k_base + kb * BK;
-                        if (PAIR && AMN) {
+                        if constexpr (AMN) {
+                            const WgradOp &op = ops.op[T.op];
                             const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
                             if (is_a) {
                                 // this CTA's 128 output rows = A columns, block hh of 64
                                 if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * A_BOX_BYTES);
-                                tma_load_2d_pair(sA + stage * A_BYTES + hh * A_BOX_BYTES,
-                                                 tail ? &tmAt : &tmA,
+                                tma_load_2d_pair(sA + stage * A_BYTES + hh * A_BOX_BYTES, tail ? &op.a_tail : &op.a,
                                                  T.mt * BMT + (int)prank * TL::A_ROWS + hh * 64, k_row, fb);
-                            } else {
+                            } else {   // 64 columns
                                 if (prank == 0) mbar_expect_tx(&ctl->full[stage], 2 * B_BOX_BYTES);
-                                const int n_col = b_row - T.j * args.b_rows;
-#pragma unroll
-                                for (int i = 0; i < TN; i++)   // TN boxes of 64 columns
-                                    tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES +
-                                                         i * (B_BOX_BYTES / TN),
-                                                     tail ? &tmBt : &tmB, n_col + 64 * i, k_row, fb);
+                                tma_load_2d_pair(sB + stage * B_BYTES + hh * B_BOX_BYTES, tail ? &op.b_tail : &op.b,
+                                                 T.nt * NOUT_TILE + (int)prank * TL::B_ROWS + hh * TL::B_BOX_ROWS, k_row,
+                                                 fb);
                             }
                         } else if (PAIR) {
                             const uint32_t fb = map_to_rank(su32(&ctl->full[stage]), lead);
@@ -901,7 +923,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 int acc = 0;
                 uint32_t acc_phase = 0;
                 for (int t = tile0; t < total; t += tile_step) {
-                    const int tnk = kmode ? decode_tile(ctl->tile_start, e, t, BMT, kept_rows, urows, nk, BK).nk : nk;
+                    const int tnk = AMN ? tile_at(t).nk : nk;
                     if (!mbar_wait<PAIR>(&ctl->tempty[acc], acc_phase ^ 1u, abort_flag, args.status)) break;
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(acc * TL::ACC_COLS);
@@ -988,12 +1010,16 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         uint8_t *stg = stg_all + ew * TL::STG;
         int acc = 0;
         uint32_t acc_phase = 0;
-        const int64_t opitch = (DSWI ? 2 : 1) * (int64_t)args.n_out;   // rows of out and aux
+        auto cols_of = [&](const Tile &T) {
+            if constexpr (AMN) return ops.op[T.op].cols;
+            else return args.n_out;
+        };
         // a tile's columns that this warp has: none if all its rows are past the end
         auto columns_of = [&](const Tile &T) {
-            return T.rows > T.mt * BMT + row_in_tile - lane ? min(COLS, args.n_out - T.nt * NOUT_TILE - col0) : 0;
+            return T.rows > T.mt * BMT + row_in_tile - lane ? min(COLS, cols_of(T) - T.nt * NOUT_TILE - col0) : 0;
         };
         // derivative epilogues: this warp's next block of aux, 32 rows x 32 columns
+        const int64_t aux_pitch = args.n_out;
         V16 fa[4];
         // this lane's first piece of a tile's part of aux, and the rows and columns from it on (negative: none).
         // No branch leads to the loads: where paths meet, the moves would wait for them.
@@ -1001,20 +1027,20 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         int prow = 0, pcol = 0;
         auto place = [&](const Tile &T, int64_t base) {
             const int row0 = T.mt * BMT + row_in_tile - lane, gcol = T.nt * NOUT_TILE + col0;
-            at = (base + row0 + (lane >> 2)) * opitch + gcol + (lane & 3) * 8;
+            at = (base + row0 + (lane >> 2)) * aux_pitch + gcol + (lane & 3) * 8;
             prow = T.rows - row0 - (lane >> 2);
             pcol = args.n_out - gcol - (lane & 3) * 8;
         };
         auto fetch = [&](int c0) {
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                fa[i] = ld_v16_if(args.aux + at + c0 + 8 * i * opitch, c0 < pcol && prow > 8 * i);
+                fa[i] = ld_v16_if(args.aux + at + c0 + 8 * i * aux_pitch, c0 < pcol && prow > 8 * i);
         };
         // a tile's part of aux into L2, a whole epilogue ahead: a block ahead does not cover DRAM's latency
         auto to_l2 = [&](const Tile &T, int64_t base) {
             const int row = T.mt * BMT + row_in_tile, gcol = T.nt * NOUT_TILE + col0;
             if (row >= T.rows) return;
-            const __nv_bfloat16 *p = args.aux + (base + row) * opitch + gcol;
+            const __nv_bfloat16 *p = args.aux + (base + row) * aux_pitch + gcol;
 #pragma unroll
             for (int c = 0; c < COLS; c += 64)
                 if (gcol + c < args.n_out) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
@@ -1030,14 +1056,14 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             while (ci >= ce) {
                 ti += tile_step;
                 if (ti >= total) return;
-                Ti = decode_tile(ctl->tile_start, e, ti, BMT, kept_rows, urows, nk, BK);
+                Ti = tile_at(ti);
                 ce = columns_of(Ti);
                 ci = 0;
             }
             if (elect_one()) {
                 uint64_t *bar = &ctl->aux[ew][q & 1];
                 uint8_t *dst = stg + (q & 1) * 4096;
-                const int y = (int)(row_base(Ti.j) + Ti.mt * BMT + row_in_tile - lane);
+                const int y = (int)(row_base(Ti) + Ti.mt * BMT + row_in_tile - lane);
                 const int x = Ti.nt * NOUT_TILE + col0 + ci;
                 mbar_expect_tx(bar, 4096);
                 tma_load_2d(dst, &tmB3, x, y, bar);
@@ -1054,8 +1080,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         Tile Tn{};
         int64_t base_n = 0;
         if (tile0 < total) {
-            Tn = decode_tile(ctl->tile_start, e, tile0, BMT, kept_rows, urows, nk, BK);
-            base_n = row_base(Tn.j);
+            Tn = tile_at(tile0);
+            base_n = row_base(Tn);
             if constexpr ((DACT || DACTP) && !DSWI) {
                 place(Tn, base_n);
                 fetch(0);
@@ -1065,10 +1091,16 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         for (int t = tile0; t < total; t += tile_step) {
             const Tile T = Tn;
             const int64_t base = base_n;
+            const int n_out = cols_of(T);
+            const int64_t opitch = (DSWI ? 2 : 1) * (int64_t)n_out;   // rows of out (and aux)
+            __nv_bfloat16 *out = args.out;
+            float *out_f32 = nullptr;
+            if constexpr (F32OUT) out_f32 = static_cast<float *>(ops.op[T.op].out);
+            else if constexpr (AMN) out = static_cast<__nv_bfloat16 *>(ops.op[T.op].out);
             const bool more = t + tile_step < total;
             if (more) {
-                Tn = decode_tile(ctl->tile_start, e, t + tile_step, BMT, kept_rows, urows, nk, BK);
-                base_n = row_base(Tn.j);
+                Tn = tile_at(t + tile_step);
+                base_n = row_base(Tn);
             }
             if (!mbar_wait<PAIR>(&ctl->tfull[acc], acc_phase, abort_flag, args.status)) break;
             tc_fence_after();
@@ -1077,8 +1109,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const int64_t grow0 = base + row - lane;
             const int live = T.rows - (row - lane);          // live rows from the warp's first on
             // a block of 32 bf16 columns from gcol on, of `out` with rows of `pitch` elements
-            auto store32 = [&](const uint32_t (&pk)[16], __nv_bfloat16 *out, int64_t pitch, int gcol) {
-                epi_store64(stg, pk, out + grow0 * pitch + gcol, 2 * pitch, live, 2 * (args.n_out - gcol), lane);
+            auto store32 = [&](const uint32_t (&pk)[16], __nv_bfloat16 *dst, int64_t pitch, int gcol) {
+                epi_store64(stg, pk, dst + grow0 * pitch + gcol, 2 * pitch, live, 2 * (n_out - gcol), lane);
             };
             const int cend = columns_of(T);
             // after block c0: the block after it, or the next tile's first, whose other blocks come into L2
@@ -1093,7 +1125,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             };
             if constexpr ((DACT || DACTP) && !DSWI)
                 if (cend <= 0) fetch_next(0, COLS);
-            const __nv_bfloat16 *brow = args.bias ? args.bias + (int64_t)T.j * args.n_out : nullptr;
+            const __nv_bfloat16 *brow = args.bias ? args.bias + (int64_t)T.j * n_out : nullptr;
             const uint32_t tbase = tmem + ((uint32_t)(sub * 32) << 16) +
                                    (uint32_t)(acc * TL::ACC_COLS + (TM == 2 ? half * BN : 0));
             if (is_swiglu(EPI)) {
@@ -1126,16 +1158,16 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             pk[i] = pack_bf16(silu(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
                                               silu(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
                     }
-                    store32(pk, args.out, opitch, gcol);
+                    store32(pk, out, opitch, gcol);
                     if (EPI == EPI_SWIGLU_SAVE) {   // a, then b
 #pragma unroll
                         for (int i = 0; i < 16; i++)
                             pk[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        store32(pk, args.aux_out, 2 * (int64_t)args.n_out, gcol);
+                        store32(pk, args.aux_out, 2 * (int64_t)n_out, gcol);
 #pragma unroll
                         for (int i = 0; i < 16; i++)
                             pk[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-                        store32(pk, args.aux_out + args.n_out, 2 * (int64_t)args.n_out, gcol);
+                        store32(pk, args.aux_out + n_out, 2 * (int64_t)n_out, gcol);
                     }
                 }
             } else {
@@ -1144,7 +1176,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 if (!DSWI && lane * 8 < COLS) {
                     const int g8 = T.nt * NOUT_TILE + col0 + lane * 8;
                     float b8[8];
-                    if (brow && g8 < args.n_out) {
+                    if (brow && g8 < n_out) {
                         Elt<__nv_bfloat16>::unpack(*reinterpret_cast<const V16 *>(brow + g8), b8);
                     } else {
 #pragma unroll
@@ -1156,12 +1188,12 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 __syncwarp();
                 // e4m3: this lane's row scale (its output row)
                 const float sa = F8 && valid ? args.a_scale[grow0 + lane] : 0.0f;
-                const float *bsc = F8 ? args.b_scale + (int64_t)T.j * args.n_out : nullptr;
+                const float *bsc = F8 ? args.b_scale + (int64_t)T.j * n_out : nullptr;
                 if constexpr (DSWI) {
                     // SwiGLU's derivative, 16 columns at a time: with 32 no registers are left for elements to
                     // overlap (a block of 32 columns took 7000 clocks at a fifth of the issue slots)
-                    __nv_bfloat16 *const o = args.out + (grow0 + (lane >> 2)) * opitch + T.nt * NOUT_TILE + col0 + (lane & 3) * 8;
-                    const int ocols = args.n_out - T.nt * NOUT_TILE - col0 - (lane & 3) * 8;
+                    __nv_bfloat16 *const o = out + (grow0 + (lane >> 2)) * opitch + T.nt * NOUT_TILE + col0 + (lane & 3) * 8;
+                    const int ocols = n_out - T.nt * NOUT_TILE - col0 - (lane & 3) * 8;
                     bool ok = true;
 #pragma unroll 1
                     for (int c0 = 0; c0 < cend; c0 += 32, q++) {
@@ -1231,7 +1263,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             const uint4 y = *reinterpret_cast<const uint4 *>(p + 2048);
                             if (row < live && c0 < ocols) {
                                 *reinterpret_cast<uint4 *>(o + 8 * i * opitch + c0) = x;
-                                *reinterpret_cast<uint4 *>(o + 8 * i * opitch + c0 + args.n_out) = y;
+                                *reinterpret_cast<uint4 *>(o + 8 * i * opitch + c0 + n_out) = y;
                             }
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies write there next
@@ -1270,7 +1302,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             const float2 d = __fmul2_rn(g, da);
                             pk[i] = pack_bf16(d.x, d.y);
                         }
-                        store32(pk, args.out, opitch, gcol);
+                        store32(pk, out, opitch, gcol);
                     }
                 } else {
 #pragma unroll 1
@@ -1301,7 +1333,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                 if (F8) {
                                     const int g8 = gcol + q * 8;
                                     float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-                                    if (g8 < args.n_out) {   // n_out is a multiple of 16
+                                    if (g8 < n_out) {   // n_out is a multiple of 16
                                         lo = reinterpret_cast<const float4 *>(bsc + g8)[0];
                                         hi = reinterpret_cast<const float4 *>(bsc + g8)[1];
                                     }
@@ -1331,12 +1363,12 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                     uint32_t w[16];
 #pragma unroll
                                     for (int i = 0; i < 16; i++) w[i] = __float_as_uint(of[16 * hc + i]);
-                                    epi_store64(stg, w, args.out_f32 + grow0 * args.n_out + gcol + 16 * hc,
-                                                4 * (int64_t)args.n_out, live, 4 * (args.n_out - gcol - 16 * hc), lane);
+                                    epi_store64(stg, w, out_f32 + grow0 * n_out + gcol + 16 * hc,
+                                                4 * (int64_t)n_out, live, 4 * (n_out - gcol - 16 * hc), lane);
                                 }
                             } else {
-                                store32(pk, args.out, opitch, gcol);
-                                if (SAVE) store32(pp, args.aux_out, (int64_t)args.n_out, gcol);
+                                store32(pk, out, opitch, gcol);
+                                if (SAVE) store32(pp, args.aux_out, (int64_t)n_out, gcol);
                             }
                         }
                     }
@@ -1467,8 +1499,7 @@ int max_clusters(K kern, size_t smem, int cl, int threads = NUM_THREADS) {
 
 template <int EPI, int TM, int BK, int CL, int TN, int EB = 2>
 moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b3,
-                       const GemmArgs &args_in, cudaStream_t stream,
-                       const CUtensorMap *a_tail = nullptr, const CUtensorMap *b_tail = nullptr) {
+                       const GemmArgs &args_in, cudaStream_t stream, const OpsOf<EPI> &ops = {}) {
     using TL = TilingOf<EPI, TM, BK, CL, TN, EB>;
     GemmArgs args = args_in;
     args.stall = take_gemm_stall() ? 1 : 0;
@@ -1486,15 +1517,22 @@ moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtenso
         if (dev >= 0 && dev < 64) units[dev] = nunits;
     }
     constexpr int NOUT_TILE = is_swiglu(EPI) ? BN / 2 : BN * TN;
-    const int64_t ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
-    int64_t upper = (int64_t)args.e * ((args.c_max + TL::BMT - 1) / TL::BMT) * ntn;
-    if (args.offsets && !args.k_counts)   // a partly filled tile an expert that has rows
-        upper = (args.n_rows / TL::BMT + (args.n_rows < args.e ? args.n_rows : args.e)) * ntn;
+    int64_t upper = 0;   // tiles at most
+    if constexpr (is_wgrad(EPI)) {
+        for (int o = 0; o < ops.n; o++)
+            upper += (int64_t)args.e * ((ops.op[o].rows + TL::BMT - 1) / TL::BMT) *
+                     ((ops.op[o].cols + NOUT_TILE - 1) / NOUT_TILE);
+    } else {
+        const int64_t ntn = (args.n_out + NOUT_TILE - 1) / NOUT_TILE;
+        upper = (int64_t)args.e * ((args.c_max + TL::BMT - 1) / TL::BMT) * ntn;
+        if (args.offsets)   // a partly filled tile an expert that has rows
+            upper = (args.n_rows / TL::BMT + (args.n_rows < args.e ? args.n_rows : args.e)) * ntn;
+    }
     int64_t grid = upper < nunits ? upper : nunits;
     if (grid < 1) grid = 1;
     if (CL == 1)
         return launch_pdl(kern, dim3((unsigned)grid), dim3(NUM_THREADS), SMEM, stream, a, b, b3,
-                          a_tail ? *a_tail : a, b_tail ? *b_tail : b, args);
+                          ops, args);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(CL * grid));
     cfg.blockDim = dim3(NUM_THREADS);
@@ -1509,8 +1547,7 @@ moe_status launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const CUtenso
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, b, b3, a_tail ? *a_tail : a,
-                                         b_tail ? *b_tail : b, args);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, b, b3, ops, args);
     note_launch();
     if (err != cudaSuccess) {
         cudaGetLastError();
@@ -1793,38 +1830,53 @@ moe_status gemm_dswiglu_bmn(const void *d_out, const void *w2, const void *ab, v
     return launch_gemm<EPI_DSWIGLU_BMN, 1, 64, 2, 1>(mA, mB, mP, g, stream);
 }
 
-// Weight gradients out[j] = A[j]^T B[j] over the first min(counts[j], *c_dev,
-// c_max) rows of expert j, both operands read MN-major in place: A rows of
-// a_cols columns at pitch a_pitch, B rows of b_cols at pitch b_pitch, c_max
-// rows per expert; a_tail / b_tail [e, 64, *] (pitches a_tpitch / b_tpitch)
-// hold each expert's partly kept last 64-row block (tail_rows_launch);
-// out [e, a_cols, b_cols], bf16, or fp32 when out_f32.  Experts without kept
-// rows are not written (their zero gradients come from
-// zero_empty_experts_launch).
-moe_status gemm_wgrad_mn(const void *a, int64_t a_pitch, int a_cols, const void *a_tail,
-                         int64_t a_tpitch, const void *b, int64_t b_pitch, int b_cols,
-                         const void *b_tail, int64_t b_tpitch, void *out, const int32_t *counts,
-                         const int32_t *c_dev, int e, int64_t c_max, int32_t *st, cudaStream_t stream,
-                         bool out_f32 = false, SortedRows so = {}) {
-    CUtensorMap mA, mAt, mB, mBt;
-    if (!make_map(&mA, a, rows_of(e, c_max, so), (uint64_t)a_cols, 64, 64, (uint64_t)a_pitch) ||
-        !make_map(&mAt, a_tail, (uint64_t)e * 64, (uint64_t)a_cols, 64, 64, (uint64_t)a_tpitch) ||
-        !make_map(&mB, b, rows_of(e, c_max, so), (uint64_t)b_cols, 64, 64, (uint64_t)b_pitch) ||
-        !make_map(&mBt, b_tail, (uint64_t)e * 64, (uint64_t)b_cols, 64, 64, (uint64_t)b_tpitch))
-        return MOE_ERR_CUDA;
-    GemmArgs g{nullptr, nullptr, st, nullptr, (__nv_bfloat16 *)out, a_cols, e, (int)c_max, b_cols,
-               (int)c_max, counts, c_dev, 0, 0};
+// A weight gradient out[j] [a_cols, b_cols] = A[j]^T B[j] over the kept rows of
+// expert j, both operands read MN-major in place; a_tail / b_tail [e, 64, *] hold
+// each expert's partly kept last 64-row block (tail_rows_launch).  Experts without
+// kept rows are not written (zero_empty_experts_launch).
+struct Wgrad {
+    const void *a;
+    int64_t a_pitch;
+    int a_cols;
+    const void *a_tail;
+    int64_t a_tpitch;
+    const void *b;
+    int b_cols;
+    const void *b_tail;
+    void *out;
+};
+
+// n of them in one launch (three launches for 64 SwiGLU experts of 1024 x 512 took 120 us, each with 7 us
+// before its first epilogue).
+moe_status gemm_wgrad_mn(const Wgrad *w, int n, const int32_t *counts, const int32_t *c_dev, int e, int64_t c_max,
+                         int32_t *st, cudaStream_t stream, bool out_f32 = false, SortedRows so = {}) {
+    WgradOps ops{};
+    ops.n = n;
+    for (int i = 0; i < n; i++) {
+        WgradOp &o = ops.op[i];
+        o.out = w[i].out;
+        o.rows = w[i].a_cols;
+        o.cols = w[i].b_cols;
+        if (!make_map(&o.a, w[i].a, rows_of(e, c_max, so), (uint64_t)o.rows, 64, 64, (uint64_t)w[i].a_pitch) ||
+            !make_map(&o.a_tail, w[i].a_tail, (uint64_t)e * 64, (uint64_t)o.rows, 64, 64, (uint64_t)w[i].a_tpitch) ||
+            !make_map(&o.b, w[i].b, rows_of(e, c_max, so), (uint64_t)o.cols, 64, 64) ||
+            !make_map(&o.b_tail, w[i].b_tail, (uint64_t)e * 64, (uint64_t)o.cols, 64, 64))
+            return MOE_ERR_CUDA;
+    }
+    GemmArgs g{};
+    g.status = st;
+    g.e = e;
+    g.K = g.b_rows = (int)c_max;
+    g.k_counts = counts;
+    g.k_cdev = c_dev;
     if (so.offsets) {   // the sorted rows are the contraction
         g.K = (int)so.n;
-        g.k_counts = g.offsets = so.offsets;
+        g.offsets = so.offsets;
         g.n_rows = so.n;
     }
-    g.skip_empty = 1;   // the zero gradients of experts without kept rows: zero_empty_experts_launch
-    if (out_f32) {
-        g.out_f32 = (float *)out;
-        return launch_gemm<EPI_WGRAD_MN_F32, 1, 64, 2, 1>(mA, mB, mB, g, stream, &mAt, &mBt);
-    }
-    return launch_gemm<EPI_WGRAD_MN, 1, 64, 2, 1>(mA, mB, mB, g, stream, &mAt, &mBt);
+    const CUtensorMap &any = ops.op[0].a;
+    return out_f32 ? launch_gemm<EPI_WGRAD_MN_F32, 1, 64, 2, 1>(any, any, any, g, stream, ops)
+                   : launch_gemm<EPI_WGRAD_MN, 1, 64, 2, 1>(any, any, any, g, stream, ops);
 }
 
 }  // namespace
@@ -1912,13 +1964,10 @@ moe_status ffn_tc_bwd_launch(const void *buf, const void *hid, const int32_t *co
         zo.op[2] = ZeroOp{d_w3, (int64_t)h * m * gb};
         MOE_TRY(zero_empty_experts_launch(zo, swiglu ? 3 : 2, c_max, e, counts, c_dev, st, stream, so));
     }
-    MOE_TRY(gemm_wgrad_mn(d_out, m, m, tDo, m, hid, h, h, tHid, h, d_w2, counts, c_dev, e, c_max, st,
-                          stream, wgrad_f32, so));
-    MOE_TRY(gemm_wgrad_mn(dpre, H2, h, tDp, H2, buf, m, m, tBuf, m, d_w1, counts, c_dev, e, c_max,
-                          st, stream, wgrad_f32, so));
-    if (swiglu)
-        MOE_TRY(gemm_wgrad_mn(dpre + h, H2, h, tDp + h, H2, buf, m, m, tBuf, m, d_w3, counts, c_dev,
-                              e, c_max, st, stream, wgrad_f32, so));
+    const Wgrad wg[3] = {{d_out, m, m, tDo, m, hid, h, tHid, d_w2},
+                         {dpre, H2, h, tDp, H2, buf, m, tBuf, d_w1},
+                         {dpre + h, H2, h, tDp + h, H2, buf, m, tBuf, d_w3}};
+    MOE_TRY(gemm_wgrad_mn(wg, swiglu ? 3 : 2, counts, c_dev, e, c_max, st, stream, wgrad_f32, so));
     // bias gradients (ReLU / GELU experts), both in one launch
     if (!swiglu && d_b1 && d_b2)
         MOE_TRY(colsum_launch(dpre, e, c_max, h, h, counts, c_dev, d_b1, st, stream, wgrad_f32,
