@@ -309,6 +309,7 @@ moe_status act_bwd_launch(const __nv_bfloat16 *pa, const __nv_bfloat16 *pb,
 namespace {
 
 constexpr int TR_WARPS = 8;   // one warp per row, 64 / TR_WARPS CTAs per expert and operand
+constexpr int TR_U = 4;
 
 __global__ void __launch_bounds__(TR_WARPS * 32)
 tail_rows_kernel(TailOps ops, int64_t c_max, const int32_t *__restrict__ counts,
@@ -327,12 +328,16 @@ tail_rows_kernel(TailOps ops, int64_t c_max, const int32_t *__restrict__ counts,
     const int nvalid = (int)(kept & 63);
     if (nvalid == 0) return;
     const int r = blockIdx.x * TR_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= ((nvalid + 15) & ~15)) return;   // the products take 16 rows at a time and stop there
     const __nv_bfloat16 *srow = src + (first + (kept - nvalid) + r) * src_pitch;
     __nv_bfloat16 *drow = dst + ((int64_t)j * 64 + r) * cols;
-    for (int c = lane * 8; c < cols; c += 32 * 8) {
-        V16 v{};
-        if (r < nvalid) v = ld_v16(srow + c);
-        st_v16(drow + c, v);
+    for (int c0 = lane * 8; c0 < cols; c0 += TR_U * 32 * 8) {   // loads of TR_U chunks under way
+        V16 v[TR_U];
+#pragma unroll
+        for (int u = 0; u < TR_U; u++) v[u] = ld_v16_if(srow + c0 + u * 256, r < nvalid && c0 + u * 256 < cols);
+#pragma unroll
+        for (int u = 0; u < TR_U; u++)
+            if (c0 + u * 256 < cols) st_v16(drow + c0 + u * 256, v[u]);
     }
 }
 

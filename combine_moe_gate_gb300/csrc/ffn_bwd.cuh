@@ -45,9 +45,9 @@ moe_status colsum_launch(const __nv_bfloat16 *src, int e, int64_t c_max, int col
 // The partly kept last 64-row block of every expert, for the MN-major weight
 // gradients, for up to TAIL_MAX_OPS operands in one launch: with kept_b =
 // min(counts[b], *c_dev, c_max) and r0 = kept_b rounded down to a multiple of
-// 64, dst[b][r] = src[b][r0 + r] for r < kept_b - r0 and 0 for the rest of
-// the 64 rows; experts whose kept rows end on a block boundary are left
-// untouched (nothing reads them).  src rows of `cols` columns at row pitch
+// 64, dst[b][r] = src[b][r0 + r] for r < kept_b - r0 and 0 from there to the
+// next multiple of 16 (the products go no further); experts whose kept rows end
+// on a block boundary are left untouched (nothing reads them).  src rows of `cols` columns at row pitch
 // `pitch`, c_max rows per expert; dst [e, 64, cols] dense.
 constexpr int TAIL_MAX_OPS = 4;
 struct TailOp {

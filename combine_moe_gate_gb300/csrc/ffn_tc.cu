@@ -17,7 +17,7 @@
 //               four boxes (128-byte swizzle) into a ring guarded by full/empty
 //               mbarriers; a pair's copies complete on the even CTA's barriers;
 //   warp 1      allocates all 512 TMEM columns in both CTAs; in the even CTA
-//               one lane issues the 2-SM tcgen05.mma (M = 256 over the pair,
+//               an elected lane issues the 2-SM tcgen05.mma (M = 256 over the pair,
 //               N = 256; kind::f16 for bf16, kind::f8f6f4 for e4m3) and
 //               tcgen05.commit to release stages and publish accumulators;
 //   warps 2-9   epilogue: tcgen05.ld 32 lanes x 32 columns, then the mode's
@@ -68,7 +68,7 @@ constexpr int STG_WARP_BYTES = 2048;
 // row-major activations [e * b_rows, M or N] (b_rows rows per expert): expert j
 // contracts over its first k_counts[j] rows; a last K block that is only
 // partly kept is read from the tail maps instead ([e * BK, M or N]: those rows
-// copied, zeros after them), so no row past an expert's kept rows is ever read.
+// copied, zeros after them to a multiple of 16), so no row past an expert's kept rows is ever read.
 // EPI_DGELU / EPI_DRELU: the activation backward fused into the recomputed
 // pre-activation: out = d_hid * act'(acc + bias) with d_hid (GemmArgs::aux)
 // laid out like out; the pre-activation itself is never stored.
@@ -923,7 +923,12 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 int acc = 0;
                 uint32_t acc_phase = 0;
                 for (int t = tile0; t < total; t += tile_step) {
-                    const int tnk = AMN ? tile_at(t).nk : nk;
+                    int tnk = nk, kept = 0;
+                    if (AMN) {
+                        const Tile T = tile_at(t);
+                        tnk = T.nk;
+                        kept = kept_rows[T.j];
+                    }
                     if (!mbar_wait<PAIR>(&ctl->tempty[acc], acc_phase ^ 1u, abort_flag, args.status)) break;
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(acc * TL::ACC_COLS);
@@ -935,6 +940,8 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                         const uint32_t b0 = su32(sB + stage * B_BYTES);
 #pragma unroll
                         for (int kk = 0; kk < ROWB / 32; kk++) {   // one MMA per 32 bytes of K
+                            // a tail's rows are there to a multiple of UK
+                            if (AMN && kb * BK + kk * UK >= kept) break;
                             if (F8) {
 #pragma unroll
                                 for (int tn = 0; tn < TN; tn++)
@@ -1682,7 +1689,7 @@ namespace moe {
 //   d_w2 = d_out^T hid, d_w1 = d_pre^T buf (d_w3 = d_b^T buf): the kept rows
 //   are the contraction, each expert over its own (an expert with none gets
 //   zeros), both operands read MN-major in place and each expert's partly
-//   kept last 64-row block from a zero-padded copy;
+//   kept last 64-row block from a zero-padded copy, all of them in one launch;
 //   d_b1, d_b2: column sums of d_pre, d_out over the kept rows.
 namespace {
 

