@@ -38,7 +38,8 @@ __device__ __forceinline__ void mma_row(float (&d)[4], const uint32_t (&a)[4], u
 template <int ACT, int NB, int FW>
 __global__ void __launch_bounds__(FW * 32, ACT == MOE_ACT_SWIGLU || NB > 1 ? 16 / FW : 32 / FW)
 ffn_few_kernel(const FewArgs g) {
-    if (ACT != FEW_OUT) pdl_enter();
+    pdl_enter();
+    if (status_bad(g.status)) return;
     constexpr bool SWI = ACT == MOE_ACT_SWIGLU;
     constexpr int M = SWI ? 2 : 1;
     __shared__ float part[FW][M][16][NB * 8 + 1];
@@ -50,26 +51,13 @@ ffn_few_kernel(const FewArgs g) {
         j += p <= y;
         bad |= o < 0 || p < o || p > g.so.n;
     }
-    j = __reduce_add_sync(0xffffffffu, j);
-    const bool none = __any_sync(0xffffffffu, bad) || j >= g.e;   // the same in every warp of the CTA
-    int64_t lo = 0, count = 0;
-    if (!none) sorted_span(g.so, j, lo, count);
-    const bool mine = !none && lo == y;
-    const int ch0 = blockIdx.x * 16;
-    if (ACT == FEW_OUT) {
-        // The offsets were there before the first product began, whose CTAs have all passed their own wait by
-        // now: this CTA's weights, 8 or 16 rows in a row, come into L2 while the last of those finish, if
-        // a line a thread does it (FFN, cold, with | without, us: 20 rows of 64 experts, 1024 x 704, 21.6 |
-        // 23.0; 20 rows of 8 experts of 4096 x 8192, 195 | 171: the first product still needs the memory).
-        const char *w0 = reinterpret_cast<const char *>(g.w + ((int64_t)j * g.n_out + ch0) * g.K);
-        const int64_t at = threadIdx.x * 128, bytes = (int64_t)min(16, g.n_out - ch0) * g.K * 2;
-        if (mine && bytes <= FW * 32 * 128 && at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + at));
-        pdl_enter();
-    }
-    if (status_bad(g.status)) return;
     if (bad) set_status(g.status, MOE_ERR_INVALID_ARG);
-    if (!mine) return;
-    const int gr = lane >> 2, t = lane & 3;
+    j = __reduce_add_sync(0xffffffffu, j);
+    if (__any_sync(0xffffffffu, bad) || j >= g.e) return;   // the same in every warp of the CTA
+    int64_t lo, count;
+    sorted_span(g.so, j, lo, count);
+    if (lo != y) return;
+    const int gr = lane >> 2, t = lane & 3, ch0 = blockIdx.x * 16;
     const int pieces = g.K / 8, groups = (pieces + 4 * FU - 1) / (4 * FU);
     const bool upper = ch0 + 8 < g.n_out;   // n_out is a multiple of 8: whole halves
     const V16 *wp[M][2];
