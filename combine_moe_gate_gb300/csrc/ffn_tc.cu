@@ -1579,12 +1579,17 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
     const uint64_t rows = so.offsets ? (uint64_t)so.n : (uint64_t)e * c_max;
     // fc1: 256-row tiles on CTA pairs (2-SM MMA), two accumulators per CTA so
     // its activation epilogue overlaps the next tile's main loop.
-    // fc2 (bias-only epilogue, long K, about one tile per pair): 256 x 512
-    // tiles on CTA pairs.
+    // fc2 (bias-only epilogue): the same tiles, or, from 24 rounds of them over the pairs on, 256 x 512 with one
+    // accumulator, which read less and whose uncovered epilogues and last round count for little then (FFN, us,
+    // 256 | 512; 16 experts of 2048 x 4096, 24576 rows, 5.5 rounds: 497 | 513; 64 of 1024 x 512, SwiGLU, 32800
+    // rows, 4 rounds: 114 | 135; 16 of 4096 x 4096, 40000 rows, 17 rounds: 1450 | 1660; 64 of 4096 x 8192,
+    // 131072 rows, 57 rounds: 11120 | 11030).
     constexpr int TM1 = 1, BK1 = 64, TM2 = 1, BK2 = 64;
-    constexpr int CL1 = 2, CL2 = 2, TN2 = 2;
+    constexpr int CL1 = 2, CL2 = 2;
     using T1 = Tiling<TM1, BK1, CL1>;
-    using T2 = Tiling<TM2, BK2, CL2, TN2>;
+    using T2 = Tiling<TM2, BK2, CL2>;
+    const int64_t row_tiles = so.offsets ? so.n / T2::BMT + (so.n < e ? so.n : e) / 2 : e * ((c_max + T2::BMT - 1) / T2::BMT);
+    const bool wide = row_tiles * ((m + 511) / 512) >= 24 * (int64_t)(sm_count() / 2);
     CUtensorMap mA1, mB1, mB3, mA2, mB2;
     const bool swiglu = act == MOE_ACT_SWIGLU;
     // one CTA's B box: a pair CTA's half tile, or a 1-SM SwiGLU tile's W1/W3 half
@@ -1594,7 +1599,7 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
         !make_map(&mB1, w1, (uint64_t)e * h, (uint64_t)m, b1_box, BK1) ||
         !make_map(&mB3, swiglu ? w3 : w1, (uint64_t)e * h, (uint64_t)m, b1_box, BK1) ||
         !make_map(&mA2, hid, rows, (uint64_t)h, T2::A_BOX_ROWS, BK2) ||
-        !make_map(&mB2, w2, (uint64_t)e * m, (uint64_t)h, T2::B_BOX_ROWS, BK2))
+        !make_map(&mB2, w2, (uint64_t)e * m, (uint64_t)h, wide ? 2 * T2::B_BOX_ROWS : T2::B_BOX_ROWS, BK2))
         return MOE_ERR_CUDA;
     GemmArgs g1{counts, c_dev, st, (const __nv_bfloat16 *)b1, (__nv_bfloat16 *)hid, c_max, e, m, h, h,
                 nullptr, nullptr, row_lo, row_hi};
@@ -1617,7 +1622,8 @@ moe_status ffn_tc_launch(const void *buf, const int32_t *counts, const int32_t *
                 nullptr, nullptr, row_lo, row_hi};
     g2.offsets = so.offsets;
     g2.n_rows = so.n;
-    return launch_gemm<EPI_BIAS, TM2, BK2, CL2, TN2>(mA2, mB2, mB2, g2, stream);
+    return wide ? launch_gemm<EPI_BIAS, TM2, BK2, CL2, 2>(mA2, mB2, mB2, g2, stream)
+                : launch_gemm<EPI_BIAS, TM2, BK2, CL2, 1>(mA2, mB2, mB2, g2, stream);
 }
 
 // ------------------------------------------------------------ e4m3 forward
