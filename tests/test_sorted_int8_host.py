@@ -52,6 +52,13 @@ def test_workspace_sizes():
 
 
 @no_gpu
+def test_products_leave_room_for_the_last_channel_tile():
+    """Channels are counted in 32 bits, and the last tile of them reaches past the end."""
+    for e, no in ((1, 2 ** 31 - 8), (1, 2 ** 31 - 256), (4, 2 ** 29 - 8)):
+        assert M.moe_product_int8_workspace_size(e, 8, 16, no) == 0
+    assert M.moe_product_int8_workspace_size(1, 8, 16, 2 ** 31 - 1024) > 0
+
+
 def test_sort_refuses():
     good = (A, 100, 8, 2, A, A, None, A, BIG, A, None)     # idx s e k rows offsets source ws bytes status stream
     check(M.load().moe_sort_routes, good,
