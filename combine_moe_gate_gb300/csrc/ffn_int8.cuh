@@ -119,8 +119,11 @@ struct I8Tile {
     int j, ct, row0, rows, n;    // expert, channel tile, first row, live rows, N
 };
 
-// Rows of a tile: even cuts, a multiple of 32.  (As rows > 192 (tiles - 1), none of the tiles is empty.)
-__device__ __forceinline__ int i8_cut(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) & ~31; }
+// Rows of a tile: even cuts, a multiple of 32.  (As rows > 192 (tiles - 1), none of the tiles is empty.  The sum
+// is unsigned: rows of more than 2^31 - 2^31 / 193 and their tiles pass 2^31.)
+__device__ __forceinline__ int i8_cut(int rows, int tiles) {
+    return (int)((((uint32_t)rows + (uint32_t)tiles - 1u) / (uint32_t)tiles + 31u) & ~31u);
+}
 
 // Tile t; an expert's row tiles vary fastest, so neighbouring CTAs read the same weights.
 __device__ __forceinline__ I8Tile i8_tile(const I8Ctl *ctl, int e, int t) {
