@@ -18,8 +18,6 @@ constexpr int ST_NT = 256, ST_NW = ST_NT / 32, ST_BLK = 256;                    
 constexpr int ST_HELD = 8;                                                        // rounds kept in registers
 constexpr int SORT_MAXB = 1025;                                                   // buckets
 
-constexpr int NO_ROUTE = (int)0x80000000;   // past the table's end (as an entry of it: an error like any other)
-
 __device__ __forceinline__ int bucket_of(int v, int e, int32_t *status) {
     if ((unsigned)v < (unsigned)e) return v;
     if (v != -1) set_status(status, MOE_ERR_INVALID_ARG);
@@ -143,15 +141,15 @@ sort_hist_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds, 
     __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * rounds * ST_NT;
     for (int r0 = 0; r0 < rounds; r0 += ST_HELD) {
-        int v[ST_HELD];   // all loads in flight before the first is looked at
+        // all loads in flight before the first is looked at; a place past the table's end is known by its
+        // position alone (an entry may hold any value)
+        int v[ST_HELD];
+        auto in_table = [&](int r) { return r0 + r < rounds && base + (r0 + r) * ST_NT + threadIdx.x < n; };
 #pragma unroll
-        for (int r = 0; r < ST_HELD; r++) {
-            const int64_t j = base + (r0 + r) * ST_NT + threadIdx.x;
-            v[r] = r0 + r < rounds && j < n ? __ldg(idx + j) : NO_ROUTE;
-        }
+        for (int r = 0; r < ST_HELD; r++) v[r] = in_table(r) ? __ldg(idx + base + (r0 + r) * ST_NT + threadIdx.x) : -1;
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++)
-            if (r0 + r < rounds) count_warp(cnt, v[r] != NO_ROUTE ? bucket_of(v[r], e, status) : -1, lt);
+            if (r0 + r < rounds) count_warp(cnt, in_table(r) ? bucket_of(v[r], e, status) : -1, lt);
     }
     __syncthreads();
     for (int q = threadIdx.x; q < nb; q += ST_NT) hist[(int64_t)q * gridDim.x + blockIdx.x] = cnt[q];
@@ -175,12 +173,10 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
     const unsigned lt = (1u << lane) - 1u;
     const int64_t at = ((int64_t)blockIdx.x * ST_NW + warp) * rounds * 32;
     int bucket[ST_HELD], rank[ST_HELD];
+    auto in_table = [&](int r) { return r < rounds && at + r * 32 + lane < n; };
     if (HELD) {
 #pragma unroll
-        for (int r = 0; r < ST_HELD; r++) {
-            const int64_t j = at + r * 32 + lane;
-            bucket[r] = r < rounds && j < n ? __ldg(idx + j) : NO_ROUTE;
-        }
+        for (int r = 0; r < ST_HELD; r++) bucket[r] = in_table(r) ? __ldg(idx + at + r * 32 + lane) : -1;
     }
     for (int q = tid; q < ST_NW * nb; q += ST_NT) cnt[q] = 0;
     // four buckets a turn: up to 32 loads under way before the first is added
@@ -215,7 +211,7 @@ sort_place_kernel(const int32_t *__restrict__ idx, int64_t n, int e, int rounds,
     if (HELD) {
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++)
-            bucket[r] = bucket[r] != NO_ROUTE ? bucket_of(bucket[r], e, status) : -1;
+            bucket[r] = in_table(r) ? bucket_of(bucket[r], e, status) : -1;
 #pragma unroll
         for (int r = 0; r < ST_HELD; r++) {
             if (r >= rounds) break;
