@@ -49,7 +49,7 @@ ffn_few_kernel(const FewArgs g) {
     for (int b = lane; b < g.e; b += 32) {   // experts that end at or before row y
         const int o = g.so.offsets[b], p = g.so.offsets[b + 1];
         j += p <= y;
-        bad |= o < 0 || p < o || p > g.so.n;
+        bad |= o < 0 || p < o || p > g.so.n || (b == 0 && o != 0);
     }
     if (bad) set_status(g.status, MOE_ERR_INVALID_ARG);
     j = __reduce_add_sync(0xffffffffu, j);

@@ -265,7 +265,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         if (args.so.offsets) {
             const int before = args.so.offsets[max(j - 1, 0)];
             o = args.so.offsets[j];
-            bad |= o < 0 || o > args.so.n || before > o;
+            bad |= o < 0 || o > args.so.n || before > o || (j == 0 && o != 0);
         }
         ctl->first[j] = o;
     }

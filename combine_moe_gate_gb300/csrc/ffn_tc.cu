@@ -752,7 +752,7 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         int kept;
         if (args.offsets) {
             const int lo = args.offsets[j], hi = args.offsets[j + 1];
-            if (lo < 0 || hi < lo || hi > args.n_rows) set_status(args.status, MOE_ERR_INVALID_ARG);
+            if (lo < 0 || hi < lo || hi > args.n_rows || (j == 0 && lo != 0)) set_status(args.status, MOE_ERR_INVALID_ARG);
             kept = max(0, in_rows(args, hi) - in_rows(args, lo));
         } else if (AMN) {
             kept = min(max(args.k_counts[j], 0), (int)min((int64_t)*args.k_cdev, (int64_t)args.K));

@@ -1,4 +1,4 @@
-"""Sorted rows where the calls can go wrong: idx entries outside the experts."""
+"""Sorted rows where the calls can go wrong: idx entries outside the experts, offsets that do not start at 0."""
 
 import pytest
 import torch
@@ -23,3 +23,22 @@ def test_order_reports_any_entry_outside_the_experts(s, entry):
     st = S.status()
     rows, offsets, source = S.sort(idx, 5, st)
     assert st.item() == 0 and rows[r, t].item() == -1 and source[-1].item() == -1
+
+
+# few rows (dot products) and many (tiles)
+@pytest.mark.parametrize("counts", [[10, 5, 3], [100, 20, 30]])
+@pytest.mark.parametrize("act", ["relu", "gelu", "swiglu"])
+def test_offsets_that_do_not_start_at_0_are_reported(counts, act):
+    p = S.experts(counts, 64, 64, act)
+    hid, pre, out = S.forward(p, act)
+    p["off"][0] = 3
+    n, st = p["n"], S.status()
+    M.moe_expert_ffn_sorted(p["x"], p["off"], p["w1"], p["b1"], p["w3"], p["w2"], p["b2"], act, torch.zeros_like(hid),
+                            torch.zeros_like(out), st)
+    assert st.item() == M.MOE_ERR_INVALID_ARG
+    st = S.status()
+    ws = torch.zeros(M.moe_expert_ffn_sorted_bwd_workspace_size(act, 3, n, 64, 64), dtype=torch.uint8, device="cuda")
+    g = {k: torch.zeros_like(p[k]) for k in ("x", "w1", "w2")}
+    M.moe_expert_ffn_sorted_bwd(p["x"], hid, pre, p["off"], p["w1"], p["w3"], p["w2"], act, p["d_out"], ws, g["x"], g["w1"],
+                                torch.zeros_like(p["w1"]) if act == "swiglu" else None, g["w2"], None, None, st)
+    assert st.item() == M.MOE_ERR_INVALID_ARG
