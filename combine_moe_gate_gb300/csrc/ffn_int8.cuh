@@ -1,5 +1,5 @@
 // Grouped products of 8-bit integer rows and weights on the tensor cores.  Included by ffn_tc.cu,
-// whose barrier, copy and TMEM helpers it shares.
+// whose barrier, copy and TMEM helpers it shares (and, of the 4-bit products, the GELU).
 //
 //   out[i, :] = act(s_x[i] s_w[j] (X[i] W[j]^T) + bias[j])   for the rows i of every expert j
 //
@@ -209,6 +209,13 @@ __device__ __forceinline__ bool i8_wait(uint64_t *b, uint32_t parity, int32_t *a
     for (int i = 0; i < 64; i++)
         if (mbar_try<CL>(b, parity)) return true;
     return mbar_wait<CL>(b, parity, abort_flag, status);
+}
+
+// GELU with a relative error, as the 4-bit products': a row that lies in the tail is scaled by it.  (There an
+// infinity becomes a NaN; both make the row's scale one.)
+__device__ __forceinline__ float2 i8_gelu2(float2 a) {
+    const float2 g = f4_gelu2(a);
+    return make_float2(a.x == INFINITY ? a.x : g.x, a.y == INFINITY ? a.y : g.y);
 }
 
 __device__ __forceinline__ float i8_relu(float v) { return v < 0.0f ? 0.0f : v; }   // a NaN stays one
@@ -543,7 +550,7 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         float2 a = make_float2(v[i], v[i + 1]);
-                        if (EPI == I8_GELU) a = gelu_erf2(a);
+                        if (EPI == I8_GELU) a = i8_gelu2(a);
                         if (EPI == I8_RELU) a = make_float2(i8_relu(a.x), i8_relu(a.y));
                         if constexpr (sizeof(OUT) == 2) {
                             sp[i * 32 + lane] = __float2bfloat16_rn(a.x);

@@ -306,7 +306,9 @@ int8_few_kernel(const FewArgs g) {
                     const float b = g.bias ? __bfloat162float(g.bias[at]) : 0.0f;
                     float v = __fmaf_rn(__int2float_rn(acc[c][r]), sx * g.w_scale[at], b);
                     if (ACT == I8_RELU) v = v < 0.0f ? 0.0f : v;
-                    if (ACT == I8_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+                    if (ACT == I8_GELU)   // Phi(v) from below where v is negative: no cancellation in the tail
+                        v = v < 0.0f ? v * 0.5f * erfcf(-v * 0.70710678118654752f)
+                                     : v * (1.0f - 0.5f * erfcf(v * 0.70710678118654752f));
                     if constexpr (sizeof(OUT) == 2)
                         static_cast<__nv_bfloat16 *>(g.out)[(r0 + r) * g.n_out + ch + c] = __float2bfloat16_rn(v);
                     else

@@ -680,11 +680,12 @@ size_t moe_expert_ffn_int8_workspace_size(moe_act act, int e, int64_t n, int m, 
  *   hid = bf16(act(x . w1^T + b1)), or bf16(silu(x . w1^T) * (x . w3^T)) (SwiGLU, no
  *         biases), quantised by rows as moe_quantize_rows_int8 does;
  *   out = bf16(hid . w2^T + b2),
- * the products as moe_product_int8 forms them.  x_q [n, m], x_scale [n]; w1, w3
- * [e, h, m], w2 [e, m, h] int8 with scales [e, h], [e, h], [e, m]; b1 [e, h], b2
- * [e, m] bf16 or NULL; out [n, m] bf16.  m and h multiples of 16 below 2^17.
- * Workspace: the hidden [n, h] bf16, then, from the next 256-byte boundary, its
- * scales [n]; a caller may read them after the call.
+ * the products as moe_product_int8 forms them.  GELU within 1e-3 of its value down to
+ * a pre-activation of -8 (a row is scaled by its maximum, which may lie there).
+ * x_q [n, m], x_scale [n]; w1, w3 [e, h, m], w2 [e, m, h] int8 with scales [e, h],
+ * [e, h], [e, m]; b1 [e, h], b2 [e, m] bf16 or NULL; out [n, m] bf16.  m and h
+ * multiples of 16 below 2^17.  Workspace: the hidden [n, h] bf16, then, from the next
+ * 256-byte boundary, its scales [n]; a caller may read them after the call.
  */
 moe_status moe_expert_ffn_int8(const void *x_q, const float *x_scale, const int32_t *offsets,
                                const void *w1_q, const float *w1_scale, const void *b1,
