@@ -233,6 +233,13 @@ __device__ __forceinline__ void sorted_span(const SortedRows &so, int j, int64_t
     count = max((int64_t)0, min((int64_t)max(so.offsets[j + 1], 0), so.n) - first);
 }
 
+// max(v, 0); a NaN stays one (fmaxf would make it 0).
+__device__ __forceinline__ float relu_nan(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(0.0f));
+    return r;
+}
+
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 }  // namespace moe

@@ -120,7 +120,7 @@ ffn_few_kernel(const FewArgs g) {
                 pre[0] = __float2bfloat16_rn(v);
                 if (SWI) pre[g.n_out] = __float2bfloat16_rn(sum[M - 1]);
             }
-            if (ACT == MOE_ACT_RELU) v = fmaxf(v, 0.0f);   // as the tiles do it
+            if (ACT == MOE_ACT_RELU) v = relu_nan(v);
             if (ACT == MOE_ACT_GELU)   // Phi(v) from below where v is negative: no cancellation in the tail
                 v = v < 0.0f ? v * 0.5f * erfcf(-v * 0.70710678118654752f)
                              : v * (1.0f - 0.5f * erfcf(v * 0.70710678118654752f));

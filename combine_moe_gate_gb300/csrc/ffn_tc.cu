@@ -1355,7 +1355,9 @@ tc_group_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                                                   : __fadd2_rn(acc2, bb[i]);
                                     if (SAVE) pp[q * 4 + i] = pack_bf16(a.x, a.y);
                                     if (GELU) a = gelu_erf2(a);
-                                    else if (RELU) a = make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
+                                    else if (RELU)   // on sorted rows a NaN stays one
+                                        a = !F8 && args.offsets ? make_float2(relu_nan(a.x), relu_nan(a.y))
+                                                                : make_float2(fmaxf(a.x, 0.0f), fmaxf(a.y, 0.0f));
                                     if constexpr (F32OUT) {
                                         of[q * 8 + 2 * i] = a.x;
                                         of[q * 8 + 2 * i + 1] = a.y;

@@ -609,7 +609,8 @@ moe_status moe_decode_sorted_bwd(const void *dy, const void *xs, moe_dtype dt, c
  * [n, 2h], rounded to bf16, for moe_expert_ffn_sorted_bwd.  x, out [n, m]; offsets
  * [e+1] int32 on the device, ascending from 0 to at most n (else, in every call on
  * sorted rows, MOE_ERR_INVALID_ARG in dev_status and unspecified rows inside the
- * buffers); weights and biases as moe_expert_ffn.  bf16 only.
+ * buffers); weights and biases as moe_expert_ffn.  A NaN in a row makes that row of
+ * hid and out NaN, under ReLU too, and no other.  bf16 only.
  */
 moe_status moe_expert_ffn_sorted(const void *x, moe_dtype dt, const int32_t *offsets,
                                  const void *w1, const void *b1, const void *w3, const void *w2,

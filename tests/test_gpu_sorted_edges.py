@@ -1,4 +1,5 @@
-"""Sorted rows where the calls can go wrong: idx entries outside the experts, offsets that do not start at 0."""
+"""Sorted rows where the calls can go wrong: idx entries outside the experts, offsets that do not start at 0, and a
+NaN in a live row."""
 
 import pytest
 import torch
@@ -42,3 +43,16 @@ def test_offsets_that_do_not_start_at_0_are_reported(counts, act):
     M.moe_expert_ffn_sorted_bwd(p["x"], hid, pre, p["off"], p["w1"], p["w3"], p["w2"], act, p["d_out"], ws, g["x"], g["w1"],
                                 torch.zeros_like(p["w1"]) if act == "swiglu" else None, g["w2"], None, None, st)
     assert st.item() == M.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("counts", [[5, 9, 2], [40, 0, 300]])
+@pytest.mark.parametrize("act", ["relu", "gelu", "swiglu"])
+@pytest.mark.parametrize("train", [False, True])
+def test_a_nan_stays_in_its_row(counts, act, train):
+    p = S.experts(counts, 72, 136, act)
+    T, at = p["total"], 7
+    p["x"][at, 3] = float("nan")
+    hid, pre, out = S.forward(p, act, train=train)
+    for t in (hid, out) + ((pre,) if train else ()):
+        assert t[at].isnan().all()
+        assert not t[:at].isnan().any() and not t[at + 1:T].isnan().any()
