@@ -227,6 +227,12 @@ __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int acc) {
     return __dp4a((int)a.w, (int)b.w, acc);
 }
 
+// acc * (sx * sw) + bias (a bias of -0: the product alone)
+__device__ __forceinline__ float scaled(int acc, float sx, float sw, float bias) {
+    return i8_scales_ok(fabsf(sx), fabsf(sw)) ? __fmaf_rn(__int2float_rn(acc), sx * sw, bias)
+                                              : i8_scaled_far((double)acc, sx, sw, bias);
+}
+
 template <int ACT, int R, typename OUT>
 __global__ void __launch_bounds__(256)
 int8_few_kernel(const FewArgs g) {
@@ -284,37 +290,32 @@ int8_few_kernel(const FewArgs g) {
                 }
             }
         }
+        // lane r * CH + c finishes row r's channel c (SwiGLU: lane r, of both sums), all of them at once
+        constexpr int CH = SWI ? 1 : CPW;
+        int sum[CPW] = {};
 #pragma unroll
-        for (int r = 0; r < R; r++) {
+        for (int r = 0; r < R; r++)
 #pragma unroll
-            for (int c = 0; c < CPW; c++) acc[c][r] = __reduce_add_sync(0xffffffffu, acc[c][r]);
-            if (r0 + r >= lo + count) continue;
-            const float sx = g.x_scale[r0 + r];
-            if constexpr (SWI) {
-                if (lane == 0) {
-                    const int64_t at = (int64_t)j * g.n_out + ch;
-                    const float a = __int2float_rn(acc[0][r]) * (sx * g.w_scale[at]);
-                    const float b = __int2float_rn(acc[1][r]) * (sx * g.w3_scale[at]);
-                    static_cast<__nv_bfloat16 *>(g.out)[(r0 + r) * g.n_out + ch] =
-                        __float2bfloat16_rn(a / (1.0f + expf(-a)) * b);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < CPW; c++) {   // n_out is even
-                    if (lane != c) continue;
-                    const int64_t at = (int64_t)j * g.n_out + ch + c;
-                    const float b = g.bias ? __bfloat162float(g.bias[at]) : 0.0f;
-                    float v = __fmaf_rn(__int2float_rn(acc[c][r]), sx * g.w_scale[at], b);
-                    if (ACT == I8_RELU) v = v < 0.0f ? 0.0f : v;
-                    if (ACT == I8_GELU)   // Phi(v) from below where v is negative: no cancellation in the tail
-                        v = v < 0.0f ? v * 0.5f * erfcf(-v * 0.70710678118654752f)
-                                     : v * (1.0f - 0.5f * erfcf(v * 0.70710678118654752f));
-                    if constexpr (sizeof(OUT) == 2)
-                        static_cast<__nv_bfloat16 *>(g.out)[(r0 + r) * g.n_out + ch + c] = __float2bfloat16_rn(v);
-                    else
-                        static_cast<float *>(g.out)[(r0 + r) * g.n_out + ch + c] = v;
-                }
+            for (int c = 0; c < CPW; c++) {
+                const int s = __reduce_add_sync(0xffffffffu, acc[c][r]);
+                if (lane == r * CH + (SWI ? 0 : c)) sum[SWI ? c : 0] = s;
             }
+        const int64_t row = r0 + lane / CH;
+        if (lane >= R * CH || row >= lo + count) continue;
+        const int64_t at = (int64_t)j * g.n_out + ch + lane % CH, to = row * g.n_out + ch + lane % CH;   // n_out is even
+        const float sx = g.x_scale[row];
+        if constexpr (SWI) {
+            const float a = scaled(sum[0], sx, g.w_scale[at], -0.0f), b = scaled(sum[1], sx, g.w3_scale[at], -0.0f);
+            static_cast<__nv_bfloat16 *>(g.out)[to] = __float2bfloat16_rn(a / (1.0f + expf(-a)) * b);
+        } else {
+            float v = scaled(sum[0], sx, g.w_scale[at], g.bias ? __bfloat162float(g.bias[at]) : 0.0f);
+            if (ACT == I8_RELU) v = v < 0.0f ? 0.0f : v;
+            if (ACT == I8_GELU) {   // Phi(v) from below where v is negative: no cancellation in the tail
+                const float t = 0.5f * erfcf(fabsf(v) * 0.70710678118654752f);
+                v *= v < 0.0f ? t : 1.0f - t;
+            }
+            if constexpr (sizeof(OUT) == 2) static_cast<__nv_bfloat16 *>(g.out)[to] = __float2bfloat16_rn(v);
+            else static_cast<float *>(g.out)[to] = v;
         }
     }
 }

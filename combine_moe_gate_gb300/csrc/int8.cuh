@@ -18,6 +18,16 @@ __device__ __forceinline__ void i8_widen(uint32_t w, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<const uint32_t *>(&b);
 }
 
+// The two scales' product is formed first where it is a normal number (or a factor is 0, infinite or a NaN, which
+// it shows as well); elsewhere it would lose its bits, or be an infinity that a sum of 0 makes a NaN, so there all
+// factors meet in 64 bits, where the scales' product is exact.
+__device__ __forceinline__ bool i8_scales_ok(float a, float b) {   // a, b: magnitudes
+    const float p = a * b;
+    return (p >= 1.17549435e-38f && p <= 3.40282347e38f) || !(a > 0.0f && a < INFINITY) || !(b > 0.0f && b < INFINITY);
+}
+__device__ __forceinline__ float i8_scaled_far(double sum, float a, float b, float bias) {
+    return (float)fma(sum, (double)a * (double)b, (double)bias);
+}
 
 enum I8Act { I8_BIAS = 0, I8_RELU = 1, I8_GELU = 2, I8_SWIGLU = 3 };   // what becomes of a sum
 

@@ -1,5 +1,5 @@
 """8-bit integer experts where the calls can go wrong: offsets that do not start at 0, hidden rows in GELU's
-tail."""
+tail, and scales whose product leaves fp32's range."""
 
 import pytest
 import torch
@@ -9,8 +9,8 @@ import test_gpu_int8 as S
 
 pytestmark = pytest.mark.gpu
 
-BF, I8 = torch.bfloat16, torch.int8
-HALF = S.HALF
+BF, F32, I8 = torch.bfloat16, torch.float32, torch.int8
+HALF, U = S.HALF, S.U
 
 
 @pytest.mark.parametrize("n", [2, 6, 90])
@@ -59,3 +59,50 @@ def test_gelu_of_a_row_in_the_tail(e, rows):
     S.near(hid, want, rel * want.abs(), "hid")
     top = want.abs().amax(1, keepdim=True)
     S.near(out, want[:, :m], 0.5 / 127 * 1.01 * top + (rel + HALF[BF] * 1.01) * want[:, :m].abs(), "out")
+
+
+# (row scale, channel scale) whose product is subnormal, below the smallest number, too large; and one of each
+# beside ordinary ones.  few rows (dot products) and many (tiles)
+@pytest.mark.parametrize("sx,sw", [(2.0 ** -70, 1.4 * 2.0 ** -72), (2.0 ** -80, 1.3 * 2.0 ** -76), (2.0 ** 70, 1.7 * 2.0 ** 60),
+                                   (2.0 ** 100, 2.0 ** -100), (2.0 ** -107, 2.0 ** -30)])
+@pytest.mark.parametrize("n", [2, 90])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_product_of_scales_far_from_1(sx, sw, n, mixed):
+    k, n_out = 512, 136
+    a, w = S.codes((n, k), 1), S.codes((1, n_out, k), 2)
+    a[n // 2] = 0                                         # 0 times whatever the scales are
+    ra = (torch.rand(n, generator=S.gen(3), device="cuda") + 0.5) * sx
+    cw = (torch.rand((1, n_out), generator=S.gen(4), device="cuda") + 0.5) * sw
+    if mixed:
+        ra[1::2] /= sx
+        cw[:, ::3] /= sw
+    out = S.product(a, ra, None, w, cw, None, F32)
+    acc = a.double() @ w[0].double().t()                  # exact: k <= 1024
+    want = acc * (ra.double()[:, None] * cw[0].double())
+    over = want.abs() >= 2.0 ** 128 * (1 - 2.0 ** -25)    # rounds to an infinity
+    assert torch.equal(out.double().isinf(), over)
+    bound = 4 * U * want.abs() + 2.0 ** -149              # three roundings, or one to a subnormal number
+    S.near(torch.where(over, 0.0, out), torch.where(over, 0.0, want), bound)
+    assert (out[n // 2] == 0).all()
+
+
+@pytest.mark.parametrize("n", [2, 90])
+def test_gated_hidden_of_scales_far_from_1(n):
+    """silu of a tiny a times a huge b is an ordinary number: a's scales multiply to a subnormal one."""
+    m = h = 64
+    x, w = S.codes((n, m), 1), S.codes((1, h, m), 2)
+    w3, w2 = S.codes((1, h, m), 3), S.codes((1, m, h), 4)
+    sx = torch.full((n,), 2.0 ** -70, device="cuda")
+    s1 = (torch.rand((1, h), generator=S.gen(5), device="cuda") + 0.5) * 2.0 ** -72
+    s3 = (torch.rand((1, h), generator=S.gen(6), device="cuda") + 0.5) * 2.0 ** 110
+    s2 = torch.ones((1, m), device="cuda")
+    ws = torch.zeros(M.moe_expert_ffn_int8_workspace_size("swiglu", 1, n, m, h), dtype=torch.uint8, device="cuda")
+    out, st = torch.zeros((n, m), dtype=BF, device="cuda"), S.status()
+    M.moe_expert_ffn_int8(x, sx, None, w, s1, None, w3, s3, w2, s2, None, "swiglu", ws, out, st)
+    assert st.item() == 0
+    a = x.double() @ w[0].double().t() * (sx.double()[:, None] * s1[0].double())
+    b = x.double() @ w3[0].double().t() * (sx.double()[:, None] * s3[0].double())
+    want = a / (1 + torch.exp(-a)) * b
+    hid = ws[: n * h * 2].view(BF).view(n, h)
+    # a: one rounding of 2^-24, or to a subnormal's 2^-150; b: two; silu 8 and its product one
+    S.near(hid, want, (HALF[BF] * 1.01 + 16 * U) * want.abs() + 2.0 ** -149 * b.abs(), "hid")
