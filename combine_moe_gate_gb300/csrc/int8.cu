@@ -323,13 +323,11 @@ int8_few_kernel(const FewArgs g) {
 template <int ACT, typename OUT>
 moe_status few_launch(const FewArgs &g, cudaStream_t stream) {
     const int per = 8 * (ACT == I8_SWIGLU ? 1 : CPW);
-    // rows a CTA meets: all of them with one expert, seldom more than two of an expert's with many
     const dim3 grid((unsigned)((g.n_out + per - 1) / per), (unsigned)(g.so.offsets ? g.so.n : 1));
-    const int64_t meet = g.e == 1 ? g.so.n : g.so.n < 2 ? g.so.n : 2;
-    if (meet == 1) return launch_pdl(int8_few_kernel<ACT, 1, OUT>, grid, dim3(256), 0, stream, g);
-    if (meet == 2) return launch_pdl(int8_few_kernel<ACT, 2, OUT>, grid, dim3(256), 0, stream, g);
-    if (meet <= 4) return launch_pdl(int8_few_kernel<ACT, 4, OUT>, grid, dim3(256), 0, stream, g);
-    return launch_pdl(int8_few_kernel<ACT, 8, OUT>, grid, dim3(256), 0, stream, g);
+    // rows in one pass over an expert's weights: up to 4 experts get two rows in all, and of many experts few
+    // have more than two
+    if (g.so.n == 1) return launch_pdl(int8_few_kernel<ACT, 1, OUT>, grid, dim3(256), 0, stream, g);
+    return launch_pdl(int8_few_kernel<ACT, 2, OUT>, grid, dim3(256), 0, stream, g);
 }
 
 moe_status few(int act, bool f32, const FewArgs &g, cudaStream_t stream) {
