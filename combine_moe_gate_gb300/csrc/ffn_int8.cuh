@@ -481,20 +481,9 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 sb = SWI && lane >= 16 ? args.w3_scale[at] : args.w_scale[at];
                 if (!SWI && args.bias) bias = __bfloat162float(args.bias[at]);
             }
-            uint32_t least = 0x7F7FFFFFu, most = 0u;   // finite magnitudes above 0 of the rows' scales
-            for (int r = lane; r < T.n; r += 32) {
-                ssc[r] = r < T.rows ? args.x_scale[(int64_t)T.row0 + r] : 0.0f;
-                const uint32_t u = __float_as_uint(ssc[r]) & 0x7FFFFFFFu;
-                if (u - 1u < 0x7F7FFFFFu) {
-                    least = min(least, u);
-                    most = max(most, u);
-                }
-            }
-            least = __reduce_min_sync(0xffffffffu, least);
-            most = __reduce_max_sync(0xffffffffu, most);
-            // whether every row's scale goes with this warp's channels', which they do in models
-            const bool near = __all_sync(0xffffffffu, i8_scales_ok(__uint_as_float(least), fabsf(sb)) &&
-                                                          i8_scales_ok(__uint_as_float(most), fabsf(sb)));
+            const I8Scale w = i8_scale(sb);
+            const float2 ws = make_float2(w.s, w.s), wu = make_float2(w.up, w.up), bias2 = make_float2(bias, bias);
+            for (int r = lane; r < T.n; r += 32) ssc[r] = r < T.rows ? args.x_scale[(int64_t)T.row0 + r] : 0.0f;
             __syncwarp();
             const bool ok = i8_wait<true>(&ctl->dfull[i & 1], (i >> 1) & 1, abort_flag, args.status);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -518,19 +507,14 @@ i8_group_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 tmem_wait_ld(r);
                 if (q + 1 == both) next_tile();
                 float v[32];
-                if (!near) {
+                // as i8_scaled, two rows at a time
 #pragma unroll
-                    for (int i = 0; i < 32; i++)
-                        v[i] = i8_scaled_far((double)__uint_as_float(r[i]), ssc[c0 + i], sb, bias);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 sa = *reinterpret_cast<const float4 *>(ssc + c0 + i);
-                        v[i] = __fmaf_rn(__uint_as_float(r[i]), sa.x * sb, bias);
-                        v[i + 1] = __fmaf_rn(__uint_as_float(r[i + 1]), sa.y * sb, bias);
-                        v[i + 2] = __fmaf_rn(__uint_as_float(r[i + 2]), sa.z * sb, bias);
-                        v[i + 3] = __fmaf_rn(__uint_as_float(r[i + 3]), sa.w * sb, bias);
-                    }
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 sum = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                    const float2 sa = *reinterpret_cast<const float2 *>(ssc + c0 + i);
+                    const float2 o = __ffma2_rn(__fmul2_rn(__fmul2_rn(sum, ws), sa), wu, bias2);
+                    v[i] = o.x;
+                    v[i + 1] = o.y;
                 }
                 if constexpr (SWI) {
                     // lane l < 16 holds a, lane l + 16 b of a channel: the first takes rows 0-15, the

@@ -227,12 +227,6 @@ __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int acc) {
     return __dp4a((int)a.w, (int)b.w, acc);
 }
 
-// acc * (sx * sw) + bias (a bias of -0: the product alone)
-__device__ __forceinline__ float scaled(int acc, float sx, float sw, float bias) {
-    return i8_scales_ok(fabsf(sx), fabsf(sw)) ? __fmaf_rn(__int2float_rn(acc), sx * sw, bias)
-                                              : i8_scaled_far((double)acc, sx, sw, bias);
-}
-
 template <int ACT, int R, typename OUT>
 __global__ void __launch_bounds__(256)
 int8_few_kernel(const FewArgs g) {
@@ -305,10 +299,12 @@ int8_few_kernel(const FewArgs g) {
         const int64_t at = (int64_t)j * g.n_out + ch + lane % CH, to = row * g.n_out + ch + lane % CH;   // n_out is even
         const float sx = g.x_scale[row];
         if constexpr (SWI) {
-            const float a = scaled(sum[0], sx, g.w_scale[at], -0.0f), b = scaled(sum[1], sx, g.w3_scale[at], -0.0f);
+            const float a = i8_scaled(__int2float_rn(sum[0]), sx, i8_scale(g.w_scale[at]), 0.0f);
+            const float b = i8_scaled(__int2float_rn(sum[1]), sx, i8_scale(g.w3_scale[at]), 0.0f);
             static_cast<__nv_bfloat16 *>(g.out)[to] = __float2bfloat16_rn(a / (1.0f + expf(-a)) * b);
         } else {
-            float v = scaled(sum[0], sx, g.w_scale[at], g.bias ? __bfloat162float(g.bias[at]) : 0.0f);
+            float v = i8_scaled(__int2float_rn(sum[0]), sx, i8_scale(g.w_scale[at]),
+                                g.bias ? __bfloat162float(g.bias[at]) : 0.0f);
             if (ACT == I8_RELU) v = v < 0.0f ? 0.0f : v;
             if (ACT == I8_GELU) {   // Phi(v) from below where v is negative: no cancellation in the tail
                 const float t = 0.5f * erfcf(fabsf(v) * 0.70710678118654752f);
@@ -342,7 +338,9 @@ moe_status few(int act, bool f32, const FewArgs &g, cudaStream_t stream) {
 // Whether n rows in all go by dot products.  Each row costs them time, the tiles hardly any, so that the rows an
 // expert has decide, of which the host knows only the average (FFN, cold, dot products | tiles, us): 1 expert
 // 4096 x 8192, 2 rows 34 | 52, 4 rows 53 | 52; 8 experts of that size, 4 rows 56 | 56, 8 rows 83 | 74; 64 experts
-// 1024 x 704, 32 rows 32 | 39, 64 rows 48 | 48; 256 experts 2048 x 512, 64 rows 70 | 75.
+// 1024 x 704, 32 rows 32 | 39, 64 rows 48 | 48; 256 experts 2048 x 512, 64 rows 70 | 75.  That is spread routing.
+// With all rows on one expert, whose weights are then read once for every two rows, this is the slower side (SwiGLU;
+// 64 experts 1024 x 704, 16 rows 38, 32 rows 62 | 28; 256 experts 2048 x 512, 32 rows 83, 64 rows 150 | 34).
 bool few_rows8(int64_t n, int e) { return n <= (e <= 4 ? 2 : e < 128 ? e / 2 : 64); }
 
 constexpr int64_t up256(int64_t b) { return (b + 255) & ~(int64_t)255; }

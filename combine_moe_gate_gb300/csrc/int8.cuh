@@ -18,15 +18,19 @@ __device__ __forceinline__ void i8_widen(uint32_t w, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// The two scales' product is formed first where it is a normal number (or a factor is 0, infinite or a NaN, which
-// it shows as well); elsewhere it would lose its bits, or be an infinity that a sum of 0 makes a NaN, so there all
-// factors meet in 64 bits, where the scales' product is exact.
-__device__ __forceinline__ bool i8_scales_ok(float a, float b) {   // a, b: magnitudes
-    const float p = a * b;
-    return (p >= 1.17549435e-38f && p <= 3.40282347e38f) || !(a > 0.0f && a < INFINITY) || !(b > 0.0f && b < INFINITY);
+// A channel's scale, as s * up with |s| in 2^-126 .. 2^96 (up is 1 but for scales of no model): a sum, in magnitude 0
+// or 1 to 2^31, times s is 0 or a normal number, and that times the row's scale loses bits or overflows only where
+// the result does.  (Row scale times channel scale first would lose bits below 2^-126 and be an infinity above
+// 2^128, which a sum of 0 makes a NaN.)
+struct I8Scale { float s, up; };
+__device__ __forceinline__ I8Scale i8_scale(float w) {
+    const float a = fabsf(w);
+    if (a > 7.9228163e28f && a < INFINITY) return {w * 5.421010862427522e-20f, 1.8446744073709552e19f};   // 2^-64, 2^64
+    if (a < 1.17549435e-38f) return {w * 1.8446744073709552e19f, 5.421010862427522e-20f};
+    return {w, 1.0f};
 }
-__device__ __forceinline__ float i8_scaled_far(double sum, float a, float b, float bias) {
-    return (float)fma(sum, (double)a * (double)b, (double)bias);
+__device__ __forceinline__ float i8_scaled(float sum, float row, const I8Scale &w, float bias) {
+    return __fmaf_rn(__fmul_rn(__fmul_rn(sum, w.s), row), w.up, bias);
 }
 
 enum I8Act { I8_BIAS = 0, I8_RELU = 1, I8_GELU = 2, I8_SWIGLU = 3 };   // what becomes of a sum

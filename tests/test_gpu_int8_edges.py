@@ -106,3 +106,18 @@ def test_gated_hidden_of_scales_far_from_1(n):
     hid = ws[: n * h * 2].view(BF).view(n, h)
     # a: one rounding of 2^-24, or to a subnormal's 2^-150; b: two; silu 8 and its product one
     S.near(hid, want, (HALF[BF] * 1.01 + 16 * U) * want.abs() + 2.0 ** -149 * b.abs(), "hid")
+
+
+@pytest.mark.parametrize("n", [2, 90])
+def test_scales_far_from_1_change_no_other_row_or_channel(n):
+    """The same bits beside rows and channels of extreme scales as beside ordinary ones."""
+    k, n_out = 528, 136
+    a, w = S.codes((n, k), 1), S.codes((1, n_out, k), 2)
+    ra = torch.rand(n, generator=S.gen(3), device="cuda") + 0.5
+    cw = torch.rand((1, n_out), generator=S.gen(4), device="cuda") + 0.5
+    bias = torch.randn((1, n_out), generator=S.gen(5), device="cuda").bfloat16()
+    out = S.product(a, ra, None, w, cw, bias, F32)
+    ra[::2] *= 2.0 ** -70
+    cw[:, 1::3] *= 2.0 ** -75
+    far = S.product(a, ra, None, w, cw, bias, F32)
+    assert torch.equal(out[1::2, ::3], far[1::2, ::3]) and torch.equal(out[1::2, 2::3], far[1::2, 2::3])
