@@ -2,8 +2,8 @@
 //
 //   hid = act(x W1^T + b1), or silu(x W1^T) * (x W3^T); out = hid W2^T + b2
 //
-// Bound by the weights' bytes, so the weights are read once for up to 32 rows and little else is asked of the
-// multiprocessor.  A CTA owns 16 output channels (SwiGLU: of W1 and of W3); its warps share K, 256 bytes
+// Bound by the weights' bytes, so the weights are read once for up to 32 rows of one expert (of many: once for every
+// 8 rows) and little else is asked of the multiprocessor.  A CTA owns 16 output channels (SwiGLU: of W1 and of W3); its warps share K, 256 bytes
 // of a channel's row at a time, and add up in shared memory in order.  The arithmetic is mma.sync
 // (16 channels x 8 rows): tcgen05 would want 128 channels, and too few CTAs would then hold the loads.
 // A sum may take its terms in any order, so the MMAs' K slots are filled as the loads come: lane 4 g + t
@@ -154,7 +154,10 @@ moe_status few_typed(const FewArgs &g, cudaStream_t stream) {
 // Whether n rows in all go this way: more rows an expert, of which the host knows only the average, cost more here
 // and nothing there (FFN, cold, here | tiles, us): 1 expert 4096 x 8192, 1 row 34 | 110, 16 rows 56 | 109, 32
 // rows 91 | 108, 64 rows 173 | 110; 8 experts of that size, 16 rows 174 | 204, 32 rows 189 | 204, 48 rows 243 | 204;
-// 64 experts 1024 x 704, 64 rows 45 | 67, 128 rows 65 | 72; 256 experts 2048 x 512, 128 rows 128 | 155.
+// 64 experts 1024 x 704, 64 rows 45 | 67, 128 rows 65 | 72; 256 experts 2048 x 512, 128 rows 128 | 155.  That is
+// spread routing.  With all rows on one expert, whose weights are then read once for every eight rows, many rows are
+// slower here (SwiGLU; 64 experts 1024 x 704, 32 rows 21, 64 rows 35, 128 rows 58 | 38; 256 experts 2048 x 512, 32 rows
+// 31, 64 rows 52, 128 rows 95 | 42).
 bool few_rows(int64_t n, int e) { return n <= (e <= 16 ? 32 : e < 64 ? 2 * e : 128); }
 
 moe_status ffn_few_launch(const void *x, const SortedRows &so, const void *w1, const void *b1, const void *w3,

@@ -30,7 +30,7 @@
 //   N <= 192   accumulators at 0 and 128,  3 stages from 320: they share columns 128 .. 191, so the next
 //              tile's MMAs wait until the epilogue has read those
 //
-// Measured (GB300).  8 experts, 16384 rows, 4096 <-> 8192: 575 us (GELU) and 550 us, 1.91 and 2.00 PFLOP/s, the
+// Measured (GB300).  8 experts, 16384 rows, 4096 <-> 8192: 582 us (GELU) and 546 us, 1.89 and 2.01 PFLOP/s, the
 // tensor pipe active 83% and 88% of the time: bound by it.  Decoding over 256 SwiGLU experts, 7168 x 2048: 480 and
 // 225 us, the weights at 5.8 and 6.1 TB/s: bound by HBM.  16 experts, 2000 tokens x 2, 2048 -> 1048: 27 us, two
 // tiles for most pairs: set-up 3 us, two main loops of 5 us, the last epilogue 2.5 us.

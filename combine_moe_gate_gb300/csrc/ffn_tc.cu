@@ -1670,8 +1670,8 @@ moe_status ffn_tc_fp8_launch(const void *buf_q, const float *buf_scale, const in
 
 }  // namespace moe
 
-// The expert-FFN backward, appended after the forward (the code above is
-// the forward GEMM unchanged).
+// The expert-FFN backward: the kernel above in its derivative, MN-major and
+// weight-gradient modes.
 #include "ffn_bwd.cuh"
 
 namespace moe {

@@ -296,7 +296,8 @@ __device__ __forceinline__ float reduce_many(float (&v)[KG], int lane) {
     return v[0];
 }
 
-// CTAs a multiprocessor: what the loads in flight and the sums leave room for without spills.
+// CTAs a multiprocessor: what the loads in flight and the sums leave room for (six forms spill 8 to 52 bytes a thread, the
+// most at one route a token with dot products).
 template <int MODE, int KG, int U>
 constexpr int mv_ctas() {
     return KG * U >= 8 ? 2 : MODE & DOTS ? 3 : 4;

@@ -664,10 +664,9 @@ size_t moe_product_int8_workspace_size(int e, int64_t n, int k, int n_out);
  * rounded once to `odt`.  a_q [n, k] int8 with a_scale [n]; b_q [e, n_out, k] int8
  * with b_scale [e, n_out] (one per output channel); bias [e, n_out] bf16 or NULL;
  * out [n, n_out].  Codes may take all of -128 .. 127, scales any value (their product
- * may leave fp32's range).  The sum is exact while its
- * partial sums stay below 2^24 (for k <= 1024 always); beyond it is an fp32 sum (of
- * few rows it is exact all the same).  k a multiple of 16 below 2^17, n_out a
- * multiple of 8.
+ * may leave fp32's range).  The sum is exact while its partial sums stay below 2^24
+ * (for k <= 1024 always); beyond it is an fp32 sum (of few rows it is exact all the
+ * same).  k a multiple of 16 below 2^17, n_out a multiple of 8.
  */
 moe_status moe_product_int8(const void *a_q, const float *a_scale, const int32_t *offsets,
                             const void *b_q, const float *b_scale, const void *bias, int e,
